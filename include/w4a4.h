@@ -291,6 +291,110 @@ w4a4_status svdq_lowrank_split(const void* w, const void* smooth_factor, int64_t
 w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t ldy, int64_t rows, int64_t cols,
                                     int32_t block, int32_t dtype, void* stream);
 
+/* ---- W8A8 layer -----------------------------------------------------------------------------
+ * An 8-bit linear layer beside the 4-bit ones, for layers that four bits hurt (the modules a
+ * checkpoint lists as not to convert): signed int8 weights with one scale per output channel,
+ * activations quantized to int8 with one scale per token, the same smoothing, the same fused block
+ * rotation, an optional bias.  Per row m of x:
+ *   x_s  = float32(x) / float32(smooth_factor)   (IEEE; no smooth_factor: x_s = x; quotients below
+ *          2^-110 in magnitude count as 0)
+ *   v    = x_s, or x_s @ H_B^T on every B-block (as in svdq_quantize_act)
+ *   amax = max_k |v|,  ascales[m] = float32(amax / 127)
+ *   qact = v * float32(127 / amax), the exact product rounded to the nearest integer, ties to even
+ *          (within [-127, 127])
+ *   y    = round( (float32(sum_k qact qweight) * ascales[m]) * wscales[n] + bias[n] )
+ * The sum is exact (int32); the arithmetic after it is float32 with one rounding to y's type.
+ * A row with amax < 2^-100 gets scale 0 and codes 0; a row that holds an infinity or a NaN (or
+ * whose smoothing or rotation overflows) gets scale NaN and codes 0, so its whole output row is
+ * NaN.  float32(sum) * ascales[m] overflows to infinity for |v| of about 2^97 and more.
+ *
+ *   x      [M, K], row r at x + r ldx elements; x_dtype W4A4_DTYPE_BF16, _F16 or _F32; 16-byte
+ *          aligned, ldx >= K, ldx % 8 == 0
+ *   smooth_factor  bf16 [K], 16-byte aligned, or NULL for none
+ *   K      >= 16, K % 16 == 0, at most W8A8_MAX_K (so that the int32 sum is exact)
+ *   hadamard_block  0 (none) or 16, 32, 64, 128 with K % hadamard_block == 0
+ *   qact   s8 [M, K], 16-byte aligned      ascales f32 [M]
+ *   qweight s8 [N, K], 16-byte aligned     wscales f32 [N]     (codes -128 .. 127)
+ *   bias   bf16 [N] or NULL
+ *   y      [M, N], row r at y + r ldy elements (ldy >= N: a column partition of a wider matrix is
+ *          fine, and nothing outside it is written); y_dtype as x_dtype
+ * w8a8_quantize_weight is the offline counterpart: w * smooth_factor instead of the quotient, per
+ * row n, the same rotation and codes; qweight and wscales are the layer's checkpoint tensors.
+ * w8a8_linear is w8a8_quantize_act into the workspace (at least w8a8_linear_workspace_bytes(M, K)
+ * bytes, 256-byte aligned, contents overwritten), then w8a8_gemm; projections of one input may
+ * share one w8a8_quantize_act instead.  Results do not depend on the batch a row is in.
+ * Errors: W4A4_ERR_UNSUPPORTED (hadamard_block, dtype, K > W8A8_MAX_K), W4A4_ERR_SHAPE (sizes,
+ * strides, a workspace too small), W4A4_ERR_NULL, W4A4_ERR_ALIGN; sizes are checked first, then
+ * the empty call (M or N == 0), then pointers, then alignment. */
+#define W8A8_MAX_K 131056
+w4a4_status w8a8_quantize_act(const void* x, int64_t ldx, int32_t x_dtype, const void* smooth_factor, int64_t M,
+                              int64_t K, int32_t hadamard_block, void* qact, float* ascales, void* stream);
+w4a4_status w8a8_quantize_weight(const void* w, int64_t ldw, int32_t w_dtype, const void* smooth_factor, int64_t N,
+                                 int64_t K, int32_t hadamard_block, void* qweight, float* wscales, void* stream);
+w4a4_status w8a8_gemm(const void* qact, const float* ascales, const void* qweight, const float* wscales,
+                      const void* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int32_t y_dtype,
+                      void* stream);
+size_t w8a8_linear_workspace_bytes(int64_t M, int64_t K);
+w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void* qweight, const float* wscales,
+                        const void* smooth_factor, const void* bias, int64_t M, int64_t N, int64_t K,
+                        int32_t hadamard_block, void* y, int64_t ldy, int32_t y_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ---- q / k head norm and rotary positions -----------------------------------------------------
+ * What the q and k partitions of a projection's output go through before attention, in one pass and
+ * one launch: per token and head of head_dim elements
+ *   u = (x * (1 / sqrt(mean(x^2) + eps))) * weight       (with W4A4_ROPE_NORM; weight may be NULL)
+ * then the rotation of the first rot = sum(axis_dims) elements in pairs: the rot / 2 pairs are
+ * divided among the position axes in order, axis a taking axis_dims[a] / 2 of them, and number i of
+ * axis a (pair p of all) turns by
+ *   angle = positions[t, a] * theta^(-2 i / axis_dims[a])
+ *   angle = positions[t, a] * theta^(-2 p / rot)         (with W4A4_ROPE_SHARED_FREQUENCIES)
+ *   (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
+ * Elements rot .. head_dim - 1 are normed only.  Angles are reduced in float64 (positions of any
+ * size, negative ones too, lose nothing); the rest is float32 with one rounding to the tensors' type.
+ * Squares that overflow float32 (|x| above about 2^63) give zeros.
+ *
+ * Elements (e0, e1) of pair p, number i of axis a whose first pair is s_a:
+ *   W4A4_ROPE_INTERLEAVED  (2 p, 2 p + 1)
+ *   W4A4_ROPE_HALF         (p, p + rot / 2)                           halves of the rotary span
+ *   W4A4_ROPE_AXIS_HALF    (2 s_a + i, 2 s_a + i + axis_dims[a] / 2)  halves of each axis's slice
+ *
+ * q and k (k may be NULL) describe [tokens, heads, head_dim] tensors with a dense last dimension:
+ * element (t, h, d) is at x + t x_token_stride + h x_head_stride + d, so partitions of a fused
+ * projection's output and head-major outputs are addressed as they lie; q and k may have different
+ * head counts.  x == y (with equal strides) works in place; any other overlap of an input and an
+ * output is undefined.  Only the addressed elements are written.
+ *   positions  [tokens, axes] int32 (int64 with W4A4_ROPE_POSITIONS_I64), dense; NULL when rot == 0
+ *   axis_dims  HOST array of `axes` even sizes (0 allowed), sum at most head_dim; axes 0 ..
+ *              W4A4_ROPE_MAX_AXES (0: norm only)
+ *   head_dim   even, 2 .. W4A4_ROPE_MAX_HEAD_DIM
+ *   dtype      W4A4_DTYPE_BF16, _F16 or _F32, of x, weight and y alike
+ * Errors: W4A4_ERR_UNSUPPORTED (dtype, layout, flags, head_dim or axes above the maximum),
+ * W4A4_ERR_SHAPE (sizes, a rotary span past head_dim, theta not positive and finite, eps negative,
+ * negative strides, outputs whose elements share an address, in place with other strides),
+ * W4A4_ERR_NULL, W4A4_ERR_ALIGN (element size).  tokens == 0 or no heads launches nothing.
+ * 16-byte aligned pointers and strides, and in the split layouts axes of multiples of 8 elements,
+ * take the vectorised path. */
+#define W4A4_ROPE_INTERLEAVED 0
+#define W4A4_ROPE_HALF 1
+#define W4A4_ROPE_AXIS_HALF 2
+#define W4A4_ROPE_NORM 1
+#define W4A4_ROPE_SHARED_FREQUENCIES 2
+#define W4A4_ROPE_POSITIONS_I64 4
+#define W4A4_ROPE_MAX_HEAD_DIM 512
+#define W4A4_ROPE_MAX_AXES 8
+typedef struct {
+  const void* x;
+  int64_t x_token_stride, x_head_stride; /* elements */
+  int64_t heads;
+  const void* weight; /* [head_dim], or NULL */
+  void* y;
+  int64_t y_token_stride, y_head_stride;
+} w4a4_heads;
+w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* k, const void* positions, int64_t tokens,
+                              int32_t head_dim, int32_t axes, const int32_t* axis_dims, int32_t layout, int32_t flags,
+                              double theta, float eps, int32_t dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

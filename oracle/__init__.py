@@ -31,6 +31,8 @@ Modules:
 * ``mx``       -- the MXFP4 variant (rotate notes, section 3.3, FP-Quant: E2M1
                   in blocks of 32 with one E8M0 power-of-two scale, group-32
                   rotation) with the same epilogue.
+* ``w8a8``     -- the int8 layer: per-token and per-channel scales.
+* ``rope``     -- RMS norm of q / k heads with the multi-axis rotary rotation.
 
 Precision: every step whose result decides an integer (a code, a scale byte)
 is done in IEEE float32, the precision the GPU kernels take that decision in;
@@ -48,4 +50,4 @@ direction, scale layout, zero-scale rule, sign of zero -- are fixed readings,
 checked only for self-consistency.
 """
 
-from . import formats, hadamard, quant, linear, mx, svd  # noqa: F401
+from . import formats, hadamard, quant, linear, mx, rope, svd, w8a8  # noqa: F401

@@ -1,0 +1,272 @@
+"""GPU parity of the q / k head norm with rotary positions (needs an MI355X) against
+``oracle/rope.py`` in 64 bits.
+
+Tolerance, per element of a rotated pair (u0, u1) with s = |u0| + |u1|, in units of 2^-24 of s: the sum
+of squares collects 8 products in a lane and at most 6 exchange steps (14 roundings, halved by the
+square root: 7), the mean and eps 2 (halved: 1), rsqrt 4 (two units in the last place), x * r and
+* weight 2, sincospi 4 (two units in the last place) and its rounded argument pi / 2 (the angle is
+rounded to 2^-25 half turns of at most 1, that is pi 2^-25 in the sine), the rotation 2: below 22.
+The angle in float64 adds |angle| * 6 * 2^-53.  Then half a unit in the last place of the storage type.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import hadamard as oh
+from oracle import rope as orope
+from test_gpu_w8a8 import DTYPES, dev, host, tdtype
+
+pytestmark = pytest.mark.gpu
+
+HALF_ULP = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11, "f32": 2.0 ** -24}
+TINY = {"bf16": 2.0 ** -133, "f16": 2.0 ** -24, "f32": 2.0 ** -149}  # a subnormal's step
+
+
+@pytest.fixture(scope="module")
+def w4():
+    import torch
+    assert torch.cuda.is_available(), "GPU tests need a ROCm GPU"
+    import w4a4_bit_quantized_amd as w
+    w.load_library()
+    return w
+
+
+def bound(u, y, dtype, dims, layout, shared, theta, pos):
+    s = np.abs(u)
+    far = np.zeros(u.shape[0])
+    for e0, e1, a, ex in orope.pair_table(dims, layout, shared):
+        s[..., e0] = s[..., e1] = np.abs(u[..., e0]) + np.abs(u[..., e1])
+        far = np.maximum(far, np.abs(pos[:, a].astype(np.float64)) * theta ** -ex)
+    err = s * (22 * 2.0 ** -24 + far[:, None, None] * 6 * 2.0 ** -53)
+    return err + (np.abs(y) + err) * HALF_ULP[dtype] + TINY[dtype]
+
+
+def check(got, x, pos, dims, dtype, weight=None, layout="interleaved", shared=False, norm=True, theta=10000.0, eps=1e-6,
+          what=""):
+    y, u = orope.norm_rope(oh.to_f32(x, dtype), pos, dims, None if weight is None else oh.to_f32(weight, dtype), eps,
+                           theta, layout, shared, norm)
+    g = oh.to_f32(host(got), dtype).astype(np.float64)
+    assert g.shape == y.shape
+    lim = bound(u, y, dtype, dims, layout, shared, theta, np.asarray(pos).reshape(len(y), len(dims)))
+    over = np.abs(g - y) > lim
+    at = np.argwhere(over)
+    assert at.size == 0, f"{what}: {len(at)} of {g.size} off, first {at[:3].tolist()}: {g[tuple(at[0])]} for {y[tuple(at[0])]}"
+
+
+def make(rng, T, H, D, dtype, scale=1.5):
+    return oh.from_f32((rng.standard_normal((T, H, D)) * scale).astype(np.float32), dtype)
+
+
+def weights(rng, D, dtype):
+    return oh.from_f32(rng.uniform(0.5, 1.5, D).astype(np.float32), dtype)
+
+
+def run(w4, rng, T, hq, hk, D, dims, dtype, layout, shared=False, weight=True, norm=True, far=1000, pos64=False, **kw):
+    import torch
+    print(f"\nT={T} heads={hq}+{hk} D={D} axes={dims} {dtype} {layout}", flush=True)
+    q, k = make(rng, T, hq, D, dtype), make(rng, T, hk, D, dtype)
+    qw, kw_ = (weights(rng, D, dtype), weights(rng, D, dtype)) if weight else (None, None)
+    pos = rng.integers(-far, far + 1, (T, len(dims)))
+    pt = torch.from_numpy(pos.astype(np.int64 if pos64 else np.int32)).cuda()
+    yq, yk = w4.qk_norm_rope(dev(q, dtype), dev(k, dtype), pt, dims, None if qw is None else dev(qw, dtype),
+                             None if kw_ is None else dev(kw_, dtype), layout=layout, shared_frequencies=shared,
+                             norm=norm, **kw)
+    torch.cuda.synchronize()
+    o = {n: kw[n] for n in ("theta", "eps") if n in kw}
+    check(yq, q, pos, dims, dtype, qw, layout, shared, norm, what="q", **o)
+    check(yk, k, pos, dims, dtype, kw_, layout, shared, norm, what="k", **o)
+
+
+LAYOUTS = ["interleaved", "half", "axis_half"]
+SHAPES = [(1, 1, 1, 64, [64]), (1, 32, 8, 128, [128]), (5, 3, 1, 128, [16, 56, 56]), (130, 24, 24, 128, [44, 42, 42]),
+          (600, 4, 2, 80, [16, 24, 24]), (4100, 5, 3, 64, [8, 24, 32]), (33, 2, 2, 256, [64, 64, 64, 64]),
+          (7, 3, 2, 512, [128, 256]), (9, 2, 1, 34, [2, 10, 6]), (3, 1, 1, 2, [2]), (17, 2, 3, 120, [40, 0, 48]),
+          (4101, 3, 1, 6, [2, 2]), (2, 2, 1, 512, [510]), (70, 40, 2, 16, [8])]
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("shape", SHAPES, ids=str)
+def test_shapes(w4, shape, layout):
+    """Head sizes, head counts, axes (an empty one among them), part of the head rotated; every type."""
+    for i, dtype in enumerate(DTYPES):
+        rng = np.random.default_rng(i + shape[0])
+        run(w4, rng, *shape, dtype, layout, shared=i == 1, pos64=i == 2)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_without_norm_or_weight(w4, layout):
+    rng = np.random.default_rng(3)
+    run(w4, rng, 20, 6, 2, 128, [32, 48, 48], "bf16", layout, weight=False)
+    run(w4, rng, 20, 6, 2, 128, [32, 48, 48], "f32", layout, norm=False)
+    run(w4, rng, 20, 6, 2, 72, [30, 42], "f16", layout, norm=False, weight=False)
+
+
+def test_far_positions_and_parameters(w4):
+    """Positions up to the ends of their types lose no accuracy; other theta and eps."""
+    rng = np.random.default_rng(4)
+    run(w4, rng, 64, 2, 1, 64, [64], "f32", "half", far=2 ** 31 - 1)
+    run(w4, rng, 64, 2, 1, 64, [32, 32], "f32", "interleaved", far=2 ** 40, pos64=True, shared=True)
+    run(w4, rng, 64, 2, 1, 64, [64], "f32", "half", far=500000, theta=5e5, eps=1e-5)
+    run(w4, rng, 64, 2, 1, 64, [64], "f32", "interleaved", far=1000, theta=0.5, eps=0.0)
+
+
+def test_norm_only(w4):
+    import torch
+    rng = np.random.default_rng(5)
+    for dtype in DTYPES:
+        x, w = make(rng, 40, 3, 128, dtype), weights(rng, 128, dtype)
+        y = w4.qk_norm_rope(dev(x, dtype), None, None, [], q_weight=dev(w, dtype))
+        assert isinstance(y, torch.Tensor)
+        check(y, x, np.zeros((40, 0)), [], dtype, w)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("start", [0, 3, 8])
+def test_partitions_in_place(w4, dtype, start):
+    """q and k partitions of a fused projection's rows, in place: v, the columns before them and the
+    rows behind the last token stay as they were, and the result is the out-of-place one."""
+    import torch
+    rng = np.random.default_rng(start)
+    T, hq, hk, D, dims = 50, 6, 2, 96, [24, 32, 40]
+    width = start + (hq + 2 * hk) * D
+    big = dev(oh.from_f32(rng.standard_normal((T + 3, width)).astype(np.float32), dtype), dtype)
+    before = big.clone()
+    q = big[:T, start:start + hq * D].unflatten(1, (hq, D))
+    k = big[:T, start + hq * D:start + (hq + hk) * D].unflatten(1, (hk, D))
+    qh, kh = host(q), host(k)
+    pos = torch.from_numpy(rng.integers(0, 99, (T, 3)).astype(np.int32)).cuda()
+    wq, wk = weights(rng, D, dtype), weights(rng, D, dtype)
+    for layout in LAYOUTS:
+        big.copy_(before)
+        a, b = w4.qk_norm_rope(q, k, pos, dims, dev(wq, dtype), dev(wk, dtype), layout=layout)
+        assert torch.equal(big, before)
+        w4.qk_norm_rope(q, k, pos, dims, dev(wq, dtype), dev(wk, dtype), layout=layout, inplace=True)
+        assert torch.equal(q, a) and torch.equal(k, b)
+        keep = torch.ones_like(big, dtype=torch.bool)
+        keep[:T, start:start + (hq + hk) * D] = False
+        assert torch.equal(big[keep], before[keep])
+        check(a, qh, pos.cpu().numpy(), dims, dtype, wq, layout)
+        check(b, kh, pos.cpu().numpy(), dims, dtype, wk, layout)
+
+
+def test_head_major_output_batches_and_broadcast(w4):
+    """(heads, tokens, head_dim) outputs, 4-D inputs, a broadcast key head; one query head alone."""
+    import torch
+    rng = np.random.default_rng(8)
+    B, S, hq, hk, D, dims = 3, 11, 4, 2, 64, [16, 48]
+    q, k = make(rng, B * S, hq, D, "bf16"), make(rng, B * S, 1, D, "bf16")
+    pos = rng.integers(0, 50, (B, S, 2)).astype(np.int32)
+    qd = dev(q, "bf16").view(B, S, hq, D)
+    kd = dev(k, "bf16").expand(B * S, hk, D)
+    pt = torch.from_numpy(pos).cuda()
+    q_out = torch.empty((hq, B * S, D), dtype=torch.bfloat16, device="cuda")
+    a = w4.qk_norm_rope(qd.view(B * S, hq, D), None, pt.view(B * S, 2), dims, q_out=q_out.transpose(0, 1))
+    b, kk = w4.qk_norm_rope(qd, kd, pt, dims)
+    assert tuple(b.shape) == (B, S, hq, D) and tuple(kk.shape) == (B * S, hk, D)
+    assert torch.equal(a, b.view(B * S, hq, D)) and torch.equal(q_out.transpose(0, 1), a)
+    check(a, q, pos.reshape(-1, 2), dims, "bf16")
+    check(kk, np.repeat(k, hk, 1), pos.reshape(-1, 2), dims, "bf16")
+
+
+def test_special_values_stay_in_their_head(w4):
+    """Zero heads stay zero; an infinity or a NaN reaches its own head only."""
+    import torch
+    rng = np.random.default_rng(9)
+    q = dev(make(rng, 6, 3, 128, "f32"), "f32")
+    pos = torch.arange(6, dtype=torch.int32, device="cuda")
+    clean = w4.qk_norm_rope(q, None, pos, [128])
+    q[1, 1] = 0.0
+    q[2, 0, 5], q[4, 2, 100] = float("inf"), float("nan")
+    y = w4.qk_norm_rope(q, None, pos, [128])
+    assert bool((y[1, 1] == 0).all())
+    assert bool(y[2, 0].isnan().any()) and bool(y[4, 2].isnan().all())
+    for t, h in ((1, 1), (2, 0), (4, 2)):
+        y[t, h] = clean[t, h]
+    assert torch.equal(y, clean)
+
+
+def test_empty_and_refused_calls(w4):
+    import torch
+    q = torch.zeros((4, 2, 64), device="cuda")
+    p = torch.zeros((4, 1), dtype=torch.int32, device="cuda")
+    a, b = w4.qk_norm_rope(q[:0], q[:0, :1], p[:0], [64])
+    assert a.shape[0] == 0 and b.shape[0] == 0
+    assert w4.qk_norm_rope(q[:, :0], None, p, [64]).numel() == 0
+    for bad, err in ((dict(axis_dims=[66]), "ERR_SHAPE"), (dict(axis_dims=[33]), "ERR_SHAPE"),
+                     (dict(axis_dims=[-2]), "ERR_SHAPE"), (dict(theta=0.0), "ERR_SHAPE"), (dict(eps=-1.0), "ERR_SHAPE"),
+                     (dict(theta=float("nan")), "ERR_SHAPE"),
+                     (dict(q_out=torch.zeros((1, 1, 64), device="cuda").expand(4, 2, 64)), "ERR_SHAPE")):
+        with pytest.raises(w4.W4A4Error, match=err):
+            w4.qk_norm_rope(q, None, p, **{"axis_dims": [64], **bad})
+    with pytest.raises(w4.W4A4Error, match="ERR_SHAPE"):
+        w4.qk_norm_rope(q[..., :33], None, p, [32])
+    with pytest.raises(w4.W4A4Error, match="ERR_UNSUPPORTED"):
+        w4.qk_norm_rope(torch.zeros((2, 1, 514), device="cuda"), None, p[:2], [64])
+    with pytest.raises(w4.W4A4Error, match="ERR_UNSUPPORTED"):
+        w4.qk_norm_rope(q, None, torch.zeros((4, 9), dtype=torch.int32, device="cuda"), [2] * 9)
+    for kw, exc in ((dict(layout="other"), ValueError), (dict(q_weight=torch.ones(32, device="cuda")), ValueError),
+                    (dict(q_weight=torch.ones(64, device="cuda", dtype=torch.bfloat16)), TypeError),
+                    (dict(q_out=torch.zeros((4, 2, 32), device="cuda")), ValueError), (dict(inplace=True, q_out=q), ValueError)):
+        with pytest.raises(exc):
+            w4.qk_norm_rope(q, None, p, [64], **kw)
+    with pytest.raises(ValueError, match="positions"):
+        w4.qk_norm_rope(q, None, p[:3], [64])
+    with pytest.raises(TypeError, match="positions"):
+        w4.qk_norm_rope(q, None, p.float(), [64])
+    with pytest.raises(ValueError, match="k has"):
+        w4.qk_norm_rope(q, q[:3], p, [64])
+    with pytest.raises(ValueError, match="flatten"):
+        w4.qk_norm_rope(torch.zeros((2, 8, 2, 64), device="cuda")[:, :2], None, p, [64])
+
+
+def test_graph_replay(w4):
+    import torch
+    rng = np.random.default_rng(10)
+    q, k = dev(make(rng, 90, 8, 128, "bf16"), "bf16"), dev(make(rng, 90, 2, 128, "bf16"), "bf16")
+    pos = torch.zeros((90, 3), dtype=torch.int32, device="cuda")
+    oq, ok = torch.empty_like(q), torch.empty_like(k)
+    args = (q, k, pos, [16, 56, 56])
+    w4.qk_norm_rope(*args, q_out=oq, k_out=ok)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        w4.qk_norm_rope(*args, q_out=oq, k_out=ok)
+    for _ in range(4):
+        q.copy_(dev(make(rng, 90, 8, 128, "bf16"), "bf16"))
+        pos.copy_(torch.from_numpy(rng.integers(0, 100, (90, 3)).astype(np.int32)))
+        a, b = w4.qk_norm_rope(*args)
+        oq.zero_()
+        ok.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(oq, a) and torch.equal(ok, b)
+
+
+def test_projection_then_norm_and_rotation(w4):
+    """As they are used together: one quantized activation, a fused 8-bit q / k / v projection into one
+    matrix, q and k normed and rotated in place, then rotated per head by the block Hadamard transform;
+    the same with the 4-bit layer's output."""
+    import torch
+    from oracle import w8a8 as ow
+    rng = np.random.default_rng(12)
+    T, K, hq, hk, D, dims = 77, 512, 4, 2, 64, [16, 24, 24]
+    N = (hq + 2 * hk) * D
+    x = oh.from_f32(rng.standard_normal((T, K)).astype(np.float32), "bf16")
+    lam = oh.from_f32(rng.uniform(0.5, 2, K).astype(np.float32), "bf16")
+    w = oh.from_f32((rng.standard_normal((N, K)) * K ** -0.5).astype(np.float32), "bf16")
+    qw, sw = w4.w8a8_quantize_weight(dev(w, "bf16"), dev(lam, "bf16"), hadamard_block=64)
+    qkv = w4.w8a8_linear(dev(x, "bf16"), dict(qweight=qw, wscales=sw, smooth_factor=dev(lam, "bf16")), hadamard_block=64)
+    codes, scales = ow.quantize_weight(oh.to_f32(w, "bf16"), oh.to_f32(lam, "bf16"), 64)
+    ref = oh.from_f32(ow.linear_f32(oh.to_f32(x, "bf16"), codes, scales, oh.to_f32(lam, "bf16"), None, 64), "bf16")
+    assert np.array_equal(host(qkv), ref)
+    v = qkv[:, (hq + hk) * D:].clone()
+    q, k = qkv[:, :hq * D].unflatten(1, (hq, D)), qkv[:, hq * D:(hq + hk) * D].unflatten(1, (hk, D))
+    pos = rng.integers(0, 64, (T, 3)).astype(np.int32)
+    wq = weights(rng, D, "bf16")
+    w4.qk_norm_rope(q, k, torch.from_numpy(pos).cuda(), dims, dev(wq, "bf16"), dev(wq, "bf16"), inplace=True)
+    check(q, ref[:, :hq * D].reshape(T, hq, D), pos, dims, "bf16", wq)
+    check(k, ref[:, hq * D:(hq + hk) * D].reshape(T, hk, D), pos, dims, "bf16", wq)
+    turned = host(qkv[:, :(hq + hk) * D])
+    w4.hadamard_transform(qkv[:, :(hq + hk) * D], block=D, inplace=True)
+    assert np.array_equal(host(qkv[:, :(hq + hk) * D]), oh.hadamard_transform(turned, D, "bf16"))
+    assert torch.equal(qkv[:, (hq + hk) * D:], v)

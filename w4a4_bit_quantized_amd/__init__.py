@@ -15,6 +15,7 @@ from .binding import (  # noqa: F401
     hadamard_transform,
     library_path,
     load_library,
+    qk_norm_rope,
     svdq_gemm_lowrank,
     svdq_linear,
     svdq_linear_workspace_bytes,
@@ -27,4 +28,9 @@ from .binding import (  # noqa: F401
     svdq_lowrank_split,
     svdq_quantize_act_mx,
     svdq_quantize_weight_mx,
+    w8a8_gemm,
+    w8a8_linear,
+    w8a8_linear_workspace_bytes,
+    w8a8_quantize_act,
+    w8a8_quantize_weight,
 )

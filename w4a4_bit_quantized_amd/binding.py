@@ -19,6 +19,13 @@ _c_i64 = ctypes.c_int64
 _c_i32 = ctypes.c_int32
 _c_p = ctypes.c_void_p
 
+
+class Heads(ctypes.Structure):
+    """w4a4_heads: one tensor of w4a4_qk_norm_rope."""
+    _fields_ = [("x", _c_p), ("x_token_stride", _c_i64), ("x_head_stride", _c_i64), ("heads", _c_i64),
+                ("weight", _c_p), ("y", _c_p), ("y_token_stride", _c_i64), ("y_head_stride", _c_i64)]
+
+
 # name -> (restype, argtypes), mirroring include/w4a4.h
 SIGNATURES = {
     "w4a4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -52,9 +59,18 @@ SIGNATURES = {
     "svdq_linear_mx_bias": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p, _c_p,
                                            _c_i64, _c_i64, _c_i64, _c_i64, _c_i32, _c_p, _c_p, ctypes.c_size_t,
                                            _c_p]),
+    "w8a8_quantize_act": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_p, _c_p]),
+    "w8a8_quantize_weight": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_i64, _c_i64, _c_i32, _c_p, _c_p, _c_p]),
+    "w8a8_gemm": (ctypes.c_int, [_c_p, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_p, _c_i64, _c_i32, _c_p]),
+    "w8a8_linear_workspace_bytes": (ctypes.c_size_t, [_c_i64, _c_i64]),
+    "w8a8_linear": (ctypes.c_int, [_c_p, _c_i64, _c_i32, _c_p, _c_p, _c_p, _c_p, _c_i64, _c_i64, _c_i64, _c_i32,
+                                   _c_p, _c_i64, _c_i32, _c_p, ctypes.c_size_t, _c_p]),
+    "w4a4_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(Heads), _c_p, _c_i64, _c_i32, _c_i32,
+                                         ctypes.POINTER(ctypes.c_int32), _c_i32, _c_i32, ctypes.c_double,
+                                         ctypes.c_float, _c_i32, _c_p]),
 }
 
-# storage type codes of w4a4_hadamard_transform
+# storage type codes of w4a4_hadamard_transform, the w8a8 entry points and w4a4_qk_norm_rope
 DTYPE_BF16, DTYPE_F16, DTYPE_F32 = 0, 1, 2
 HADAMARD_MAX_BLOCK = 4096
 
@@ -543,3 +559,263 @@ def svdq_lowrank_split(w, smooth_factor, rank, oversample=16, power_iters=4, see
                                 pu.ctypes.data if R else None, resid.ctypes.data, sv.ctypes.data)
     _check(st, "svdq_lowrank_split")
     return pd, pu, resid, sv[:R]
+
+
+# ---- W8A8 layer (int8, one scale per token and per output channel) --------------------------
+
+W8A8_MAX_K = 131056
+
+
+def _dtype_code(dtype, name):
+    torch = _torch()
+    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
+    if dtype not in codes:
+        raise TypeError(f"{name} must be bf16, f16 or f32, got {dtype}")
+    return codes[dtype]
+
+
+def _device_tensor(t, name):
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a device tensor, got {t.device}")
+    return t.device
+
+
+def _on(device, call, *args):
+    """``call(*args, stream)`` with ``device`` current and its current stream (a stream launches on
+    its own device only while that device is current)."""
+    torch = _torch()
+    stream = torch.cuda.current_stream(device).cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return call(*args, stream)
+    with torch.cuda.device(device):
+        return call(*args, stream)
+
+
+def _addr(t):
+    return t.data_ptr() if t is not None else None
+
+
+def _w8a8_rows(t, name):
+    """(rows, K, row stride, dtype code, device) of a quantizer input."""
+    dev = _device_tensor(t, name)
+    code = _dtype_code(t.dtype, name)
+    rows, K, ld = _rows_view(t, name)
+    return rows, K, ld, code, dev
+
+
+def _check_smooth(smooth_factor, K, dev):
+    if smooth_factor is not None:
+        _dev(smooth_factor, "smooth_factor", (_torch().bfloat16,), dev)
+        _shape(smooth_factor, "smooth_factor", (K,))
+
+
+def _check_w8a8_weights(qweight, wscales, bias, K, dev):
+    torch = _torch()
+    _dev(qweight, "qweight", (torch.int8,), dev)
+    if qweight.dim() != 2:
+        raise ValueError(f"qweight must be 2-D (N, K), got shape {tuple(qweight.shape)}")
+    N = int(qweight.shape[0])
+    _shape(qweight, "qweight", (N, K))
+    _dev(wscales, "wscales", (torch.float32,), dev)
+    _shape(wscales, "wscales", (N,))
+    if bias is not None:
+        _dev(bias, "bias", (torch.bfloat16,), dev)
+        _shape(bias, "bias", (N,))
+    return N
+
+
+def _w8a8_out(out, lead, M, N, out_dtype, default, dev):
+    """(y, its row stride, its dtype code): `out` checked, or a new tensor (*lead, N)."""
+    torch = _torch()
+    if out is None:
+        dtype = default if out_dtype is None else out_dtype
+        code = _dtype_code(dtype, "out_dtype")
+        return torch.empty((*lead, N), dtype=dtype, device=dev), N, code
+    if _device_tensor(out, "out") != dev:
+        raise ValueError(f"out is on {out.device}, expected {dev}")
+    if out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError(f"out must have dtype {out_dtype}, got {out.dtype}")
+    if tuple(out.shape) not in ((*lead, N), (M, N)):
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {(*lead, N)}")
+    code = _dtype_code(out.dtype, "out")
+    return out, _rows_view(out, "out")[2], code
+
+
+def w8a8_linear_workspace_bytes(M, K):
+    return int(load_library().w8a8_linear_workspace_bytes(int(M), int(K)))
+
+
+def w8a8_quantize_act(x, smooth_factor=None, hadamard_block=0):
+    """x (..., K) bf16, f16 or f32 -> (qact (M, K) int8, ascales (M,) f32), one scale per token.
+
+    x needs a dense last dimension; a 2-D x may be a column partition of a wider matrix (16-byte
+    aligned, row stride a multiple of 8).  smooth_factor (K,) bf16 is optional."""
+    torch = _torch()
+    lib = load_library()
+    M, K, ldx, code, dev = _w8a8_rows(x, "x")
+    _check_smooth(smooth_factor, K, dev)
+    qact = torch.empty((M, K), dtype=torch.int8, device=dev)
+    ascales = torch.empty((M,), dtype=torch.float32, device=dev)
+    st = _on(dev, lib.w8a8_quantize_act, x.data_ptr(), ldx, code, _addr(smooth_factor), M, K, int(hadamard_block),
+             qact.data_ptr(), ascales.data_ptr())
+    _check(st, "w8a8_quantize_act")
+    return qact, ascales
+
+
+def w8a8_quantize_weight(w, smooth_factor=None, hadamard_block=0):
+    """w (N, K) bf16, f16 or f32 -> (qweight (N, K) int8, wscales (N,) f32), one scale per output channel."""
+    torch = _torch()
+    lib = load_library()
+    N, K, ldw, code, dev = _w8a8_rows(w, "w")
+    _check_smooth(smooth_factor, K, dev)
+    qweight = torch.empty((N, K), dtype=torch.int8, device=dev)
+    wscales = torch.empty((N,), dtype=torch.float32, device=dev)
+    st = _on(dev, lib.w8a8_quantize_weight, w.data_ptr(), ldw, code, _addr(smooth_factor), N, K, int(hadamard_block),
+             qweight.data_ptr(), wscales.data_ptr())
+    _check(st, "w8a8_quantize_weight")
+    return qweight, wscales
+
+
+def w8a8_gemm(qact, ascales, qweight, wscales, bias=None, out=None, out_dtype=None):
+    """int8 GEMM -> y (M, N): (qact @ qweight^T) * ascales[:, None] * wscales + bias.
+
+    ``out_dtype`` is bf16 (default), f16 or f32; ``out`` may be a column partition of a wider
+    matrix.  ``bias`` (N,) bf16 is optional."""
+    torch = _torch()
+    lib = load_library()
+    dev = _device_tensor(qact, "qact")
+    _dev(qact, "qact", (torch.int8,))
+    if qact.dim() != 2:
+        raise ValueError(f"qact must be 2-D (M, K), got shape {tuple(qact.shape)}")
+    M, K = (int(d) for d in qact.shape)
+    _dev(ascales, "ascales", (torch.float32,), dev)
+    _shape(ascales, "ascales", (M,))
+    N = _check_w8a8_weights(qweight, wscales, bias, K, dev)
+    y, ldy, code = _w8a8_out(out, (M,), M, N, out_dtype, torch.bfloat16, dev)
+    st = _on(dev, lib.w8a8_gemm, qact.data_ptr(), ascales.data_ptr(), qweight.data_ptr(), wscales.data_ptr(),
+             _addr(bias), M, N, K, y.data_ptr(), ldy, code)
+    _check(st, "w8a8_gemm")
+    return y
+
+
+def w8a8_linear(x, layer, hadamard_block=0, workspace=None, out=None, out_dtype=None):
+    """The whole 8-bit layer.  ``x`` (..., K) bf16, f16 or f32; leading dims are flattened into M.
+
+    ``layer`` maps qweight (N, K) int8 and wscales (N,) f32, and optionally smooth_factor (K,) bf16
+    and bias (N,) bf16, to device tensors.  ``out_dtype`` defaults to x's.  ``workspace`` (u8, at
+    least w8a8_linear_workspace_bytes bytes) and ``out`` may be passed to avoid allocation; without
+    them they come from torch's allocator on the current stream."""
+    torch = _torch()
+    lib = load_library()
+    M, K, ldx, code, dev = _w8a8_rows(x, "x")
+    smooth, bias = layer.get("smooth_factor"), layer.get("bias")
+    _check_smooth(smooth, K, dev)
+    qweight, wscales = layer["qweight"], layer["wscales"]
+    N = _check_w8a8_weights(qweight, wscales, bias, K, dev)
+    y, ldy, ycode = _w8a8_out(out, tuple(x.shape[:-1]), M, N, out_dtype, x.dtype, dev)
+    if workspace is None:
+        workspace = torch.empty(max(int(lib.w8a8_linear_workspace_bytes(M, K)), 1), dtype=torch.uint8, device=dev)
+    else:
+        _dev(workspace, "workspace", (torch.uint8,), dev)
+        need = int(lib.w8a8_linear_workspace_bytes(M, K))
+        if workspace.numel() < need:
+            raise ValueError(f"workspace holds {workspace.numel()} bytes, the call needs {need}")
+    st = _on(dev, lib.w8a8_linear, x.data_ptr(), ldx, code, qweight.data_ptr(), wscales.data_ptr(), _addr(smooth),
+             _addr(bias), M, N, K, int(hadamard_block), y.data_ptr(), ldy, ycode, workspace.data_ptr(),
+             workspace.numel())
+    _check(st, "w8a8_linear")
+    return y
+
+
+# ---- q / k head norm and rotary positions ----------------------------------------------------
+
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1, "axis_half": 2}
+ROPE_NORM, ROPE_SHARED_FREQUENCIES, ROPE_POSITIONS_I64 = 1, 2, 4
+ROPE_MAX_HEAD_DIM, ROPE_MAX_AXES = 512, 8
+
+
+def _heads_view(t, name):
+    """(tokens, heads, head_dim, token stride, head stride) of a (T, H, D) or (B, S, H, D) tensor with a
+    dense last dimension; the leading two of four dimensions have to flatten without copying."""
+    if t.dim() not in (3, 4):
+        raise ValueError(f"{name} must be (tokens, heads, head_dim) or (batch, tokens, heads, head_dim), "
+                         f"got shape {tuple(t.shape)}")
+    shape, st = t.shape, t.stride()
+    if shape[-1] > 1 and st[-1] != 1:
+        raise ValueError(f"{name} must have a dense last dimension")
+    T, ts = int(shape[-3]), st[-3]
+    if t.dim() == 4:
+        if shape[0] > 1 and T > 1 and st[0] != T * st[1]:
+            raise ValueError(f"{name}'s batch and token dimensions do not flatten (strides {tuple(st)})")
+        if T == 1:
+            ts = st[0]
+        T *= int(shape[0])
+    return T, int(shape[-2]), int(shape[-1]), ts, st[-2]
+
+
+def _rope_side(x, y, weight, name, T, D, dtype, dev):
+    if x.dtype != dtype or x.device != dev:
+        raise ValueError(f"{name} must match q in dtype and device")
+    if y.shape != x.shape or y.dtype != dtype or y.device != dev:
+        raise ValueError(f"the output for {name} must match it in shape, dtype and device")
+    t, h, d, ts, hs = _heads_view(x, name)
+    if (t, d) != (T, D):
+        raise ValueError(f"{name} has {t} tokens and head_dim {d}, expected {T} and {D}")
+    if weight is not None:
+        _dev(weight, f"{name}_weight", (dtype,), dev)
+        _shape(weight, f"{name}_weight", (D,))
+    _, _, _, yts, yhs = _heads_view(y, f"{name}'s output")
+    return Heads(x.data_ptr(), ts, hs, h, _addr(weight), y.data_ptr(), yts, yhs)
+
+
+def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1e-6, theta=10000.0,
+                 layout="interleaved", shared_frequencies=False, norm=True, inplace=False, q_out=None, k_out=None):
+    """RMS norm of each head of q and k and the rotary rotation by one or more position axes, in one pass.
+
+    q (T, Hq, D) and k (T, Hk, D), or (B, S, H, D): bf16, f16 or f32 with a dense last dimension and
+    any token and head strides (partitions of a fused projection's output are fine); k may be None.
+    positions (T, len(axis_dims)) int32 or int64, contiguous ((T,) for one axis, (B, S, ...) too); axis
+    a rotates axis_dims[a] elements, further elements are only normed.  ``layout``: "interleaved"
+    pairs (2p, 2p + 1), "half" (p, p + rot / 2), "axis_half" (halves of each axis's slice).
+    ``shared_frequencies``: one ladder theta^(-2p / rot) over all pairs instead of one per axis.
+    norm=False only rotates.  Returns (q_out, k_out), or q_out when k is None; new contiguous tensors
+    unless ``inplace`` or given."""
+    torch = _torch()
+    lib = load_library()
+    dev = _device_tensor(q, "q")
+    code = _dtype_code(q.dtype, "q")
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    T, _, D, _, _ = _heads_view(q, "q")
+    if inplace and (q_out is not None or k_out is not None):
+        raise ValueError("inplace takes no outputs")
+    if k is None and (k_out is not None or k_weight is not None):
+        raise ValueError("k_out and k_weight need k")
+    dims = [int(d) for d in axis_dims]
+    flags = (ROPE_NORM if norm else 0) | (ROPE_SHARED_FREQUENCIES if shared_frequencies else 0)
+    if dims:
+        _dev(positions, "positions", (torch.int32, torch.int64), dev)
+        lead = tuple(q.shape[:-2])
+        if tuple(positions.shape) not in ((T, len(dims)), (*lead, len(dims))) and not (
+                len(dims) == 1 and tuple(positions.shape) in ((T,), lead)):
+            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(T, len(dims))}")
+        if positions.dtype == torch.int64:
+            flags |= ROPE_POSITIONS_I64
+    if inplace:
+        q_out, k_out = q, k
+    else:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
+        if k is not None and k_out is None:
+            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
+    qs = _rope_side(q, q_out, q_weight, "q", T, D, q.dtype, dev)
+    ks = None
+    if k is not None:
+        _device_tensor(k, "k")
+        ks = _rope_side(k, k_out, k_weight, "k", T, D, q.dtype, dev)
+    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ctypes.byref(ks) if ks is not None else None,
+             positions.data_ptr() if dims else None, T, D, len(dims), (ctypes.c_int32 * max(len(dims), 1))(*dims),
+             ROPE_LAYOUTS[layout], flags, float(theta), float(eps), code)
+    _check(st, "w4a4_qk_norm_rope")
+    return q_out if k is None else (q_out, k_out)

@@ -364,3 +364,205 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
 }
 
 }  // extern "C"
+
+// ---- W8A8 layer ------------------------------------------------------------------------------
+
+namespace {
+
+// Sizes, then types: shared by the quantizers, the GEMM and the layer.
+w4a4_status check_w8a8(int64_t K, int32_t hb, int32_t dtype) {
+  if (hb != 0 && hb != 16 && hb != 32 && hb != 64 && hb != 128) return W4A4_ERR_UNSUPPORTED;
+  if (K > W8A8_MAX_K || dtype < W4A4_DTYPE_BF16 || dtype > W4A4_DTYPE_F32) return W4A4_ERR_UNSUPPORTED;
+  if (K < 16 || K % 16 != 0) return W4A4_ERR_SHAPE;
+  if (hb != 0 && K % hb != 0) return W4A4_ERR_SHAPE;
+  return W4A4_OK;
+}
+
+w4a4_status validate_quantize_w8a8(const void* x, int64_t ldx, int32_t x_dtype, const void* smooth_factor, int64_t rows,
+                                   int64_t K, int32_t hb, const void* q, const void* scales) {
+  w4a4_status st = check_w8a8(K, hb, x_dtype);
+  if (st != W4A4_OK) return st;
+  if (rows < 0 || rows > kMaxDim || ldx < K || ldx % 8 != 0) return W4A4_ERR_SHAPE;
+  if (rows == 0) return W4A4_OK;
+  if (!x || !q || !scales) return W4A4_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(smooth_factor, 16) || !aligned(q, 16) || !aligned(scales, 4)) return W4A4_ERR_ALIGN;
+  return W4A4_OK;
+}
+
+w4a4_status quantize_w8a8(bool act, const void* x, int64_t ldx, int32_t x_dtype, const void* smooth_factor, int64_t rows,
+                          int64_t K, int32_t hb, void* q, float* scales, void* stream) {
+  if (!w4a4::launch_quantize_i8) return W4A4_ERR_HIP;
+  const float norm = hb ? (float)(1.0 / std::sqrt((double)hb)) : 1.0f;
+  (void)hipGetLastError();
+  return from_hip(w4a4::launch_quantize_i8(act, x, ldx, smooth_factor, rows, K, hb, x_dtype, norm, q, scales,
+                                           static_cast<hipStream_t>(stream)));
+}
+
+w4a4_status validate_gemm_w8a8(const void* qact, const void* ascales, const void* qweight, const void* wscales,
+                               const void* bias, int64_t M, int64_t N, int64_t K, const void* y, int64_t ldy,
+                               int32_t y_dtype) {
+  w4a4_status st = check_w8a8(K, 0, y_dtype);
+  if (st != W4A4_OK) return st;
+  if (M < 0 || N < 0 || M > kMaxDim || N > kMaxDim || ldy < N) return W4A4_ERR_SHAPE;
+  if (((M + 63) / 64) * ((N + 63) / 64) > kMaxDim) return W4A4_ERR_SHAPE;  // 1-D grid of output tiles
+  if (M == 0 || N == 0) return W4A4_OK;
+  if (!qact || !ascales || !qweight || !wscales || !y) return W4A4_ERR_NULL;
+  if (!aligned(qact, 16) || !aligned(qweight, 16) || !aligned(ascales, 4) || !aligned(wscales, 4) ||
+      !aligned(bias, 2) || !aligned(y, y_dtype == W4A4_DTYPE_F32 ? 4 : 2))
+    return W4A4_ERR_ALIGN;
+  return W4A4_OK;
+}
+
+w4a4_status gemm_w8a8(const void* qact, const float* ascales, const void* qweight, const float* wscales,
+                      const void* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int32_t y_dtype,
+                      void* stream) {
+  if (!w4a4::launch_gemm_i8) return W4A4_ERR_HIP;
+  (void)hipGetLastError();
+  return from_hip(w4a4::launch_gemm_i8(qact, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype,
+                                       static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+w4a4_status w8a8_quantize_act(const void* x, int64_t ldx, int32_t x_dtype, const void* smooth_factor, int64_t M,
+                              int64_t K, int32_t hadamard_block, void* qact, float* ascales, void* stream) {
+  w4a4_status st = validate_quantize_w8a8(x, ldx, x_dtype, smooth_factor, M, K, hadamard_block, qact, ascales);
+  if (st != W4A4_OK || M == 0) return st;
+  return quantize_w8a8(true, x, ldx, x_dtype, smooth_factor, M, K, hadamard_block, qact, ascales, stream);
+}
+
+w4a4_status w8a8_quantize_weight(const void* w, int64_t ldw, int32_t w_dtype, const void* smooth_factor, int64_t N,
+                                 int64_t K, int32_t hadamard_block, void* qweight, float* wscales, void* stream) {
+  w4a4_status st = validate_quantize_w8a8(w, ldw, w_dtype, smooth_factor, N, K, hadamard_block, qweight, wscales);
+  if (st != W4A4_OK || N == 0) return st;
+  return quantize_w8a8(false, w, ldw, w_dtype, smooth_factor, N, K, hadamard_block, qweight, wscales, stream);
+}
+
+w4a4_status w8a8_gemm(const void* qact, const float* ascales, const void* qweight, const float* wscales,
+                      const void* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int32_t y_dtype,
+                      void* stream) {
+  w4a4_status st = validate_gemm_w8a8(qact, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype);
+  if (st != W4A4_OK || M == 0 || N == 0) return st;
+  return gemm_w8a8(qact, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype, stream);
+}
+
+size_t w8a8_linear_workspace_bytes(int64_t M, int64_t K) {
+  if (M < 0 || M > kMaxDim || check_w8a8(K, 0, W4A4_DTYPE_BF16) != W4A4_OK) return 0;
+  return align256((size_t)M * (size_t)K) + align256((size_t)M * sizeof(float));
+}
+
+w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void* qweight, const float* wscales,
+                        const void* smooth_factor, const void* bias, int64_t M, int64_t N, int64_t K,
+                        int32_t hadamard_block, void* y, int64_t ldy, int32_t y_dtype, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  // sizes and types of both halves first, then the empty call, the pointers, the alignments
+  w4a4_status st = validate_quantize_w8a8(nullptr, ldx, x_dtype, nullptr, 0, K, hadamard_block, nullptr, nullptr);
+  if (st != W4A4_OK) return st;
+  st = validate_gemm_w8a8(nullptr, nullptr, nullptr, nullptr, nullptr, M, 0, K, nullptr, ldy, y_dtype);
+  if (st != W4A4_OK) return st;
+  if (N < 0 || N > kMaxDim || ldy < N || ((M + 63) / 64) * ((N + 63) / 64) > kMaxDim) return W4A4_ERR_SHAPE;
+  if (M == 0 || N == 0) return W4A4_OK;
+  if (!workspace) return W4A4_ERR_NULL;
+  if (workspace_bytes < w8a8_linear_workspace_bytes(M, K)) return W4A4_ERR_SHAPE;
+  if (!aligned(workspace, 256)) return W4A4_ERR_ALIGN;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  float* ascales = reinterpret_cast<float*>(ws + align256((size_t)M * (size_t)K));
+  st = validate_quantize_w8a8(x, ldx, x_dtype, smooth_factor, M, K, hadamard_block, ws, ascales);
+  if (st != W4A4_OK) return st;
+  st = validate_gemm_w8a8(ws, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype);
+  if (st != W4A4_OK) return st;
+  st = quantize_w8a8(true, x, ldx, x_dtype, smooth_factor, M, K, hadamard_block, ws, ascales, stream);
+  if (st != W4A4_OK) return st;
+  return gemm_w8a8(ws, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype, stream);
+}
+
+}  // extern "C"
+
+// ---- q / k head norm and rotary positions ------------------------------------------------------
+
+namespace {
+
+constexpr int64_t kMaxHeads = 1 << 15;
+
+// One tensor's sizes: input strides may be anything from 0 up (a broadcast head is read again);
+// output elements must not share an address: heads inside tokens or tokens inside heads.
+w4a4_status check_heads(const w4a4_heads& h, int64_t T, int64_t D) {
+  if (h.heads < 0 || h.heads > kMaxHeads) return W4A4_ERR_SHAPE;
+  if (h.heads == 0 || T == 0) return W4A4_OK;
+  if (h.x_token_stride < 0 || h.x_head_stride < 0 || h.y_token_stride < 0 || h.y_head_stride < 0) return W4A4_ERR_SHAPE;
+  const int64_t most = (int64_t)1 << 40;
+  if (h.x_token_stride > most || h.x_head_stride > most || h.y_token_stride > most || h.y_head_stride > most)
+    return W4A4_ERR_SHAPE;
+  // (T, heads <= 2^31, strides <= 2^40: the products below need 128 bits only where they are refused)
+  auto inside = [](int64_t n, int64_t s, int64_t width, int64_t outer, int64_t count) {
+    return (n == 1 || s >= width) && (count == 1 || (__int128)outer >= (__int128)(n - 1) * s + width);
+  };
+  if (!inside(h.heads, h.y_head_stride, D, h.y_token_stride, T) &&
+      !inside(T, h.y_token_stride, D, h.y_head_stride, h.heads))
+    return W4A4_ERR_SHAPE;
+  if (h.x == h.y && h.x != nullptr &&
+      ((T > 1 && h.x_token_stride != h.y_token_stride) || (h.heads > 1 && h.x_head_stride != h.y_head_stride)))
+    return W4A4_ERR_SHAPE;
+  return W4A4_OK;
+}
+
+w4a4::RopeHeads rope_heads(const w4a4_heads& h) {
+  return {h.x, h.x_token_stride, h.x_head_stride, (int)h.heads, h.weight, h.y, h.y_token_stride, h.y_head_stride};
+}
+
+}  // namespace
+
+extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* k, const void* positions,
+                                         int64_t tokens, int32_t head_dim, int32_t axes, const int32_t* axis_dims,
+                                         int32_t layout, int32_t flags, double theta, float eps, int32_t dtype,
+                                         void* stream) {
+  if (dtype < W4A4_DTYPE_BF16 || dtype > W4A4_DTYPE_F32) return W4A4_ERR_UNSUPPORTED;
+  if (layout < W4A4_ROPE_INTERLEAVED || layout > W4A4_ROPE_AXIS_HALF) return W4A4_ERR_UNSUPPORTED;
+  if ((flags & ~(W4A4_ROPE_NORM | W4A4_ROPE_SHARED_FREQUENCIES | W4A4_ROPE_POSITIONS_I64)) != 0) return W4A4_ERR_UNSUPPORTED;
+  if (head_dim > W4A4_ROPE_MAX_HEAD_DIM || axes > W4A4_ROPE_MAX_AXES) return W4A4_ERR_UNSUPPORTED;
+  if (tokens < 0 || tokens > kMaxDim || head_dim < 2 || head_dim % 2 != 0 || axes < 0) return W4A4_ERR_SHAPE;
+  if (axes > 0 && !axis_dims) return W4A4_ERR_NULL;
+  if (!(theta > 0.0) || !std::isfinite(theta) || !(eps >= 0.0f) || !std::isfinite(eps)) return W4A4_ERR_SHAPE;
+  w4a4::RopeArgs a{};
+  int64_t rot = 0;
+  for (int x = 0; x < axes; ++x) {
+    if (axis_dims[x] < 0 || axis_dims[x] % 2 != 0 || axis_dims[x] > head_dim) return W4A4_ERR_SHAPE;
+    rot += axis_dims[x];
+    a.start[x + 1] = (int)(rot / 2);
+  }
+  if (rot > head_dim) return W4A4_ERR_SHAPE;
+  if (!q) return W4A4_ERR_NULL;
+  const w4a4_heads none{};
+  const w4a4_heads& kk = k ? *k : none;
+  for (const w4a4_heads* h : {q, &kk}) {
+    w4a4_status st = check_heads(*h, tokens, head_dim);
+    if (st != W4A4_OK) return st;
+  }
+  if (tokens == 0 || q->heads + kk.heads == 0) return W4A4_OK;
+  if (rot > 0 && !positions) return W4A4_ERR_NULL;
+  const uintptr_t es = dtype == W4A4_DTYPE_F32 ? 4 : 2;
+  for (const w4a4_heads* h : {q, &kk})
+    if (h->heads > 0 && (!h->x || !h->y)) return W4A4_ERR_NULL;
+  for (const w4a4_heads* h : {q, &kk})
+    if (h->heads > 0 && (!aligned(h->x, es) || !aligned(h->y, es) || !aligned(h->weight, es))) return W4A4_ERR_ALIGN;
+  if (rot > 0 && !aligned(positions, (flags & W4A4_ROPE_POSITIONS_I64) ? 8 : 4)) return W4A4_ERR_ALIGN;
+  a.q = rope_heads(*q);
+  a.k = rope_heads(kk);
+  a.pos = positions;
+  a.tokens = (int)tokens;
+  a.D = head_dim;
+  a.axes = axes;
+  a.rot2 = (int)(rot / 2);
+  a.layout = layout;
+  a.norm = (flags & W4A4_ROPE_NORM) != 0;
+  a.shared = (flags & W4A4_ROPE_SHARED_FREQUENCIES) != 0;
+  a.pos64 = (flags & W4A4_ROPE_POSITIONS_I64) != 0;
+  a.eps = eps;
+  a.inv_d = (float)(1.0 / head_dim);
+  a.log2_theta = std::log2(theta);
+  if (!w4a4::launch_qk_norm_rope) return W4A4_ERR_HIP;
+  (void)hipGetLastError();
+  return from_hip(w4a4::launch_qk_norm_rope(a, dtype, static_cast<hipStream_t>(stream)));
+}

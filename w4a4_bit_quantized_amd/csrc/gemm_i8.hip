@@ -1,0 +1,362 @@
+// int8 GEMM of the W8A8 layer (gfx950): one scale per token and per output channel.
+//
+//   y[m, n] = store( (float32(sum_k qact[m, k] qweight[n, k]) * ascales[m]) * wscales[n] + bias[n] )
+// The sum is exact in int32 (K <= 131056: |sum| <= K * 127 * 128 < 2^31); the conversion to
+// float32, the two products and the sum round to nearest, then one rounding to the storage type.
+//
+// Both operands are K-contiguous bytes, so every 16-byte chunk is matrix-core operand data as it
+// stands: v_mfma_i32_32x32x32_i8 takes 16 K-columns per lane (row l % 32, columns 16 (l / 32) ..).
+// Weights are the first operand, activations the second: lane l then holds column m = l % 32 of
+// the product and four consecutive n per accumulator quad.
+//
+// Chunks past K (K is a multiple of 16, a K-step has 128 columns) are read from a 16-byte block of
+// zeros, rows past M or N repeat the last row and are not stored.
+#include <cstring>
+
+#include "device_common.h"
+#include "gemm_common.h"
+#include "launch.h"
+
+namespace w4a4 {
+
+namespace {
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+__device__ __attribute__((aligned(16))) const uint32_t zero_chunk[4] = {0u, 0u, 0u, 0u};
+
+// Storage types of y: 0 bf16, 1 f16, 2 f32.
+template <int YT>
+struct YType {
+  static constexpr int ES = YT == 2 ? 4 : 2;
+};
+
+__device__ __forceinline__ uint32_t pack_f16x2(float a, float b) {
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, f16x2_t{(_Float16)a, (_Float16)b});  // round to nearest even
+}
+
+template <int YT>
+__device__ __forceinline__ void store_one(void* y, size_t i, float v) {
+  if constexpr (YT == 2) static_cast<float*>(y)[i] = v;
+  else if constexpr (YT == 1) static_cast<_Float16*>(y)[i] = (_Float16)v;
+  else static_cast<uint16_t*>(y)[i] = (uint16_t)pack_bf16x2(v, v);
+}
+
+// ---- tiled GEMM ----------------------------------------------------------------------------------
+
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S>
+struct TileI8 {
+  static constexpr int WAVES = WAVES_M * WAVES_N;
+  static constexpr int THREADS = 64 * WAVES;
+  static constexpr int BM = WAVES_M * FM * 32, BN = WAVES_N * FN * 32;
+  static constexpr int ROWS = BM + BN;             // activation rows, then weight rows
+  static constexpr int STEP = 128;                 // K columns (bytes) per stage: whole 128-byte lines
+  static constexpr int STAGE = ROWS * STEP;
+  static constexpr int ROUNDS = ROWS / (8 * WAVES);  // a wave's direct load fills 8 rows
+  static constexpr int REGION = 32 * FN * 32 * 4;  // a wave's epilogue region: 32 rows of f32
+  static constexpr int EPI = WAVES * REGION + BN * 8;
+  static constexpr int LDS = S * STAGE > EPI ? S * STAGE : EPI;
+  static_assert(ROWS % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole rounds per operand");
+  static_assert(LDS <= 160 * 1024, "LDS of one CU");
+  static_assert(ROUNDS * (S - 1) < 64, "vmcnt range");
+};
+
+// LDS slot of chunk c of row r: c ^ ((r >> 1) & 7).  16 consecutive rows reading one chunk then
+// touch 16 distinct 16-byte columns of the 256 bytes of banks.
+__device__ __forceinline__ int i8_swizzle(int row) { return (row >> 1) & 7; }
+
+// 16 bytes per lane from `src` to LDS at dst + 16 lane (dst is the wave's).
+__device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
+}
+
+// Direct loads of one K-step into a stage, ROUNDS instructions per wave: 16 bytes per lane, 8 rows of
+// 128 bytes per instruction.
+template <class T>
+__device__ __forceinline__ void i8_issue(uint8_t* stage, int wave, uint32_t k0, uint32_t K, const uint8_t* abase,
+                                         const uint8_t* bbase, const uint32_t* off, const uint32_t* col) {
+  if (k0 + T::STEP <= K) {
+#pragma unroll
+    for (int r = 0; r < T::ROUNDS; ++r)
+      load_lds16((r * T::WAVES * 8 < T::BM ? abase : bbase) + k0 + off[r], stage + (r * T::WAVES + wave) * 1024);
+  } else {
+#pragma unroll
+    for (int r = 0; r < T::ROUNDS; ++r) {
+      const uint8_t* p = (r * T::WAVES * 8 < T::BM ? abase : bbase) + k0 + off[r];
+      if (k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
+      load_lds16(p, stage + (r * T::WAVES + wave) * 1024);
+    }
+  }
+}
+
+// Operands of K-columns 32 ks .. + 32 of a stage.  Fragment and wave offsets are multiples of 32
+// rows, so the swizzle depends on the lane's row within 32 only.
+template <int FM, int FN>
+__device__ __forceinline__ void i8_read(const uint8_t* stage, int ks, int ra, int rb, int h, i32x4_t (&a)[FM],
+                                        i32x4_t (&b)[FN]) {
+  const int c = 16 * ((2 * ks + h) ^ i8_swizzle(ra));
+#pragma unroll
+  for (int j = 0; j < FN; ++j) b[j] = *reinterpret_cast<const i32x4_t*>(stage + (rb + j * 32) * 128 + c);
+#pragma unroll
+  for (int i = 0; i < FM; ++i) a[i] = *reinterpret_cast<const i32x4_t*>(stage + (ra + i * 32) * 128 + c);
+}
+
+template <int FM, int FN>
+__device__ __forceinline__ void i8_mma(i32x16_t (&acc)[FM][FN], const i32x4_t (&a)[FM], const i32x4_t (&b)[FN]) {
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+}
+
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int YT>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
+    const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
+    const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
+    int64_t ldy) {
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+  const int l32 = lane & 31, h = lane >> 5;
+  int tm, tn;
+  tile_of((int)blockIdx.x, (int)gridDim.x, (M + T::BM - 1) / T::BM, (N + T::BN - 1) / T::BN, tm, tn);
+  const int m0 = tm * T::BM, n0 = tn * T::BN;
+  const int nkt = (K + T::STEP - 1) / T::STEP;
+  const uint8_t* abase = qa + (size_t)m0 * K;
+  const uint8_t* bbase = qw + (size_t)n0 * K;
+  const int rows_a = min(T::BM, M - m0), rows_b = min(T::BN, N - n0);
+
+  // byte offset in the operand and K-column of this lane's chunk in every round
+  uint32_t off[T::ROUNDS], col[T::ROUNDS];
+#pragma unroll
+  for (int r = 0; r < T::ROUNDS; ++r) {
+    const int row = (r * T::WAVES + wave) * 8 + (lane >> 3);
+    col[r] = 16u * (uint32_t)((lane & 7) ^ i8_swizzle(row));
+    const int src = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
+    off[r] = (uint32_t)src * (uint32_t)K + col[r];
+  }
+  const int ra = wm * FM * 32 + l32, rb = T::BM + wn * FN * 32 + l32;
+  i32x16_t acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+  // K-steps 0 .. S - 2 in flight; past the last one the last is loaded again, so that every step
+  // waits on the same count.
+#pragma unroll
+  for (int j = 0; j < S - 1; ++j)
+    i8_issue<T>(lds + j * T::STAGE, wave, (uint32_t)min(j, nkt - 1) * T::STEP, (uint32_t)K, abase, bbase, off, col);
+  vm_wait_barrier<(S - 2) * T::ROUNDS>();
+  i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
+  int slot = 0;
+  i8_issue<T>(lds + (S - 1) * T::STAGE, wave, (uint32_t)min(S - 1, nkt - 1) * T::STEP, (uint32_t)K, abase, bbase, off, col);
+  i8_read<FM, FN>(lds, 0, ra, rb, h, a0, b0);
+  for (int kt = 0; kt < nkt; ++kt) {
+    uint8_t* cur = lds + slot * T::STAGE;
+    i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
+    i8_mma<FM, FN>(acc, a0, b0);
+    i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
+    i8_mma<FM, FN>(acc, a1, b1);
+    i8_read<FM, FN>(cur, 3, ra, rb, h, a1, b1);
+    i8_mma<FM, FN>(acc, a0, b0);
+    // the next K-step has landed and every wave has read this one's operands
+    vm_wait_barrier<(S - 2) * T::ROUNDS>();
+    i8_issue<T>(cur, wave, (uint32_t)min(kt + S, nkt - 1) * T::STEP, (uint32_t)K, abase, bbase, off, col);
+    slot = slot == S - 1 ? 0 : slot + 1;
+    i8_read<FM, FN>(lds + slot * T::STAGE, 0, ra, rb, h, a0, b0);
+    i8_mma<FM, FN>(acc, a1, b1);
+  }
+  vm_wait_barrier<0>();
+
+  // Epilogue: the channel scales and biases of the tile once in LDS; each wave passes one 32-row
+  // fragment row at a time through its own region and stores whole 16-byte runs of y rows.
+  float* s_lds = reinterpret_cast<float*>(lds + T::WAVES * T::REGION);
+  float* b_lds = s_lds + T::BN;
+  for (int c = t; c < T::BN; c += T::THREADS) {
+    const int n = n0 + c;
+    s_lds[c] = n < N ? sw[n] : 0.0f;
+    b_lds[c] = (bias != nullptr && n < N) ? bf16_bits_to_f32(bias[n]) : 0.0f;
+  }
+  __syncthreads();
+  constexpr int ES = YType<YT>::ES;
+  constexpr int RSB = FN * 32 * ES;   // bytes per region row
+  constexpr int CPR = RSB / 16;       // 16-byte chunks per region row
+  uint8_t* reg = lds + wave * T::REGION;
+  const int mb = m0 + wm * FM * 32, nb = n0 + wn * FN * 32;
+  const bool vec = ((reinterpret_cast<uintptr_t>(y) | ((uint64_t)ldy * ES)) & 15) == 0;
+  const bool has_bias = bias != nullptr;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const float as = sa[min(mb + i * 32 + l32, M - 1)];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int col = wn * FN * 32 + j * 32 + 8 * q + 4 * h;
+        const float4_t s = *reinterpret_cast<const float4_t*>(s_lds + col);
+        const float4_t b = *reinterpret_cast<const float4_t*>(b_lds + col);
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[e] = ((float)acc[i][j][4 * q + e] * as) * s[e];
+          if (has_bias) v[e] += b[e];
+        }
+        // chunk ch of row r sits at (ch + r / 2) % CPR
+        if constexpr (YT == 2) {
+          const int ch = 8 * j + 2 * q + h;
+          *reinterpret_cast<float4_t*>(reg + l32 * RSB + 16 * ((ch + (l32 >> 1)) % CPR)) = float4_t{v[0], v[1], v[2], v[3]};
+        } else {
+          const int ch = 4 * j + q;
+          const u32x2_t p = YT == 1 ? u32x2_t{pack_f16x2(v[0], v[1]), pack_f16x2(v[2], v[3])}
+                                    : u32x2_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+          *reinterpret_cast<u32x2_t*>(reg + l32 * RSB + 16 * ((ch + (l32 >> 1)) % CPR) + 8 * h) = p;
+        }
+      }
+    wave_lds_sync();
+    constexpr int EPC = 16 / ES;  // elements per chunk
+#pragma unroll
+    for (int it = 0; it < CPR / 2; ++it) {
+      const int c = it * 64 + lane, r = c / CPR, ch = c % CPR;
+      const uint8_t* src = reg + r * RSB + 16 * ((ch + (r >> 1)) % CPR);
+      const int m = mb + i * 32 + r, n = nb + EPC * ch;
+      if (m < M && n < N) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
+        uint8_t* dst = static_cast<uint8_t*>(y) + ((size_t)m * ldy + n) * ES;
+        if (vec && n + EPC <= N) {
+          *reinterpret_cast<u32x4_t*>(dst) = v;
+        } else {
+#pragma unroll
+          for (int e = 0; e < EPC; ++e)
+            if (n + e < N) {
+              if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[e] = v[e];
+              else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+            }
+        }
+      }
+    }
+    wave_lds_sync();  // the region is rewritten by the next fragment row
+  }
+}
+
+// ---- small batches: weight streaming ---------------------------------------------------------------
+// A workgroup of WAVES waves owns 16 weight rows and up to 16 MB activation rows; its waves split K
+// (wave w takes K-steps w, w + WAVES, ... of 64 columns), each streaming its weights from HBM and
+// its activations from L2 straight into matrix-core operand registers (v_mfma_i32_16x16x64_i8: row
+// l % 16, columns 16 (l / 16) ..), and their int32 partial sums meet in LDS.
+constexpr int SK_WAVES = 8;
+
+template <int MB, int YT>
+__global__ __launch_bounds__(64 * SK_WAVES) void gemm_i8_skinny_kernel(
+    const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
+    const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
+    int64_t ldy) {
+  __shared__ int part[SK_WAVES][MB * 256];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 16;
+  const uint8_t* wp = qw + (size_t)min(n0 + l16, N - 1) * K + 16 * g;
+  const uint8_t* ap[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) ap[i] = qa + (size_t)min(16 * i + l16, M - 1) * K + 16 * g;
+  i32x4_t acc[MB];
+#pragma unroll
+  for (int i = 0; i < MB; ++i) acc[i] = i32x4_t{0, 0, 0, 0};
+  constexpr int U = MB >= 4 ? 4 : 8;  // K-steps loaded before they are multiplied
+  const int steps = (K + 63) / 64;
+  for (int s0 = wave; s0 < steps; s0 += SK_WAVES * U) {
+    i32x4_t wv[U], av[U][MB];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int k = 64 * (s0 + SK_WAVES * u);
+      const bool in = k + 16 * g < K;  // chunks past K are zero on both sides
+      wv[u] = in ? *reinterpret_cast<const i32x4_t*>(wp + k) : i32x4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < MB; ++i) av[u][i] = in ? *reinterpret_cast<const i32x4_t*>(ap[i] + k) : i32x4_t{0, 0, 0, 0};
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MB; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], av[u][i], acc[i], 0, 0, 0);
+  }
+  // acc[i][r] is the partial sum of m = 16 i + l16, n = n0 + 4 g + r
+#pragma unroll
+  for (int i = 0; i < MB; ++i) *reinterpret_cast<i32x4_t*>(&part[wave][i * 256 + l16 * 16 + 4 * g]) = acc[i];
+  __syncthreads();
+  for (int o = t; o < MB * 256; o += 64 * SK_WAVES) {
+    const int m = o >> 4, n = n0 + (o & 15);
+    if (m >= M || n >= N) continue;
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < SK_WAVES; ++w) sum += part[w][o];
+    float v = ((float)sum * sa[m]) * sw[n];
+    if (bias != nullptr) v += bf16_bits_to_f32(bias[n]);
+    store_one<YT>(y, (size_t)m * ldy + n, v);
+  }
+}
+
+struct GArgs {
+  const uint8_t* qa;
+  const float* sa;
+  const uint8_t* qw;
+  const float* sw;
+  const uint16_t* bias;
+  int M, N, K;
+  void* y;
+  int64_t ldy;
+  hipStream_t stream;
+};
+
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int YT>
+hipError_t run_tile(const GArgs& a) {
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S>;
+  const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
+  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
+      a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
+  return hipGetLastError();
+}
+
+template <int MB, int YT>
+hipError_t run_skinny(const GArgs& a) {
+  gemm_i8_skinny_kernel<MB, YT><<<dim3((unsigned)((a.N + 15) / 16)), 64 * SK_WAVES, 0, a.stream>>>(
+      a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
+  return hipGetLastError();
+}
+
+template <int YT>
+hipError_t run(const GArgs& a) {
+  const char* forced = test_hook("W8A8_GEMM_TILE");
+  auto is = [&](const char* s) { return forced && !strcmp(forced, s); };
+  if (forced ? is("skinny") && a.M <= 64 : a.M <= 64) {
+    if (a.M <= 16) return run_skinny<1, YT>(a);
+    if (a.M <= 32) return run_skinny<2, YT>(a);
+    return run_skinny<4, YT>(a);
+  }
+  const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
+  const int64_t t128 = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
+  if (forced ? is("256") : t256 >= 192) return run_tile<2, 4, 4, 2, 2, YT>(a);
+  if (forced ? is("128") : t128 >= 192) return run_tile<2, 2, 2, 2, 4, YT>(a);
+  return run_tile<2, 2, 1, 1, 4, YT>(a);
+}
+
+}  // namespace
+
+hipError_t launch_gemm_i8(const void* qact, const float* ascales, const void* qweight, const float* wscales,
+                          const void* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy, int ydtype,
+                          hipStream_t stream) {
+  const GArgs a{static_cast<const uint8_t*>(qact), ascales, static_cast<const uint8_t*>(qweight), wscales,
+                static_cast<const uint16_t*>(bias), (int)M, (int)N, (int)K, y, ldy, stream};
+  switch (ydtype) {
+    case 0: return run<0>(a);
+    case 1: return run<1>(a);
+    default: return run<2>(a);
+  }
+}
+
+}  // namespace w4a4

@@ -8,6 +8,11 @@
 
 namespace w4a4 {
 
+// Launchers that a host-only build of the C-ABI layer (argument validation without kernels) may
+// leave out: their references are weak, and an entry point whose launcher is missing returns
+// W4A4_ERR_HIP.
+#define W4A4_KERNELS __attribute__((weak))
+
 // Kernel-path overrides.  Only the test build of the library (compiled with W4A4_TEST_HOOKS)
 // reads them, from the environment, so that tests can force every kernel variant; in the
 // product build every hook is absent and the automatic choice always applies.
@@ -67,6 +72,47 @@ hipError_t launch_gemm_skinny_mx(const void* qact, const void* ascales, const fl
 // norm = float32(1 / sqrt(block)).  x == y (with ldx == ldy) transforms in place.
 hipError_t launch_hadamard(const void* x, int64_t ldx, void* y, int64_t ldy, int64_t rows, int64_t cols, int block,
                            int dtype, float norm, hipStream_t stream);
+
+// int8 quantizer of the W8A8 layer over rows x K (K a multiple of 16; x with a row stride of ldx
+// elements, 16-byte aligned rows; dtype 0 bf16, 1 f16, 2 f32): divides by `lam` (act) or multiplies
+// by it, `lam` may be null; block 0 or 16, 32, 64, 128 with norm = float32(1 / sqrt(block)).
+hipError_t W4A4_KERNELS launch_quantize_i8(bool act, const void* x, int64_t ldx, const void* lam, int64_t rows,
+                                           int64_t K, int block, int dtype, float norm, void* q, float* scales,
+                                           hipStream_t stream);
+
+// int8 GEMM with scales per row and column and an optional bias (bf16 [N], may be null); y has a
+// row stride of ldy elements and the given type.
+hipError_t W4A4_KERNELS launch_gemm_i8(const void* qact, const float* ascales, const void* qweight,
+                                       const float* wscales, const void* bias, int64_t M, int64_t N, int64_t K, void* y,
+                                       int64_t ldy, int ydtype, hipStream_t stream);
+
+// Heads of one tensor of qk_norm_rope: element (token, head, d) at x + token ts + head hs + d.
+struct RopeHeads {
+  const void* x;
+  int64_t ts, hs;
+  int heads;
+  const void* weight;
+  void* y;
+  int64_t yts, yhs;
+};
+
+constexpr int ROPE_MAX_AXES = 8;
+
+struct RopeArgs {
+  RopeHeads q, k;
+  const void* pos;                // [tokens, axes], int32 or int64
+  int tokens, D, axes;
+  int rot2;                       // rotated pairs
+  int start[ROPE_MAX_AXES + 1];   // first pair of every axis, then rot2
+  int layout;                     // 0 interleaved, 1 halves of the span, 2 halves of each axis's slice
+  bool norm, shared, pos64;
+  float eps, inv_d;
+  double log2_theta;
+  int tb, hb, log2g;              // set by the launcher: tokens and heads per workgroup, lanes per head
+};
+
+// RMS norm and rotary rotation of q and k heads; dtype 0 bf16, 1 f16, 2 f32.
+hipError_t W4A4_KERNELS launch_qk_norm_rope(RopeArgs args, int dtype, hipStream_t stream);
 
 // Device address of the static workspace of svdq_linear_noalloc on the current device (looked up
 // once per device), or NULL when the lookup fails.

@@ -1,0 +1,327 @@
+// RMS norm of query and key heads with the rotary position rotation in the same pass (gfx950).
+//
+// For every token t and head of D elements:
+//   r = 1 / sqrt(mean(x^2) + eps),  u = (x * r) * weight          (optional norm, optional weight)
+//   pair p of the rotary span belongs to one position axis a, is number i of its dim_a / 2 pairs, and
+//   turns by  pos[t, a] * theta^(-2 i / dim_a)      (each axis its own frequencies)
+//         or  pos[t, a] * theta^(-2 p / rot)        (one ladder of frequencies over all pairs)
+//   (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
+// Elements past the rotary span are only normed.  float32 throughout, one rounding at the store.
+// The angle is formed in turns in float64 and reduced to half a turn there, so a position of any
+// size costs no accuracy: what is left, |r| <= 1/2, is rounded to float32 and passed to sincospi.
+//
+// Bound: HBM (every element read and written once).  A group of G lanes (a power of two) holds one
+// head of one token, 2 V elements per lane: V pairs, so a rotation never leaves its lane and the only
+// exchange is the sum of squares (DPP within 16 lanes).  A workgroup takes TB tokens; their cosines and
+// sines are made once, in LDS, and shared by all their heads.  The heads of a few items are loaded
+// before the first of them is used.
+#include <math.h>
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace w4a4 {
+
+namespace {
+
+constexpr int RT = 256;  // threads per workgroup
+
+template <int DT>
+__device__ __forceinline__ constexpr int esize() { return DT == 2 ? 4 : 2; }
+
+// N consecutive elements (N = 1, 4 or 8; whole vectors are aligned to their size, at most 16 bytes).
+template <int DT, int N>
+__device__ __forceinline__ void load_n(const uint8_t* p, float* v) {
+  if constexpr (N == 1) {
+    if constexpr (DT == 2) v[0] = *reinterpret_cast<const float*>(p);
+    else if constexpr (DT == 1) v[0] = (float)*reinterpret_cast<const _Float16*>(p);
+    else v[0] = bf16_bits_to_f32(*reinterpret_cast<const uint16_t*>(p));
+  } else if constexpr (DT == 2) {
+#pragma unroll
+    for (int c = 0; c < N; c += 4) {
+      const float4_t f = *reinterpret_cast<const float4_t*>(p + 4 * c);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[c + e] = f[e];
+    }
+  } else {
+    uint32_t w[N / 2];
+    if constexpr (N == 8) {
+      const u32x4_t f = *reinterpret_cast<const u32x4_t*>(p);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = f[e];
+    } else {
+      const u32x2_t f = *reinterpret_cast<const u32x2_t*>(p);
+      w[0] = f[0];
+      w[1] = f[1];
+    }
+#pragma unroll
+    for (int e = 0; e < N / 2; ++e) {
+      if constexpr (DT == 1) {
+        const half2_t h = __builtin_bit_cast(half2_t, w[e]);
+        v[2 * e] = (float)h[0];
+        v[2 * e + 1] = (float)h[1];
+      } else {
+        v[2 * e] = __uint_as_float(w[e] << 16);
+        v[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {  // round to nearest even
+  if constexpr (DT == 1) {
+    return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
+  } else {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf16x2_t));
+  }
+}
+
+template <int DT, int N>
+__device__ __forceinline__ void store_n(uint8_t* p, const float* v) {
+  if constexpr (N == 1) {
+    if constexpr (DT == 2) *reinterpret_cast<float*>(p) = v[0];
+    else *reinterpret_cast<uint16_t*>(p) = (uint16_t)pack2<DT>(v[0], v[0]);
+  } else if constexpr (DT == 2) {
+#pragma unroll
+    for (int c = 0; c < N; c += 4)
+      *reinterpret_cast<float4_t*>(p + 4 * c) = float4_t{v[c], v[c + 1], v[c + 2], v[c + 3]};
+  } else if constexpr (N == 8) {
+    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                                             pack2<DT>(v[6], v[7])};
+  } else {
+    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+
+// Sum over the aligned group of G lanes (the same value in every lane: each step adds two values
+// that all lanes of both halves share).
+__device__ __forceinline__ float group_sum(float v, int G) {
+  if (G >= 2) v += dpp<0xB1>(v);    // quad_perm [1,0,3,2]
+  if (G >= 4) v += dpp<0x4E>(v);    // quad_perm [2,3,0,1]
+  if (G >= 8) v += dpp<0x141>(v);   // row_half_mirror
+  if (G >= 16) v += dpp<0x140>(v);  // row_mirror
+  if (G >= 32) v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x1F | (16 << 10)));
+  if (G >= 64) v += __shfl_xor(v, 32);
+  return v;
+}
+
+// Where the first and second elements of pairs p .. p + V - 1 start.  Layout 0: interleaved; 1: halves
+// of the rotary span; 2: halves of each axis's slice.  Past the span (p >= rot2) the chunk's 2 V
+// elements are taken as they lie: they are not rotated.
+template <int V>
+__device__ __forceinline__ void pair_elements(const RopeArgs& a, int p, int& e0, int& e1) {
+  e0 = 2 * p;
+  e1 = 2 * p + V;
+  if (p < a.rot2) {
+    if (a.layout == 1) {
+      e0 = p;
+      e1 = p + a.rot2;
+    } else if (a.layout == 2) {
+      int x = 0;
+      while (x + 1 < a.axes && p >= a.start[x + 1]) ++x;
+      e0 = a.start[x] + p;  // 2 start + (p - start)
+      e1 = e0 + a.start[x + 1] - a.start[x];
+    }
+  }
+}
+
+// INTER (V = 4): the lane's V pairs are 2 V consecutive elements; otherwise V consecutive elements at
+// e0 and V at e1.  IT: chunks of V pairs per lane; UN: items in flight.
+template <int DT, int V, bool INTER, int IT, int UN>
+__global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
+  extern __shared__ __attribute__((aligned(16))) float trig[];  // [TB][D / 2] cosines, then sines
+  const int t = threadIdx.x;
+  const int D2 = a.D / 2, G = 1 << a.log2g;
+  const int t0 = blockIdx.x * a.tb;
+  const int nt = min(a.tb, a.tokens - t0);
+  const int heads = a.q.heads + a.k.heads;
+  const int h0 = blockIdx.y * a.hb, nh = min(a.hb, heads - h0);
+  constexpr int ES = esize<DT>();
+
+  float* cos_t = trig;
+  float* sin_t = trig + a.tb * D2;
+  for (int i = t; i < nt * D2; i += RT) {
+    const int tok = i / D2, p = i - tok * D2;
+    float c = 1.0f, s = 0.0f;
+    if (p < a.rot2) {
+      int x = 0;
+      while (x + 1 < a.axes && p >= a.start[x + 1]) ++x;
+      const double e = a.shared ? (double)p / a.rot2 : (double)(p - a.start[x]) / (a.start[x + 1] - a.start[x]);
+      const size_t at = (size_t)(t0 + tok) * a.axes + x;
+      const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[at]
+                                 : (double)static_cast<const int32_t*>(a.pos)[at];
+      const double turns = pos * (exp2(-e * a.log2_theta) * 0.15915494309189535);
+      sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+    }
+    cos_t[i] = c;
+    sin_t[i] = s;
+  }
+
+  // this lane's chunks: the same pairs for every item
+  const int gl = t & (G - 1), grp = t >> a.log2g, ng = RT >> a.log2g;
+  int e0[IT], e1[IT];
+  bool in[IT];
+  float wq[IT][2 * V], wk[IT][2 * V];
+#pragma unroll
+  for (int c = 0; c < IT; ++c) {
+    const int p = (gl + c * G) * V;
+    in[c] = p < D2;
+    pair_elements<V>(a, in[c] ? p : 0, e0[c], e1[c]);
+#pragma unroll
+    for (int i = 0; i < 2 * V; ++i) wq[c][i] = wk[c][i] = 1.0f;
+    if (in[c]) {
+      auto weights = [&](const void* w, float* to) {
+        if (w == nullptr) return;
+        const uint8_t* b = static_cast<const uint8_t*>(w);
+        if constexpr (INTER) {
+          load_n<DT, 2 * V>(b + e0[c] * ES, to);
+        } else {
+          load_n<DT, V>(b + e0[c] * ES, to);
+          load_n<DT, V>(b + e1[c] * ES, to + V);
+        }
+      };
+      weights(a.q.weight, wq[c]);
+      weights(a.k.weight, wk[c]);
+    }
+  }
+  __syncthreads();
+
+  int tok = 0, head = grp;  // item of this group: token t0 + tok, head h0 + head
+  while (head >= nh) { head -= nh; ++tok; }
+  while (tok < nt) {
+    float v[UN][IT][2 * V];
+    int it_tok[UN];
+    bool it_q[UN];
+    uint8_t* dst[UN];
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      const bool valid = tok < nt;
+      const int hd = h0 + head;
+      const bool isq = hd < a.q.heads;
+      it_tok[u] = valid ? tok : -1;
+      it_q[u] = isq;
+      const int hh = isq ? hd : hd - a.q.heads;
+      const int64_t tt = t0 + tok;
+      const uint8_t* src = static_cast<const uint8_t*>(isq ? a.q.x : a.k.x) +
+                           (tt * (isq ? a.q.ts : a.k.ts) + hh * (isq ? a.q.hs : a.k.hs)) * ES;
+      dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
+               (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
+#pragma unroll
+      for (int c = 0; c < IT; ++c) {
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) v[u][c][i] = 0.0f;
+        if (valid && in[c]) {
+          if constexpr (INTER) {
+            load_n<DT, 2 * V>(src + e0[c] * ES, v[u][c]);
+          } else {
+            load_n<DT, V>(src + e0[c] * ES, v[u][c]);
+            load_n<DT, V>(src + e1[c] * ES, v[u][c] + V);
+          }
+        }
+      }
+      head += ng;
+      while (head >= nh) { head -= nh; ++tok; }
+    }
+#pragma unroll
+    for (int u = 0; u < UN; ++u) {
+      float r = 1.0f;
+      if (a.norm) {
+        float s = 0.0f;
+#pragma unroll
+        for (int c = 0; c < IT; ++c)
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) s = fmaf(v[u][c][i], v[u][c][i], s);
+        s = group_sum(s, G);
+        r = rsqrtf(fmaf(s, a.inv_d, a.eps));
+      }
+      if (it_tok[u] < 0) continue;
+#pragma unroll
+      for (int c = 0; c < IT; ++c) {
+        if (!in[c]) continue;
+        float o[2 * V];
+#pragma unroll
+        for (int i = 0; i < 2 * V; ++i) o[i] = a.norm ? (v[u][c][i] * r) * (it_q[u] ? wq[c][i] : wk[c][i]) : v[u][c][i];
+        const int at = it_tok[u] * D2 + (gl + c * G) * V;
+        float cs[V], sn[V];
+        if constexpr (V == 4) {
+          const float4_t cc = *reinterpret_cast<const float4_t*>(cos_t + at);
+          const float4_t ss = *reinterpret_cast<const float4_t*>(sin_t + at);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) { cs[i] = cc[i]; sn[i] = ss[i]; }
+        } else {
+          cs[0] = cos_t[at];
+          sn[0] = sin_t[at];
+        }
+        // pairs of this chunk: (o[i0], o[i1]); a chunk past the span (not interleaved) has cos 1, sin 0
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int i0 = INTER ? 2 * i : i, i1 = INTER ? 2 * i + 1 : V + i;
+          const float x0 = o[i0], x1 = o[i1];
+          o[i0] = fmaf(x0, cs[i], -(x1 * sn[i]));
+          o[i1] = fmaf(x0, sn[i], x1 * cs[i]);
+        }
+        if constexpr (INTER) {
+          store_n<DT, 2 * V>(dst[u] + e0[c] * ES, o);
+        } else {
+          store_n<DT, V>(dst[u] + e0[c] * ES, o);
+          store_n<DT, V>(dst[u] + e1[c] * ES, o + V);
+        }
+      }
+    }
+  }
+}
+
+template <int DT, int V, bool INTER, int IT, int UN>
+hipError_t run(const RopeArgs& a, hipStream_t st) {
+  const int heads = a.q.heads + a.k.heads;
+  const dim3 grid((unsigned)((a.tokens + a.tb - 1) / a.tb), (unsigned)((heads + a.hb - 1) / a.hb));
+  const size_t lds = (size_t)a.tb * a.D * sizeof(float);
+  qk_norm_rope_kernel<DT, V, INTER, IT, UN><<<grid, RT, lds, st>>>(a);
+  return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run_dt(RopeArgs a, bool vec, hipStream_t st) {
+  const int lanes = vec ? a.D / 8 : (a.D / 2 < 64 ? a.D / 2 : 64);
+  a.log2g = 0;
+  while ((1 << a.log2g) < lanes) ++a.log2g;
+  const int ng = RT >> a.log2g, heads = a.q.heads + a.k.heads;
+  // few tokens: one pass per workgroup, heads split over workgroups; many: several tokens each
+  a.tb = a.tokens >= 4096 ? 4 : 1;
+  a.hb = a.tokens < 512 && heads > ng ? ng : heads;
+  if (!vec) return run<DT, 1, false, 4, 1>(a, st);
+  return a.layout == 0 ? run<DT, 4, true, 1, 4>(a, st) : run<DT, 4, false, 1, 4>(a, st);
+}
+
+bool aligned16(const RopeHeads& h, int es) {
+  const uint64_t m = reinterpret_cast<uintptr_t>(h.x) | reinterpret_cast<uintptr_t>(h.y) |
+                     reinterpret_cast<uintptr_t>(h.weight) |
+                     ((uint64_t)(h.ts | h.hs | h.yts | h.yhs) * (uint64_t)es);
+  return h.heads == 0 || (m & 15) == 0;
+}
+
+}  // namespace
+
+hipError_t launch_qk_norm_rope(RopeArgs a, int dtype, hipStream_t stream) {
+  const int es = dtype == 2 ? 4 : 2;
+  // 4-pair vectors need whole 8-element chunks of the head, and in the split layouts whole chunks
+  // of 4 pairs in the span and in every slice
+  bool vec = a.D % 8 == 0 && aligned16(a.q, es) && aligned16(a.k, es);
+  if (a.layout == 1) vec = vec && a.rot2 % 4 == 0;
+  if (a.layout == 2)
+    for (int x = 0; x < a.axes; ++x) vec = vec && a.start[x + 1] % 4 == 0;
+  switch (dtype) {
+    case 0: return run_dt<0>(a, vec, stream);
+    case 1: return run_dt<1>(a, vec, stream);
+    default: return run_dt<2>(a, vec, stream);
+  }
+}
+
+}  // namespace w4a4
