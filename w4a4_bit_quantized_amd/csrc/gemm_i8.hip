@@ -60,7 +60,7 @@ struct TileI8 {
   static constexpr int LDS = S * STAGE > EPI ? S * STAGE : EPI;
   static_assert(ROWS % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole rounds per operand");
   static_assert(LDS <= 160 * 1024, "LDS of one CU");
-  static_assert(ROUNDS * (S - 1) < 64, "vmcnt range");
+  static_assert(ROUNDS * S < 64, "vmcnt range");
 };
 
 // LDS slot of chunk c of row r: c ^ ((r >> 1) & 7).  16 consecutive rows reading one chunk then
@@ -72,18 +72,18 @@ __device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds(src, (lds_void*)dst, 16, 0, 0);
 }
 
-// Direct loads of one K-step into a stage, ROUNDS instructions per wave: 16 bytes per lane, 8 rows of
-// 128 bytes per instruction.
-template <class T>
+// Rounds R0 .. R1 - 1 of one K-step's direct loads into a stage (16 bytes per lane, 8 rows of 128 bytes
+// per instruction).
+template <class T, int R0, int R1>
 __device__ __forceinline__ void i8_issue(uint8_t* stage, int wave, uint32_t k0, uint32_t K, const uint8_t* abase,
                                          const uint8_t* bbase, const uint32_t* off, const uint32_t* col) {
   if (k0 + T::STEP <= K) {
 #pragma unroll
-    for (int r = 0; r < T::ROUNDS; ++r)
+    for (int r = R0; r < R1; ++r)
       load_lds16((r * T::WAVES * 8 < T::BM ? abase : bbase) + k0 + off[r], stage + (r * T::WAVES + wave) * 1024);
   } else {
 #pragma unroll
-    for (int r = 0; r < T::ROUNDS; ++r) {
+    for (int r = R0; r < R1; ++r) {
       const uint8_t* p = (r * T::WAVES * 8 < T::BM ? abase : bbase) + k0 + off[r];
       if (k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
       load_lds16(p, stage + (r * T::WAVES + wave) * 1024);
@@ -109,6 +109,19 @@ __device__ __forceinline__ void i8_mma(i32x16_t (&acc)[FM][FN], const i32x4_t (&
   for (int i = 0; i < FM; ++i)
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
+}
+
+// Order of a quarter K-step: its matrix instructions with the next quarter's LDS reads between them
+// (and the direct loads, where the quarter issues them).
+template <int FM, int FN, int LOADS>
+__device__ __forceinline__ void i8_interleave() {
+#pragma unroll
+  for (int g = 0; g < FM * FN; ++g) {
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
+    if (g < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // direct load
+  }
+  __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int YT>
@@ -148,30 +161,45 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
 
-  // K-steps 0 .. S - 2 in flight; past the last one the last is loaded again, so that every step
-  // waits on the same count.
+  // K-steps in the order kt0, kt0 + 1, ..., nkt - 1, 0, ..., kt0 - 1 (integer sums do not depend on it):
+  // each XCD starts an eighth of K further on, so the eight of them fetch different columns of the
+  // panels that they share from HBM and find the others' in the Infinity Cache.  Past the last K-step
+  // the last is loaded again, so that every step waits on the same count.
+  const int kt0 = (int)(blockIdx.x & 7) * nkt / 8;
+  auto k_of = [&](int kt) {
+    const int p = min(kt, nkt - 1) + kt0;
+    return (uint32_t)(p >= nkt ? p - nkt : p) * T::STEP;
+  };
+  constexpr int R = T::ROUNDS, RH = T::ROUNDS / 2;
 #pragma unroll
   for (int j = 0; j < S - 1; ++j)
-    i8_issue<T>(lds + j * T::STAGE, wave, (uint32_t)min(j, nkt - 1) * T::STEP, (uint32_t)K, abase, bbase, off, col);
-  vm_wait_barrier<(S - 2) * T::ROUNDS>();
+    i8_issue<T, 0, R>(lds + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
+  vm_wait_barrier<(S - 2) * R>();
   i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
   int slot = 0;
-  i8_issue<T>(lds + (S - 1) * T::STAGE, wave, (uint32_t)min(S - 1, nkt - 1) * T::STEP, (uint32_t)K, abase, bbase, off, col);
   i8_read<FM, FN>(lds, 0, ra, rb, h, a0, b0);
+  i8_issue<T, 0, RH>(lds + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
   for (int kt = 0; kt < nkt; ++kt) {
     uint8_t* cur = lds + slot * T::STAGE;
+    // the second half of the loads of K-step kt + S - 1, into the slot of kt - 1
+    i8_issue<T, RH, R>(lds + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
+                       bbase, off, col);
     i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
     i8_mma<FM, FN>(acc, a0, b0);
+    i8_interleave<FM, FN, R - RH>();
     i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
     i8_mma<FM, FN>(acc, a1, b1);
+    i8_interleave<FM, FN, 0>();
     i8_read<FM, FN>(cur, 3, ra, rb, h, a1, b1);
     i8_mma<FM, FN>(acc, a0, b0);
-    // the next K-step has landed and every wave has read this one's operands
-    vm_wait_barrier<(S - 2) * T::ROUNDS>();
-    i8_issue<T>(cur, wave, (uint32_t)min(kt + S, nkt - 1) * T::STEP, (uint32_t)K, abase, bbase, off, col);
+    i8_interleave<FM, FN, 0>();
+    // K-step kt + 1 has landed and every wave has read the operands of kt: its slot is free
+    vm_wait_barrier<(S - 2) * R>();
+    i8_issue<T, 0, RH>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
     slot = slot == S - 1 ? 0 : slot + 1;
     i8_read<FM, FN>(lds + slot * T::STAGE, 0, ra, rb, h, a0, b0);
     i8_mma<FM, FN>(acc, a1, b1);
+    i8_interleave<FM, FN, RH>();
   }
   vm_wait_barrier<0>();
 
@@ -338,11 +366,22 @@ hipError_t run(const GArgs& a) {
     if (a.M <= 32) return run_skinny<2, YT>(a);
     return run_skinny<4, YT>(a);
   }
-  const int64_t t256 = (int64_t)((a.M + 255) / 256) * ((a.N + 255) / 256);
-  const int64_t t128 = (int64_t)((a.M + 127) / 128) * ((a.N + 127) / 128);
-  if (forced ? is("256") : t256 >= 192) return run_tile<2, 4, 4, 2, 2, YT>(a);
-  if (forced ? is("128") : t128 >= 192) return run_tile<2, 2, 2, 2, 4, YT>(a);
-  return run_tile<2, 2, 1, 1, 4, YT>(a);
+  auto tiles = [&](int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
+  // Less than one tile per CU: the K loop's latency bounds the launch, and the largest tile that still
+  // gives every CU at most one costs fewest bytes (128 x 8192 x 4096: 15.4 us in 64 x 64 tiles, 16.9 in
+  // 64 x 128, 19.6 in 128 x 128; 512 x 5120 x 5120: 34.6, 27.3, 23.7).
+  if (forced ? is("64") : tiles(64, 64) <= 256) return run_tile<2, 2, 1, 1, 4, YT>(a);
+  if (forced ? is("64x128") : tiles(64, 128) <= 256) return run_tile<2, 2, 1, 2, 3, YT>(a);
+  if (forced ? is("128") : tiles(128, 128) <= 256) return run_tile<2, 4, 2, 1, 4, YT>(a);
+  // Several rounds of 256 tiles: the shape with the least time, rounds by the measured time of a
+  // 128-column K-step (128 x 256: 0.88 us, 256 x 192: 1.22, 256 x 256: 1.45), so a last round that is
+  // mostly empty is cheap (4096 x 2560 x 12288: 139 us in 160 tiles of 256 x 256, 123 in 224 of 256 x 192;
+  // 4096 x 2048 x 2048: 31.7 in 128, 23.2 in 256 of 128 x 256; 4096 x 13824 x 5120: 284 / 290 / 318).
+  const int64_t c0 = (tiles(128, 256) + 255) / 256 * 88, c1 = (tiles(256, 192) + 255) / 256 * 122,
+                c2 = (tiles(256, 256) + 255) / 256 * 145;
+  if (forced ? is("256") : c2 <= c1 && c2 <= c0) return run_tile<2, 4, 4, 2, 2, YT>(a);
+  if (forced ? is("256x192") : c1 <= c0) return run_tile<4, 2, 2, 3, 2, YT>(a);
+  return run_tile<2, 4, 2, 2, 3, YT>(a);
 }
 
 }  // namespace
