@@ -46,18 +46,21 @@ __device__ __forceinline__ void store_one(void* y, size_t i, float v) {
 
 // ---- tiled GEMM ----------------------------------------------------------------------------------
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S>
+// KG groups of WAVES_M x WAVES_N waves split K (group k takes the K-steps k, k + KG, ...), each with a ring
+// of S stages of its own; their partial sums meet in LDS.
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG>
 struct TileI8 {
-  static constexpr int WAVES = WAVES_M * WAVES_N;
-  static constexpr int THREADS = 64 * WAVES;
+  static constexpr int WAVES = WAVES_M * WAVES_N;  // of a group
+  static constexpr int THREADS = 64 * WAVES * KG;
   static constexpr int BM = WAVES_M * FM * 32, BN = WAVES_N * FN * 32;
   static constexpr int ROWS = BM + BN;             // activation rows, then weight rows
   static constexpr int STEP = 128;                 // K columns (bytes) per stage: whole 128-byte lines
   static constexpr int STAGE = ROWS * STEP;
   static constexpr int ROUNDS = ROWS / (8 * WAVES);  // a wave's direct load fills 8 rows
   static constexpr int REGION = 32 * FN * 32 * 4;  // a wave's epilogue region: 32 rows of f32
-  static constexpr int EPI = WAVES * REGION + BN * 8;
-  static constexpr int LDS = S * STAGE > EPI ? S * STAGE : EPI;
+  static constexpr int PART = (KG - 1) * BM * BN * 4;  // partial sums of the groups after the first
+  static constexpr int EPI = WAVES * REGION + BN * 8 > PART ? WAVES * REGION + BN * 8 : PART;
+  static constexpr int LDS = KG * S * STAGE > EPI ? KG * S * STAGE : EPI;
   static_assert(ROWS % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole rounds per operand");
   static_assert(LDS <= 160 * 1024, "LDS of one CU");
   static_assert(ROUNDS * S < 64, "vmcnt range");
@@ -124,15 +127,16 @@ __device__ __forceinline__ void i8_interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int YT>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int YT>
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
     int64_t ldy) {
-  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S>;
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, lane = t & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int kg = __builtin_amdgcn_readfirstlane(t >> 6) / T::WAVES;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6) % T::WAVES;
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int l32 = lane & 31, h = lane >> 5;
   int tm, tn;
@@ -165,24 +169,28 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
   // each XCD starts an eighth of K further on, so the eight of them fetch different columns of the
   // panels that they share from HBM and find the others' in the Infinity Cache.  Past the last K-step
   // the last is loaded again, so that every step waits on the same count.
+  // A group whose last K-step does not exist takes columns past K, which are zeros.
+  const int ni = (nkt + KG - 1) / KG;
   const int kt0 = (int)(blockIdx.x & 7) * nkt / 8;
-  auto k_of = [&](int kt) {
-    const int p = min(kt, nkt - 1) + kt0;
-    return (uint32_t)(p >= nkt ? p - nkt : p) * T::STEP;
+  auto k_of = [&](int i) {
+    const int p = KG * min(i, ni - 1) + kg;
+    const int q = p + kt0 >= nkt ? p + kt0 - nkt : p + kt0;
+    return (uint32_t)(p < nkt ? q : nkt) * T::STEP;
   };
+  uint8_t* ring = lds + kg * S * T::STAGE;
   constexpr int R = T::ROUNDS, RH = T::ROUNDS / 2;
 #pragma unroll
   for (int j = 0; j < S - 1; ++j)
-    i8_issue<T, 0, R>(lds + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
+    i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
   vm_wait_barrier<(S - 2) * R>();
   i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
   int slot = 0;
-  i8_read<FM, FN>(lds, 0, ra, rb, h, a0, b0);
-  i8_issue<T, 0, RH>(lds + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
-  for (int kt = 0; kt < nkt; ++kt) {
-    uint8_t* cur = lds + slot * T::STAGE;
+  i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
+  i8_issue<T, 0, RH>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
+  for (int kt = 0; kt < ni; ++kt) {
+    uint8_t* cur = ring + slot * T::STAGE;
     // the second half of the loads of K-step kt + S - 1, into the slot of kt - 1
-    i8_issue<T, RH, R>(lds + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
+    i8_issue<T, RH, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
                        bbase, off, col);
     i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
     i8_mma<FM, FN>(acc, a0, b0);
@@ -197,11 +205,34 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
     vm_wait_barrier<(S - 2) * R>();
     i8_issue<T, 0, RH>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
     slot = slot == S - 1 ? 0 : slot + 1;
-    i8_read<FM, FN>(lds + slot * T::STAGE, 0, ra, rb, h, a0, b0);
+    i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
     i8_mma<FM, FN>(acc, a1, b1);
     i8_interleave<FM, FN, RH>();
   }
   vm_wait_barrier<0>();
+  if constexpr (KG > 1) {
+    int* part = reinterpret_cast<int*>(lds);
+    constexpr int N16 = FM * FN * 16;
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (kg > 0) part[(((kg - 1) * T::WAVES + wave) * N16 + (i * FN + j) * 16 + r) * 64 + lane] = acc[i][j][r];
+    __syncthreads();
+    if (kg == 0)
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+#pragma unroll
+            for (int p = 0; p < KG - 1; ++p)
+              acc[i][j][r] += part[((p * T::WAVES + wave) * N16 + (i * FN + j) * 16 + r) * 64 + lane];
+    __syncthreads();
+  }
 
   // Epilogue: the channel scales and biases of the tile once in LDS; each wave passes one 32-row
   // fragment row at a time through its own region and stores whole 16-byte runs of y rows.
@@ -213,6 +244,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
     b_lds[c] = (bias != nullptr && n < N) ? bf16_bits_to_f32(bias[n]) : 0.0f;
   }
   __syncthreads();
+  if (KG > 1 && kg > 0) return;
   constexpr int ES = YType<YT>::ES;
   constexpr int RSB = FN * 32 * ES;   // bytes per region row
   constexpr int CPR = RSB / 16;       // 16-byte chunks per region row
@@ -274,55 +306,113 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N) void gemm_i8_kernel(
 }
 
 // ---- small batches: weight streaming ---------------------------------------------------------------
-// A workgroup of WAVES waves owns 16 weight rows and up to 16 MB activation rows; its waves split K
-// (wave w takes K-steps w, w + WAVES, ... of 64 columns), each streaming its weights from HBM and
-// its activations from L2 straight into matrix-core operand registers (v_mfma_i32_16x16x64_i8: row
-// l % 16, columns 16 (l / 16) ..), and their int32 partial sums meet in LDS.
-constexpr int SK_WAVES = 8;
+// A workgroup owns 32 weight rows and up to 16 MB activation rows; its KW waves split K: wave w takes
+// the 128-column K-steps w, w + KW, ..., each through an LDS ring of its own, S - 1 K-steps ahead by
+// direct loads of whole 128-byte lines.  Nothing in the loop is shared, so it has no barrier: a wave
+// waits for its own loads only.  v_mfma_i32_16x16x64_i8 (row l % 16, columns 16 (l / 16) ..) keeps the
+// activation side at 16 rows; the int32 partial sums of the waves meet in LDS.
+template <int MB, int KW, int S>
+struct SkinnyI8 {
+  static constexpr int ROWS = 16 * MB + 32;  // activation rows, then weight rows
+  static constexpr int STAGE = ROWS * 128;
+  static constexpr int LOADS = ROWS / 8;
+  static constexpr int RING = KW * S * STAGE;
+  static constexpr int PART = KW * MB * 16 * 32 * 4;
+  static constexpr int LDS = RING > PART ? RING : PART;
+  static_assert(LDS <= 160 * 1024 && LOADS * (S - 1) < 64, "LDS of one CU, vmcnt range");
+};
 
-template <int MB, int YT>
-__global__ __launch_bounds__(64 * SK_WAVES) void gemm_i8_skinny_kernel(
+template <class T, int MB>
+__device__ __forceinline__ void skinny_issue(uint8_t* stage, uint32_t k0, uint32_t K, const uint8_t* qa,
+                                             const uint8_t* wbase, const uint32_t* off, const uint32_t* col) {
+  const bool whole = k0 + 128 <= K;
+#pragma unroll
+  for (int r = 0; r < T::LOADS; ++r) {
+    const uint8_t* p = (r < 2 * MB ? qa : wbase) + (k0 + off[r]);
+    if (!whole && k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
+    load_lds16(p, stage + r * 1024);
+  }
+}
+
+template <int MB>
+__device__ __forceinline__ void skinny_mma(i32x4_t (&acc)[MB][2], const i32x4_t (&a)[2][MB], const i32x4_t (&w)[2][2]) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int i = 0; i < MB; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s][i], acc[i][j], 0, 0, 0);
+}
+
+template <int MB, int KW, int S, int YT>
+__global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
     int64_t ldy) {
-  __shared__ int part[SK_WAVES][MB * 256];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  using T = SkinnyI8<MB, KW, S>;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 16;
-  const uint8_t* wp = qw + (size_t)min(n0 + l16, N - 1) * K + 16 * g;
-  const uint8_t* ap[MB];
+  const int n0 = blockIdx.x * 32;
+  const uint8_t* wbase = qw + (size_t)n0 * K;
+  uint8_t* ring = lds + wave * S * T::STAGE;
+  uint32_t off[T::LOADS], col[T::LOADS];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) ap[i] = qa + (size_t)min(16 * i + l16, M - 1) * K + 16 * g;
-  i32x4_t acc[MB];
-#pragma unroll
-  for (int i = 0; i < MB; ++i) acc[i] = i32x4_t{0, 0, 0, 0};
-  constexpr int U = MB >= 4 ? 4 : 8;  // K-steps loaded before they are multiplied
-  const int steps = (K + 63) / 64;
-  for (int s0 = wave; s0 < steps; s0 += SK_WAVES * U) {
-    i32x4_t wv[U], av[U][MB];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = 64 * (s0 + SK_WAVES * u);
-      const bool in = k + 16 * g < K;  // chunks past K are zero on both sides
-      wv[u] = in ? *reinterpret_cast<const i32x4_t*>(wp + k) : i32x4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < MB; ++i) av[u][i] = in ? *reinterpret_cast<const i32x4_t*>(ap[i] + k) : i32x4_t{0, 0, 0, 0};
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < MB; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u], av[u][i], acc[i], 0, 0, 0);
+  for (int r = 0; r < T::LOADS; ++r) {
+    const int row = 8 * r + (lane >> 3);
+    col[r] = 16u * (uint32_t)((lane & 7) ^ i8_swizzle(row));
+    const int src = row < 16 * MB ? min(row, M - 1) : min(row - 16 * MB, N - 1 - n0);
+    off[r] = (uint32_t)src * (uint32_t)K + col[r];
   }
-  // acc[i][r] is the partial sum of m = 16 i + l16, n = n0 + 4 g + r
+  const int nkt = (K + 127) / 128;
+  const int steps = (nkt - wave + KW - 1) / KW;  // of this wave
+  i32x4_t acc[MB][2];
 #pragma unroll
-  for (int i = 0; i < MB; ++i) *reinterpret_cast<i32x4_t*>(&part[wave][i * 256 + l16 * 16 + 4 * g]) = acc[i];
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+  if (steps > 0) {
+    auto k_of = [&](int i) { return 128u * (uint32_t)(wave + KW * min(i, steps - 1)); };
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i)
+      skinny_issue<T, MB>(ring + i * T::STAGE, k_of(i), (uint32_t)K, qa, wbase, off, col);
+    int slot = 0;
+    for (int i = 0; i < steps; ++i) {
+      // K-step i has landed; the operands of K-step i - 1 are in registers, so its slot is free
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((S - 2) * T::LOADS) : "memory");
+      skinny_issue<T, MB>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, k_of(i + S - 1), (uint32_t)K, qa, wbase, off,
+                          col);
+      const uint8_t* cur = ring + slot * T::STAGE;
+      i32x4_t a[2][MB], w[2][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int c = 16 * ((4 * s + g) ^ i8_swizzle(l16));
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[s][j] = *reinterpret_cast<const i32x4_t*>(cur + (16 * MB + 16 * j + l16) * 128 + c);
+#pragma unroll
+        for (int m = 0; m < MB; ++m) a[s][m] = *reinterpret_cast<const i32x4_t*>(cur + (16 * m + l16) * 128 + c);
+      }
+      skinny_mma<MB>(acc, a, w);
+      slot = slot == S - 1 ? 0 : slot + 1;
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __syncthreads();  // every wave has left its ring
+  // acc[i][j][r] is the partial sum of m = 16 i + l16, n = n0 + 16 j + 4 g + r
+  int* part = reinterpret_cast<int*>(lds);
+#pragma unroll
+  for (int i = 0; i < MB; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<i32x4_t*>(part + ((wave * MB * 16 + 16 * i + l16) * 32 + 16 * j + 4 * g)) = acc[i][j];
   __syncthreads();
-  for (int o = t; o < MB * 256; o += 64 * SK_WAVES) {
-    const int m = o >> 4, n = n0 + (o & 15);
+  for (int o = t; o < MB * 512; o += 64 * KW) {
+    const int m = o >> 5, n = n0 + (o & 31);
     if (m >= M || n >= N) continue;
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < SK_WAVES; ++w) sum += part[w][o];
+    for (int w = 0; w < KW; ++w) sum += part[w * MB * 512 + o];
     float v = ((float)sum * sa[m]) * sw[n];
     if (bias != nullptr) v += bf16_bits_to_f32(bias[n]);
     store_one<YT>(y, (size_t)m * ldy + n, v);
@@ -341,18 +431,18 @@ struct GArgs {
   hipStream_t stream;
 };
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int YT>
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int YT>
 hipError_t run_tile(const GArgs& a) {
-  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S>;
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG>;
   const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
-  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
+  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, KG, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
       a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
   return hipGetLastError();
 }
 
-template <int MB, int YT>
+template <int MB, int KW, int S, int YT>
 hipError_t run_skinny(const GArgs& a) {
-  gemm_i8_skinny_kernel<MB, YT><<<dim3((unsigned)((a.N + 15) / 16)), 64 * SK_WAVES, 0, a.stream>>>(
+  gemm_i8_skinny_kernel<MB, KW, S, YT><<<dim3((unsigned)((a.N + 31) / 32)), 64 * KW, 0, a.stream>>>(
       a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
   return hipGetLastError();
 }
@@ -361,27 +451,35 @@ template <int YT>
 hipError_t run(const GArgs& a) {
   const char* forced = test_hook("W8A8_GEMM_TILE");
   auto is = [&](const char* s) { return forced && !strcmp(forced, s); };
-  if (forced ? is("skinny") && a.M <= 64 : a.M <= 64) {
-    if (a.M <= 16) return run_skinny<1, YT>(a);
-    if (a.M <= 32) return run_skinny<2, YT>(a);
-    return run_skinny<4, YT>(a);
-  }
   auto tiles = [&](int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
-  // Less than one tile per CU: the K loop's latency bounds the launch, and the largest tile that still
-  // gives every CU at most one costs fewest bytes (128 x 8192 x 4096: 15.4 us in 64 x 64 tiles, 16.9 in
-  // 64 x 128, 19.6 in 128 x 128; 512 x 5120 x 5120: 34.6, 27.3, 23.7).
-  if (forced ? is("64") : tiles(64, 64) <= 256) return run_tile<2, 2, 1, 1, 4, YT>(a);
-  if (forced ? is("64x128") : tiles(64, 128) <= 256) return run_tile<2, 2, 1, 2, 3, YT>(a);
-  if (forced ? is("128") : tiles(128, 128) <= 256) return run_tile<2, 4, 2, 1, 4, YT>(a);
+  // Up to 32 rows: stream the weights (16 x 13824 x 5120: 13.6 us, 5.2 TB/s; 64-row tiles 17.6).  From 17
+  // rows on, past 256 workgroups, a ring of two K-steps lets two workgroups share a CU (32 x 13824 x
+  // 5120: 15.0 us, 16.9 with three).
+  if (forced ? is("skinny") && a.M <= 32 : a.M <= 32) {
+    if (a.M <= 16) return run_skinny<1, 4, 3, YT>(a);
+    return a.N <= 8192 ? run_skinny<2, 4, 3, YT>(a) : run_skinny<2, 4, 2, YT>(a);
+  }
+  // At most one tile per CU: the K loop's latency bounds the launch, so K is split over groups of waves
+  // and the smallest tile that still leaves every CU at most one wins (128 x 2048 x 2048: 32 x 32 tiles
+  // 5.6 us, 64 x 32 6.4, 64 x 64 7.4, 8.8 without the split; 128 x 4096 x 4096: 64 x 32 9.3, 64 x 64 11.3;
+  // 128 x 8192 x 4096: 64 x 64 12.0, 64 x 128 14.5, 128 x 128 19.8).
+  if (forced ? is("32") : tiles(32, 32) <= 256) return run_tile<1, 1, 1, 1, 3, 4, YT>(a);
+  if (forced ? is("64x32") : tiles(64, 32) <= 256) return run_tile<2, 1, 1, 1, 3, 4, YT>(a);
+  if (forced ? is("64") : tiles(64, 64) <= 256) return run_tile<2, 2, 1, 1, 3, 2, YT>(a);
+  // (the split pays from about K = 2048: 256 x 5120 x 5120 17.3 us against 19.4, 301 x 4099 x 1552
+  // 12.6 against 12.1)
+  if (forced ? is("64x128k2") : tiles(64, 128) <= 256 && a.K >= 2048) return run_tile<2, 2, 1, 2, 3, 2, YT>(a);
+  if (forced ? is("64x128") : tiles(64, 128) <= 256) return run_tile<2, 2, 1, 2, 3, 1, YT>(a);
+  if (forced ? is("128") : tiles(128, 128) <= 256) return run_tile<2, 4, 2, 1, 4, 1, YT>(a);
   // Several rounds of 256 tiles: the shape with the least time, rounds by the measured time of a
   // 128-column K-step (128 x 256: 0.88 us, 256 x 192: 1.22, 256 x 256: 1.45), so a last round that is
   // mostly empty is cheap (4096 x 2560 x 12288: 139 us in 160 tiles of 256 x 256, 123 in 224 of 256 x 192;
   // 4096 x 2048 x 2048: 31.7 in 128, 23.2 in 256 of 128 x 256; 4096 x 13824 x 5120: 284 / 290 / 318).
   const int64_t c0 = (tiles(128, 256) + 255) / 256 * 88, c1 = (tiles(256, 192) + 255) / 256 * 122,
                 c2 = (tiles(256, 256) + 255) / 256 * 145;
-  if (forced ? is("256") : c2 <= c1 && c2 <= c0) return run_tile<2, 4, 4, 2, 2, YT>(a);
-  if (forced ? is("256x192") : c1 <= c0) return run_tile<4, 2, 2, 3, 2, YT>(a);
-  return run_tile<2, 4, 2, 2, 3, YT>(a);
+  if (forced ? is("256") : c2 <= c1 && c2 <= c0) return run_tile<2, 4, 4, 2, 2, 1, YT>(a);
+  if (forced ? is("256x192") : c1 <= c0) return run_tile<4, 2, 2, 3, 2, 1, YT>(a);
+  return run_tile<2, 4, 2, 2, 3, 1, YT>(a);
 }
 
 }  // namespace
