@@ -119,9 +119,15 @@ def _check(status, what):
         raise W4A4Error(f"{what} failed: {name} ({msg})", status)
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream(device):
@@ -565,13 +571,17 @@ def svdq_lowrank_split(w, smooth_factor, rank, oversample=16, power_iters=4, see
 
 W8A8_MAX_K = 131056
 
+_DTYPE_CODES = {}
+
 
 def _dtype_code(dtype, name):
-    torch = _torch()
-    codes = {torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32}
-    if dtype not in codes:
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16, torch.float32: DTYPE_F32})
+    code = _DTYPE_CODES.get(dtype)
+    if code is None:
         raise TypeError(f"{name} must be bf16, f16 or f32, got {dtype}")
-    return codes[dtype]
+    return code
 
 
 def _device_tensor(t, name):
@@ -582,14 +592,24 @@ def _device_tensor(t, name):
     return t.device
 
 
-def _on(device, call, *args):
-    """``call(*args, stream)`` with ``device`` current and its current stream (a stream launches on
-    its own device only while that device is current)."""
+def _dense(t, name, dtype, shape, dev):
+    """``t`` is a contiguous tensor of this dtype, shape and device.  (One test in the ordinary case: small
+    calls are bound by the host; the general checks word the error.)"""
+    if not (isinstance(t, _torch().Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape
+            and t.is_contiguous()):
+        _dev(t, name, (dtype,), dev)
+        _shape(t, name, shape)
+
+
+def _on(dev, call, *args):
+    """``call(*args, stream)`` with ``dev`` current and its current stream (a stream launches on its own
+    device only while that device is current)."""
     torch = _torch()
-    stream = torch.cuda.current_stream(device).cuda_stream
-    if torch.cuda.current_device() == device.index:
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the stream's handle without a Stream object
+    stream = raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == dev.index:
         return call(*args, stream)
-    with torch.cuda.device(device):
+    with torch.cuda.device(dev):
         return call(*args, stream)
 
 
@@ -607,32 +627,28 @@ def _w8a8_rows(t, name):
 
 def _check_smooth(smooth_factor, K, dev):
     if smooth_factor is not None:
-        _dev(smooth_factor, "smooth_factor", (_torch().bfloat16,), dev)
-        _shape(smooth_factor, "smooth_factor", (K,))
+        _dense(smooth_factor, "smooth_factor", _torch().bfloat16, (K,), dev)
 
 
 def _check_w8a8_weights(qweight, wscales, bias, K, dev):
     torch = _torch()
-    _dev(qweight, "qweight", (torch.int8,), dev)
+    _device_tensor(qweight, "qweight")
     if qweight.dim() != 2:
         raise ValueError(f"qweight must be 2-D (N, K), got shape {tuple(qweight.shape)}")
-    N = int(qweight.shape[0])
-    _shape(qweight, "qweight", (N, K))
-    _dev(wscales, "wscales", (torch.float32,), dev)
-    _shape(wscales, "wscales", (N,))
+    N = qweight.shape[0]
+    _dense(qweight, "qweight", torch.int8, (N, K), dev)
+    _dense(wscales, "wscales", torch.float32, (N,), dev)
     if bias is not None:
-        _dev(bias, "bias", (torch.bfloat16,), dev)
-        _shape(bias, "bias", (N,))
+        _dense(bias, "bias", torch.bfloat16, (N,), dev)
     return N
 
 
 def _w8a8_out(out, lead, M, N, out_dtype, default, dev):
     """(y, its row stride, its dtype code): `out` checked, or a new tensor (*lead, N)."""
-    torch = _torch()
     if out is None:
         dtype = default if out_dtype is None else out_dtype
         code = _dtype_code(dtype, "out_dtype")
-        return torch.empty((*lead, N), dtype=dtype, device=dev), N, code
+        return _torch().empty((*lead, N), dtype=dtype, device=dev), N, code
     if _device_tensor(out, "out") != dev:
         raise ValueError(f"out is on {out.device}, expected {dev}")
     if out_dtype is not None and out.dtype != out_dtype:
@@ -647,35 +663,32 @@ def w8a8_linear_workspace_bytes(M, K):
     return int(load_library().w8a8_linear_workspace_bytes(int(M), int(K)))
 
 
+def _w8a8_quantize(call, x, name, smooth_factor, hadamard_block):
+    torch = _torch()
+    rows, K, ld, code, dev = _w8a8_rows(x, name)
+    _check_smooth(smooth_factor, K, dev)
+    q = torch.empty((rows, K), dtype=torch.int8, device=dev)
+    scales = torch.empty((rows,), dtype=torch.float32, device=dev)
+    st = _on(dev, call, x.data_ptr(), ld, code, _addr(smooth_factor), rows, K, int(hadamard_block), q.data_ptr(),
+             scales.data_ptr())
+    return st, q, scales
+
+
 def w8a8_quantize_act(x, smooth_factor=None, hadamard_block=0):
     """x (..., K) bf16, f16 or f32 -> (qact (M, K) int8, ascales (M,) f32), one scale per token.
 
     x needs a dense last dimension; a 2-D x may be a column partition of a wider matrix (16-byte
     aligned, row stride a multiple of 8).  smooth_factor (K,) bf16 is optional."""
-    torch = _torch()
-    lib = load_library()
-    M, K, ldx, code, dev = _w8a8_rows(x, "x")
-    _check_smooth(smooth_factor, K, dev)
-    qact = torch.empty((M, K), dtype=torch.int8, device=dev)
-    ascales = torch.empty((M,), dtype=torch.float32, device=dev)
-    st = _on(dev, lib.w8a8_quantize_act, x.data_ptr(), ldx, code, _addr(smooth_factor), M, K, int(hadamard_block),
-             qact.data_ptr(), ascales.data_ptr())
+    st, q, scales = _w8a8_quantize(load_library().w8a8_quantize_act, x, "x", smooth_factor, hadamard_block)
     _check(st, "w8a8_quantize_act")
-    return qact, ascales
+    return q, scales
 
 
 def w8a8_quantize_weight(w, smooth_factor=None, hadamard_block=0):
     """w (N, K) bf16, f16 or f32 -> (qweight (N, K) int8, wscales (N,) f32), one scale per output channel."""
-    torch = _torch()
-    lib = load_library()
-    N, K, ldw, code, dev = _w8a8_rows(w, "w")
-    _check_smooth(smooth_factor, K, dev)
-    qweight = torch.empty((N, K), dtype=torch.int8, device=dev)
-    wscales = torch.empty((N,), dtype=torch.float32, device=dev)
-    st = _on(dev, lib.w8a8_quantize_weight, w.data_ptr(), ldw, code, _addr(smooth_factor), N, K, int(hadamard_block),
-             qweight.data_ptr(), wscales.data_ptr())
+    st, q, scales = _w8a8_quantize(load_library().w8a8_quantize_weight, w, "w", smooth_factor, hadamard_block)
     _check(st, "w8a8_quantize_weight")
-    return qweight, wscales
+    return q, scales
 
 
 def w8a8_gemm(qact, ascales, qweight, wscales, bias=None, out=None, out_dtype=None):
@@ -686,12 +699,11 @@ def w8a8_gemm(qact, ascales, qweight, wscales, bias=None, out=None, out_dtype=No
     torch = _torch()
     lib = load_library()
     dev = _device_tensor(qact, "qact")
-    _dev(qact, "qact", (torch.int8,))
     if qact.dim() != 2:
         raise ValueError(f"qact must be 2-D (M, K), got shape {tuple(qact.shape)}")
-    M, K = (int(d) for d in qact.shape)
-    _dev(ascales, "ascales", (torch.float32,), dev)
-    _shape(ascales, "ascales", (M,))
+    M, K = qact.shape
+    _dense(qact, "qact", torch.int8, (M, K), dev)
+    _dense(ascales, "ascales", torch.float32, (M,), dev)
     N = _check_w8a8_weights(qweight, wscales, bias, K, dev)
     y, ldy, code = _w8a8_out(out, (M,), M, N, out_dtype, torch.bfloat16, dev)
     st = _on(dev, lib.w8a8_gemm, qact.data_ptr(), ascales.data_ptr(), qweight.data_ptr(), wscales.data_ptr(),
@@ -714,17 +726,17 @@ def w8a8_linear(x, layer, hadamard_block=0, workspace=None, out=None, out_dtype=
     _check_smooth(smooth, K, dev)
     qweight, wscales = layer["qweight"], layer["wscales"]
     N = _check_w8a8_weights(qweight, wscales, bias, K, dev)
-    y, ldy, ycode = _w8a8_out(out, tuple(x.shape[:-1]), M, N, out_dtype, x.dtype, dev)
+    y, ldy, ycode = _w8a8_out(out, x.shape[:-1], M, N, out_dtype, x.dtype, dev)
+    need = lib.w8a8_linear_workspace_bytes(M, K)
     if workspace is None:
-        workspace = torch.empty(max(int(lib.w8a8_linear_workspace_bytes(M, K)), 1), dtype=torch.uint8, device=dev)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     else:
         _dev(workspace, "workspace", (torch.uint8,), dev)
-        need = int(lib.w8a8_linear_workspace_bytes(M, K))
-        if workspace.numel() < need:
-            raise ValueError(f"workspace holds {workspace.numel()} bytes, the call needs {need}")
+        need = workspace.numel()
+        if need < lib.w8a8_linear_workspace_bytes(M, K):
+            raise ValueError(f"workspace holds {need} bytes, the call needs {lib.w8a8_linear_workspace_bytes(M, K)}")
     st = _on(dev, lib.w8a8_linear, x.data_ptr(), ldx, code, qweight.data_ptr(), wscales.data_ptr(), _addr(smooth),
-             _addr(bias), M, N, K, int(hadamard_block), y.data_ptr(), ldy, ycode, workspace.data_ptr(),
-             workspace.numel())
+             _addr(bias), M, N, K, int(hadamard_block), y.data_ptr(), ldy, ycode, workspace.data_ptr(), need)
     _check(st, "w8a8_linear")
     return y
 
@@ -734,40 +746,45 @@ def w8a8_linear(x, layer, hadamard_block=0, workspace=None, out=None, out_dtype=
 ROPE_LAYOUTS = {"interleaved": 0, "half": 1, "axis_half": 2}
 ROPE_NORM, ROPE_SHARED_FREQUENCIES, ROPE_POSITIONS_I64 = 1, 2, 4
 ROPE_MAX_HEAD_DIM, ROPE_MAX_AXES = 512, 8
+_I32_ARRAYS = {}  # ctypes array types by length
 
 
 def _heads_view(t, name):
     """(tokens, heads, head_dim, token stride, head stride) of a (T, H, D) or (B, S, H, D) tensor with a
     dense last dimension; the leading two of four dimensions have to flatten without copying."""
-    if t.dim() not in (3, 4):
-        raise ValueError(f"{name} must be (tokens, heads, head_dim) or (batch, tokens, heads, head_dim), "
-                         f"got shape {tuple(t.shape)}")
     shape, st = t.shape, t.stride()
-    if shape[-1] > 1 and st[-1] != 1:
-        raise ValueError(f"{name} must have a dense last dimension")
-    T, ts = int(shape[-3]), st[-3]
-    if t.dim() == 4:
+    if len(shape) == 3:
+        T, ts = shape[0], st[0]
+    elif len(shape) == 4:
+        T, ts = shape[1], st[1]
         if shape[0] > 1 and T > 1 and st[0] != T * st[1]:
             raise ValueError(f"{name}'s batch and token dimensions do not flatten (strides {tuple(st)})")
         if T == 1:
             ts = st[0]
-        T *= int(shape[0])
-    return T, int(shape[-2]), int(shape[-1]), ts, st[-2]
+        T *= shape[0]
+    else:
+        raise ValueError(f"{name} must be (tokens, heads, head_dim) or (batch, tokens, heads, head_dim), "
+                         f"got shape {tuple(shape)}")
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name} must have a dense last dimension")
+    return T, shape[-2], shape[-1], ts, st[-2]
 
 
-def _rope_side(x, y, weight, name, T, D, dtype, dev):
-    if x.dtype != dtype or x.device != dev:
-        raise ValueError(f"{name} must match q in dtype and device")
-    if y.shape != x.shape or y.dtype != dtype or y.device != dev:
-        raise ValueError(f"the output for {name} must match it in shape, dtype and device")
-    t, h, d, ts, hs = _heads_view(x, name)
-    if (t, d) != (T, D):
-        raise ValueError(f"{name} has {t} tokens and head_dim {d}, expected {T} and {D}")
+def _rope_side(x, view, out, weight, name, dtype, dev):
+    """The descriptor of one tensor, and its output (``out``, or a new contiguous tensor)."""
+    t, h, d, ts, hs = view
     if weight is not None:
-        _dev(weight, f"{name}_weight", (dtype,), dev)
-        _shape(weight, f"{name}_weight", (D,))
-    _, _, _, yts, yhs = _heads_view(y, f"{name}'s output")
-    return Heads(x.data_ptr(), ts, hs, h, _addr(weight), y.data_ptr(), yts, yhs)
+        _dense(weight, f"{name}_weight", dtype, (d,), dev)
+    if out is None:
+        out = _torch().empty(x.shape, dtype=dtype, device=dev)
+        yts, yhs = h * d, d
+    elif out is x:
+        yts, yhs = ts, hs
+    else:
+        if not isinstance(out, _torch().Tensor) or out.shape != x.shape or out.dtype != dtype or out.device != dev:
+            raise ValueError(f"the output for {name} must match it in shape, dtype and device")
+        _, _, _, yts, yhs = _heads_view(out, f"{name}'s output")
+    return Heads(x.data_ptr(), ts, hs, h, _addr(weight), out.data_ptr(), yts, yhs), out
 
 
 def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1e-6, theta=10000.0,
@@ -785,37 +802,46 @@ def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1
     torch = _torch()
     lib = load_library()
     dev = _device_tensor(q, "q")
-    code = _dtype_code(q.dtype, "q")
-    if layout not in ROPE_LAYOUTS:
+    dtype = q.dtype
+    code = _dtype_code(dtype, "q")
+    layout_code = ROPE_LAYOUTS.get(layout)
+    if layout_code is None:
         raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
-    T, _, D, _, _ = _heads_view(q, "q")
-    if inplace and (q_out is not None or k_out is not None):
-        raise ValueError("inplace takes no outputs")
+    view = _heads_view(q, "q")
+    T, D = view[0], view[2]
+    if inplace:
+        if q_out is not None or k_out is not None:
+            raise ValueError("inplace takes no outputs")
+        q_out, k_out = q, k
     if k is None and (k_out is not None or k_weight is not None):
         raise ValueError("k_out and k_weight need k")
-    dims = [int(d) for d in axis_dims]
     flags = (ROPE_NORM if norm else 0) | (ROPE_SHARED_FREQUENCIES if shared_frequencies else 0)
-    if dims:
-        _dev(positions, "positions", (torch.int32, torch.int64), dev)
-        lead = tuple(q.shape[:-2])
-        if tuple(positions.shape) not in ((T, len(dims)), (*lead, len(dims))) and not (
-                len(dims) == 1 and tuple(positions.shape) in ((T,), lead)):
-            raise ValueError(f"positions has shape {tuple(positions.shape)}, expected {(T, len(dims))}")
-        if positions.dtype == torch.int64:
+    n = len(axis_dims)
+    pos = None
+    if n:
+        if not isinstance(positions, torch.Tensor) or positions.device != dev or not positions.is_contiguous() or (
+                positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
+            _dev(positions, "positions", (torch.int32, torch.int64), dev)
+        shape = positions.shape
+        if shape != (T, n) and shape != (*q.shape[:-2], n) and not (n == 1 and (shape == (T,) or shape == q.shape[:-2])):
+            raise ValueError(f"positions has shape {tuple(shape)}, expected {(T, n)}")
+        if positions.dtype is torch.int64:
             flags |= ROPE_POSITIONS_I64
-    if inplace:
-        q_out, k_out = q, k
-    else:
-        q_out = torch.empty(q.shape, dtype=q.dtype, device=dev) if q_out is None else q_out
-        if k is not None and k_out is None:
-            k_out = torch.empty(k.shape, dtype=k.dtype, device=dev)
-    qs = _rope_side(q, q_out, q_weight, "q", T, D, q.dtype, dev)
+        pos = positions.data_ptr()
+    qs, q_out = _rope_side(q, view, q_out, q_weight, "q", dtype, dev)
     ks = None
     if k is not None:
-        _device_tensor(k, "k")
-        ks = _rope_side(k, k_out, k_weight, "k", T, D, q.dtype, dev)
-    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ctypes.byref(ks) if ks is not None else None,
-             positions.data_ptr() if dims else None, T, D, len(dims), (ctypes.c_int32 * max(len(dims), 1))(*dims),
-             ROPE_LAYOUTS[layout], flags, float(theta), float(eps), code)
+        if _device_tensor(k, "k") != dev or k.dtype != dtype:
+            raise ValueError("k must match q in dtype and device")
+        kview = _heads_view(k, "k")
+        if kview[0] != T or kview[2] != D:
+            raise ValueError(f"k has {kview[0]} tokens and head_dim {kview[2]}, expected {T} and {D}")
+        ks, k_out = _rope_side(k, kview, k_out, k_weight, "k", dtype, dev)
+        ks = ctypes.byref(ks)
+    array = _I32_ARRAYS.get(n)
+    if array is None:
+        array = _I32_ARRAYS[n] = ctypes.c_int32 * n
+    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ks, pos, T, D, n, array(*axis_dims), layout_code, flags,
+             theta, eps, code)
     _check(st, "w4a4_qk_norm_rope")
     return q_out if k is None else (q_out, k_out)
