@@ -296,15 +296,16 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
  * checkpoint lists as not to convert): signed int8 weights with one scale per output channel,
  * activations quantized to int8 with one scale per token, the same smoothing, the same fused block
  * rotation, an optional bias.  Per row m of x:
- *   x_s  = float32(x) / float32(smooth_factor)   (IEEE; no smooth_factor: x_s = x; quotients below
- *          2^-110 in magnitude count as 0)
- *   v    = x_s, or x_s @ H_B^T on every B-block (as in svdq_quantize_act)
- *   amax = max_k |v|,  ascales[m] = float32(amax / 127)
- *   qact = v * float32(127 / amax), the exact product rounded to the nearest integer, ties to even
+ *   x_s  = float32(x) / float32(smooth_factor)   (round to nearest; below 2^-110 in magnitude within
+ *          2^-133; no smooth_factor: x_s = x)
+ *   u    = x_s, or the butterflies of svdq_quantize_act on every B-block, not yet normalised
+ *   amax = max_k |u|,  ascales[m] = float32(float32(amax * norm) / 127), norm = float32(1/sqrt(B))
+ *          (1 without rotation)
+ *   qact = u * float32(127 / amax), the exact product rounded to the nearest integer, ties to even
  *          (within [-127, 127])
  *   y    = round( (float32(sum_k qact qweight) * ascales[m]) * wscales[n] + bias[n] )
  * The sum is exact (int32); the arithmetic after it is float32 with one rounding to y's type.
- * A row with amax < 2^-100 gets scale 0 and codes 0; a row that holds an infinity or a NaN (or
+ * A row with amax * norm < 2^-100 gets scale 0 and codes 0; a row that holds an infinity or a NaN (or
  * whose smoothing or rotation overflows) gets scale NaN and codes 0, so its whole output row is
  * NaN.  float32(sum) * ascales[m] overflows to infinity for |v| of about 2^97 and more.
  *

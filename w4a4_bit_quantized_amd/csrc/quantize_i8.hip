@@ -1,25 +1,34 @@
 // Per-token (activations) and per-channel (weights) int8 quantizer of the W8A8 layer (gfx950).
 //
-//   v     = x / smooth_factor (activations, float32, round to nearest) or w * smooth_factor (weights);
-//           quotients of magnitude below 2^-110 count as 0
-//   v     = v @ H_B^T per contiguous B-block (optional; butterfly spans 1, 2, ..., B/2, then one
-//           multiply by float32(1/sqrt(B)), the rotation of the FP4 quantizer)
-//   amax  = max_k |v[row, k]|,  scale[row] = float32(amax / 127)
-//   code  = v * float32(127 / amax), the exact product rounded to the nearest integer, ties to even
-// A row with amax < 2^-100 gets scale 0 and codes 0; a row that holds an infinity or a NaN gets
-// scale NaN and codes 0, so that every output of that row is NaN.
+//   v     = x / smooth_factor (activations, float32, round to nearest) or w * smooth_factor (weights)
+//   u     = v, or the butterflies of v per contiguous B-block (spans 1, 2, ..., B/2)
+//   amax  = max_k |u[row, k]|
+//   code  = u * float32(127 / amax), the exact product rounded to the nearest integer, ties to even
+//   scale = float32(float32(amax * norm) / 127),  norm = float32(1/sqrt(B)), 1 without rotation
+// so that code * scale stands for the normalised rotation's value: the normalisation is one
+// multiply per row instead of one per element.  A row with amax * norm < 2^-100 gets scale 0 and codes
+// 0; a row that holds an infinity or a NaN gets scale NaN and codes 0, so that every output of that
+// row is NaN.
 //
 // Two-part division.  With rh = RN(1/lambda) and rl = RN(RN(1 - lambda rh) rh) the sum rh + rl is
 // within 2^-46 of 1/lambda, and q = RN(x rh + RN(x rl)) (one multiply, one fused multiply-add)
-// differs from the exact quotient by less than 2^-45 before its one rounding.  lambda has 8
-// significant bits, so a quotient x / lambda that is no midpoint of two float32 values is at least
-// 2^-34 of its value away from every one, and none is a midpoint (midpoint * lambda would need
-// more bits than x has): q is the correctly rounded quotient as long as x rl stays a normal
-// number, that is for |q| >= 2^-110, and smaller quotients count as 0 on either path.  This holds
-// for bf16, f16 and f32 x and lambda in [2^-32, 2^32]; a wave with another lambda divides.
+// differs from the exact quotient by less than 2^-45 of it before its one rounding.  lambda has 8
+// significant bits, so a quotient x / lambda is at least 2^-33 of its value away from every midpoint
+// of two float32 values (a midpoint times lambda has more bits than x): q is the correctly rounded
+// quotient as long as x rl stays a normal number, that is for |q| >= 2^-110.  A smaller quotient is
+// within 2^-133 of x / lambda; in a row that does not count as zero its code is 0 either way.  This
+// holds for bf16, f16 and f32 x and lambda in [2^-32, 2^32]; a wave with another lambda divides.
 //
-// Rounding.  fma(v, inv, 1.5 * 2^23) rounds the exact product to an integer (the sum's ulp is 1)
+// Rounding.  fma(u, inv, 1.5 * 2^23) rounds the exact product to an integer (the sum's ulp is 1)
 // whose two's complement low byte is the code.
+//
+// Rotation.  A lane holds 8 consecutive columns: spans 1, 2, 4 stay inside it.  The spans 8 .. 64 pair
+// lanes of a 16-lane row, all by one DPP operand of a fused multiply-add: v + s * (partner's v) with
+// s = +-1 is a + b in the lower lane and -(a - b) in the upper one, the rounding of the difference and
+// the opposite sign.  The sign is the same for all values of a lane and stays with them (a partner
+// differs in one lane bit only), so it is undone by the sign of the lane's inv.  DPP pairs lanes l ^ 1,
+// l ^ 2, l ^ 7 and l ^ 8 in one operand but not l ^ 4, so the lanes 4 .. 7 of 8 hold their four chunks in
+// reverse order, which makes l ^ 7 the partner of span 32.
 //
 // Bound: HBM (x read once, codes written once).  A row stays in the registers of one workgroup
 // between its maximum and its codes; the reciprocals of lambda are made once per workgroup and
@@ -35,7 +44,6 @@ constexpr uint32_t ABS_MASK = 0x7FFFFFFFu;
 constexpr uint32_t INF_BITS = 0x7F800000u;
 constexpr float ROUND_MAGIC = 12582912.0f;  // 1.5 * 2^23
 constexpr float TINY_ROW = 7.888609052210118e-31f;   // 2^-100
-constexpr float TINY_QUOTIENT = 7.703719777548943e-34f;  // 2^-110
 
 // Eight consecutive elements as loaded (storage types: 0 bf16, 1 f16, 2 f32).
 template <int DT>
@@ -94,34 +102,51 @@ __device__ __forceinline__ void lambda8(const uint16_t* lam, int64_t col, float 
   }
 }
 
-__device__ __forceinline__ float drop_tiny(float q) { return fabsf(q) < TINY_QUOTIENT ? 0.0f : q; }
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(__builtin_amdgcn_mov_dpp(__float_as_int(v), CTRL, 0xF, 0xF, true));
+}
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int DPP_XOR1 = 0xB1, DPP_XOR2 = 0x4E, DPP_XOR7 = 0x141, DPP_XOR15 = 0x140;
 
-// The value of lane l ^ D within 16 lanes, by DPP.
-template <int D>
-__device__ __forceinline__ float lane16_xor(float v) {
-  const int b = __float_as_int(v);
-  if constexpr (D == 1) return __int_as_float(__builtin_amdgcn_mov_dpp(b, 0xB1, 0xF, 0xF, true));
-  if constexpr (D == 2) return __int_as_float(__builtin_amdgcn_mov_dpp(b, 0x4E, 0xF, 0xF, true));
-  if constexpr (D == 4)  // l ^ 7 (row_half_mirror), then l ^ 3 (quad_perm [3,2,1,0])
-    return __int_as_float(__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp(b, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true));
-  return __int_as_float(__builtin_amdgcn_mov_dpp(b, 0x128, 0xF, 0xF, true));  // row_ror:8
+// Which chunk of 8 columns thread t holds (see the top of the file).
+__device__ __forceinline__ int chunk_of(int t) { return t ^ ((t & 4) ? 3 : 0); }
+
+// Signs of a lane's values after the rotation, as a factor.
+__device__ __forceinline__ float lane_sign(int lane, int block) {
+  // bits of the lane's chunk index: spans 8, 16, 32, 64
+  const int j = chunk_of(lane) & (block / 8 - 1);
+  return (__popc(j) & 1) ? -1.0f : 1.0f;
 }
 
-// One butterfly stage between lanes l and l ^ D: the lower lane keeps a + b, the upper a - b.
-template <int D, int C>
-__device__ __forceinline__ void lane_stage(float (&v)[C][8], int lane) {
-  const uint32_t flip = (lane & D) ? 0x80000000u : 0u;
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      v[c][i] = lane16_xor<D>(v[c][i]) + __uint_as_float(__float_as_uint(v[c][i]) ^ flip);
-}
+// v + s * (partner's v) for 8 values: v_fmac_f32 with a DPP first operand, which the compiler does not
+// form from a move and an fma.  The leading s_nop covers the two wait states between a vector
+// instruction that writes a register and one that reads it through DPP.
+#define W8A8_FMAC_DPP(CTRL)                                                                                   \
+  asm("s_nop 1\n\t"                                                                                           \
+      "v_fmac_f32_dpp %0, %0, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %1, %1, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %2, %2, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %3, %3, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %4, %4, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %5, %5, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %6, %6, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t"                                     \
+      "v_fmac_f32_dpp %7, %7, %8 " CTRL " row_mask:0xf bank_mask:0xf"                                         \
+      : "+v"(v[0]), "+v"(v[1]), "+v"(v[2]), "+v"(v[3]), "+v"(v[4]), "+v"(v[5]), "+v"(v[6]), "+v"(v[7])        \
+      : "v"(s))
+__device__ __forceinline__ void stage_xor1(float (&v)[8], float s) { W8A8_FMAC_DPP("quad_perm:[1,0,3,2]"); }
+__device__ __forceinline__ void stage_xor2(float (&v)[8], float s) { W8A8_FMAC_DPP("quad_perm:[2,3,0,1]"); }
+__device__ __forceinline__ void stage_xor7(float (&v)[8], float s) { W8A8_FMAC_DPP("row_half_mirror"); }
+__device__ __forceinline__ void stage_xor8(float (&v)[8], float s) { W8A8_FMAC_DPP("row_ror:8"); }
+#undef W8A8_FMAC_DPP
 
-// Rotation of C chunks of 8 columns; consecutive lanes hold consecutive chunks.  `block` is 16, 32,
-// 64 or 128 (the same for the whole launch).
+// Butterflies of C chunks of 8 columns per lane, up to the lane's sign.  `block` is 16, 32, 64 or 128 (the
+// same for the whole launch).
 template <int C>
-__device__ __forceinline__ void rotate(float (&v)[C][8], int block, float norm, int lane) {
+__device__ __forceinline__ void rotate(float (&v)[C][8], int block, int lane) {
 #pragma unroll
   for (int s = 1; s < 8; s *= 2)
 #pragma unroll
@@ -133,35 +158,52 @@ __device__ __forceinline__ void rotate(float (&v)[C][8], int block, float norm, 
           v[c][i] = a + b;
           v[c][i + s] = a - b;
         }
-  lane_stage<1, C>(v, lane);
-  if (block >= 32) lane_stage<2, C>(v, lane);
-  if (block >= 64) lane_stage<4, C>(v, lane);
-  if (block >= 128) lane_stage<8, C>(v, lane);
+  const int j = chunk_of(lane);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    stage_xor1(v[c], (j & 1) ? -1.0f : 1.0f);
+    if (block >= 32) stage_xor2(v[c], (j & 2) ? -1.0f : 1.0f);
+    if (block >= 64) stage_xor7(v[c], (j & 4) ? -1.0f : 1.0f);
+    if (block >= 128) stage_xor8(v[c], (j & 8) ? -1.0f : 1.0f);
+  }
+}
+
+// Largest magnitude of C chunks as bits (a NaN above an infinity above every number).
+template <int C>
+__device__ __forceinline__ uint32_t chunk_max(const float (&v)[C][8]) {
+  uint32_t m = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[c][i] *= norm;
-}
-
-__device__ __forceinline__ uint32_t wave_max(uint32_t m) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, d));
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[c][i]) & ABS_MASK);
   return m;
 }
 
-// Scale and 127 / amax of a row from the bits of its maximum magnitude; inv is 0 where the codes are 0.
-__device__ __forceinline__ void row_scale(uint32_t bits, float& scale, float& inv) {
-  const float amax = __uint_as_float(bits);
-  if (bits >= INF_BITS) {
-    scale = __uint_as_float(0x7FC00000u);
-    inv = 0.0f;
-  } else if (amax < TINY_ROW) {
-    scale = 0.0f;
-    inv = 0.0f;
-  } else {
-    scale = amax / 127.0f;
-    inv = 127.0f / amax;
-  }
+// Maximum over a row of 16 lanes.
+__device__ __forceinline__ uint32_t lanes16_max(uint32_t m) {
+  m = max(m, dpp<DPP_XOR1>(m));
+  m = max(m, dpp<DPP_XOR2>(m));
+  m = max(m, dpp<DPP_XOR7>(m));
+  return max(m, dpp<DPP_XOR15>(m));
+}
+
+// Maxima of m0 and of m1 over a wave: the first in the lower 32 lanes, the second in the upper.
+__device__ __forceinline__ uint32_t wave_max2(uint32_t m0, uint32_t m1) {
+  auto a = __builtin_amdgcn_permlane32_swap(m0, m1, false, false);
+  uint32_t m = lanes16_max(max(a[0], a[1]));
+  auto b = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  return max(b[0], b[1]);
+}
+
+// 127 / amax of a row from the bits of its maximum magnitude; 0 where the codes are 0.
+__device__ __forceinline__ float row_inv(uint32_t bits, float norm) {
+  const float amax = __uint_as_float(bits), inv = 127.0f / amax;
+  return bits >= INF_BITS || amax * norm < TINY_ROW ? 0.0f : inv;
+}
+
+__device__ __forceinline__ float row_scale(uint32_t bits, float norm) {
+  const float amax = __uint_as_float(bits), scale = (amax * norm) / 127.0f;
+  return bits >= INF_BITS ? __uint_as_float(0x7FC00000u) : amax * norm < TINY_ROW ? 0.0f : scale;
 }
 
 // Eight codes of one chunk, packed.  inv == 0 gives 0 for every finite or non-finite value.
@@ -179,97 +221,100 @@ __device__ __forceinline__ u32x2_t codes8(const float (&v)[8], float inv) {
   return inv == 0.0f ? u32x2_t{0u, 0u} : r;
 }
 
-// Activations, one row per workgroup at a time (rows blockIdx, blockIdx + gridDim, ...): thread t
-// holds columns 8 (c T + t) .. + 8 for c < C, C T 8 >= K.
-template <int DT, bool ROT, int T, int C>
-__global__ __launch_bounds__(T) void quant_i8_kernel(const void* __restrict__ x, int64_t ldx,
-                                                     const uint16_t* __restrict__ lam, int rows, int K, int block,
-                                                     float norm, int8_t* __restrict__ q, float* __restrict__ scales) {
-  constexpr int NW = T / 64;
-  __shared__ uint32_t red[2][NW];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+// Activations, R rows per workgroup at a time (blockIdx R + 0 .. R - 1, then gridDim R rows further on):
+// thread t holds the chunks c T + chunk_of(t) of 8 columns for c < C; T = blockDim, C T 8 >= K.
+template <int DT, bool ROT, int C, int R>
+__global__ __launch_bounds__(1024) void quant_i8_kernel(const void* __restrict__ x, int64_t ldx,
+                                                        const uint16_t* __restrict__ lam, int rows, int K, int block,
+                                                        float norm, int8_t* __restrict__ q,
+                                                        float* __restrict__ scales) {
+  __shared__ uint32_t red[2][R][16];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, T = blockDim.x;
   const bool smooth = lam != nullptr;
-  int row = blockIdx.x;
-  Raw8<DT> raw[C];
+  if (t < 32 * R) red[0][0][t] = 0;  // waves that do not exist
+  int row = blockIdx.x * R;
+  Raw8<DT> raw[R][C];
   const size_t es = DT == 2 ? 4 : 2;
-  auto load_row = [&](int r) {
-    const void* xr = static_cast<const uint8_t*>(x) + (size_t)r * ldx * es;
+  int col[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = 8 * (c * T + t);
-      raw[c] = col < K ? load_raw<DT>(xr, col) : zero_raw<DT>();
+  for (int c = 0; c < C; ++c) col[c] = 8 * (c * T + (ROT ? chunk_of(t) : t));
+  auto load_rows = [&](int row0) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const void* xr = static_cast<const uint8_t*>(x) + (size_t)(row0 + r) * ldx * es;
+#pragma unroll
+      for (int c = 0; c < C; ++c) raw[r][c] = col[c] < K && row0 + r < rows ? load_raw<DT>(xr, col[c]) : zero_raw<DT>();
     }
   };
-  load_row(row);
+  load_rows(row);
   float rh[C][8], rl[C][8];
   bool plain = true;  // every lambda of this lane takes the two-part division
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int col = 8 * (c * T + t);
     float l[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) l[i] = 1.0f;
-    if (smooth && col < K) lambda8(lam, col, l);
+    if (smooth && col[c] < K) lambda8(lam, col[c], l);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float m = fabsf(l[i]);
       plain = plain && m >= 2.3283064365386963e-10f && m <= 4294967296.0f;
-      rh[c][i] = 1.0f / l[i];
+      // any approximation within a few units in the last place serves: rh + rl is what counts
+      rh[c][i] = __builtin_amdgcn_rcpf(l[i]);
       rl[c][i] = fmaf(-l[i], rh[c][i], 1.0f) * rh[c][i];
     }
   }
   const bool wave_plain = __all(plain);
+  const float sign = ROT ? lane_sign(lane, block) : 1.0f;
+  __syncthreads();  // red is cleared
   int par = 0;
   while (true) {
-    float v[C][8];
+    float v[R][C][8];
 #pragma unroll
-    for (int c = 0; c < C; ++c) widen8<DT>(raw[c], v[c]);
-    if (smooth) {
-      if (wave_plain) {
+    for (int r = 0; r < R; ++r)
 #pragma unroll
-        for (int c = 0; c < C; ++c)
+      for (int c = 0; c < C; ++c) {
+        widen8<DT>(raw[r][c], v[r][c]);
+        if (smooth) {
+          if (wave_plain) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], rh[c][i], v[c][i] * rl[c][i]);
-      } else {
-        for (int c = 0; c < C; ++c) {
-          const int col = 8 * (c * T + t);
-          float l[8];
-          if (col < K) {
-            lambda8(lam, col, l);
+            for (int i = 0; i < 8; ++i) v[r][c][i] = fmaf(v[r][c][i], rh[c][i], v[r][c][i] * rl[c][i]);
+          } else {  // one element at a time (the values move through v[r][c][0]), to spend no registers on it
+#pragma unroll 1
+            for (int i = 0; i < 8; ++i) {
+              const float f = col[c] < K ? v[r][c][0] / bf16_bits_to_f32(lam[col[c] + i]) : 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] / l[i];
+              for (int e = 0; e < 7; ++e) v[r][c][e] = v[r][c][e + 1];
+              v[r][c][7] = f;
+            }
           }
         }
       }
-      if (ROT) {
+    const int next = row + gridDim.x * R;
+    if (next < rows) load_rows(next);
+    uint32_t m[R];
 #pragma unroll
-        for (int c = 0; c < C; ++c)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[c][i] = drop_tiny(v[c][i]);
-      }
+    for (int r = 0; r < R; ++r) {
+      if (ROT) rotate<C>(v[r], block, lane);
+      m[r] = chunk_max<C>(v[r]);
     }
-    const int next = row + gridDim.x;
-    if (next < rows) load_row(next);
-    if (ROT) rotate<C>(v, block, norm, lane);
-    uint32_t m = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[c][i]) & ABS_MASK);
-    m = wave_max(m);
-    if (lane == 0) red[par][wave] = m;
+    // lanes 0 .. 31 go on with the first row, 32 .. 63 with the second (with R = 1, both with the one)
+    const uint32_t mw = wave_max2(m[0], m[R - 1]);
+    const int lr = R > 1 ? lane >> 5 : 0;
+    if ((lane & 31) == 0) red[par][lr][wave] = mw;
     __syncthreads();  // the other parity's slots are rewritten only after the next barrier
+    const uint32_t bits = lanes16_max(red[par][lr][lane & 15]);
+    const float inv = row_inv(bits, norm);
+    if (wave == 0 && (lane & 31) == 0 && row + lr < rows) scales[row + lr] = row_scale(bits, norm);
 #pragma unroll
-    for (int w = 0; w < NW; ++w) m = max(m, red[par][w]);
-    float scale, inv;
-    row_scale(m, scale, inv);
-    int8_t* qr = q + (size_t)row * K;
+    for (int r = 0; r < R; ++r) {
+      if (R > 1 && row + r >= rows) break;
+      const float f = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(inv), 32 * r));
+      int8_t* qr = q + (size_t)(row + r) * K;
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int col = 8 * (c * T + t);
-      if (col < K) *reinterpret_cast<u32x2_t*>(qr + col) = codes8(v[c], inv);
+      for (int c = 0; c < C; ++c)
+        if (col[c] < K) *reinterpret_cast<u32x2_t*>(qr + col[c]) = codes8(v[r][c], ROT ? f * sign : f);
     }
-    if (t == 0) scales[row] = scale;
     row = next;
     if (row >= rows) break;
     par ^= 1;
@@ -295,35 +340,31 @@ __global__ __launch_bounds__(256) void quant_i8_long_kernel(const void* __restri
         lambda8(lam, col, l);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[0][i] = ACT ? v[0][i] / l[i] : v[0][i] * l[i];
-        if (ROT && ACT) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[0][i] = drop_tiny(v[0][i]);
-        }
       }
-      if (ROT) rotate<1>(v, block, norm, lane);
+      if (ROT) rotate<1>(v, block, lane);
     };
     uint32_t m = 0;
+    const int tc = 8 * (ROT ? chunk_of(t) : t);
     for (int c0 = 0; c0 < K; c0 += 2048) {
       float v[1][8];
-      values(c0 + 8 * t, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[0][i]) & ABS_MASK);
+      values(c0 + tc, v);
+      m = max(m, chunk_max<1>(v));
     }
-    m = wave_max(m);
+    m = wave_max2(m, m);
     if (lane == 0) red[t >> 6] = m;
     __syncthreads();
     m = max(max(red[0], red[1]), max(red[2], red[3]));
     __syncthreads();
-    float scale, inv;
-    row_scale(m, scale, inv);
+    float inv = row_inv(m, norm);
+    if (ROT) inv *= lane_sign(lane, block);
     int8_t* qr = q + (size_t)row * K;
     for (int c0 = 0; c0 < K; c0 += 2048) {
-      const int col = c0 + 8 * t;
+      const int col = c0 + tc;
       float v[1][8];
       values(col, v);
       if (col < K) *reinterpret_cast<u32x2_t*>(qr + col) = codes8(v[0], inv);
     }
-    if (t == 0) scales[row] = scale;
+    if (t == 0) scales[row] = row_scale(m, norm);
   }
 }
 
@@ -338,26 +379,20 @@ struct QArgs {
   hipStream_t stream;
 };
 
-template <int DT, bool ROT, int T, int C>
-hipError_t run_short(const QArgs& a, int grid) {
-  quant_i8_kernel<DT, ROT, T, C><<<dim3((unsigned)(a.rows < grid ? a.rows : grid)), T, 0, a.stream>>>(
+template <int DT, bool ROT, int C, int R>
+hipError_t run_short(const QArgs& a, int waves_per_cu) {
+  // whole waves, just enough for the row's chunks; workgroups to fill the CUs once
+  const int T = (a.K / 8 + 64 * C - 1) / (64 * C) * 64;
+  const int grid = 256 * (waves_per_cu / (T / 64)), need = (a.rows + R - 1) / R;
+  quant_i8_kernel<DT, ROT, C, R><<<dim3((unsigned)(need < grid ? need : grid)), T, 0, a.stream>>>(
       a.x, a.ldx, a.lam, a.rows, a.K, a.block, a.norm, a.q, a.scales);
   return hipGetLastError();
 }
 
 template <int DT, bool ROT>
 hipError_t run(const QArgs& a, bool act) {
-  if (act && a.K <= 16384) {
-    // few rows: as many threads per row as it has chunks, for latency; many rows: smaller
-    // workgroups, several per CU, each keeping its reciprocals over several rows
-    if (a.rows < 1024) return a.K <= 8192 ? run_short<DT, ROT, 1024, 1>(a, 1024) : run_short<DT, ROT, 1024, 2>(a, 1024);
-    if (a.K <= 2048) return run_short<DT, ROT, 256, 1>(a, 2048);
-    if (a.K <= 4096) return run_short<DT, ROT, 256, 2>(a, 1024);
-    if (a.K <= 6144) return run_short<DT, ROT, 256, 3>(a, 1024);
-    if (a.K <= 8192) return run_short<DT, ROT, 256, 4>(a, 1024);
-    if (a.K <= 12288) return run_short<DT, ROT, 512, 3>(a, 512);
-    return run_short<DT, ROT, 512, 4>(a, 512);
-  }
+  if (act && a.K <= 8192) return a.rows >= 2048 ? run_short<DT, ROT, 1, 2>(a, 24) : run_short<DT, ROT, 1, 1>(a, 32);
+  if (act && a.K <= 16384) return a.rows >= 2048 ? run_short<DT, ROT, 2, 2>(a, 16) : run_short<DT, ROT, 2, 1>(a, 16);
   const dim3 grid((unsigned)(a.rows < 4096 ? a.rows : 4096));
   if (act)
     quant_i8_long_kernel<DT, ROT, true><<<grid, 256, 0, a.stream>>>(a.x, a.ldx, a.lam, a.rows, a.K, a.block, a.norm, a.q, a.scales);
