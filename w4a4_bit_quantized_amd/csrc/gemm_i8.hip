@@ -114,15 +114,18 @@ __device__ __forceinline__ void i8_mma(i32x16_t (&acc)[FM][FN], const i32x4_t (&
     for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
 }
 
-// Order of a quarter K-step: its matrix instructions with the next quarter's LDS reads between them
-// (and the direct loads, where the quarter issues them).
+// Order of a quarter K-step: its matrix instructions with the next quarter's LDS reads between them, and
+// the quarter's LOADS direct loads between its last ones (a wave that waits to issue a load issues no
+// matrix instruction either: a quarter of a K-step's loads right after the barrier and the rest in
+// the next quarter measured 118 us at 2560 x 2560 x 12288, all of them after the barrier 136, all in
+// the next quarter 125; 4096 x 13824 x 5120: 301, 311 and 312).
 template <int FM, int FN, int LOADS>
 __device__ __forceinline__ void i8_interleave() {
 #pragma unroll
   for (int g = 0; g < FM * FN; ++g) {
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
-    if (g < LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // direct load
+    if (g >= FM * FN - LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // direct load
   }
   __builtin_amdgcn_sched_barrier(0);
 }
@@ -135,8 +138,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
   using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, lane = t & 63;
-  const int kg = __builtin_amdgcn_readfirstlane(t >> 6) / T::WAVES;
-  const int wave = __builtin_amdgcn_readfirstlane(t >> 6) % T::WAVES;
+  const int w = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int kg = KG > 1 ? w / T::WAVES : 0, wave = KG > 1 ? w % T::WAVES : w;
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int l32 = lane & 31, h = lane >> 5;
   int tm, tn;
@@ -175,10 +178,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
   auto k_of = [&](int i) {
     const int p = KG * min(i, ni - 1) + kg;
     const int q = p + kt0 >= nkt ? p + kt0 - nkt : p + kt0;
-    return (uint32_t)(p < nkt ? q : nkt) * T::STEP;
+    return (uint32_t)(KG == 1 || p < nkt ? q : nkt) * T::STEP;
   };
   uint8_t* ring = lds + kg * S * T::STAGE;
-  constexpr int R = T::ROUNDS, RH = T::ROUNDS / 2;
+  constexpr int R = T::ROUNDS, RA = T::ROUNDS / 4;
 #pragma unroll
   for (int j = 0; j < S - 1; ++j)
     i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
@@ -186,15 +189,15 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
   i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
   int slot = 0;
   i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
-  i8_issue<T, 0, RH>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
+  i8_issue<T, 0, RA>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
   for (int kt = 0; kt < ni; ++kt) {
     uint8_t* cur = ring + slot * T::STAGE;
-    // the second half of the loads of K-step kt + S - 1, into the slot of kt - 1
-    i8_issue<T, RH, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
+    // the rest of the loads of K-step kt + S - 1, into the slot of kt - 1
+    i8_issue<T, RA, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
                        bbase, off, col);
     i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
     i8_mma<FM, FN>(acc, a0, b0);
-    i8_interleave<FM, FN, R - RH>();
+    i8_interleave<FM, FN, R - RA>();
     i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
     i8_mma<FM, FN>(acc, a1, b1);
     i8_interleave<FM, FN, 0>();
@@ -203,11 +206,11 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
     i8_interleave<FM, FN, 0>();
     // K-step kt + 1 has landed and every wave has read the operands of kt: its slot is free
     vm_wait_barrier<(S - 2) * R>();
-    i8_issue<T, 0, RH>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
+    i8_issue<T, 0, RA>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
     slot = slot == S - 1 ? 0 : slot + 1;
     i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
     i8_mma<FM, FN>(acc, a1, b1);
-    i8_interleave<FM, FN, RH>();
+    i8_interleave<FM, FN, RA>();
   }
   vm_wait_barrier<0>();
   if constexpr (KG > 1) {
