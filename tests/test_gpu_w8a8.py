@@ -266,6 +266,53 @@ def test_linear(w4, case):
         same_bits(host(y3).reshape(M, N), ref, "3-D")
 
 
+@pytest.mark.parametrize("K", [16, 144, 2048, 2064, 4096, 4112, 8192, 8208])
+@pytest.mark.parametrize("xd", DTYPES)
+def test_linear_one_token(w4, hooks, K, xd):
+    """One token (one launch up to K = 8192): against the oracle and the two-launch layer, with and
+    without smoothing, rotation and bias, at ragged channel counts, and with a row that counts as zero or NaN."""
+    import torch
+    rng = np.random.default_rng(K)
+    for N, block, yd, special in ((1, 0, "bf16", 0), (37, 16, "f32", 0), (96, 128 if K % 128 == 0 else 0, "f16", 0),
+                                  (40, 0, "f32", 1), (40, 16, "f32", 2)):
+        x, lam = rows(rng, 1, K, xd), factors(rng, K)
+        if special:
+            xf = oh.to_f32(x, xd).copy()
+            if special == 1:
+                xf[:] = 0
+            else:
+                xf[0, K // 2] = np.nan
+            x = oh.from_f32(xf, xd)
+        qw, sw = codes(rng, N, K), rng.uniform(0.001, 0.01, N).astype(np.float32)
+        b = oh.from_f32(rng.uniform(-1, 1, N).astype(np.float32), "bf16") if block else None
+        smooth = N != 1
+        layer = dict(qweight=torch.from_numpy(qw).cuda(), wscales=torch.from_numpy(sw).cuda())
+        if smooth:
+            layer["smooth_factor"] = dev(lam, "bf16")
+        if b is not None:
+            layer["bias"] = dev(b, "bf16")
+        ref = oh.from_f32(ow.linear_f32(oh.to_f32(x, xd), qw, sw, oh.to_f32(lam, "bf16") if smooth else None,
+                                        None if b is None else oh.to_f32(b, "bf16"), block), yd)
+        for mode in ("1", "0"):
+            hooks.setenv("W8A8_ONE_LAUNCH", mode)
+            y = w4.w8a8_linear(dev(x, xd), layer, hadamard_block=block, out_dtype=tdtype(yd))
+            same_bits(host(y), ref, f"K={K} N={N} {xd} {yd} one launch {mode}")
+
+
+def test_linear_one_token_extreme_factors(w4):
+    """Smoothing factors outside the two-part division's range, in the one-launch layer."""
+    import torch
+    rng = np.random.default_rng(1)
+    K, N = 512, 33
+    x = rows(rng, 1, K, "bf16")
+    qw, sw = codes(rng, N, K), np.ones(N, np.float32)
+    for values in ([2.0 ** -40, 1.0], [2.0 ** 50, 2.0], [0.0, 1.0], [np.inf, 2.0], [-3.0, 1.0]):
+        lam = oh.from_f32(np.resize(np.array(values, np.float32), K), "bf16")
+        y = w4.w8a8_linear(dev(x, "bf16"), dict(qweight=torch.from_numpy(qw).cuda(), wscales=torch.from_numpy(sw).cuda(),
+                                                smooth_factor=dev(lam, "bf16")), out_dtype=torch.float32)
+        same_bits(host(y), ow.linear_f32(oh.to_f32(x, "bf16"), qw, sw, oh.to_f32(lam, "bf16")), f"factors {values}")
+
+
 def test_linear_nonfinite_rows_stay_alone(w4):
     """A row with an infinity or a NaN is NaN throughout; the other rows are as without it."""
     import torch

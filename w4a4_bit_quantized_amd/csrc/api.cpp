@@ -389,12 +389,13 @@ w4a4_status validate_quantize_w8a8(const void* x, int64_t ldx, int32_t x_dtype, 
   return W4A4_OK;
 }
 
+float rotation_norm(int32_t hb) { return hb ? (float)(1.0 / std::sqrt((double)hb)) : 1.0f; }
+
 w4a4_status quantize_w8a8(bool act, const void* x, int64_t ldx, int32_t x_dtype, const void* smooth_factor, int64_t rows,
                           int64_t K, int32_t hb, void* q, float* scales, void* stream) {
   if (!w4a4::launch_quantize_i8) return W4A4_ERR_HIP;
-  const float norm = hb ? (float)(1.0 / std::sqrt((double)hb)) : 1.0f;
   (void)hipGetLastError();
-  return from_hip(w4a4::launch_quantize_i8(act, x, ldx, smooth_factor, rows, K, hb, x_dtype, norm, q, scales,
+  return from_hip(w4a4::launch_quantize_i8(act, x, ldx, smooth_factor, rows, K, hb, x_dtype, rotation_norm(hb), q, scales,
                                            static_cast<hipStream_t>(stream)));
 }
 
@@ -473,6 +474,12 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
   if (st != W4A4_OK) return st;
   st = validate_gemm_w8a8(ws, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype);
   if (st != W4A4_OK) return st;
+  if (w4a4::linear_i8_one_launch && w4a4::linear_i8_one_launch(M, K)) {
+    (void)hipGetLastError();
+    return from_hip(w4a4::launch_linear_i8_token(x, x_dtype, smooth_factor, hadamard_block,
+                                                 rotation_norm(hadamard_block), qweight, wscales, bias, N, K, y, y_dtype,
+                                                 static_cast<hipStream_t>(stream)));
+  }
   st = quantize_w8a8(true, x, ldx, x_dtype, smooth_factor, M, K, hadamard_block, ws, ascales, stream);
   if (st != W4A4_OK) return st;
   return gemm_w8a8(ws, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype, stream);

@@ -16,6 +16,7 @@
 #include "device_common.h"
 #include "gemm_common.h"
 #include "launch.h"
+#include "quantize_i8.h"
 
 namespace w4a4 {
 
@@ -422,6 +423,158 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
   }
 }
 
+// ---- one token: quantizer and weight streaming in one launch ---------------------------------------
+// Each workgroup (4 waves, 32 channels) starts its weight rings, quantizes the token itself (it is in L2,
+// and its arithmetic hides behind the first weights' way from HBM) into codes in LDS, and goes on as the
+// streaming kernel above with the activation operand read from there.  Every workgroup repeats the
+// quantizer's work; what is saved is a launch and the wait between the two (2048 x 6144: 7.4 to 6.1 us,
+// 5120 x 13824: 15.9 to 15.0, and 3 us of the host's time; with two tokens 5120 x 13824 takes 17.2 us
+// this way and 16.2 in two launches).  The codes are those of the quantizer kernel bit for bit.
+constexpr int TK_WAVES = 4, TK_S = 3;
+
+struct TokenArgs {
+  const void* x;
+  const uint16_t* lam;
+  int block;
+  float norm;
+  const uint8_t* qw;
+  const float* sw;
+  const uint16_t* bias;
+  int N, K, ydtype;
+  void* y;
+};
+
+__device__ __forceinline__ void token_issue(uint8_t* stage, uint32_t k0, uint32_t K, const uint8_t* wbase,
+                                            const uint32_t* off, const uint32_t* col) {
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint8_t* p = wbase + (k0 + off[r]);
+    if (k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
+    load_lds16(p, stage + r * 1024);
+  }
+}
+
+__device__ __forceinline__ void token_mma(i32x4_t (&acc)[2], const i32x4_t (&a)[2], const i32x4_t (&w)[2][2]) {
+#pragma unroll
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s], acc[j], 0, 0, 0);
+}
+
+// C: chunks of 8 columns per thread, 2048 C >= K.
+template <int DT, bool ROT, int C>
+__global__ __launch_bounds__(64 * TK_WAVES) void linear_i8_token_kernel(const TokenArgs p) {
+  extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
+  __shared__ uint32_t red[TK_WAVES];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int l16 = lane & 15, g = lane >> 4;
+  const int n0 = blockIdx.x * 32, N = p.N, K = p.K;
+  const uint8_t* wbase = p.qw + (size_t)n0 * K;
+  uint8_t* ring = dyn + wave * TK_S * 4096;
+  uint8_t* codes = dyn + TK_WAVES * TK_S * 4096;
+  uint32_t off[4], col[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const int row = 8 * r + (lane >> 3);
+    col[r] = 16u * (uint32_t)((lane & 7) ^ i8_swizzle(row));
+    off[r] = (uint32_t)min(row, N - 1 - n0) * (uint32_t)K + col[r];
+  }
+  const int nkt = (K + 127) / 128, steps = (nkt - wave + TK_WAVES - 1) / TK_WAVES;
+  auto k_of = [&](int i) { return 128u * (uint32_t)(wave + TK_WAVES * min(i, steps - 1)); };
+  if (steps > 0) {
+#pragma unroll
+    for (int i = 0; i < TK_S - 1; ++i) token_issue(ring + i * 4096, k_of(i), (uint32_t)K, wbase, off, col);
+  }
+
+  const int tc = 8 * (ROT ? chunk_of(t) : t);
+  float v[C][8];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int k = 2048 * c + tc;
+    widen8<DT>(k < K ? load_raw<DT>(p.x, k) : zero_raw<DT>(), v[c]);
+  }
+  if (p.lam != nullptr) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int k = 2048 * c + tc;
+      float l[8], rh[8], rl[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) l[i] = 1.0f;
+      if (k < K) lambda8(p.lam, k, l);
+      if (__all(reciprocals8(l, rh, rl))) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], rh[i], v[c][i] * rl[i]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] / l[i];
+      }
+    }
+  }
+  if (ROT) rotate<C>(v, p.block, lane);
+  const uint32_t mx = chunk_max<C>(v), mw = wave_max2(mx, mx);
+  if (lane == 0) red[wave] = mw;
+  // (LDS only: the weights in flight are not waited for)
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  const uint32_t bits = max(max(red[0], red[1]), max(red[2], red[3]));
+  const float inv = row_inv(bits, p.norm) * (ROT ? lane_sign(lane, p.block) : 1.0f);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int k = 2048 * c + tc;
+    if (k < K) *reinterpret_cast<u32x2_t*>(codes + k) = codes8(v[c], inv);
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+
+  // all 16 activation rows of the instruction are the token (one column of the product is stored); columns
+  // past K, up to the K-step's end, meet zero weights
+  const uint8_t* arow = codes + 16 * g;
+  i32x4_t acc[2] = {i32x4_t{0, 0, 0, 0}, i32x4_t{0, 0, 0, 0}};
+  if (steps > 0) {
+    int slot = 0;
+    for (int i = 0; i < steps; ++i) {
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((TK_S - 2) * 4) : "memory");
+      token_issue(ring + (slot == 0 ? TK_S - 1 : slot - 1) * 4096, k_of(i + TK_S - 1), (uint32_t)K, wbase, off, col);
+      const uint8_t* cur = ring + slot * 4096;
+      const uint8_t* ac = arow + k_of(i);
+      i32x4_t a[2], w[2][2];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int c = 16 * ((4 * s + g) ^ i8_swizzle(l16));
+        a[s] = *reinterpret_cast<const i32x4_t*>(ac + 64 * s);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) w[s][j] = *reinterpret_cast<const i32x4_t*>(cur + (16 * j + l16) * 128 + c);
+      }
+      token_mma(acc, a, w);
+      slot = slot == TK_S - 1 ? 0 : slot + 1;
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+  __syncthreads();  // every wave has left its ring
+  int* part = reinterpret_cast<int*>(dyn);
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (l16 == 0) *reinterpret_cast<i32x4_t*>(part + wave * 32 + 16 * j + 4 * g) = acc[j];
+  __syncthreads();
+  const int n = n0 + t;
+  if (t < 32 && n < N) {
+    const int sum = part[t] + part[32 + t] + part[64 + t] + part[96 + t];
+    float f = ((float)sum * row_scale(bits, p.norm)) * p.sw[n];
+    if (p.bias != nullptr) f += bf16_bits_to_f32(p.bias[n]);
+    if (p.ydtype == 2) store_one<2>(p.y, n, f);
+    else if (p.ydtype == 1) store_one<1>(p.y, n, f);
+    else store_one<0>(p.y, n, f);
+  }
+}
+
+template <int DT, bool ROT>
+hipError_t run_token(const TokenArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.N + 31) / 32)), block(64 * TK_WAVES);
+  const size_t lds = TK_WAVES * TK_S * 4096 + (size_t)(a.K + 127) / 128 * 128;
+  if (a.K <= 4096) linear_i8_token_kernel<DT, ROT, 2><<<grid, block, lds, stream>>>(a);
+  else linear_i8_token_kernel<DT, ROT, 4><<<grid, block, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
 struct GArgs {
   const uint8_t* qa;
   const float* sa;
@@ -496,6 +649,23 @@ hipError_t launch_gemm_i8(const void* qact, const float* ascales, const void* qw
     case 0: return run<0>(a);
     case 1: return run<1>(a);
     default: return run<2>(a);
+  }
+}
+
+bool linear_i8_one_launch(int64_t M, int64_t K) {
+  const char* forced = test_hook("W8A8_ONE_LAUNCH");  // "0" keeps the two launches
+  return M == 1 && K <= 8192 && !(forced && forced[0] == '0');
+}
+
+hipError_t launch_linear_i8_token(const void* x, int xdtype, const void* lam, int block, float norm,
+                                  const void* qweight, const float* wscales, const void* bias, int64_t N, int64_t K,
+                                  void* y, int ydtype, hipStream_t stream) {
+  const TokenArgs a{x, static_cast<const uint16_t*>(lam), block, norm, static_cast<const uint8_t*>(qweight),
+                    wscales, static_cast<const uint16_t*>(bias), (int)N, (int)K, ydtype, y};
+  switch (xdtype) {
+    case 0: return block ? run_token<0, true>(a, stream) : run_token<0, false>(a, stream);
+    case 1: return block ? run_token<1, true>(a, stream) : run_token<1, false>(a, stream);
+    default: return block ? run_token<2, true>(a, stream) : run_token<2, false>(a, stream);
   }
 }
 
