@@ -568,7 +568,10 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
   a.pos64 = (flags & W4A4_ROPE_POSITIONS_I64) != 0;
   a.eps = eps;
   a.inv_d = (float)(1.0 / head_dim);
-  a.log2_theta = std::log2(theta);
+  for (int x = 0; x < axes; ++x) {
+    const int pairs = a.shared ? a.rot2 : a.start[x + 1] - a.start[x];
+    a.step[x] = pairs > 0 ? std::log2(theta) / pairs : 0.0;
+  }
   if (!w4a4::launch_qk_norm_rope) return W4A4_ERR_HIP;
   (void)hipGetLastError();
   return from_hip(w4a4::launch_qk_norm_rope(a, dtype, static_cast<hipStream_t>(stream)));

@@ -113,8 +113,9 @@ struct RopeArgs {
   int layout;                     // 0 interleaved, 1 halves of the span, 2 halves of each axis's slice
   bool norm, shared, pos64;
   float eps, inv_d;
-  double log2_theta;
-  int tb, hb, log2g;              // set by the launcher: tokens and heads per workgroup, lanes per head
+  double step[ROPE_MAX_AXES];     // log2(theta) / pairs of each axis (shared: of the span, in the first)
+  // set by the launcher: tokens and heads of a workgroup's pass, log2 of the lanes per head and of the pairs
+  int tb, hb, log2g, log2p;
 };
 
 // RMS norm and rotary rotation of q and k heads; dtype 0 bf16, 1 f16, 2 f32.

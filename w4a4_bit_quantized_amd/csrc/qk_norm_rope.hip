@@ -12,9 +12,10 @@
 //
 // Bound: HBM (every element read and written once).  A group of G lanes (a power of two) holds one
 // head of one token, 2 V elements per lane: V pairs, so a rotation never leaves its lane and the only
-// exchange is the sum of squares (DPP within 16 lanes).  A workgroup takes TB tokens; their cosines and
-// sines are made once, in LDS, and shared by all their heads.  The heads of a few items are loaded
-// before the first of them is used.
+// exchange is the sum of squares (DPP within 16 lanes).  A workgroup takes a few tokens per pass; their
+// cosines and sines are made once, in LDS, and shared by all their heads, and each thread forms its pair's
+// frequency once per launch.  Measured: 32760 tokens of 24 + 24 heads of 128 in bf16 152 us (5.3 TB/s of
+// reads and writes), 4608 tokens 21.7 us (5.2 TB/s), one token of 32 + 8 heads 4.3 us.
 #include <math.h>
 
 #include "device_common.h"
@@ -25,6 +26,10 @@ namespace w4a4 {
 namespace {
 
 constexpr int RT = 256;  // threads per workgroup
+// Workgroups of a launch with many tokens: six per CU, all resident, which then walk the tokens in
+// strides of the whole launch (2048 of them: 180 us at 32760 tokens of 48 heads of 128, 1536: 159;
+// a contiguous run of tokens for each: 172; one pass per workgroup: 169).
+constexpr int MAX_WGS = 1536;
 
 template <int DT>
 __device__ __forceinline__ constexpr int esize() { return DT == 2 ? 4 : 2; }
@@ -78,6 +83,9 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {  // round to neare
   }
 }
 
+// (16-bit vectors leave by non-temporal stores: 4608 tokens of 48 heads of 128 took 28.4 us with ordinary
+// ones, 22.9 with these; an f32 lane's two halves of 32 bytes are better merged in L2, 87 against 91 us
+// for 8000 tokens)
 template <int DT, int N>
 __device__ __forceinline__ void store_n(uint8_t* p, const float* v) {
   if constexpr (N == 1) {
@@ -88,10 +96,10 @@ __device__ __forceinline__ void store_n(uint8_t* p, const float* v) {
     for (int c = 0; c < N; c += 4)
       *reinterpret_cast<float4_t*>(p + 4 * c) = float4_t{v[c], v[c + 1], v[c + 2], v[c + 3]};
   } else if constexpr (N == 8) {
-    *reinterpret_cast<u32x4_t*>(p) = u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
-                                             pack2<DT>(v[6], v[7])};
+    __builtin_nontemporal_store(u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
+                                        pack2<DT>(v[6], v[7])}, reinterpret_cast<u32x4_t*>(p));
   } else {
-    *reinterpret_cast<u32x2_t*>(p) = u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    __builtin_nontemporal_store(u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])}, reinterpret_cast<u32x2_t*>(p));
   }
 }
 
@@ -136,32 +144,22 @@ __device__ __forceinline__ void pair_elements(const RopeArgs& a, int p, int& e0,
 // e0 and V at e1.  IT: chunks of V pairs per lane; UN: items in flight.
 template <int DT, int V, bool INTER, int IT, int UN>
 __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float trig[];  // [TB][D / 2] cosines, then sines
+  extern __shared__ __attribute__((aligned(16))) float trig[];  // two halves of [tb][D / 2] cosines, then sines
   const int t = threadIdx.x;
   const int D2 = a.D / 2, G = 1 << a.log2g;
-  const int t0 = blockIdx.x * a.tb;
-  const int nt = min(a.tb, a.tokens - t0);
   const int heads = a.q.heads + a.k.heads;
   const int h0 = blockIdx.y * a.hb, nh = min(a.hb, heads - h0);
   constexpr int ES = esize<DT>();
 
-  float* cos_t = trig;
-  float* sin_t = trig + a.tb * D2;
-  for (int i = t; i < nt * D2; i += RT) {
-    const int tok = i / D2, p = i - tok * D2;
-    float c = 1.0f, s = 0.0f;
-    if (p < a.rot2) {
-      int x = 0;
-      while (x + 1 < a.axes && p >= a.start[x + 1]) ++x;
-      const double e = a.shared ? (double)p / a.rot2 : (double)(p - a.start[x]) / (a.start[x + 1] - a.start[x]);
-      const size_t at = (size_t)(t0 + tok) * a.axes + x;
-      const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[at]
-                                 : (double)static_cast<const int32_t*>(a.pos)[at];
-      const double turns = pos * (exp2(-e * a.log2_theta) * 0.15915494309189535);
-      sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
-    }
-    cos_t[i] = c;
-    sin_t[i] = s;
+  // The angle of this thread's pair (of 2^log2p >= D / 2, for tokens t >> log2p, + 256 >> log2p, ...), in turns
+  // per position.
+  const int ap = t & ((1 << a.log2p) - 1), at0 = t >> a.log2p, atn = RT >> a.log2p;
+  double freq = 0.0;
+  int axis = 0;
+  if (ap < a.rot2) {
+    while (axis + 1 < a.axes && ap >= a.start[axis + 1]) ++axis;
+    const int i = a.shared ? ap : ap - a.start[axis];
+    freq = exp2(-(double)i * a.step[a.shared ? 0 : axis]) * 0.15915494309189535;  // 1 / (2 pi)
   }
 
   // this lane's chunks: the same pairs for every item
@@ -191,87 +189,106 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
       weights(a.k.weight, wk[c]);
     }
   }
-  __syncthreads();
+  int half = 0;
+  for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.tokens; t0 += (int64_t)gridDim.x * a.tb, half ^= 1) {
+    const int nt = (int)min((int64_t)a.tb, a.tokens - t0);
+    float* cos_t = trig + half * a.tb * a.D;
+    float* sin_t = cos_t + a.tb * D2;
+    if (ap < D2)
+      for (int tk = at0; tk < nt; tk += atn) {
+        float c = 1.0f, s = 0.0f;
+        if (ap < a.rot2) {
+          const size_t at = (size_t)(t0 + tk) * a.axes + axis;
+          const double pos = a.pos64 ? (double)static_cast<const int64_t*>(a.pos)[at]
+                                     : (double)static_cast<const int32_t*>(a.pos)[at];
+          const double turns = pos * freq;
+          sincospif(2.0f * (float)(turns - rint(turns)), &s, &c);
+        }
+        cos_t[tk * D2 + ap] = c;
+        sin_t[tk * D2 + ap] = s;
+      }
+    __syncthreads();  // (the other half is rewritten only after the next one)
 
-  int tok = 0, head = grp;  // item of this group: token t0 + tok, head h0 + head
-  while (head >= nh) { head -= nh; ++tok; }
-  while (tok < nt) {
-    float v[UN][IT][2 * V];
-    int it_tok[UN];
-    bool it_q[UN];
-    uint8_t* dst[UN];
+    int tok = 0, head = grp;  // item of this group: token t0 + tok, head h0 + head
+    while (head >= nh) { head -= nh; ++tok; }
+    while (tok < nt) {
+      float v[UN][IT][2 * V];
+      int it_tok[UN];
+      bool it_q[UN];
+      uint8_t* dst[UN];
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      const bool valid = tok < nt;
-      const int hd = h0 + head;
-      const bool isq = hd < a.q.heads;
-      it_tok[u] = valid ? tok : -1;
-      it_q[u] = isq;
-      const int hh = isq ? hd : hd - a.q.heads;
-      const int64_t tt = t0 + tok;
-      const uint8_t* src = static_cast<const uint8_t*>(isq ? a.q.x : a.k.x) +
-                           (tt * (isq ? a.q.ts : a.k.ts) + hh * (isq ? a.q.hs : a.k.hs)) * ES;
-      dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
-               (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
+      for (int u = 0; u < UN; ++u) {
+        const bool valid = tok < nt;
+        const int hd = h0 + head;
+        const bool isq = hd < a.q.heads;
+        it_tok[u] = valid ? tok : -1;
+        it_q[u] = isq;
+        const int hh = isq ? hd : hd - a.q.heads;
+        const int64_t tt = t0 + tok;
+        const uint8_t* src = static_cast<const uint8_t*>(isq ? a.q.x : a.k.x) +
+                             (tt * (isq ? a.q.ts : a.k.ts) + hh * (isq ? a.q.hs : a.k.hs)) * ES;
+        dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
+                 (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
 #pragma unroll
-      for (int c = 0; c < IT; ++c) {
+        for (int c = 0; c < IT; ++c) {
 #pragma unroll
-        for (int i = 0; i < 2 * V; ++i) v[u][c][i] = 0.0f;
-        if (valid && in[c]) {
-          if constexpr (INTER) {
-            load_n<DT, 2 * V>(src + e0[c] * ES, v[u][c]);
-          } else {
-            load_n<DT, V>(src + e0[c] * ES, v[u][c]);
-            load_n<DT, V>(src + e1[c] * ES, v[u][c] + V);
+          for (int i = 0; i < 2 * V; ++i) v[u][c][i] = 0.0f;
+          if (valid && in[c]) {
+            if constexpr (INTER) {
+              load_n<DT, 2 * V>(src + e0[c] * ES, v[u][c]);
+            } else {
+              load_n<DT, V>(src + e0[c] * ES, v[u][c]);
+              load_n<DT, V>(src + e1[c] * ES, v[u][c] + V);
+            }
           }
         }
+        head += ng;
+        while (head >= nh) { head -= nh; ++tok; }
       }
-      head += ng;
-      while (head >= nh) { head -= nh; ++tok; }
-    }
 #pragma unroll
-    for (int u = 0; u < UN; ++u) {
-      float r = 1.0f;
-      if (a.norm) {
-        float s = 0.0f;
+      for (int u = 0; u < UN; ++u) {
+        float r = 1.0f;
+        if (a.norm) {
+          float s = 0.0f;
 #pragma unroll
-        for (int c = 0; c < IT; ++c)
+          for (int c = 0; c < IT; ++c)
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) s = fmaf(v[u][c][i], v[u][c][i], s);
-        s = group_sum(s, G);
-        r = rsqrtf(fmaf(s, a.inv_d, a.eps));
-      }
-      if (it_tok[u] < 0) continue;
-#pragma unroll
-      for (int c = 0; c < IT; ++c) {
-        if (!in[c]) continue;
-        float o[2 * V];
-#pragma unroll
-        for (int i = 0; i < 2 * V; ++i) o[i] = a.norm ? (v[u][c][i] * r) * (it_q[u] ? wq[c][i] : wk[c][i]) : v[u][c][i];
-        const int at = it_tok[u] * D2 + (gl + c * G) * V;
-        float cs[V], sn[V];
-        if constexpr (V == 4) {
-          const float4_t cc = *reinterpret_cast<const float4_t*>(cos_t + at);
-          const float4_t ss = *reinterpret_cast<const float4_t*>(sin_t + at);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { cs[i] = cc[i]; sn[i] = ss[i]; }
-        } else {
-          cs[0] = cos_t[at];
-          sn[0] = sin_t[at];
+            for (int i = 0; i < 2 * V; ++i) s = fmaf(v[u][c][i], v[u][c][i], s);
+          s = group_sum(s, G);
+          r = rsqrtf(fmaf(s, a.inv_d, a.eps));
         }
-        // pairs of this chunk: (o[i0], o[i1]); a chunk past the span (not interleaved) has cos 1, sin 0
+        if (it_tok[u] < 0) continue;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int i0 = INTER ? 2 * i : i, i1 = INTER ? 2 * i + 1 : V + i;
-          const float x0 = o[i0], x1 = o[i1];
-          o[i0] = fmaf(x0, cs[i], -(x1 * sn[i]));
-          o[i1] = fmaf(x0, sn[i], x1 * cs[i]);
-        }
-        if constexpr (INTER) {
-          store_n<DT, 2 * V>(dst[u] + e0[c] * ES, o);
-        } else {
-          store_n<DT, V>(dst[u] + e0[c] * ES, o);
-          store_n<DT, V>(dst[u] + e1[c] * ES, o + V);
+        for (int c = 0; c < IT; ++c) {
+          if (!in[c]) continue;
+          float o[2 * V];
+#pragma unroll
+          for (int i = 0; i < 2 * V; ++i) o[i] = a.norm ? (v[u][c][i] * r) * (it_q[u] ? wq[c][i] : wk[c][i]) : v[u][c][i];
+          const int at = it_tok[u] * D2 + (gl + c * G) * V;
+          float cs[V], sn[V];
+          if constexpr (V == 4) {
+            const float4_t cc = *reinterpret_cast<const float4_t*>(cos_t + at);
+            const float4_t ss = *reinterpret_cast<const float4_t*>(sin_t + at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { cs[i] = cc[i]; sn[i] = ss[i]; }
+          } else {
+            cs[0] = cos_t[at];
+            sn[0] = sin_t[at];
+          }
+          // pairs of this chunk: (o[i0], o[i1]); a chunk past the span (not interleaved) has cos 1, sin 0
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const int i0 = INTER ? 2 * i : i, i1 = INTER ? 2 * i + 1 : V + i;
+            const float x0 = o[i0], x1 = o[i1];
+            o[i0] = fmaf(x0, cs[i], -(x1 * sn[i]));
+            o[i1] = fmaf(x0, sn[i], x1 * cs[i]);
+          }
+          if constexpr (INTER) {
+            store_n<DT, 2 * V>(dst[u] + e0[c] * ES, o);
+          } else {
+            store_n<DT, V>(dst[u] + e0[c] * ES, o);
+            store_n<DT, V>(dst[u] + e1[c] * ES, o + V);
+          }
         }
       }
     }
@@ -281,8 +298,9 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
 template <int DT, int V, bool INTER, int IT, int UN>
 hipError_t run(const RopeArgs& a, hipStream_t st) {
   const int heads = a.q.heads + a.k.heads;
-  const dim3 grid((unsigned)((a.tokens + a.tb - 1) / a.tb), (unsigned)((heads + a.hb - 1) / a.hb));
-  const size_t lds = (size_t)a.tb * a.D * sizeof(float);
+  const int64_t blocks = ((int64_t)a.tokens + a.tb - 1) / a.tb;
+  const dim3 grid((unsigned)(blocks < MAX_WGS ? blocks : MAX_WGS), (unsigned)((heads + a.hb - 1) / a.hb));
+  const size_t lds = 2 * (size_t)a.tb * a.D * sizeof(float);
   qk_norm_rope_kernel<DT, V, INTER, IT, UN><<<grid, RT, lds, st>>>(a);
   return hipGetLastError();
 }
@@ -293,11 +311,17 @@ hipError_t run_dt(RopeArgs a, bool vec, hipStream_t st) {
   a.log2g = 0;
   while ((1 << a.log2g) < lanes) ++a.log2g;
   const int ng = RT >> a.log2g, heads = a.q.heads + a.k.heads;
+  a.log2p = 0;
+  while ((1 << a.log2p) < a.D / 2) ++a.log2p;
   // few tokens: one pass per workgroup, heads split over workgroups; many: several tokens each
-  a.tb = a.tokens >= 4096 ? 4 : 1;
   a.hb = a.tokens < 512 && heads > ng ? ng : heads;
-  if (!vec) return run<DT, 1, false, 4, 1>(a, st);
-  return a.layout == 0 ? run<DT, 4, true, 1, 4>(a, st) : run<DT, 4, false, 1, 4>(a, st);
+  // tokens per pass: about six items for every lane group, so that a pass is worth its angles and its barrier
+  const int64_t per = ((int64_t)a.tokens + MAX_WGS - 1) / MAX_WGS;  // (fewer where not every workgroup has a pass)
+  const int full = heads > 0 ? 6 * ng / heads : 1;
+  a.tb = full < 1 ? 1 : full > 8 ? 8 : full;
+  if (per < a.tb) a.tb = (int)per;
+  if (!vec) return a.D <= 128 ? run<DT, 1, false, 1, 4>(a, st) : run<DT, 1, false, 4, 1>(a, st);
+  return a.layout == 0 ? run<DT, 4, true, 1, 2>(a, st) : run<DT, 4, false, 1, 2>(a, st);
 }
 
 bool aligned16(const RopeHeads& h, int es) {
