@@ -181,7 +181,7 @@ def check_gemm(w4, M, N, K, ydtype, bias, seed=0, out=None):
     same_bits(host(y), oh.from_f32(ref, ydtype), f"{M}x{N}x{K} {ydtype}")
 
 
-GEMM_SHAPES = [(1, 1, 16), (1, 33, 64), (7, 200, 1040), (16, 256, 512), (17, 100, 528), (32, 64, 2048), (33, 130, 144),
+GEMM_SHAPES = [(330, 741, 64), (281, 434, 80), (350, 4044, 48), (4099, 4099, 64), (4090, 4100, 64), (1100, 4110, 96), (1, 1, 16), (1, 33, 64), (7, 200, 1040), (16, 256, 512), (17, 100, 528), (32, 64, 2048), (33, 130, 144),
                (64, 96, 4096), (65, 64, 128), (65, 1, 16), (100, 131, 272), (128, 4096, 256), (130, 9000, 400),
                (513, 3001, 128), (640, 4096, 1040), (1100, 8200, 144), (2048, 6200, 1552), (300, 40, 16400)]
 
@@ -227,7 +227,7 @@ def test_gemm_largest_sum(w4):
 def test_gemm_into_a_partition(w4, M, N, ydtype):
     """An output partition of a wider matrix, aligned and not: nothing outside it is written."""
     import torch
-    for start, width in ((16, N + 48), (3, N + 8)):
+    for start, width in ((16, N + 48), (3, N + 8), (4, N + 12), (2, N + 9)):
         big = torch.full((M + 2, width), 7.0, dtype=tdtype(ydtype), device="cuda")
         check_gemm(w4, M, N, 272, ydtype, True, out=big[1:M + 1, start:start + N])
         keep = torch.ones_like(big, dtype=torch.bool)

@@ -131,6 +131,86 @@ __device__ __forceinline__ void i8_interleave() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// A wave's epilogue region (32 rows of FN * 32 elements of ES bytes; 16-byte chunk ch of row r at
+// (ch + r / 2) % CPR) to y rows m0 .., columns n0 ..: 16 bytes per lane where every row of y starts on
+// such a boundary, else 8, else the aligned dwords of each row with single elements at its ends (lanes on
+// consecutive addresses throughout; with eight single elements per lane 3332 x 7413 x 64 took 65 us).
+template <int FN, int ES>
+__device__ __forceinline__ void store_region(const uint8_t* reg, int lane, uint8_t* y, int64_t ldy, int m0, int n0,
+                                             int M, int N) {
+  constexpr int RSB = FN * 32 * ES, CPR = RSB / 16;
+  const uint64_t mis = reinterpret_cast<uintptr_t>(y) | ((uint64_t)ldy * ES);
+  auto at = [&](int r, int byte) { return reg + r * RSB + 16 * ((byte / 16 + (r >> 1)) % CPR) + byte % 16; };
+  if ((mis & 15) == 0) {
+#pragma unroll
+    for (int it = 0; it < CPR / 2; ++it) {
+      const int c = it * 64 + lane, r = c / CPR, b = 16 * (c % CPR);
+      const int m = m0 + r, n = n0 + b / ES;
+      if (m >= M || n >= N) continue;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(r, b));
+      uint8_t* dst = y + ((size_t)m * ldy + n) * ES;
+      if (n + 16 / ES <= N) {
+        *reinterpret_cast<u32x4_t*>(dst) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16 / ES; ++e)
+          if (n + e < N) {
+            if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[e] = v[e];
+            else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+          }
+      }
+    }
+  } else if (ES == 2 && (mis & 7) == 0) {
+#pragma unroll 4
+    for (int it = 0; it < CPR; ++it) {
+      const int c = it * 64 + lane, r = c / (2 * CPR), b = 8 * (c % (2 * CPR));
+      const int m = m0 + r, n = n0 + b / 2;
+      if (m >= M || n >= N) continue;
+      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at(r, b));
+      uint8_t* dst = y + ((size_t)m * ldy + n) * ES;
+      if (n + 4 <= N) {
+        *reinterpret_cast<u32x2_t*>(dst) = v;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (n + e < N) reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+      }
+    }
+  } else {
+    constexpr int DPR = RSB / 4, LPR = DPR % 32 == 0 ? 32 : 16, RPI = 64 / LPR;  // dwords, lanes per row; rows at a time
+    const int r0 = lane / LPR, d0 = lane % LPR, cols = min(FN * 32, N - n0);
+    uint8_t* row = y + ((size_t)(m0 + r0) * ldy + n0) * ES;
+    const size_t step = (size_t)RPI * ldy * ES;
+#pragma unroll
+    for (int it = 0; it < 32 / RPI; ++it, row += step) {
+      const int r = it * RPI + r0;
+      if (m0 + r >= M) continue;
+      if constexpr (ES == 4) {
+#pragma unroll
+        for (int d = d0; d < DPR; d += LPR)
+          if (d < cols) reinterpret_cast<uint32_t*>(row)[d] = *reinterpret_cast<const uint32_t*>(at(r, 4 * d));
+      } else {
+        // elements e and e + 1 share an aligned dword of y; a row that starts inside one leaves its first
+        // element to the first lane
+        uint16_t* out = reinterpret_cast<uint16_t*>(row);
+        const int sh = (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1);
+        if (sh && d0 == 0 && cols > 0) out[0] = *reinterpret_cast<const uint16_t*>(at(r, 0));
+#pragma unroll
+        for (int d = d0; d < DPR; d += LPR) {
+          const int e = 2 * d + sh;
+          if (e + 1 < cols) {
+            const uint32_t lo = *reinterpret_cast<const uint16_t*>(at(r, 2 * e));
+            const uint32_t hi = *reinterpret_cast<const uint16_t*>(at(r, 2 * e + 2));
+            *reinterpret_cast<uint32_t*>(out + e) = lo | (hi << 16);
+          } else if (e < cols) {
+            out[e] = *reinterpret_cast<const uint16_t*>(at(r, 2 * e));
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int YT>
 __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
@@ -254,7 +334,6 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
   constexpr int CPR = RSB / 16;       // 16-byte chunks per region row
   uint8_t* reg = lds + wave * T::REGION;
   const int mb = m0 + wm * FM * 32, nb = n0 + wn * FN * 32;
-  const bool vec = ((reinterpret_cast<uintptr_t>(y) | ((uint64_t)ldy * ES)) & 15) == 0;
   const bool has_bias = bias != nullptr;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -284,27 +363,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
         }
       }
     wave_lds_sync();
-    constexpr int EPC = 16 / ES;  // elements per chunk
-#pragma unroll
-    for (int it = 0; it < CPR / 2; ++it) {
-      const int c = it * 64 + lane, r = c / CPR, ch = c % CPR;
-      const uint8_t* src = reg + r * RSB + 16 * ((ch + (r >> 1)) % CPR);
-      const int m = mb + i * 32 + r, n = nb + EPC * ch;
-      if (m < M && n < N) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(src);
-        uint8_t* dst = static_cast<uint8_t*>(y) + ((size_t)m * ldy + n) * ES;
-        if (vec && n + EPC <= N) {
-          *reinterpret_cast<u32x4_t*>(dst) = v;
-        } else {
-#pragma unroll
-          for (int e = 0; e < EPC; ++e)
-            if (n + e < N) {
-              if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[e] = v[e];
-              else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-            }
-        }
-      }
-    }
+    store_region<FN, ES>(reg, lane, static_cast<uint8_t*>(y), ldy, mb + i * 32, nb, M, N);
     wave_lds_sync();  // the region is rewritten by the next fragment row
   }
 }
