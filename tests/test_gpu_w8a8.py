@@ -194,7 +194,7 @@ def test_gemm_shapes(w4, shape):
 
 
 @pytest.mark.parametrize("tile", ["skinny", "32", "64x32", "64", "64x128k2", "64x128", "128", "128x256", "256x192", "256"])
-@pytest.mark.parametrize("shape", [(1, 16, 16), (16, 48, 128), (32, 65, 144), (32, 8200, 272), (64, 260, 2064)])
+@pytest.mark.parametrize("shape", [(1, 16, 16), (16, 48, 128), (16, 4111, 400), (32, 65, 144), (32, 4130, 272), (32, 8200, 272), (64, 260, 2064)])
 @pytest.mark.parametrize("ydtype", DTYPES)
 def test_gemm_every_kernel(w4, hooks, tile, shape, ydtype):
     """Every kernel at sizes smaller than its tile, at odd sizes, and with K ending inside a K-step."""
@@ -274,7 +274,8 @@ def test_linear_one_token(w4, hooks, K, xd):
     import torch
     rng = np.random.default_rng(K)
     for N, block, yd, special in ((1, 0, "bf16", 0), (37, 16, "f32", 0), (96, 128 if K % 128 == 0 else 0, "f16", 0),
-                                  (40, 0, "f32", 1), (40, 16, "f32", 2)):
+                                  (40, 0, "f32", 1), (40, 16, "f32", 2),
+                                  (4127, 0, "bf16", 0)):
         x, lam = rows(rng, 1, K, xd), factors(rng, K)
         if special:
             xf = oh.to_f32(x, xd).copy()

@@ -369,18 +369,18 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
 }
 
 // ---- small batches: weight streaming ---------------------------------------------------------------
-// A workgroup owns 32 weight rows and up to 16 MB activation rows; its KW waves split K: wave w takes
+// A workgroup owns 16 NB weight rows and up to 16 MB activation rows; its KW waves split K: wave w takes
 // the 128-column K-steps w, w + KW, ..., each through an LDS ring of its own, S - 1 K-steps ahead by
 // direct loads of whole 128-byte lines.  Nothing in the loop is shared, so it has no barrier: a wave
 // waits for its own loads only.  v_mfma_i32_16x16x64_i8 (row l % 16, columns 16 (l / 16) ..) keeps the
 // activation side at 16 rows; the int32 partial sums of the waves meet in LDS.
-template <int MB, int KW, int S>
+template <int MB, int NB, int KW, int S>
 struct SkinnyI8 {
-  static constexpr int ROWS = 16 * MB + 32;  // activation rows, then weight rows
+  static constexpr int ROWS = 16 * (MB + NB);  // activation rows, then weight rows
   static constexpr int STAGE = ROWS * 128;
   static constexpr int LOADS = ROWS / 8;
   static constexpr int RING = KW * S * STAGE;
-  static constexpr int PART = KW * MB * 16 * 32 * 4;
+  static constexpr int PART = KW * MB * NB * 256 * 4;
   static constexpr int LDS = RING > PART ? RING : PART;
   static_assert(LDS <= 160 * 1024 && LOADS * (S - 1) < 64, "LDS of one CU, vmcnt range");
 };
@@ -397,27 +397,27 @@ __device__ __forceinline__ void skinny_issue(uint8_t* stage, uint32_t k0, uint32
   }
 }
 
-template <int MB>
-__device__ __forceinline__ void skinny_mma(i32x4_t (&acc)[MB][2], const i32x4_t (&a)[2][MB], const i32x4_t (&w)[2][2]) {
+template <int MB, int NB>
+__device__ __forceinline__ void skinny_mma(i32x4_t (&acc)[MB][NB], const i32x4_t (&a)[2][MB], const i32x4_t (&w)[2][NB]) {
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
     for (int i = 0; i < MB; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s][i], acc[i][j], 0, 0, 0);
+      for (int j = 0; j < NB; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s][i], acc[i][j], 0, 0, 0);
 }
 
-template <int MB, int KW, int S, int YT>
+template <int MB, int NB, int KW, int S, int YT>
 __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
     int64_t ldy) {
-  using T = SkinnyI8<MB, KW, S>;
+  using T = SkinnyI8<MB, NB, KW, S>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 32;
+  const int n0 = blockIdx.x * (16 * NB);
   const uint8_t* wbase = qw + (size_t)n0 * K;
   uint8_t* ring = lds + wave * S * T::STAGE;
   uint32_t off[T::LOADS], col[T::LOADS];
@@ -430,11 +430,11 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
   }
   const int nkt = (K + 127) / 128;
   const int steps = (nkt - wave + KW - 1) / KW;  // of this wave
-  i32x4_t acc[MB][2];
+  i32x4_t acc[MB][NB];
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
+    for (int j = 0; j < NB; ++j) acc[i][j] = i32x4_t{0, 0, 0, 0};
   if (steps > 0) {
     auto k_of = [&](int i) { return 128u * (uint32_t)(wave + KW * min(i, steps - 1)); };
 #pragma unroll
@@ -447,16 +447,16 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
       skinny_issue<T, MB>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, k_of(i + S - 1), (uint32_t)K, qa, wbase, off,
                           col);
       const uint8_t* cur = ring + slot * T::STAGE;
-      i32x4_t a[2][MB], w[2][2];
+      i32x4_t a[2][MB], w[2][NB];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int c = 16 * ((4 * s + g) ^ i8_swizzle(l16));
 #pragma unroll
-        for (int j = 0; j < 2; ++j) w[s][j] = *reinterpret_cast<const i32x4_t*>(cur + (16 * MB + 16 * j + l16) * 128 + c);
+        for (int j = 0; j < NB; ++j) w[s][j] = *reinterpret_cast<const i32x4_t*>(cur + (16 * MB + 16 * j + l16) * 128 + c);
 #pragma unroll
         for (int m = 0; m < MB; ++m) a[s][m] = *reinterpret_cast<const i32x4_t*>(cur + (16 * m + l16) * 128 + c);
       }
-      skinny_mma<MB>(acc, a, w);
+      skinny_mma<MB, NB>(acc, a, w);
       slot = slot == S - 1 ? 0 : slot + 1;
     }
   }
@@ -467,15 +467,15 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
 #pragma unroll
   for (int i = 0; i < MB; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<i32x4_t*>(part + ((wave * MB * 16 + 16 * i + l16) * 32 + 16 * j + 4 * g)) = acc[i][j];
+    for (int j = 0; j < NB; ++j)
+      *reinterpret_cast<i32x4_t*>(part + ((wave * MB * 16 + 16 * i + l16) * 16 * NB + 16 * j + 4 * g)) = acc[i][j];
   __syncthreads();
-  for (int o = t; o < MB * 512; o += 64 * KW) {
-    const int m = o >> 5, n = n0 + (o & 31);
+  for (int o = t; o < MB * NB * 256; o += 64 * KW) {
+    const int m = o / (16 * NB), n = n0 + o % (16 * NB);
     if (m >= M || n >= N) continue;
     int sum = 0;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) sum += part[w * MB * 512 + o];
+    for (int w = 0; w < KW; ++w) sum += part[w * MB * NB * 256 + o];
     float v = ((float)sum * sa[m]) * sw[n];
     if (bias != nullptr) v += bf16_bits_to_f32(bias[n]);
     store_one<YT>(y, (size_t)m * ldy + n, v);
@@ -483,13 +483,13 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
 }
 
 // ---- one token: quantizer and weight streaming in one launch ---------------------------------------
-// Each workgroup (4 waves, 32 channels) starts its weight rings, quantizes the token itself (it is in L2,
+// Each workgroup (KW waves, 16 NB channels) starts its weight rings, quantizes the token itself (it is in L2,
 // and its arithmetic hides behind the first weights' way from HBM) into codes in LDS, and goes on as the
 // streaming kernel above with the activation operand read from there.  Every workgroup repeats the
 // quantizer's work; what is saved is a launch and the wait between the two (2048 x 6144: 7.4 to 6.1 us,
 // 5120 x 13824: 15.9 to 15.0, and 3 us of the host's time; with two tokens 5120 x 13824 takes 17.2 us
 // this way and 16.2 in two launches).  The codes are those of the quantizer kernel bit for bit.
-constexpr int TK_WAVES = 4, TK_S = 3;
+constexpr int TK_S = 3;
 
 struct TokenArgs {
   const void* x;
@@ -503,60 +503,63 @@ struct TokenArgs {
   void* y;
 };
 
+template <int NB>
 __device__ __forceinline__ void token_issue(uint8_t* stage, uint32_t k0, uint32_t K, const uint8_t* wbase,
                                             const uint32_t* off, const uint32_t* col) {
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < 2 * NB; ++r) {
     const uint8_t* p = wbase + (k0 + off[r]);
     if (k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
     load_lds16(p, stage + r * 1024);
   }
 }
 
-__device__ __forceinline__ void token_mma(i32x4_t (&acc)[2], const i32x4_t (&a)[2], const i32x4_t (&w)[2][2]) {
+template <int NB>
+__device__ __forceinline__ void token_mma(i32x4_t (&acc)[NB], const i32x4_t (&a)[2], const i32x4_t (&w)[2][NB]) {
 #pragma unroll
   for (int s = 0; s < 2; ++s)
 #pragma unroll
-    for (int j = 0; j < 2; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s], acc[j], 0, 0, 0);
+    for (int j = 0; j < NB; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s], acc[j], 0, 0, 0);
 }
 
-// C: chunks of 8 columns per thread, 2048 C >= K.
-template <int DT, bool ROT, int C>
-__global__ __launch_bounds__(64 * TK_WAVES) void linear_i8_token_kernel(const TokenArgs p) {
+// C: chunks of 8 columns per thread, 512 KW C >= K.
+template <int DT, bool ROT, int C, int NB, int KW>
+__global__ __launch_bounds__(64 * KW) void linear_i8_token_kernel(const TokenArgs p) {
+  constexpr int STAGE = 2048 * NB, COLS = 512 * KW;  // bytes of a K-step's weight rows; columns of one chunk each
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  __shared__ uint32_t red[TK_WAVES];
+  __shared__ uint32_t red[KW];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int l16 = lane & 15, g = lane >> 4;
-  const int n0 = blockIdx.x * 32, N = p.N, K = p.K;
+  const int n0 = blockIdx.x * (16 * NB), N = p.N, K = p.K;
   const uint8_t* wbase = p.qw + (size_t)n0 * K;
-  uint8_t* ring = dyn + wave * TK_S * 4096;
-  uint8_t* codes = dyn + TK_WAVES * TK_S * 4096;
-  uint32_t off[4], col[4];
+  uint8_t* ring = dyn + wave * TK_S * STAGE;
+  uint8_t* codes = dyn + KW * TK_S * STAGE;
+  uint32_t off[2 * NB], col[2 * NB];
 #pragma unroll
-  for (int r = 0; r < 4; ++r) {
+  for (int r = 0; r < 2 * NB; ++r) {
     const int row = 8 * r + (lane >> 3);
     col[r] = 16u * (uint32_t)((lane & 7) ^ i8_swizzle(row));
     off[r] = (uint32_t)min(row, N - 1 - n0) * (uint32_t)K + col[r];
   }
-  const int nkt = (K + 127) / 128, steps = (nkt - wave + TK_WAVES - 1) / TK_WAVES;
-  auto k_of = [&](int i) { return 128u * (uint32_t)(wave + TK_WAVES * min(i, steps - 1)); };
+  const int nkt = (K + 127) / 128, steps = (nkt - wave + KW - 1) / KW;
+  auto k_of = [&](int i) { return 128u * (uint32_t)(wave + KW * min(i, steps - 1)); };
   if (steps > 0) {
 #pragma unroll
-    for (int i = 0; i < TK_S - 1; ++i) token_issue(ring + i * 4096, k_of(i), (uint32_t)K, wbase, off, col);
+    for (int i = 0; i < TK_S - 1; ++i) token_issue<NB>(ring + i * STAGE, k_of(i), (uint32_t)K, wbase, off, col);
   }
 
   const int tc = 8 * (ROT ? chunk_of(t) : t);
   float v[C][8];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int k = 2048 * c + tc;
+    const int k = COLS * c + tc;
     widen8<DT>(k < K ? load_raw<DT>(p.x, k) : zero_raw<DT>(), v[c]);
   }
   if (p.lam != nullptr) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
-      const int k = 2048 * c + tc;
+      const int k = COLS * c + tc;
       float l[8], rh[8], rl[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) l[i] = 1.0f;
@@ -575,11 +578,13 @@ __global__ __launch_bounds__(64 * TK_WAVES) void linear_i8_token_kernel(const To
   if (lane == 0) red[wave] = mw;
   // (LDS only: the weights in flight are not waited for)
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  const uint32_t bits = max(max(red[0], red[1]), max(red[2], red[3]));
+  uint32_t bits = 0;
+#pragma unroll
+  for (int w = 0; w < KW; ++w) bits = max(bits, red[w]);
   const float inv = row_inv(bits, p.norm) * (ROT ? lane_sign(lane, p.block) : 1.0f);
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int k = 2048 * c + tc;
+    const int k = COLS * c + tc;
     if (k < K) *reinterpret_cast<u32x2_t*>(codes + k) = codes8(v[c], inv);
   }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
@@ -587,23 +592,25 @@ __global__ __launch_bounds__(64 * TK_WAVES) void linear_i8_token_kernel(const To
   // all 16 activation rows of the instruction are the token (one column of the product is stored); columns
   // past K, up to the K-step's end, meet zero weights
   const uint8_t* arow = codes + 16 * g;
-  i32x4_t acc[2] = {i32x4_t{0, 0, 0, 0}, i32x4_t{0, 0, 0, 0}};
+  i32x4_t acc[NB];
+#pragma unroll
+  for (int j = 0; j < NB; ++j) acc[j] = i32x4_t{0, 0, 0, 0};
   if (steps > 0) {
     int slot = 0;
     for (int i = 0; i < steps; ++i) {
-      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((TK_S - 2) * 4) : "memory");
-      token_issue(ring + (slot == 0 ? TK_S - 1 : slot - 1) * 4096, k_of(i + TK_S - 1), (uint32_t)K, wbase, off, col);
-      const uint8_t* cur = ring + slot * 4096;
+      asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"((TK_S - 2) * 2 * NB) : "memory");
+      token_issue<NB>(ring + (slot == 0 ? TK_S - 1 : slot - 1) * STAGE, k_of(i + TK_S - 1), (uint32_t)K, wbase, off, col);
+      const uint8_t* cur = ring + slot * STAGE;
       const uint8_t* ac = arow + k_of(i);
-      i32x4_t a[2], w[2][2];
+      i32x4_t a[2], w[2][NB];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
         const int c = 16 * ((4 * s + g) ^ i8_swizzle(l16));
         a[s] = *reinterpret_cast<const i32x4_t*>(ac + 64 * s);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) w[s][j] = *reinterpret_cast<const i32x4_t*>(cur + (16 * j + l16) * 128 + c);
+        for (int j = 0; j < NB; ++j) w[s][j] = *reinterpret_cast<const i32x4_t*>(cur + (16 * j + l16) * 128 + c);
       }
-      token_mma(acc, a, w);
+      token_mma<NB>(acc, a, w);
       slot = slot == TK_S - 1 ? 0 : slot + 1;
     }
   }
@@ -611,12 +618,14 @@ __global__ __launch_bounds__(64 * TK_WAVES) void linear_i8_token_kernel(const To
   __syncthreads();  // every wave has left its ring
   int* part = reinterpret_cast<int*>(dyn);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
-    if (l16 == 0) *reinterpret_cast<i32x4_t*>(part + wave * 32 + 16 * j + 4 * g) = acc[j];
+  for (int j = 0; j < NB; ++j)
+    if (l16 == 0) *reinterpret_cast<i32x4_t*>(part + wave * 16 * NB + 16 * j + 4 * g) = acc[j];
   __syncthreads();
   const int n = n0 + t;
-  if (t < 32 && n < N) {
-    const int sum = part[t] + part[32 + t] + part[64 + t] + part[96 + t];
+  if (t < 16 * NB && n < N) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < KW; ++w) sum += part[w * 16 * NB + t];
     float f = ((float)sum * row_scale(bits, p.norm)) * p.sw[n];
     if (p.bias != nullptr) f += bf16_bits_to_f32(p.bias[n]);
     if (p.ydtype == 2) store_one<2>(p.y, n, f);
@@ -625,13 +634,18 @@ __global__ __launch_bounds__(64 * TK_WAVES) void linear_i8_token_kernel(const To
   }
 }
 
+template <int DT, bool ROT, int C, int NB, int KW>
+hipError_t run_token_c(const TokenArgs& a, hipStream_t stream) {
+  const size_t lds = KW * TK_S * 2048 * NB + (size_t)(a.K + 127) / 128 * 128;
+  linear_i8_token_kernel<DT, ROT, C, NB, KW><<<dim3((unsigned)((a.N + 16 * NB - 1) / (16 * NB))), 64 * KW, lds, stream>>>(a);
+  return hipGetLastError();
+}
+
 template <int DT, bool ROT>
 hipError_t run_token(const TokenArgs& a, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.N + 31) / 32)), block(64 * TK_WAVES);
-  const size_t lds = TK_WAVES * TK_S * 4096 + (size_t)(a.K + 127) / 128 * 128;
-  if (a.K <= 4096) linear_i8_token_kernel<DT, ROT, 2><<<grid, block, lds, stream>>>(a);
-  else linear_i8_token_kernel<DT, ROT, 4><<<grid, block, lds, stream>>>(a);
-  return hipGetLastError();
+  // (the split of the streaming kernel: see run)
+  if (a.N <= 4096) return a.K <= 4096 ? run_token_c<DT, ROT, 1, 1, 8>(a, stream) : run_token_c<DT, ROT, 2, 1, 8>(a, stream);
+  return a.K <= 4096 ? run_token_c<DT, ROT, 2, 2, 4>(a, stream) : run_token_c<DT, ROT, 4, 2, 4>(a, stream);
 }
 
 struct GArgs {
@@ -655,9 +669,9 @@ hipError_t run_tile(const GArgs& a) {
   return hipGetLastError();
 }
 
-template <int MB, int KW, int S, int YT>
+template <int MB, int NB, int KW, int S, int YT>
 hipError_t run_skinny(const GArgs& a) {
-  gemm_i8_skinny_kernel<MB, KW, S, YT><<<dim3((unsigned)((a.N + 31) / 32)), 64 * KW, 0, a.stream>>>(
+  gemm_i8_skinny_kernel<MB, NB, KW, S, YT><<<dim3((unsigned)((a.N + 16 * NB - 1) / (16 * NB))), 64 * KW, 0, a.stream>>>(
       a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
   return hipGetLastError();
 }
@@ -670,9 +684,12 @@ hipError_t run(const GArgs& a) {
   // Up to 32 rows: stream the weights (16 x 13824 x 5120: 13.6 us, 5.2 TB/s; 64-row tiles 17.6).  From 17
   // rows on, past 256 workgroups, a ring of two K-steps lets two workgroups share a CU (32 x 13824 x
   // 5120: 15.0 us, 16.9 with three).
+  // Up to 4096 channels, 16 of them and 8 waves per workgroup still make at most one per CU (16 x 1024 x
+  // 8192: 5.9 us, 7.2 with 32 and 4; 16 x 6144 x 2048: 7.0 and 5.2).
   if (forced ? is("skinny") && a.M <= 32 : a.M <= 32) {
-    if (a.M <= 16) return run_skinny<1, 4, 3, YT>(a);
-    return a.N <= 8192 ? run_skinny<2, 4, 3, YT>(a) : run_skinny<2, 4, 2, YT>(a);
+    if (a.N <= 4096) return a.M <= 16 ? run_skinny<1, 1, 8, 3, YT>(a) : run_skinny<2, 1, 8, 3, YT>(a);
+    if (a.M <= 16) return run_skinny<1, 2, 4, 3, YT>(a);
+    return a.N <= 8192 ? run_skinny<2, 2, 4, 3, YT>(a) : run_skinny<2, 2, 4, 2, YT>(a);
   }
   // At most one tile per CU: the K loop's latency bounds the launch, so K is split over groups of waves
   // and the smallest tile that still leaves every CU at most one wins (128 x 2048 x 2048: 32 x 32 tiles
