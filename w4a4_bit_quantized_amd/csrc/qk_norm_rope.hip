@@ -307,7 +307,11 @@ hipError_t run(const RopeArgs& a, hipStream_t st) {
 
 template <int DT>
 hipError_t run_dt(RopeArgs a, bool vec, hipStream_t st) {
-  const int lanes = vec ? a.D / 8 : (a.D / 2 < 64 ? a.D / 2 : 64);
+  // Element-wise heads: 4 pairs per lane, or 2 of 2 items up to D = 128 where the lanes are still many
+  // (8000 tokens of 32 heads of 128, bf16: 53 us with 2, 60 with 4; 2071 tokens of 72 heads of 72, f16: 30 and
+  // 25; 16000 heads of 64, f32: 38 and 53; one pair per lane took 67, 39 and 39).
+  const bool two = !vec && a.D <= 128 && (a.D > 96 || DT == 2);
+  const int lanes = vec ? a.D / 8 : two ? (a.D / 2 + 1) / 2 : (a.D / 2 + 3) / 4;
   a.log2g = 0;
   while ((1 << a.log2g) < lanes) ++a.log2g;
   const int ng = RT >> a.log2g, heads = a.q.heads + a.k.heads;
@@ -320,7 +324,7 @@ hipError_t run_dt(RopeArgs a, bool vec, hipStream_t st) {
   const int full = heads > 0 ? 6 * ng / heads : 1;
   a.tb = full < 1 ? 1 : full > 8 ? 8 : full;
   if (per < a.tb) a.tb = (int)per;
-  if (!vec) return a.D <= 128 ? run<DT, 1, false, 1, 4>(a, st) : run<DT, 1, false, 4, 1>(a, st);
+  if (!vec) return two ? run<DT, 1, false, 2, 2>(a, st) : run<DT, 1, false, 4, 1>(a, st);
   return a.layout == 0 ? run<DT, 4, true, 1, 2>(a, st) : run<DT, 4, false, 1, 2>(a, st);
 }
 
