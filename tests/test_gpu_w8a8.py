@@ -383,3 +383,21 @@ def test_graph_replay_and_side_stream(w4):
             y = w4.w8a8_linear(x, layer, hadamard_block=16)
         torch.cuda.current_stream().wait_stream(s)
         assert torch.equal(y, ref)
+
+
+def test_layer_object(w4):
+    """W8A8Linear: quantized once from a weight, called with and without an output."""
+    import torch
+    from w4a4_bit_quantized_amd import checkpoint
+    rng = np.random.default_rng(21)
+    K, N = 256, 48
+    w, lam = rows(rng, N, K, "bf16", K ** -0.5), factors(rng, K)
+    b = oh.from_f32(rng.uniform(-1, 1, N).astype(np.float32), "bf16")
+    layer = checkpoint.W8A8Linear.from_weight(dev(w, "bf16"), dev(lam, "bf16"), dev(b, "bf16"), hadamard_block=32)
+    qw, sw = ow.quantize_weight(oh.to_f32(w, "bf16"), oh.to_f32(lam, "bf16"), 32)
+    x = rows(rng, 12, K, "bf16")
+    ref = ow.linear_f32(oh.to_f32(x, "bf16"), qw, sw, oh.to_f32(lam, "bf16"), oh.to_f32(b, "bf16"), 32)
+    same_bits(host(layer(dev(x, "bf16"))), oh.from_f32(ref, "bf16"))
+    out = torch.empty((12, N), dtype=torch.float32, device="cuda")
+    assert layer(dev(x, "bf16"), out=out) is out
+    same_bits(host(out), ref)

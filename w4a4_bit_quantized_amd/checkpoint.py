@@ -12,6 +12,8 @@ stay unconverted.
   ``smooth_factor (K,)``, ``wcscales (N,)``, ``wtscale (1,)`` bf16, K % 16 == 0, and an optional
   ``bias (N,)`` bf16.
 * ``W4A4Linear`` holds one converted layer on the GPU and calls ``svdq_linear``.
+* ``W8A8Linear`` holds one layer in 8 bits and calls ``w8a8_linear``: for an unconverted module whose
+  caller chooses 8 bits over its checkpoint precision (``from_weight`` quantizes it once).
 
 Nothing here computes: the layer itself is the C-ABI library.
 """
@@ -112,3 +114,50 @@ class W4A4Linear:
 
     def __call__(self, x, out=None):
         return self._binding.svdq_linear(x, self.tensors, self.hadamard_block, out=out)
+
+
+def check_layer_w8a8(tensors):
+    """Check one 8-bit layer's tensors: ``qweight (N, K)`` int8, ``wscales (N,)`` float32, and optionally
+    ``smooth_factor (K,)`` and ``bias (N,)`` bf16, K % 16 == 0.  Returns (N, K)."""
+    import torch
+    missing = [s for s in ("qweight", "wscales") if s not in tensors]
+    if missing:
+        raise ContractError(f"missing tensors: {missing}")
+    if tensors["qweight"].dim() != 2:
+        raise ContractError("qweight must be (N, K)")
+    N, K = _shape(tensors["qweight"])
+    if K % 16:
+        raise ContractError(f"K = {K} must be divisible by 16")
+    want = {"qweight": ((N, K), torch.int8), "wscales": ((N,), torch.float32),
+            "smooth_factor": ((K,), torch.bfloat16), "bias": ((N,), torch.bfloat16)}
+    for name, (shape, dtype) in want.items():
+        t = tensors.get(name)
+        if t is None:
+            continue
+        if _shape(t) != shape:
+            raise ContractError(f"{name} has shape {_shape(t)}, expected {shape}")
+        if t.dtype != dtype:
+            raise ContractError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    return N, K
+
+
+class W8A8Linear:
+    """One 8-bit linear layer on the GPU: y = w8a8_linear(x, tensors)."""
+
+    def __init__(self, tensors, hadamard_block=0):
+        from . import binding
+        self.N, self.K = check_layer_w8a8(tensors)
+        self.tensors = {k: tensors[k] for k in ("qweight", "wscales", "smooth_factor", "bias")
+                        if tensors.get(k) is not None}
+        self.hadamard_block = int(hadamard_block)
+        self._binding = binding
+
+    @classmethod
+    def from_weight(cls, weight, smooth_factor=None, bias=None, hadamard_block=0):
+        """Quantize a device weight (N, K) (bf16, f16 or f32) with w8a8_quantize_weight."""
+        from . import binding
+        qweight, wscales = binding.w8a8_quantize_weight(weight, smooth_factor, hadamard_block)
+        return cls(dict(qweight=qweight, wscales=wscales, smooth_factor=smooth_factor, bias=bias), hadamard_block)
+
+    def __call__(self, x, out=None, out_dtype=None):
+        return self._binding.w8a8_linear(x, self.tensors, self.hadamard_block, out=out, out_dtype=out_dtype)
