@@ -621,6 +621,9 @@ def _w8a8_rows(t, name):
     """(rows, K, row stride, dtype code, device) of a quantizer input."""
     dev = _device_tensor(t, name)
     code = _dtype_code(t.dtype, name)
+    shape = t.shape
+    if len(shape) == 2 and t.is_contiguous():
+        return shape[0], shape[1], shape[1], code, dev
     rows, K, ld = _rows_view(t, name)
     return rows, K, ld, code, dev
 
@@ -776,7 +779,8 @@ def _rope_side(x, view, out, weight, name, dtype, dev):
     if weight is not None:
         _dense(weight, f"{name}_weight", dtype, (d,), dev)
     if out is None:
-        out = _torch().empty(x.shape, dtype=dtype, device=dev)
+        torch = _torch()
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
         yts, yhs = h * d, d
     elif out is x:
         yts, yhs = ts, hs
