@@ -185,6 +185,34 @@ def test_special_values_stay_in_their_head(w4):
     assert torch.equal(y, clean)
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_elements_past_the_span_are_kept(w4, layout, dtype):
+    """Without the norm, elements past the rotary span leave bit for bit, infinities, NaNs and signed zeros
+    beside each other too; the rotated ones are not touched by them."""
+    import torch
+    rng = np.random.default_rng(11)
+    special = np.array([np.inf, 1.0, -0.0, -1.0, np.nan, 2.0, 0.0, -np.inf, 3.0, 1e-8], np.float32)
+    for D, dims in ((64, [8, 16]), (64, [6]), (66, [24, 8]), (128, [16, 2, 6]), (132, [2]), (16, [])):
+        rot = sum(dims)
+        xf = oh.to_f32(make(rng, 5, 3, D, dtype), dtype).copy()
+        xf[..., rot:] = np.resize(special, (5, 3, D - rot))
+        x = oh.from_f32(xf, dtype)
+        pos = rng.integers(0, 50, (5, len(dims)))
+        pt = torch.from_numpy(pos.astype(np.int32)).cuda() if dims else None
+        got = host(w4.qk_norm_rope(dev(x, dtype), None, pt, dims, layout=layout, norm=False))
+        past, want = got[..., rot:], np.ascontiguousarray(x[..., rot:])
+        nan = np.isnan(oh.to_f32(want, dtype))
+        assert (np.isnan(oh.to_f32(past, dtype)) == nan).all(), f"D={D} axes={dims}"
+        assert (np.ascontiguousarray(past).view(np.uint8).reshape(*past.shape, -1)[~nan]
+                == want.view(np.uint8).reshape(*want.shape, -1)[~nan]).all(), f"D={D} axes={dims}"
+        if rot:
+            zero = xf.copy()
+            zero[..., rot:] = 0
+            y = host(w4.qk_norm_rope(dev(oh.from_f32(zero, dtype), dtype), None, pt, dims, layout=layout, norm=False))
+            assert (got[..., :rot] == y[..., :rot]).all()
+
+
 def test_empty_and_refused_calls(w4):
     import torch
     q = torch.zeros((4, 2, 64), device="cuda")

@@ -275,13 +275,15 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
             cs[0] = cos_t[at];
             sn[0] = sin_t[at];
           }
-          // pairs of this chunk: (o[i0], o[i1]); a chunk past the span (not interleaved) has cos 1, sin 0
+          // pairs of this chunk: (o[i0], o[i1]).  Elements past the span are kept, not turned by an angle of 0:
+          // an infinity times the sine 0 would be a NaN in its neighbour.
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const int i0 = INTER ? 2 * i : i, i1 = INTER ? 2 * i + 1 : V + i;
+            const bool turn = (gl + c * G) * V + i < a.rot2;
             const float x0 = o[i0], x1 = o[i1];
-            o[i0] = fmaf(x0, cs[i], -(x1 * sn[i]));
-            o[i1] = fmaf(x0, sn[i], x1 * cs[i]);
+            o[i0] = turn ? fmaf(x0, cs[i], -(x1 * sn[i])) : x0;
+            o[i1] = turn ? fmaf(x0, sn[i], x1 * cs[i]) : x1;
           }
           if constexpr (INTER) {
             store_n<DT, 2 * V>(dst[u] + e0[c] * ES, o);
