@@ -313,6 +313,7 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
  *          aligned, ldx >= K, ldx % 8 == 0
  *   smooth_factor  bf16 [K], 16-byte aligned, or NULL for none
  *   K      >= 16, K % 16 == 0, at most W8A8_MAX_K (so that the int32 sum is exact)
+ *   M, N   at most W8A8_MAX_ROWS, M * N at most 2^37; strides of several rows at most 2^32
  *   hadamard_block  0 (none) or 16, 32, 64, 128 with K % hadamard_block == 0
  *   qact   s8 [M, K], 16-byte aligned      ascales f32 [M]
  *   qweight s8 [N, K], 16-byte aligned     wscales f32 [N]     (codes -128 .. 127)
@@ -328,6 +329,7 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
  * strides, a workspace too small), W4A4_ERR_NULL, W4A4_ERR_ALIGN; sizes are checked first, then
  * the empty call (M or N == 0), then pointers, then alignment. */
 #define W8A8_MAX_K 131056
+#define W8A8_MAX_ROWS (1 << 28)
 w4a4_status w8a8_quantize_act(const void* x, int64_t ldx, int32_t x_dtype, const void* smooth_factor, int64_t M,
                               int64_t K, int32_t hadamard_block, void* qact, float* ascales, void* stream);
 w4a4_status w8a8_quantize_weight(const void* w, int64_t ldw, int32_t w_dtype, const void* smooth_factor, int64_t N,
@@ -372,7 +374,8 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  *   dtype      W4A4_DTYPE_BF16, _F16 or _F32, of x, weight and y alike
  * Errors: W4A4_ERR_UNSUPPORTED (dtype, layout, flags, head_dim or axes above the maximum),
  * W4A4_ERR_SHAPE (sizes, a rotary span past head_dim, theta not positive and finite, eps negative,
- * negative strides, outputs whose elements share an address, in place with other strides),
+ * negative strides or more than 2^40, offsets past 2^60, outputs whose elements share an address, in
+ * place with other strides),
  * W4A4_ERR_NULL, W4A4_ERR_ALIGN (element size).  tokens == 0 or no heads launches nothing.
  * 16-byte aligned pointers and strides, and in the split layouts axes of multiples of 8 elements,
  * take the vectorised path. */

@@ -67,6 +67,29 @@ def test_linear_validation(lib):
     assert f(ws=P + 128) == ERR_ALIGN and f(x=P + 8) == ERR_ALIGN and f(b=P + 1) == ERR_ALIGN
 
 
+def test_sizes_that_pass_32_and_64_bits(lib):
+    """Row counts whose padded or strided successors pass 2^31, grids past 2^32 threads, and byte offsets past
+    2^63 are refused; one row may have any stride."""
+    rows = 1 << 28
+    q = lambda M, ld: lib.w8a8_quantize_act(P, ld, 0, None, M, 64, 0, P, P + 2, None)
+    assert q(rows, 64) == ERR_ALIGN and q(rows + 1, 64) == ERR_SHAPE and q((1 << 31) - 1, 64) == ERR_SHAPE
+    assert q(2, 1 << 32) == ERR_ALIGN and q(2, (1 << 32) + 8) == ERR_SHAPE and q(1, 1 << 60) == ERR_ALIGN
+    g = lambda M, N, ldy: lib.w8a8_gemm(P, P + 2, P, P, None, M, N, 16, P, ldy, 0, None)
+    assert g(rows, 512, 512) == ERR_ALIGN and g(rows, 513, 513) == ERR_SHAPE and g(rows + 1, 1, 1) == ERR_SHAPE
+    assert g(1, rows, rows) == ERR_ALIGN and g(1, rows + 1, rows + 1) == ERR_SHAPE and g(1 << 19, 1 << 19, 1 << 19) == ERR_SHAPE
+    assert g(2, 8, (1 << 32) + 1) == ERR_SHAPE and g(1, 8, 1 << 60) == ERR_ALIGN
+    f = lambda M, N, ldx, ldy: lib.w8a8_linear(P, ldx, 0, P, P + 2, None, None, M, N, 16, 0, P, ldy, 0, P, 1 << 40, None)
+    assert f(rows, 512, 16, 512) == ERR_ALIGN and f(rows, 513, 16, 513) == ERR_SHAPE and f(rows + 1, 1, 16, 1) == ERR_SHAPE
+    assert f(2, 8, (1 << 32) + 8, 8) == ERR_SHAPE and f(1, 8, 1 << 60, 8) == ERR_ALIGN
+    assert lib.w8a8_linear_workspace_bytes(rows, 16) > 0 and lib.w8a8_linear_workspace_bytes(rows + 1, 16) == 0
+    far = dict(T=(1 << 31) - 1, q=_heads(ts=1 << 29, w=P + 1, yts=512))
+    assert _rope(lib, **far) == ERR_ALIGN
+    far["q"].x_token_stride = 1 << 30
+    assert _rope(lib, **far) == ERR_SHAPE
+    assert _rope(lib, q=_heads(heads=1 << 15, hs=1 << 40, w=P + 1, yts=1 << 21)) == ERR_ALIGN
+    assert _rope(lib, T=(1 << 31) - 1, q=_heads(yts=1 << 40, w=P + 1)) == ERR_SHAPE
+
+
 def _heads(x=P, ts=512, hs=64, heads=8, w=None, y=P + 0x100000, yts=512, yhs=64):
     return binding.Heads(x, ts, hs, heads, w, y, yts, yhs)
 
@@ -120,7 +143,7 @@ def test_rope_strides(lib):
 
 def test_constants_match_header():
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "w4a4.h")).read()
-    for name, value in (("W8A8_MAX_K", binding.W8A8_MAX_K), ("W4A4_ROPE_MAX_HEAD_DIM", binding.ROPE_MAX_HEAD_DIM),
+    for name, value in (("W8A8_MAX_K", binding.W8A8_MAX_K), ("W8A8_MAX_ROWS", "(1 << 28)"), ("W4A4_ROPE_MAX_HEAD_DIM", binding.ROPE_MAX_HEAD_DIM),
                         ("W4A4_ROPE_MAX_AXES", binding.ROPE_MAX_AXES), ("W4A4_ROPE_NORM", binding.ROPE_NORM),
                         ("W4A4_ROPE_SHARED_FREQUENCIES", binding.ROPE_SHARED_FREQUENCIES),
                         ("W4A4_ROPE_POSITIONS_I64", binding.ROPE_POSITIONS_I64),

@@ -369,6 +369,15 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
 
 namespace {
 
+// Rows of a stride above this many elements are refused: the last row's byte offset, at most
+// 2^28 * 2^32 * 4, stays inside 64 bits.
+constexpr int64_t kMaxStride = (int64_t)1 << 32;
+// Output elements: the smallest tile of a launch of more than 256 has 128 x 256 of them, so a launch has
+// at most 2^22 + 2^21 + 2^20 workgroups of 512 threads, less than the 2^32 threads a grid may have.
+constexpr int64_t kMaxOutputs = (int64_t)1 << 37;
+
+bool far_rows(int64_t rows, int64_t ld) { return rows > 1 && ld > kMaxStride; }
+
 // Sizes, then types: shared by the quantizers, the GEMM and the layer.
 w4a4_status check_w8a8(int64_t K, int32_t hb, int32_t dtype) {
   if (hb != 0 && hb != 16 && hb != 32 && hb != 64 && hb != 128) return W4A4_ERR_UNSUPPORTED;
@@ -382,7 +391,7 @@ w4a4_status validate_quantize_w8a8(const void* x, int64_t ldx, int32_t x_dtype, 
                                    int64_t K, int32_t hb, const void* q, const void* scales) {
   w4a4_status st = check_w8a8(K, hb, x_dtype);
   if (st != W4A4_OK) return st;
-  if (rows < 0 || rows > kMaxDim || ldx < K || ldx % 8 != 0) return W4A4_ERR_SHAPE;
+  if (rows < 0 || rows > W8A8_MAX_ROWS || ldx < K || ldx % 8 != 0 || far_rows(rows, ldx)) return W4A4_ERR_SHAPE;
   if (rows == 0) return W4A4_OK;
   if (!x || !q || !scales) return W4A4_ERR_NULL;
   if (!aligned(x, 16) || !aligned(smooth_factor, 16) || !aligned(q, 16) || !aligned(scales, 4)) return W4A4_ERR_ALIGN;
@@ -399,14 +408,18 @@ w4a4_status quantize_w8a8(bool act, const void* x, int64_t ldx, int32_t x_dtype,
                                            static_cast<hipStream_t>(stream)));
 }
 
+w4a4_status check_outputs_w8a8(int64_t M, int64_t N, int64_t ldy) {
+  if (M < 0 || N < 0 || M > W8A8_MAX_ROWS || N > W8A8_MAX_ROWS || ldy < N || far_rows(M, ldy)) return W4A4_ERR_SHAPE;
+  return M * N > kMaxOutputs ? W4A4_ERR_SHAPE : W4A4_OK;
+}
+
 w4a4_status validate_gemm_w8a8(const void* qact, const void* ascales, const void* qweight, const void* wscales,
                                const void* bias, int64_t M, int64_t N, int64_t K, const void* y, int64_t ldy,
                                int32_t y_dtype) {
   w4a4_status st = check_w8a8(K, 0, y_dtype);
   if (st != W4A4_OK) return st;
-  if (M < 0 || N < 0 || M > kMaxDim || N > kMaxDim || ldy < N) return W4A4_ERR_SHAPE;
-  if (((M + 63) / 64) * ((N + 63) / 64) > kMaxDim) return W4A4_ERR_SHAPE;  // 1-D grid of output tiles
-  if (M == 0 || N == 0) return W4A4_OK;
+  st = check_outputs_w8a8(M, N, ldy);
+  if (st != W4A4_OK || M == 0 || N == 0) return st;
   if (!qact || !ascales || !qweight || !wscales || !y) return W4A4_ERR_NULL;
   if (!aligned(qact, 16) || !aligned(qweight, 16) || !aligned(ascales, 4) || !aligned(wscales, 4) ||
       !aligned(bias, 2) || !aligned(y, y_dtype == W4A4_DTYPE_F32 ? 4 : 2))
@@ -450,7 +463,7 @@ w4a4_status w8a8_gemm(const void* qact, const float* ascales, const void* qweigh
 }
 
 size_t w8a8_linear_workspace_bytes(int64_t M, int64_t K) {
-  if (M < 0 || M > kMaxDim || check_w8a8(K, 0, W4A4_DTYPE_BF16) != W4A4_OK) return 0;
+  if (M < 0 || M > W8A8_MAX_ROWS || check_w8a8(K, 0, W4A4_DTYPE_BF16) != W4A4_OK) return 0;
   return align256((size_t)M * (size_t)K) + align256((size_t)M * sizeof(float));
 }
 
@@ -461,9 +474,11 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
   // sizes and types of both halves first, then the empty call, the pointers, the alignments
   w4a4_status st = validate_quantize_w8a8(nullptr, ldx, x_dtype, nullptr, 0, K, hadamard_block, nullptr, nullptr);
   if (st != W4A4_OK) return st;
-  st = validate_gemm_w8a8(nullptr, nullptr, nullptr, nullptr, nullptr, M, 0, K, nullptr, ldy, y_dtype);
+  st = check_w8a8(K, 0, y_dtype);
   if (st != W4A4_OK) return st;
-  if (N < 0 || N > kMaxDim || ldy < N || ((M + 63) / 64) * ((N + 63) / 64) > kMaxDim) return W4A4_ERR_SHAPE;
+  st = check_outputs_w8a8(M, N, ldy);
+  if (st != W4A4_OK) return st;
+  if (far_rows(M, ldx)) return W4A4_ERR_SHAPE;
   if (M == 0 || N == 0) return W4A4_OK;
   if (!workspace) return W4A4_ERR_NULL;
   if (workspace_bytes < w8a8_linear_workspace_bytes(M, K)) return W4A4_ERR_SHAPE;
@@ -502,7 +517,11 @@ w4a4_status check_heads(const w4a4_heads& h, int64_t T, int64_t D) {
   const int64_t most = (int64_t)1 << 40;
   if (h.x_token_stride > most || h.x_head_stride > most || h.y_token_stride > most || h.y_head_stride > most)
     return W4A4_ERR_SHAPE;
-  // (T, heads <= 2^31, strides <= 2^40: the products below need 128 bits only where they are refused)
+  // (T, heads <= 2^31, strides <= 2^40: the products need 128 bits only where they are refused)
+  auto far = [&](int64_t ts, int64_t hs) {
+    return (__int128)(T - 1) * ts + (__int128)(h.heads - 1) * hs > (int64_t)1 << 60;
+  };
+  if (far(h.x_token_stride, h.x_head_stride) || far(h.y_token_stride, h.y_head_stride)) return W4A4_ERR_SHAPE;
   auto inside = [](int64_t n, int64_t s, int64_t width, int64_t outer, int64_t count) {
     return (n == 1 || s >= width) && (count == 1 || (__int128)outer >= (__int128)(n - 1) * s + width);
   };
