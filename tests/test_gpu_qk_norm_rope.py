@@ -213,6 +213,28 @@ def test_elements_past_the_span_are_kept(w4, layout, dtype):
             assert (got[..., :rot] == y[..., :rot]).all()
 
 
+def test_weights_that_do_not_count(w4):
+    """Through the C interface: the weight of a tensor without heads is not read (here its address is not one of
+    the type's), and without the norm no weight is applied."""
+    import ctypes
+    import torch
+    from w4a4_bit_quantized_amd import binding
+    lib = w4.load_library()
+    x = torch.randn(5, 2, 64, device="cuda")
+    w = torch.full((66,), 3.0, device="cuda")
+    pos = torch.arange(5, dtype=torch.int32, device="cuda")
+    dims = (ctypes.c_int32 * 1)(64)
+    for flags, weight in ((1, None), (0, w)):
+        y = torch.zeros_like(x)
+        none = binding.Heads(None, 0, 0, 0, w.data_ptr() + 1, None, 0, 0)
+        some = binding.Heads(x.data_ptr(), 128, 64, 2, None if weight is None else w.data_ptr(), y.data_ptr(), 128, 64)
+        st = lib.w4a4_qk_norm_rope(ctypes.byref(none), ctypes.byref(some), pos.data_ptr(), 5, 64, 1, dims, 0, flags,
+                                   1e4, 1e-6, 2, torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        want = w4.qk_norm_rope(x, None, pos, [64], norm=bool(flags))
+        assert torch.equal(y, want)
+
+
 def test_empty_and_refused_calls(w4):
     import torch
     q = torch.zeros((4, 2, 64), device="cuda")

@@ -534,8 +534,10 @@ w4a4_status check_heads(const w4a4_heads& h, int64_t T, int64_t D) {
   return W4A4_OK;
 }
 
-w4a4::RopeHeads rope_heads(const w4a4_heads& h) {
-  return {h.x, h.x_token_stride, h.x_head_stride, (int)h.heads, h.weight, h.y, h.y_token_stride, h.y_head_stride};
+// (the kernel reads a weight that is not null: only one that counts is passed on)
+w4a4::RopeHeads rope_heads(const w4a4_heads& h, bool norm) {
+  return {h.x, h.x_token_stride, h.x_head_stride, (int)h.heads, norm && h.heads > 0 ? h.weight : nullptr,
+          h.y, h.y_token_stride, h.y_head_stride};
 }
 
 }  // namespace
@@ -574,8 +576,8 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
   for (const w4a4_heads* h : {q, &kk})
     if (h->heads > 0 && (!aligned(h->x, es) || !aligned(h->y, es) || !aligned(h->weight, es))) return W4A4_ERR_ALIGN;
   if (rot > 0 && !aligned(positions, (flags & W4A4_ROPE_POSITIONS_I64) ? 8 : 4)) return W4A4_ERR_ALIGN;
-  a.q = rope_heads(*q);
-  a.k = rope_heads(kk);
+  a.q = rope_heads(*q, (flags & W4A4_ROPE_NORM) != 0);
+  a.k = rope_heads(kk, (flags & W4A4_ROPE_NORM) != 0);
   a.pos = positions;
   a.tokens = (int)tokens;
   a.D = head_dim;
