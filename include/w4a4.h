@@ -324,7 +324,10 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
  * row n, the same rotation and codes; qweight and wscales are the layer's checkpoint tensors.
  * w8a8_linear is w8a8_quantize_act into the workspace (at least w8a8_linear_workspace_bytes(M, K)
  * bytes, 256-byte aligned, contents overwritten), then w8a8_gemm; projections of one input may
- * share one w8a8_quantize_act instead.  Results do not depend on the batch a row is in.
+ * share one w8a8_quantize_act instead.  Results do not depend on the batch a row is in (only the
+ * quotients below 2^-110 of a smoothing factor outside [2^-32, 2^32] may round otherwise).
+ * Outputs and the workspace share no element with an input or with each other (y == x is
+ * refused); a call on another stream at the same time takes another workspace.
  * Errors: W4A4_ERR_UNSUPPORTED (hadamard_block, dtype, K > W8A8_MAX_K), W4A4_ERR_SHAPE (sizes,
  * strides, a workspace too small), W4A4_ERR_NULL, W4A4_ERR_ALIGN; sizes are checked first, then
  * the empty call (M or N == 0), then pointers, then alignment. */
@@ -353,9 +356,11 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  *   angle = positions[t, a] * theta^(-2 i / axis_dims[a])
  *   angle = positions[t, a] * theta^(-2 p / rot)         (with W4A4_ROPE_SHARED_FREQUENCIES)
  *   (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
- * Elements rot .. head_dim - 1 are normed only.  Angles are reduced in float64 (positions of any
- * size, negative ones too, lose nothing); the rest is float32 with one rounding to the tensors' type.
- * Squares that overflow float32 (|x| above about 2^63) give zeros.
+ * Elements rot .. head_dim - 1 are normed only.  Angles are formed and reduced in float64 (to
+ * within 6 * 2^-53 of the token's largest angle: from positions of about 2^28 on, this shows in
+ * float32; positions past 2^53 are rounded to float64 first); the rest is float32 with one rounding
+ * to the tensors' type.  Squares that overflow float32 (|x| above about 2^63) give zeros; with
+ * eps = 0, a head whose squares all underflow gives infinities, and one of zeros NaN.
  *
  * Elements (e0, e1) of pair p, number i of axis a whose first pair is s_a:
  *   W4A4_ROPE_INTERLEAVED  (2 p, 2 p + 1)
@@ -366,7 +371,8 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  * element (t, h, d) is at x + t x_token_stride + h x_head_stride + d, so partitions of a fused
  * projection's output and head-major outputs are addressed as they lie; q and k may have different
  * head counts.  x == y (with equal strides) works in place; any other overlap of an input and an
- * output is undefined.  Only the addressed elements are written.
+ * output, or of the two outputs, is undefined (q's y == k's y is refused).  Only the addressed
+ * elements are written.
  *   positions  [tokens, axes] int32 (int64 with W4A4_ROPE_POSITIONS_I64), dense; NULL when rot == 0
  *   axis_dims  HOST array of `axes` even sizes (0 allowed), sum at most head_dim; axes 0 ..
  *              W4A4_ROPE_MAX_AXES (0: norm only)

@@ -90,6 +90,15 @@ def test_sizes_that_pass_32_and_64_bits(lib):
     assert _rope(lib, T=(1 << 31) - 1, q=_heads(yts=1 << 40, w=P + 1)) == ERR_SHAPE
 
 
+def test_outputs_on_top_of_inputs(lib):
+    f = lambda M: lib.w8a8_linear(P, 64, 0, P, P, None, None, M, 64, 64, 0, P, 64, 0, P, 1 << 20, None)
+    assert f(4) == ERR_SHAPE and f(1) == ERR_SHAPE and f(0) == OK
+    side = lambda **kw: _heads(w=P + 1, **kw)
+    assert _rope(lib, q=side(), k=side()) == ERR_SHAPE                      # both outputs in one place
+    assert _rope(lib, q=side(x=P, y=P), k=side(x=P, y=P)) == ERR_SHAPE      # q and k the same tensor, in place
+    assert _rope(lib, q=side(), k=side(y=P + 0x200000)) == ERR_ALIGN        # the same input twice is fine
+
+
 def _heads(x=P, ts=512, hs=64, heads=8, w=None, y=P + 0x100000, yts=512, yhs=64):
     return binding.Heads(x, ts, hs, heads, w, y, yts, yhs)
 

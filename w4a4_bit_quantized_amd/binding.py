@@ -721,7 +721,7 @@ def w8a8_linear(x, layer, hadamard_block=0, workspace=None, out=None, out_dtype=
     ``layer`` maps qweight (N, K) int8 and wscales (N,) f32, and optionally smooth_factor (K,) bf16
     and bias (N,) bf16, to device tensors.  ``out_dtype`` defaults to x's.  ``workspace`` (u8, at
     least w8a8_linear_workspace_bytes bytes) and ``out`` may be passed to avoid allocation; without
-    them they come from torch's allocator on the current stream."""
+    them they come from torch's allocator on the current stream.  ``out`` shares no element with x."""
     torch = _torch()
     lib = load_library()
     M, K, ldx, code, dev = _w8a8_rows(x, "x")
@@ -801,7 +801,8 @@ def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1
     a rotates axis_dims[a] elements, further elements are only normed.  ``layout``: "interleaved"
     pairs (2p, 2p + 1), "half" (p, p + rot / 2), "axis_half" (halves of each axis's slice).
     ``shared_frequencies``: one ladder theta^(-2p / rot) over all pairs instead of one per axis.
-    norm=False only rotates.  Returns (q_out, k_out), or q_out when k is None; new contiguous tensors
+    norm=False only rotates.  q and k may be one tensor, but not ``inplace``: outputs share no element
+    with each other, or with an input that is not theirs.  Returns (q_out, k_out), or q_out when k is None; new contiguous tensors
     unless ``inplace`` or given."""
     torch = _torch()
     lib = load_library()

@@ -489,6 +489,8 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
   if (st != W4A4_OK) return st;
   st = validate_gemm_w8a8(ws, ascales, qweight, wscales, bias, M, N, K, y, ldy, y_dtype);
   if (st != W4A4_OK) return st;
+  // y would be written while other workgroups of a one-launch call still read x
+  if (x && x == y) return W4A4_ERR_SHAPE;
   if (w4a4::linear_i8_one_launch && w4a4::linear_i8_one_launch(M, K)) {
     (void)hipGetLastError();
     return from_hip(w4a4::launch_linear_i8_token(x, x_dtype, smooth_factor, hadamard_block,
@@ -569,6 +571,7 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
     if (st != W4A4_OK) return st;
   }
   if (tokens == 0 || q->heads + kk.heads == 0) return W4A4_OK;
+  if (q->heads > 0 && kk.heads > 0 && q->y && q->y == kk.y) return W4A4_ERR_SHAPE;
   if (rot > 0 && !positions) return W4A4_ERR_NULL;
   const uintptr_t es = dtype == W4A4_DTYPE_F32 ? 4 : 2;
   for (const w4a4_heads* h : {q, &kk})

@@ -7,8 +7,10 @@
 //         or  pos[t, a] * theta^(-2 p / rot)        (one ladder of frequencies over all pairs)
 //   (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
 // Elements past the rotary span are only normed.  float32 throughout, one rounding at the store.
-// The angle is formed in turns in float64 and reduced to half a turn there, so a position of any
-// size costs no accuracy: what is left, |r| <= 1/2, is rounded to float32 and passed to sincospi.
+// The angle is formed in turns in float64 and reduced to half a turn there: what is left, |r| <= 1/2, is
+// rounded to float32 and passed to sincospi.  The float64 part is off by at most 6 * 2^-53 of the
+// largest angle (i step and its exp2: 2.5 roundings of an exponent e, so 2.5 e 2^-53 theta^.. <=
+// 2.5 / 2.7 of the first pair's angle; the two products, 1 / (2 pi) and exp2 itself: 4).
 //
 // Bound: HBM (every element read and written once).  A group of G lanes (a power of two) holds one
 // head of one token, 2 V elements per lane: V pairs, so a rotation never leaves its lane and the only
