@@ -269,6 +269,31 @@ def test_empty_and_refused_calls(w4):
         w4.qk_norm_rope(torch.zeros((2, 8, 2, 64), device="cuda")[:, :2], None, p, [64])
 
 
+def test_one_tensor_as_q_and_k(w4):
+    """One input for both (with different weights), broadcast tokens and heads, on two streams at once."""
+    import torch
+    rng = np.random.default_rng(31)
+    T, H, D, dims = 40, 6, 96, [32, 64]
+    x, a, b = make(rng, T, H, D, "bf16"), weights(rng, D, "bf16"), weights(rng, D, "bf16")
+    pos = rng.integers(0, 500, (T, 2))
+    xt, pt = dev(x, "bf16"), torch.from_numpy(pos).cuda()
+    row, head = dev(x[:1], "bf16").expand(T, H, D), dev(x[:, :1], "bf16").expand(T, H, D)
+    torch.cuda.synchronize()
+    got = []
+    for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+        with torch.cuda.stream(s):
+            got.append((w4.qk_norm_rope(xt, xt, pt, dims, dev(a, "bf16"), dev(b, "bf16"), layout="half"),
+                        w4.qk_norm_rope(row, head, pt, dims, layout="axis_half")))
+    torch.cuda.synchronize()
+    for (q, k), (r, h) in got:
+        check(q, x, pos, dims, "bf16", a, "half")
+        check(k, x, pos, dims, "bf16", b, "half")
+        check(r, np.repeat(x[:1], T, 0), pos, dims, "bf16", None, "axis_half")
+        check(h, np.repeat(x[:, :1], H, 1), pos, dims, "bf16", None, "axis_half")
+    with pytest.raises(w4.W4A4Error, match="ERR_SHAPE"):
+        w4.qk_norm_rope(xt, xt, pt, dims, inplace=True)
+
+
 def test_graph_replay(w4):
     import torch
     rng = np.random.default_rng(10)

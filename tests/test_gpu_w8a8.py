@@ -385,6 +385,48 @@ def test_graph_replay_and_side_stream(w4):
         assert torch.equal(y, ref)
 
 
+def test_two_streams_and_one_token_graph(w4):
+    """Calls on two streams at once, each with a workspace of its own, among them one-token calls; two captured
+    one-token calls replayed in turn with eager ones between; the same input for several layers."""
+    import torch
+    rng = np.random.default_rng(21)
+    K = 1040
+    x1, x2 = dev(rows(rng, 1, K, "bf16"), "bf16"), dev(rows(rng, 700, K, "bf16"), "bf16")
+    layers = []
+    for N in (328, 1037):
+        qw, sw = w4.w8a8_quantize_weight(dev(rows(rng, N, K, "bf16"), "bf16"))
+        layers.append(dict(qweight=qw, wscales=sw, smooth_factor=dev(factors(rng, K), "bf16")))
+    want = [[w4.w8a8_linear(x, l, hadamard_block=16) for l in layers] for x in (x1, x2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for turn in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                for l in layers:
+                    got[i].append([w4.w8a8_linear(x, l, hadamard_block=16) for x in (x1, x2)])
+    torch.cuda.synchronize()
+    for g in got:
+        for j, ys in enumerate(g):
+            for y, w in zip(ys, (want[0][j % 2], want[1][j % 2])):
+                assert torch.equal(y, w)
+    ws = torch.empty(w4.w8a8_linear_workspace_bytes(1, K), dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.empty_like(w) for w in want[0]], []
+    for l, o in zip(layers, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            w4.w8a8_linear(x1, l, hadamard_block=16, workspace=ws, out=o)
+        graphs.append(g)
+    for _ in range(4):
+        x1.copy_(dev(rows(rng, 1, K, "bf16"), "bf16"))
+        ref = [w4.w8a8_linear(x1, l, hadamard_block=16) for l in layers]
+        for g, o in zip(graphs, outs):
+            o.zero_()
+            g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(outs, ref))
+
+
 def test_layer_object(w4):
     """W8A8Linear: quantized once from a weight, called with and without an output."""
     import torch
