@@ -142,11 +142,23 @@ __device__ __forceinline__ void pair_elements(const RopeArgs& a, int p, int& e0,
   }
 }
 
+// Bytes between the LDS rows of the staged form (below): a head of 16-bit elements, and 16 more so that the
+// lane groups of a wave start on different banks.
+__host__ __device__ constexpr int row_stride(int D) { return 2 * D + 16; }
+
 // INTER (V = 4): the lane's V pairs are 2 V consecutive elements; otherwise V consecutive elements at
 // e0 and V at e1.  IT: chunks of V pairs per lane; UN: items in flight.
-template <int DT, int V, bool INTER, int IT, int UN>
+//
+// STAGED (V = 1, IT = 4, UN = 1, 16-bit types): for heads on 16-byte boundaries whose pairs are not.  A lane
+// group loads its head in 16-byte chunks into a row of its own in LDS, takes its pairs from there, puts the
+// results in their places and stores the row in chunks again; no other wave touches the row.
+// 32760 tokens of 48 heads of 128, halves of axes of 44, 42 and 42: 178 us, element by element 283 (two items
+// in flight: 206, four: 219).  With 4-byte chunks, for heads of 66 on 4-byte boundaries, it loses: 57 against 52.
+template <int DT, int V, bool INTER, int IT, int UN, bool STAGED>
 __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
-  extern __shared__ __attribute__((aligned(16))) float trig[];  // two halves of [tb][D / 2] cosines, then sines
+  static_assert(!STAGED || (DT != 2 && V == 1 && IT == 4 && UN == 1 && !INTER), "the staged form");
+  // two halves of [tb][D / 2] cosines, then sines; then (STAGED) a row for every lane group
+  extern __shared__ __attribute__((aligned(16))) float trig[];
   const int t = threadIdx.x;
   const int D2 = a.D / 2, G = 1 << a.log2g;
   const int heads = a.q.heads + a.k.heads;
@@ -191,6 +203,8 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
       weights(a.k.weight, wk[c]);
     }
   }
+  uint8_t* row = reinterpret_cast<uint8_t*>(trig + 2 * a.tb * a.D) + grp * row_stride(a.D);
+  const bool has_chunk = 8 * gl < a.D;
   int half = 0;
   for (int64_t t0 = (int64_t)blockIdx.x * a.tb; t0 < a.tokens; t0 += (int64_t)gridDim.x * a.tb, half ^= 1) {
     const int nt = (int)min((int64_t)a.tb, a.tokens - t0);
@@ -231,6 +245,11 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
                              (tt * (isq ? a.q.ts : a.k.ts) + hh * (isq ? a.q.hs : a.k.hs)) * ES;
         dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
                  (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
+        if constexpr (STAGED) {
+          if (valid && has_chunk) *reinterpret_cast<u32x4_t*>(row + 16 * gl) = *reinterpret_cast<const u32x4_t*>(src + 16 * gl);
+          wave_lds_sync();
+          src = row;
+        }
 #pragma unroll
         for (int c = 0; c < IT; ++c) {
 #pragma unroll
@@ -290,31 +309,39 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
           if constexpr (INTER) {
             store_n<DT, 2 * V>(dst[u] + e0[c] * ES, o);
           } else {
-            store_n<DT, V>(dst[u] + e0[c] * ES, o);
-            store_n<DT, V>(dst[u] + e1[c] * ES, o + V);
+            uint8_t* to = STAGED ? row : dst[u];
+            store_n<DT, V>(to + e0[c] * ES, o);
+            store_n<DT, V>(to + e1[c] * ES, o + V);
           }
+        }
+        if constexpr (STAGED) {
+          wave_lds_sync();
+          if (has_chunk)
+            __builtin_nontemporal_store(*reinterpret_cast<const u32x4_t*>(row + 16 * gl),
+                                        reinterpret_cast<u32x4_t*>(dst[u] + 16 * gl));
+          wave_lds_sync();  // the row is written again
         }
       }
     }
   }
 }
 
-template <int DT, int V, bool INTER, int IT, int UN>
+template <int DT, int V, bool INTER, int IT, int UN, bool STAGED>
 hipError_t run(const RopeArgs& a, hipStream_t st) {
   const int heads = a.q.heads + a.k.heads;
   const int64_t blocks = ((int64_t)a.tokens + a.tb - 1) / a.tb;
   const dim3 grid((unsigned)(blocks < MAX_WGS ? blocks : MAX_WGS), (unsigned)((heads + a.hb - 1) / a.hb));
-  const size_t lds = 2 * (size_t)a.tb * a.D * sizeof(float);
-  qk_norm_rope_kernel<DT, V, INTER, IT, UN><<<grid, RT, lds, st>>>(a);
+  const size_t lds = 2 * (size_t)a.tb * a.D * sizeof(float) + (STAGED ? (size_t)(RT >> a.log2g) * row_stride(a.D) : 0);
+  qk_norm_rope_kernel<DT, V, INTER, IT, UN, STAGED><<<grid, RT, lds, st>>>(a);
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t run_dt(RopeArgs a, bool vec, hipStream_t st) {
+hipError_t run_dt(RopeArgs a, bool vec, bool staged, hipStream_t st) {
   // Element-wise heads: 4 pairs per lane, or 2 of 2 items up to D = 128 where the lanes are still many
   // (8000 tokens of 32 heads of 128, bf16: 53 us with 2, 60 with 4; 2071 tokens of 72 heads of 72, f16: 30 and
   // 25; 16000 heads of 64, f32: 38 and 53; one pair per lane took 67, 39 and 39).
-  const bool two = !vec && a.D <= 128 && (a.D > 96 || DT == 2);
+  const bool two = !vec && !(staged && DT != 2) && a.D <= 128 && (a.D > 96 || DT == 2);
   const int lanes = vec ? a.D / 8 : two ? (a.D / 2 + 1) / 2 : (a.D / 2 + 3) / 4;
   a.log2g = 0;
   while ((1 << a.log2g) < lanes) ++a.log2g;
@@ -328,31 +355,35 @@ hipError_t run_dt(RopeArgs a, bool vec, hipStream_t st) {
   const int full = heads > 0 ? 6 * ng / heads : 1;
   a.tb = full < 1 ? 1 : full > 8 ? 8 : full;
   if (per < a.tb) a.tb = (int)per;
-  if (!vec) return two ? run<DT, 1, false, 2, 2>(a, st) : run<DT, 1, false, 4, 1>(a, st);
-  return a.layout == 0 ? run<DT, 4, true, 1, 2>(a, st) : run<DT, 4, false, 1, 2>(a, st);
+  if (vec) return a.layout == 0 ? run<DT, 4, true, 1, 2, false>(a, st) : run<DT, 4, false, 1, 2, false>(a, st);
+  if constexpr (DT != 2)
+    if (staged) return run<DT, 1, false, 4, 1, true>(a, st);
+  return two ? run<DT, 1, false, 2, 2, false>(a, st) : run<DT, 1, false, 4, 1, false>(a, st);
 }
 
-bool aligned16(const RopeHeads& h, int es) {
-  const uint64_t m = reinterpret_cast<uintptr_t>(h.x) | reinterpret_cast<uintptr_t>(h.y) |
-                     reinterpret_cast<uintptr_t>(h.weight) |
-                     ((uint64_t)(h.ts | h.hs | h.yts | h.yhs) * (uint64_t)es);
-  return h.heads == 0 || (m & 15) == 0;
+// The address bits of every element that a tensor's heads start at.
+uint64_t low_bits(const RopeHeads& h, int es) {
+  if (h.heads == 0) return 0;
+  return reinterpret_cast<uintptr_t>(h.x) | reinterpret_cast<uintptr_t>(h.y) |
+         ((uint64_t)(h.ts | h.hs | h.yts | h.yhs) * (uint64_t)es);
 }
 
 }  // namespace
 
 hipError_t launch_qk_norm_rope(RopeArgs a, int dtype, hipStream_t stream) {
   const int es = dtype == 2 ? 4 : 2;
-  // 4-pair vectors need whole 8-element chunks of the head, and in the split layouts whole chunks
-  // of 4 pairs in the span and in every slice
-  bool vec = a.D % 8 == 0 && aligned16(a.q, es) && aligned16(a.k, es);
+  // heads of whole 16-byte chunks on 16-byte boundaries; 4-pair vectors also need such weights, and in the
+  // split layouts whole chunks of 4 pairs in the span and in every slice
+  const bool chunks = a.D % 8 == 0 && ((low_bits(a.q, es) | low_bits(a.k, es)) & 15) == 0;
+  bool vec = chunks && ((reinterpret_cast<uintptr_t>(a.q.weight) | reinterpret_cast<uintptr_t>(a.k.weight)) & 15) == 0;
   if (a.layout == 1) vec = vec && a.rot2 % 4 == 0;
   if (a.layout == 2)
     for (int x = 0; x < a.axes; ++x) vec = vec && a.start[x + 1] % 4 == 0;
+  const bool staged = chunks && !vec;  // (16-bit types; one token of 40 heads: 5.1 us, element by element 4.6; 300 tokens: 6.6 and 7.2)
   switch (dtype) {
-    case 0: return run_dt<0>(a, vec, stream);
-    case 1: return run_dt<1>(a, vec, stream);
-    default: return run_dt<2>(a, vec, stream);
+    case 0: return run_dt<0>(a, vec, staged, stream);
+    case 1: return run_dt<1>(a, vec, staged, stream);
+    default: return run_dt<2>(a, vec, staged, stream);
   }
 }
 
