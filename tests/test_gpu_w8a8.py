@@ -193,7 +193,7 @@ def test_gemm_shapes(w4, shape):
     check_gemm(w4, M, N, K, DTYPES[(M + N) % 3], bias=(M + K) % 2 == 0)
 
 
-@pytest.mark.parametrize("tile", ["skinny", "32", "64x32", "64", "64x128k2", "64x128", "128", "128x256", "256x192", "256"])
+@pytest.mark.parametrize("tile", ["skinny", "32", "64x32", "64", "64k2", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
 @pytest.mark.parametrize("shape", [(1, 16, 16), (16, 48, 128), (16, 4111, 400), (32, 65, 144), (32, 4130, 272), (32, 8200, 272), (64, 260, 2064)])
 @pytest.mark.parametrize("ydtype", DTYPES)
 def test_gemm_every_kernel(w4, hooks, tile, shape, ydtype):
@@ -203,7 +203,7 @@ def test_gemm_every_kernel(w4, hooks, tile, shape, ydtype):
     check_gemm(w4, *shape, ydtype, bias=True)
 
 
-@pytest.mark.parametrize("tile", ["32", "64x32", "64", "64x128k2", "64x128", "128", "128x256", "256x192", "256"])
+@pytest.mark.parametrize("tile", ["32", "64x32", "64", "64k2", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
 def test_gemm_tiled_larger(w4, hooks, tile):
     hooks.setenv("W8A8_GEMM_TILE", tile)
     for shape in ((300, 523, 1040), (513, 1032, 640), (257, 255, 16)):

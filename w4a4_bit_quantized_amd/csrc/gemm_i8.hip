@@ -49,20 +49,30 @@ __device__ __forceinline__ void store_one(void* y, size_t i, float v) {
 
 // KG groups of WAVES_M x WAVES_N waves split K (group k takes the K-steps k, k + KG, ...), each with a ring
 // of S stages of its own; their partial sums meet in LDS.
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG>
+//
+// NL > 0: NL further waves do nothing but the direct loads.  A wave whose load waits for its turn issues no
+// matrix instruction either, so with loads in every wave the two times add up where a wave has few matrix
+// instructions per K-step (L2-resident operands, 128 x 128 x 128 per step: 217 ns of loads and 222 of matrix
+// instructions take 418 together); with waves of their own the loads run beside them (1021 x 2050 x 4096 in
+// 128 x 128 tiles: 24.8 to 21.1 us; 1024 x 4096 x 4096: 25.9 to 23.4; 256 x 5120 x 5120 in 64 x 128: 17.6 to
+// 16.5).  Four loaders, one per SIMD: two of them cannot issue fast enough, eight measured as four.  They
+// are a third wave per SIMD, which leaves 168 registers to each: the tiles of 256 rows need more.
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL>
 struct TileI8 {
   static constexpr int WAVES = WAVES_M * WAVES_N;  // of a group
-  static constexpr int THREADS = 64 * WAVES * KG;
+  static constexpr int LW = NL ? NL / KG : WAVES;  // waves that load (of a group)
+  static constexpr int THREADS = 64 * (WAVES * KG + NL);
   static constexpr int BM = WAVES_M * FM * 32, BN = WAVES_N * FN * 32;
   static constexpr int ROWS = BM + BN;             // activation rows, then weight rows
   static constexpr int STEP = 128;                 // K columns (bytes) per stage: whole 128-byte lines
   static constexpr int STAGE = ROWS * STEP;
-  static constexpr int ROUNDS = ROWS / (8 * WAVES);  // a wave's direct load fills 8 rows
+  static constexpr int ROUNDS = ROWS / (8 * LW);   // a wave's direct load fills 8 rows
   static constexpr int REGION = 32 * FN * 32 * 4;  // a wave's epilogue region: 32 rows of f32
   static constexpr int PART = (KG - 1) * BM * BN * 4;  // partial sums of the groups after the first
   static constexpr int EPI = WAVES * REGION + BN * 8 > PART ? WAVES * REGION + BN * 8 : PART;
   static constexpr int LDS = KG * S * STAGE > EPI ? KG * S * STAGE : EPI;
-  static_assert(ROWS % (8 * WAVES) == 0 && BM % (8 * WAVES) == 0, "whole rounds per operand");
+  static_assert(ROWS % (8 * LW) == 0 && BM % (8 * LW) == 0, "whole rounds per operand");
+  static_assert(NL % KG == 0 && (KG == 1 || NL > 0), "groups have loaders, as many each");
   static_assert(LDS <= 160 * 1024, "LDS of one CU");
   static_assert(ROUNDS * S < 64, "vmcnt range");
 };
@@ -84,13 +94,13 @@ __device__ __forceinline__ void i8_issue(uint8_t* stage, int wave, uint32_t k0, 
   if (k0 + T::STEP <= K) {
 #pragma unroll
     for (int r = R0; r < R1; ++r)
-      load_lds16((r * T::WAVES * 8 < T::BM ? abase : bbase) + k0 + off[r], stage + (r * T::WAVES + wave) * 1024);
+      load_lds16((r * T::LW * 8 < T::BM ? abase : bbase) + k0 + off[r], stage + (r * T::LW + wave) * 1024);
   } else {
 #pragma unroll
     for (int r = R0; r < R1; ++r) {
-      const uint8_t* p = (r * T::WAVES * 8 < T::BM ? abase : bbase) + k0 + off[r];
+      const uint8_t* p = (r * T::LW * 8 < T::BM ? abase : bbase) + k0 + off[r];
       if (k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
-      load_lds16(p, stage + (r * T::WAVES + wave) * 1024);
+      load_lds16(p, stage + (r * T::LW + wave) * 1024);
     }
   }
 }
@@ -211,16 +221,18 @@ __device__ __forceinline__ void store_region(const uint8_t* reg, int lane, uint8
   }
 }
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int YT>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, int YT>
+__global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
     int64_t ldy) {
-  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG>;
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
-  const int kg = KG > 1 ? w / T::WAVES : 0, wave = KG > 1 ? w % T::WAVES : w;
+  const bool loader = NL > 0 && w >= T::WAVES * KG;
+  const int wl = loader ? w - T::WAVES * KG : w, per = loader ? T::LW : T::WAVES;  // waves of a group
+  const int kg = KG > 1 ? wl / per : 0, wave = KG > 1 ? wl % per : wl;
   const int wm = wave / WAVES_N, wn = wave % WAVES_N;
   const int l32 = lane & 31, h = lane >> 5;
   int tm, tn;
@@ -235,7 +247,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
   uint32_t off[T::ROUNDS], col[T::ROUNDS];
 #pragma unroll
   for (int r = 0; r < T::ROUNDS; ++r) {
-    const int row = (r * T::WAVES + wave) * 8 + (lane >> 3);
+    const int row = (r * T::LW + wave) * 8 + (lane >> 3);
     col[r] = 16u * (uint32_t)((lane & 7) ^ i8_swizzle(row));
     const int src = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
     off[r] = (uint32_t)src * (uint32_t)K + col[r];
@@ -263,35 +275,75 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
   };
   uint8_t* ring = lds + kg * S * T::STAGE;
   constexpr int R = T::ROUNDS, RA = T::ROUNDS / 4;
+  if constexpr (NL > 0) {
+    if (loader) {
+      __builtin_amdgcn_s_setprio(3);  // (1024 x 8192 x 8192 in 128 x 256 tiles: 67.0 us, 68.7 without)
 #pragma unroll
-  for (int j = 0; j < S - 1; ++j)
-    i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
-  vm_wait_barrier<(S - 2) * R>();
-  i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
-  int slot = 0;
-  i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
-  i8_issue<T, 0, RA>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
-  for (int kt = 0; kt < ni; ++kt) {
-    uint8_t* cur = ring + slot * T::STAGE;
-    // the rest of the loads of K-step kt + S - 1, into the slot of kt - 1
-    i8_issue<T, RA, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
-                       bbase, off, col);
-    i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
-    i8_mma<FM, FN>(acc, a0, b0);
-    i8_interleave<FM, FN, R - RA>();
-    i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
-    i8_mma<FM, FN>(acc, a1, b1);
-    i8_interleave<FM, FN, 0>();
-    i8_read<FM, FN>(cur, 3, ra, rb, h, a1, b1);
-    i8_mma<FM, FN>(acc, a0, b0);
-    i8_interleave<FM, FN, 0>();
-    // K-step kt + 1 has landed and every wave has read the operands of kt: its slot is free
+      for (int j = 0; j < S - 1; ++j)
+        i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
+      vm_wait_barrier<(S - 2) * R>();
+      int slot = 0;
+      for (int kt = 0; kt < ni; ++kt) {
+        // K-step kt + S - 1 into the slot of kt - 1, whose operands every wave had read at the last barrier
+        i8_issue<T, 0, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
+                          bbase, off, col);
+        vm_wait_barrier<(S - 2) * R>();  // kt + 1 has landed
+        slot = slot == S - 1 ? 0 : slot + 1;
+      }
+    } else {
+      vm_wait_barrier<0>();
+      i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
+      int slot = 0;
+      i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
+      for (int kt = 0; kt < ni; ++kt) {
+        const uint8_t* cur = ring + slot * T::STAGE;
+        i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
+        i8_mma<FM, FN>(acc, a0, b0);
+        i8_interleave<FM, FN, 0>();
+        i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
+        i8_mma<FM, FN>(acc, a1, b1);
+        i8_interleave<FM, FN, 0>();
+        i8_read<FM, FN>(cur, 3, ra, rb, h, a1, b1);
+        i8_mma<FM, FN>(acc, a0, b0);
+        i8_interleave<FM, FN, 0>();
+        vm_wait_barrier<0>();  // the operands of kt are in registers; the loaders saw kt + 1 land
+        slot = slot == S - 1 ? 0 : slot + 1;
+        i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
+        i8_mma<FM, FN>(acc, a1, b1);
+        i8_interleave<FM, FN, 0>();
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < S - 1; ++j)
+      i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
     vm_wait_barrier<(S - 2) * R>();
-    i8_issue<T, 0, RA>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
-    slot = slot == S - 1 ? 0 : slot + 1;
-    i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
-    i8_mma<FM, FN>(acc, a1, b1);
-    i8_interleave<FM, FN, RA>();
+    i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
+    int slot = 0;
+    i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
+    i8_issue<T, 0, RA>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
+    for (int kt = 0; kt < ni; ++kt) {
+      uint8_t* cur = ring + slot * T::STAGE;
+      // the rest of the loads of K-step kt + S - 1, into the slot of kt - 1
+      i8_issue<T, RA, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
+                         bbase, off, col);
+      i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
+      i8_mma<FM, FN>(acc, a0, b0);
+      i8_interleave<FM, FN, R - RA>();
+      i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
+      i8_mma<FM, FN>(acc, a1, b1);
+      i8_interleave<FM, FN, 0>();
+      i8_read<FM, FN>(cur, 3, ra, rb, h, a1, b1);
+      i8_mma<FM, FN>(acc, a0, b0);
+      i8_interleave<FM, FN, 0>();
+      // K-step kt + 1 has landed and every wave has read the operands of kt: its slot is free
+      vm_wait_barrier<(S - 2) * R>();
+      i8_issue<T, 0, RA>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
+      slot = slot == S - 1 ? 0 : slot + 1;
+      i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
+      i8_mma<FM, FN>(acc, a1, b1);
+      i8_interleave<FM, FN, RA>();
+    }
   }
   vm_wait_barrier<0>();
   if constexpr (KG > 1) {
@@ -303,9 +355,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
       for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r)
-          if (kg > 0) part[(((kg - 1) * T::WAVES + wave) * N16 + (i * FN + j) * 16 + r) * 64 + lane] = acc[i][j][r];
+          if (kg > 0 && !loader) part[(((kg - 1) * T::WAVES + wave) * N16 + (i * FN + j) * 16 + r) * 64 + lane] = acc[i][j][r];
     __syncthreads();
-    if (kg == 0)
+    if (kg == 0 && !loader)
 #pragma unroll
       for (int i = 0; i < FM; ++i)
 #pragma unroll
@@ -328,7 +380,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KG) void gemm_i8_kernel(
     b_lds[c] = (bias != nullptr && n < N) ? bf16_bits_to_f32(bias[n]) : 0.0f;
   }
   __syncthreads();
-  if (KG > 1 && kg > 0) return;
+  if (loader || kg > 0) return;
   constexpr int ES = YType<YT>::ES;
   constexpr int RSB = FN * 32 * ES;   // bytes per region row
   constexpr int CPR = RSB / 16;       // 16-byte chunks per region row
@@ -660,11 +712,11 @@ struct GArgs {
   hipStream_t stream;
 };
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int YT>
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, int YT>
 hipError_t run_tile(const GArgs& a) {
-  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG>;
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL>;
   const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
-  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, KG, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
+  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, KG, NL, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
       a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
   return hipGetLastError();
 }
@@ -691,27 +743,45 @@ hipError_t run(const GArgs& a) {
     if (a.M <= 16) return run_skinny<1, 2, 4, 3, YT>(a);
     return a.N <= 8192 ? run_skinny<2, 2, 4, 3, YT>(a) : run_skinny<2, 2, 4, 2, YT>(a);
   }
-  // At most one tile per CU: the K loop's latency bounds the launch, so K is split over groups of waves
-  // and the smallest tile that still leaves every CU at most one wins (128 x 2048 x 2048: 32 x 32 tiles
-  // 5.6 us, 64 x 32 6.4, 64 x 64 7.4, 8.8 without the split; 128 x 4096 x 4096: 64 x 32 9.3, 64 x 64 11.3;
-  // 128 x 8192 x 4096: 64 x 64 12.0, 64 x 128 14.5, 128 x 128 19.8).
-  if (forced ? is("32") : tiles(32, 32) <= 256) return run_tile<1, 1, 1, 1, 3, 4, YT>(a);
-  if (forced ? is("64x32") : tiles(64, 32) <= 256) return run_tile<2, 1, 1, 1, 3, 4, YT>(a);
-  if (forced ? is("64") : tiles(64, 64) <= 256) return run_tile<2, 2, 1, 1, 3, 2, YT>(a);
-  // (the split pays from about K = 2048: 256 x 5120 x 5120 17.3 us against 19.4, 301 x 4099 x 1552
-  // 12.6 against 12.1)
-  if (forced ? is("64x128k2") : tiles(64, 128) <= 256 && a.K >= 2048) return run_tile<2, 2, 1, 2, 3, 2, YT>(a);
-  if (forced ? is("64x128") : tiles(64, 128) <= 256) return run_tile<2, 2, 1, 2, 3, 1, YT>(a);
-  if (forced ? is("128") : tiles(128, 128) <= 256) return run_tile<2, 4, 2, 1, 4, 1, YT>(a);
-  // Several rounds of 256 tiles: the shape with the least time, rounds by the measured time of a
-  // 128-column K-step (128 x 256: 0.88 us, 256 x 192: 1.22, 256 x 256: 1.45), so a last round that is
-  // mostly empty is cheap (4096 x 2560 x 12288: 139 us in 160 tiles of 256 x 256, 123 in 224 of 256 x 192;
-  // 4096 x 2048 x 2048: 31.7 in 128, 23.2 in 256 of 128 x 256; 4096 x 13824 x 5120: 284 / 290 / 318).
-  const int64_t c0 = (tiles(128, 256) + 255) / 256 * 88, c1 = (tiles(256, 192) + 255) / 256 * 122,
-                c2 = (tiles(256, 256) + 255) / 256 * 145;
-  if (forced ? is("256") : c2 <= c1 && c2 <= c0) return run_tile<2, 4, 4, 2, 2, 1, YT>(a);
-  if (forced ? is("256x192") : c1 <= c0) return run_tile<4, 2, 2, 3, 2, 1, YT>(a);
-  return run_tile<2, 4, 2, 2, 3, 1, YT>(a);
+  // At most one tile per CU: the K loop's latency bounds the launch, and the smallest tile that still leaves
+  // every CU at most one wins (128 x 2048 x 2048: 32 x 32 tiles 5.3 us, 64 x 32 6.0, 64 x 64 7.4; 128 x 4096 x
+  // 4096: 64 x 32 9.1, 32 x 32 12.9; 128 x 8192 x 4096: 64 x 64 12.3, 64 x 128 13.3, 128 x 128 17.1).  The two
+  // smallest, whose waves are few, split K over groups of them.
+  if (forced ? is("32") : tiles(32, 32) <= 256) return run_tile<1, 1, 1, 1, 3, 4, 4, YT>(a);
+  if (forced ? is("64x32") : tiles(64, 32) <= 256) return run_tile<2, 1, 1, 1, 4, 2, 4, YT>(a);
+  if (tiles(64, 64) <= 256 || forced) {
+    // (the split pays from about K = 4096: 67 x 6384 x 12080 by 14 %; 256 x 4096 x 2048 8.3 us without, 8.6 with)
+    if (forced ? is("64k2") : a.K >= 4096) return run_tile<2, 2, 1, 1, 4, 2, 4, YT>(a);
+    if (!forced || is("64")) return run_tile<2, 2, 1, 1, 4, 1, 4, YT>(a);
+  }
+  if (tiles(64, 128) <= 256 || forced) {
+    // (four stages from about K = 2048: 256 x 5120 x 5120 16.9 us, 17.8 with three; 301 x 4099 x 1552 11.6 and 11.2)
+    if (forced ? is("64x128s4") : a.K >= 2048) return run_tile<2, 4, 1, 1, 4, 1, 4, YT>(a);
+    if (!forced || is("64x128")) return run_tile<2, 4, 1, 1, 3, 1, 4, YT>(a);
+  }
+  // Otherwise, in rounds of 256 tiles, the shape with the least time: rounds by the measured time of a
+  // 128-column K-step (10 ns).  A last round that is mostly empty then costs little (4096 x 2560 x 12288: 137 us
+  // in 224 tiles of 256 x 192, 144 in 160 of 256 x 256; 300 x 13824 x 5120: 33 in 216 of 128 x 192, 36 in 162 of
+  // 128 x 256; 1021 x 2050 x 4096: 20 in 136 of 128 x 128, 29 in 88 of 128 x 192).  Over 60 drawn shapes the rule is 0.3 %
+  // behind the best of the five, and at most 6 %.
+  struct { const char* name; int64_t bm, bn, step; } const shapes[] = {
+      {"128", 128, 128, 53}, {"128x192", 128, 192, 68}, {"128x256", 128, 256, 85}, {"256x192", 256, 192, 122}, {"256", 256, 256, 145}};
+  int best = 0;
+  int64_t least = 0;
+  for (int i = 0; i < 5; ++i) {
+    const int64_t cost = (tiles(shapes[i].bm, shapes[i].bn) + 255) / 256 * shapes[i].step;
+    if (forced ? is(shapes[i].name) : i == 0 || cost < least) {
+      best = i;
+      least = cost;
+    }
+  }
+  switch (best) {
+    case 0: return run_tile<2, 4, 2, 1, 3, 1, 4, YT>(a);  // (a fourth stage: 0 to 4 % slower)
+    case 1: return run_tile<2, 3, 2, 2, 3, 1, 4, YT>(a);
+    case 2: return run_tile<2, 4, 2, 2, 3, 1, 4, YT>(a);
+    case 3: return run_tile<4, 2, 2, 3, 2, 1, 0, YT>(a);
+    default: return run_tile<2, 4, 4, 2, 2, 1, 0, YT>(a);
+  }
 }
 
 }  // namespace
