@@ -193,7 +193,7 @@ def test_gemm_shapes(w4, shape):
     check_gemm(w4, M, N, K, DTYPES[(M + N) % 3], bias=(M + K) % 2 == 0)
 
 
-@pytest.mark.parametrize("tile", ["skinny", "32", "64x32", "64", "64k2", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
+@pytest.mark.parametrize("tile", ["skinny", "32", "64x32", "64", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
 @pytest.mark.parametrize("shape", [(1, 16, 16), (16, 48, 128), (16, 4111, 400), (32, 65, 144), (32, 4130, 272), (32, 8200, 272), (64, 260, 2064)])
 @pytest.mark.parametrize("ydtype", DTYPES)
 def test_gemm_every_kernel(w4, hooks, tile, shape, ydtype):
@@ -203,11 +203,28 @@ def test_gemm_every_kernel(w4, hooks, tile, shape, ydtype):
     check_gemm(w4, *shape, ydtype, bias=True)
 
 
-@pytest.mark.parametrize("tile", ["32", "64x32", "64", "64k2", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
+@pytest.mark.parametrize("tile", ["32", "64x32", "64", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
 def test_gemm_tiled_larger(w4, hooks, tile):
     hooks.setenv("W8A8_GEMM_TILE", tile)
     for shape in ((300, 523, 1040), (513, 1032, 640), (257, 255, 16)):
         check_gemm(w4, *shape, "bf16", bias=False)
+
+
+@pytest.mark.parametrize("tile", ["skinny", "32", "64x32", "64", "64x128", "64x128s4", "128", "128x192", "128x256", "256x192", "256"])
+def test_gemm_rows_off_lines(w4, hooks, tile):
+    """Rows that start anywhere in a 128-byte line (K modulo 128, operands at offsets of 16 bytes), in buffers
+    of exactly their size."""
+    import torch
+    hooks.setenv("W8A8_GEMM_TILE", tile)
+    rng = np.random.default_rng(len(tile))
+    M, N = (29, 75) if tile == "skinny" else (131, 203)
+    sa, sw = rng.uniform(0.01, 0.1, M).astype(np.float32), rng.uniform(0.001, 0.01, N).astype(np.float32)
+    for K, oa, ob in ((16, 1, 0), (112, 0, 3), (128, 7, 0), (256, 0, 5), (384, 2, 6), (144, 0, 0), (1168, 3, 1), (1232, 0, 0),
+                      (496, 5, 5), (2000, 0, 0), (1536, 4, 4), (4176, 0, 2)):
+        qa, qw = codes(rng, M, K), codes(rng, N, K)
+        put = lambda q, o: torch.cat([torch.full((16 * o,), 99, dtype=torch.int8), torch.from_numpy(q).flatten()]).cuda()[16 * o:].view(q.shape)
+        y = w4.w8a8_gemm(put(qa, oa), torch.from_numpy(sa).cuda(), put(qw, ob), torch.from_numpy(sw).cuda(), out_dtype=torch.float32)
+        same_bits(host(y), ow.gemm_f32(qa, sa, qw, sw, None), f"K={K} offsets {oa} {ob}")
 
 
 def test_gemm_largest_sum(w4):

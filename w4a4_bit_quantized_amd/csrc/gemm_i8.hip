@@ -57,7 +57,14 @@ __device__ __forceinline__ void store_one(void* y, size_t i, float v) {
 // 128 x 128 tiles: 24.8 to 21.1 us; 1024 x 4096 x 4096: 25.9 to 23.4; 256 x 5120 x 5120 in 64 x 128: 17.6 to
 // 16.5).  Four loaders, one per SIMD: two of them cannot issue fast enough, eight measured as four.  They
 // are a third wave per SIMD, which leaves 168 registers to each: the tiles of 256 rows need more.
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL>
+//
+// SHIFT: rows off 128-byte boundaries (K % 128 != 0, or such operands).  Read from its own start, every
+// 128-byte chunk of a row would touch two lines of memory (1024 x 2048 x 4112: 20.2 us, x 4096: 15.8).  Instead
+// a stage holds one aligned line of every row, its window: window w of a row that starts s 16-byte chunks into
+// a line holds its chunks 8 w - s .. 8 w - s + 7, and K-step kt takes chunk 8 kt + c from place c + s of window kt
+// or, past its end, of window kt + 1.  s depends on the row modulo 8 only (K % 16 == 0), so a lane's rows
+// share it.  One more window is resident, and places before a row's start or past its end hold zeros.
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, bool SHIFT>
 struct TileI8 {
   static constexpr int WAVES = WAVES_M * WAVES_N;  // of a group
   static constexpr int LW = NL ? NL / KG : WAVES;  // waves that load (of a group)
@@ -73,6 +80,7 @@ struct TileI8 {
   static constexpr int LDS = KG * S * STAGE > EPI ? KG * S * STAGE : EPI;
   static_assert(ROWS % (8 * LW) == 0 && BM % (8 * LW) == 0, "whole rounds per operand");
   static_assert(NL % KG == 0 && (KG == 1 || NL > 0), "groups have loaders, as many each");
+  static_assert(!SHIFT || (NL > 0 && S >= 3), "two windows resident, one on its way");
   static_assert(LDS <= 160 * 1024, "LDS of one CU");
   static_assert(ROUNDS * S < 64, "vmcnt range");
 };
@@ -87,18 +95,21 @@ __device__ __forceinline__ void load_lds16(const uint8_t* src, uint8_t* dst) {
 }
 
 // Rounds R0 .. R1 - 1 of one K-step's direct loads into a stage (16 bytes per lane, 8 rows of 128 bytes
-// per instruction).
-template <class T, int R0, int R1>
+// per instruction).  off is the chunk's offset from abase or bbase + k0 (SHIFT: plus 112, so that it is not
+// negative), col its K-column minus k0 (SHIFT: possibly negative; as unsigned numbers, columns before the row's
+// start are past its end).
+template <class T, bool SHIFT, int R0, int R1>
 __device__ __forceinline__ void i8_issue(uint8_t* stage, int wave, uint32_t k0, uint32_t K, const uint8_t* abase,
                                          const uint8_t* bbase, const uint32_t* off, const uint32_t* col) {
-  if (k0 + T::STEP <= K) {
+  if ((!SHIFT || k0 >= T::STEP) && k0 + T::STEP <= K) {
 #pragma unroll
     for (int r = R0; r < R1; ++r)
-      load_lds16((r * T::LW * 8 < T::BM ? abase : bbase) + k0 + off[r], stage + (r * T::LW + wave) * 1024);
+      load_lds16((r * T::LW * 8 < T::BM ? abase : bbase) + k0 - (SHIFT ? 112 : 0) + off[r],
+                 stage + (r * T::LW + wave) * 1024);
   } else {
 #pragma unroll
     for (int r = R0; r < R1; ++r) {
-      const uint8_t* p = (r * T::LW * 8 < T::BM ? abase : bbase) + k0 + off[r];
+      const uint8_t* p = (r * T::LW * 8 < T::BM ? abase : bbase) + k0 - (SHIFT ? 112 : 0) + off[r];
       if (k0 + col[r] >= K) p = reinterpret_cast<const uint8_t*>(zero_chunk);
       load_lds16(p, stage + (r * T::LW + wave) * 1024);
     }
@@ -125,6 +136,32 @@ __device__ __forceinline__ void i8_mma(i32x16_t (&acc)[FM][FN], const i32x4_t (&
     for (int j = 0; j < FN; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b[j], a[i], acc[i][j], 0, 0, 0);
 }
 
+// The same for Q quarters of a K-step from `ks` on, in windows cur and nxt where the lane's rows start sa
+// and sb chunks into a line.
+template <int Q, int FM, int FN>
+struct I8Ops {
+  i32x4_t a[Q][FM], b[Q][FN];
+};
+
+template <bool SHIFT, int Q, int FM, int FN>
+__device__ __forceinline__ void i8_read(const uint8_t* cur, const uint8_t* nxt, int ks, int ra, int rb, int h, int sa,
+                                        int sb, I8Ops<Q, FM, FN>& o) {
+#pragma unroll
+  for (int q = 0; q < Q; ++q) {
+    if constexpr (!SHIFT) {
+      i8_read<FM, FN>(cur, ks + q, ra, rb, h, o.a[q], o.b[q]);
+    } else {
+      const int pa = 2 * (ks + q) + h + sa, pb = 2 * (ks + q) + h + sb;
+      const uint8_t* wa = (pa & 8 ? nxt : cur) + 16 * ((pa & 7) ^ i8_swizzle(ra));
+      const uint8_t* wb = (pb & 8 ? nxt : cur) + 16 * ((pb & 7) ^ i8_swizzle(rb));
+#pragma unroll
+      for (int j = 0; j < FN; ++j) o.b[q][j] = *reinterpret_cast<const i32x4_t*>(wb + (rb + j * 32) * 128);
+#pragma unroll
+      for (int i = 0; i < FM; ++i) o.a[q][i] = *reinterpret_cast<const i32x4_t*>(wa + (ra + i * 32) * 128);
+    }
+  }
+}
+
 // Order of a quarter K-step: its matrix instructions with the next quarter's LDS reads between them, and
 // the quarter's LOADS direct loads between its last ones (a wave that waits to issue a load issues no
 // matrix instruction either: a quarter of a K-step's loads right after the barrier and the rest in
@@ -137,6 +174,18 @@ __device__ __forceinline__ void i8_interleave() {
     __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);  // LDS read
     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // MFMA
     if (g >= FM * FN - LOADS) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // direct load
+  }
+  __builtin_amdgcn_sched_barrier(0);
+}
+
+// The same for Q quarters without loads.
+template <int Q, int FM, int FN>
+__device__ __forceinline__ void i8_interleave_q() {
+  constexpr int MF = Q * FM * FN;
+#pragma unroll
+  for (int g = 0; g < MF; ++g) {
+    __builtin_amdgcn_sched_group_barrier(0x100, (Q * (FM + FN) + MF - 1) / MF, 0);  // LDS reads
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);                              // MFMA
   }
   __builtin_amdgcn_sched_barrier(0);
 }
@@ -221,12 +270,12 @@ __device__ __forceinline__ void store_region(const uint8_t* reg, int lane, uint8
   }
 }
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, int YT>
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, bool SHIFT, int YT>
 __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_kernel(
     const uint8_t* __restrict__ qa, const float* __restrict__ sa, const uint8_t* __restrict__ qw,
     const float* __restrict__ sw, const uint16_t* __restrict__ bias, int M, int N, int K, void* __restrict__ y,
     int64_t ldy) {
-  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL>;
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL, SHIFT>;
   __shared__ __attribute__((aligned(16))) uint8_t lds[T::LDS];
   const int t = threadIdx.x, lane = t & 63;
   const int w = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -243,16 +292,21 @@ __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_ke
   const uint8_t* bbase = qw + (size_t)n0 * K;
   const int rows_a = min(T::BM, M - m0), rows_b = min(T::BN, N - n0);
 
+  // how far into a 128-byte line a row starts, in 16-byte chunks
+  auto shift_of = [&](const uint8_t* base, int row) {
+    return SHIFT ? (int)((reinterpret_cast<uintptr_t>(base) >> 4) + (uint32_t)row * ((uint32_t)K >> 4)) & 7 : 0;
+  };
   // byte offset in the operand and K-column of this lane's chunk in every round
   uint32_t off[T::ROUNDS], col[T::ROUNDS];
 #pragma unroll
   for (int r = 0; r < T::ROUNDS; ++r) {
     const int row = (r * T::LW + wave) * 8 + (lane >> 3);
-    col[r] = 16u * (uint32_t)((lane & 7) ^ i8_swizzle(row));
     const int src = row < T::BM ? min(row, rows_a - 1) : min(row - T::BM, rows_b - 1);
-    off[r] = (uint32_t)src * (uint32_t)K + col[r];
+    col[r] = 16u * (uint32_t)(((lane & 7) ^ i8_swizzle(row)) - shift_of(row < T::BM ? abase : bbase, src));
+    off[r] = (uint32_t)src * (uint32_t)K + col[r] + (SHIFT ? 112u : 0u);
   }
   const int ra = wm * FM * 32 + l32, rb = T::BM + wn * FN * 32 + l32;
+  const int sha = shift_of(abase, ra), shb = shift_of(bbase, rb - T::BM);
   i32x16_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -265,67 +319,71 @@ __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_ke
   // each XCD starts an eighth of K further on, so the eight of them fetch different columns of the
   // panels that they share from HBM and find the others' in the Infinity Cache.  Past the last K-step
   // the last is loaded again, so that every step waits on the same count.
-  // A group whose last K-step does not exist takes columns past K, which are zeros.
-  const int ni = (nkt + KG - 1) / KG;
-  const int kt0 = (int)(blockIdx.x & 7) * nkt / 8;
+  // A group whose last K-step does not exist takes columns past K, which are zeros.  With SHIFT the groups
+  // take runs of K-steps (each needs its successor's window too), and the cycle is padded with K-steps of
+  // zeros, one at least: its windows are the last lines of the rows and then the first.
+  const int ni = (nkt + (SHIFT ? 1 : 0) + KG - 1) / KG, cycle = SHIFT ? ni * KG : nkt;
+  const int kt0 = (int)(blockIdx.x & 7) * cycle / 8;
   auto k_of = [&](int i) {
-    const int p = KG * min(i, ni - 1) + kg;
-    const int q = p + kt0 >= nkt ? p + kt0 - nkt : p + kt0;
-    return (uint32_t)(KG == 1 || p < nkt ? q : nkt) * T::STEP;
+    const int p = SHIFT ? kg * ni + min(i, ni) : KG * min(i, ni - 1) + kg;
+    const int q = p + kt0 >= cycle ? p + kt0 - cycle : p + kt0;
+    return (uint32_t)(SHIFT || KG == 1 || p < nkt ? q : nkt) * T::STEP;
   };
   uint8_t* ring = lds + kg * S * T::STAGE;
   constexpr int R = T::ROUNDS, RA = T::ROUNDS / 4;
   if constexpr (NL > 0) {
     if (loader) {
       __builtin_amdgcn_s_setprio(3);  // (1024 x 8192 x 8192 in 128 x 256 tiles: 67.0 us, 68.7 without)
+      constexpr int AHEAD = (SHIFT ? S - 3 : S - 2) * R;  // loads of stages that are not needed yet
 #pragma unroll
       for (int j = 0; j < S - 1; ++j)
-        i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
-      vm_wait_barrier<(S - 2) * R>();
+        i8_issue<T, SHIFT, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
+      vm_wait_barrier<AHEAD>();
       int slot = 0;
       for (int kt = 0; kt < ni; ++kt) {
-        // K-step kt + S - 1 into the slot of kt - 1, whose operands every wave had read at the last barrier
-        i8_issue<T, 0, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
-                          bbase, off, col);
-        vm_wait_barrier<(S - 2) * R>();  // kt + 1 has landed
+        // stage kt + S - 1 into the slot of kt - 1, whose operands every wave had read at the last barrier
+        i8_issue<T, SHIFT, 0, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K,
+                                 abase, bbase, off, col);
+        vm_wait_barrier<AHEAD>();  // stage kt + 1 (SHIFT: kt + 2) has landed
         slot = slot == S - 1 ? 0 : slot + 1;
       }
     } else {
+      // operands are read a quarter of a K-step ahead, or half of one where a quarter is a single matrix
+      // instruction (64 x 64 tiles, 128 x 8192 x 4096: 12.3 to 11.0 us; more waves or products per wave do not gain)
+      constexpr int Q = FM * FN == 1 ? 2 : 1, P = 4 / Q;
       vm_wait_barrier<0>();
-      i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
+      I8Ops<Q, FM, FN> o[2];
+      auto after = [](int slot) { return slot == S - 1 ? 0 : slot + 1; };
       int slot = 0;
-      i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
+      i8_read<SHIFT>(ring, ring + T::STAGE, 0, ra, rb, h, sha, shb, o[0]);
       for (int kt = 0; kt < ni; ++kt) {
-        const uint8_t* cur = ring + slot * T::STAGE;
-        i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
-        i8_mma<FM, FN>(acc, a0, b0);
-        i8_interleave<FM, FN, 0>();
-        i8_read<FM, FN>(cur, 2, ra, rb, h, a0, b0);
-        i8_mma<FM, FN>(acc, a1, b1);
-        i8_interleave<FM, FN, 0>();
-        i8_read<FM, FN>(cur, 3, ra, rb, h, a1, b1);
-        i8_mma<FM, FN>(acc, a0, b0);
-        i8_interleave<FM, FN, 0>();
-        vm_wait_barrier<0>();  // the operands of kt are in registers; the loaders saw kt + 1 land
-        slot = slot == S - 1 ? 0 : slot + 1;
-        i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
-        i8_mma<FM, FN>(acc, a1, b1);
-        i8_interleave<FM, FN, 0>();
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          if (p == P - 1) {
+            vm_wait_barrier<0>();  // the operands of kt are in registers; the loaders saw the next ones land
+            slot = after(slot);
+          }
+          i8_read<SHIFT>(ring + slot * T::STAGE, ring + after(slot) * T::STAGE, (p + 1) * Q % 4, ra, rb, h, sha, shb,
+                         o[(p + 1) & 1]);
+#pragma unroll
+          for (int q = 0; q < Q; ++q) i8_mma<FM, FN>(acc, o[p & 1].a[q], o[p & 1].b[q]);
+          i8_interleave_q<Q, FM, FN>();
+        }
       }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < S - 1; ++j)
-      i8_issue<T, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
+      i8_issue<T, false, 0, R>(ring + j * T::STAGE, wave, k_of(j), (uint32_t)K, abase, bbase, off, col);
     vm_wait_barrier<(S - 2) * R>();
     i32x4_t a0[FM], b0[FN], a1[FM], b1[FN];
     int slot = 0;
     i8_read<FM, FN>(ring, 0, ra, rb, h, a0, b0);
-    i8_issue<T, 0, RA>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
+    i8_issue<T, false, 0, RA>(ring + (S - 1) * T::STAGE, wave, k_of(S - 1), (uint32_t)K, abase, bbase, off, col);
     for (int kt = 0; kt < ni; ++kt) {
       uint8_t* cur = ring + slot * T::STAGE;
       // the rest of the loads of K-step kt + S - 1, into the slot of kt - 1
-      i8_issue<T, RA, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
+      i8_issue<T, false, RA, R>(ring + (slot == 0 ? S - 1 : slot - 1) * T::STAGE, wave, k_of(kt + S - 1), (uint32_t)K, abase,
                          bbase, off, col);
       i8_read<FM, FN>(cur, 1, ra, rb, h, a1, b1);
       i8_mma<FM, FN>(acc, a0, b0);
@@ -338,7 +396,7 @@ __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_ke
       i8_interleave<FM, FN, 0>();
       // K-step kt + 1 has landed and every wave has read the operands of kt: its slot is free
       vm_wait_barrier<(S - 2) * R>();
-      i8_issue<T, 0, RA>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
+      i8_issue<T, false, 0, RA>(cur, wave, k_of(kt + S), (uint32_t)K, abase, bbase, off, col);
       slot = slot == S - 1 ? 0 : slot + 1;
       i8_read<FM, FN>(ring + slot * T::STAGE, 0, ra, rb, h, a0, b0);
       i8_mma<FM, FN>(acc, a1, b1);
@@ -712,13 +770,20 @@ struct GArgs {
   hipStream_t stream;
 };
 
-template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, int YT>
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, bool SHIFT, int YT>
 hipError_t run_tile(const GArgs& a) {
-  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL>;
+  using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL, SHIFT>;
   const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
-  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, KG, NL, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
+  gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, KG, NL, SHIFT, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
       a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
   return hipGetLastError();
+}
+
+// S stages where rows are whole lines, S2 where they are not (unless lines are not to be looked at).
+template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int S2, int KG, int YT>
+hipError_t run_lines(const GArgs& a, bool lines) {
+  return lines ? run_tile<WAVES_M, WAVES_N, FM, FN, S, KG, 4, false, YT>(a)
+               : run_tile<WAVES_M, WAVES_N, FM, FN, S2, KG, 4, true, YT>(a);
 }
 
 template <int MB, int NB, int KW, int S, int YT>
@@ -747,18 +812,13 @@ hipError_t run(const GArgs& a) {
   // every CU at most one wins (128 x 2048 x 2048: 32 x 32 tiles 5.3 us, 64 x 32 6.0, 64 x 64 7.4; 128 x 4096 x
   // 4096: 64 x 32 9.1, 32 x 32 12.9; 128 x 8192 x 4096: 64 x 64 12.3, 64 x 128 13.3, 128 x 128 17.1).  The two
   // smallest, whose waves are few, split K over groups of them.
-  if (forced ? is("32") : tiles(32, 32) <= 256) return run_tile<1, 1, 1, 1, 3, 4, 4, YT>(a);
-  if (forced ? is("64x32") : tiles(64, 32) <= 256) return run_tile<2, 1, 1, 1, 4, 2, 4, YT>(a);
-  if (tiles(64, 64) <= 256 || forced) {
-    // (the split pays from about K = 4096: 67 x 6384 x 12080 by 14 %; 256 x 4096 x 2048 8.3 us without, 8.6 with)
-    if (forced ? is("64k2") : a.K >= 4096) return run_tile<2, 2, 1, 1, 4, 2, 4, YT>(a);
-    if (!forced || is("64")) return run_tile<2, 2, 1, 1, 4, 1, 4, YT>(a);
-  }
-  if (tiles(64, 128) <= 256 || forced) {
-    // (four stages from about K = 2048: 256 x 5120 x 5120 16.9 us, 17.8 with three; 301 x 4099 x 1552 11.6 and 11.2)
-    if (forced ? is("64x128s4") : a.K >= 2048) return run_tile<2, 4, 1, 1, 4, 1, 4, YT>(a);
-    if (!forced || is("64x128")) return run_tile<2, 4, 1, 1, 3, 1, 4, YT>(a);
-  }
+  const bool lines = ((reinterpret_cast<uintptr_t>(a.qa) | reinterpret_cast<uintptr_t>(a.qw) | (uintptr_t)a.K) & 127) == 0;
+  if (forced ? is("32") : tiles(32, 32) <= 256) return run_lines<1, 1, 1, 1, 3, 4, 4, YT>(a, lines);
+  if (forced ? is("64x32") : tiles(64, 32) <= 256) return run_lines<2, 1, 1, 1, 4, 5, 2, YT>(a, lines);
+  if (forced ? is("64") : tiles(64, 64) <= 256) return run_lines<2, 2, 1, 1, 4, 5, 1, YT>(a, lines);
+  // (four stages from about K = 2048: 256 x 5120 x 5120 16.9 us, 17.8 with three; 301 x 4099 x 1552 11.6 and 11.2)
+  if (forced ? is("64x128s4") : tiles(64, 128) <= 256 && a.K >= 2048) return run_lines<2, 4, 1, 1, 4, 5, 1, YT>(a, lines);
+  if (forced ? is("64x128") : tiles(64, 128) <= 256) return run_lines<2, 4, 1, 1, 3, 4, 1, YT>(a, lines);
   // Otherwise, in rounds of 256 tiles, the shape with the least time: rounds by the measured time of a
   // 128-column K-step (10 ns).  A last round that is mostly empty then costs little (4096 x 2560 x 12288: 137 us
   // in 224 tiles of 256 x 192, 144 in 160 of 256 x 256; 300 x 13824 x 5120: 33 in 216 of 128 x 192, 36 in 162 of
@@ -776,11 +836,11 @@ hipError_t run(const GArgs& a) {
     }
   }
   switch (best) {
-    case 0: return run_tile<2, 4, 2, 1, 3, 1, 4, YT>(a);  // (a fourth stage: 0 to 4 % slower)
-    case 1: return run_tile<2, 3, 2, 2, 3, 1, 4, YT>(a);
-    case 2: return run_tile<2, 4, 2, 2, 3, 1, 4, YT>(a);
-    case 3: return run_tile<4, 2, 2, 3, 2, 1, 0, YT>(a);
-    default: return run_tile<2, 4, 4, 2, 2, 1, 0, YT>(a);
+    case 0: return run_lines<2, 4, 2, 1, 3, 4, 1, YT>(a, lines);  // (a fourth stage for whole lines: 0 to 4 % slower)
+    case 1: return run_lines<2, 3, 2, 2, 3, 4, 1, YT>(a, lines);
+    case 2: return run_tile<2, 4, 2, 2, 3, 1, 4, false, YT>(a);
+    case 3: return run_tile<4, 2, 2, 3, 2, 1, 0, false, YT>(a);
+    default: return run_tile<2, 4, 4, 2, 2, 1, 0, false, YT>(a);
   }
 }
 
