@@ -307,6 +307,17 @@ __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_ke
   }
   const int ra = wm * FM * 32 + l32, rb = T::BM + wn * FN * 32 + l32;
   const int sha = shift_of(abase, ra), shb = shift_of(bbase, rb - T::BM);
+  // scales and bias, on their way while the K loop runs
+  static_assert(T::THREADS >= T::BN, "a channel for every thread at most");
+  const int mb = m0 + wm * FM * 32, nb = n0 + wn * FN * 32;
+  const bool has_bias = bias != nullptr;
+  float chan_s = 0.0f, chan_b = 0.0f, row_s[FM];
+  if (t < T::BN && n0 + t < N) {
+    chan_s = sw[n0 + t];
+    if (has_bias) chan_b = bf16_bits_to_f32(bias[n0 + t]);
+  }
+#pragma unroll
+  for (int i = 0; i < FM; ++i) row_s[i] = sa[min(mb + i * 32 + l32, M - 1)];
   i32x16_t acc[FM][FN];
 #pragma unroll
   for (int i = 0; i < FM; ++i)
@@ -432,10 +443,9 @@ __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_ke
   // fragment row at a time through its own region and stores whole 16-byte runs of y rows.
   float* s_lds = reinterpret_cast<float*>(lds + T::WAVES * T::REGION);
   float* b_lds = s_lds + T::BN;
-  for (int c = t; c < T::BN; c += T::THREADS) {
-    const int n = n0 + c;
-    s_lds[c] = n < N ? sw[n] : 0.0f;
-    b_lds[c] = (bias != nullptr && n < N) ? bf16_bits_to_f32(bias[n]) : 0.0f;
+  if (t < T::BN) {
+    s_lds[t] = chan_s;
+    b_lds[t] = chan_b;
   }
   __syncthreads();
   if (loader || kg > 0) return;
@@ -443,11 +453,9 @@ __global__ __launch_bounds__(64 * (WAVES_M * WAVES_N * KG + NL)) void gemm_i8_ke
   constexpr int RSB = FN * 32 * ES;   // bytes per region row
   constexpr int CPR = RSB / 16;       // 16-byte chunks per region row
   uint8_t* reg = lds + wave * T::REGION;
-  const int mb = m0 + wm * FM * 32, nb = n0 + wn * FN * 32;
-  const bool has_bias = bias != nullptr;
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
-    const float as = sa[min(mb + i * 32 + l32, M - 1)];
+    const float as = row_s[i];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
