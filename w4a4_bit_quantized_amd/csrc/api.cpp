@@ -372,8 +372,8 @@ namespace {
 // Rows of a stride above this many elements are refused: the last row's byte offset, at most
 // 2^28 * 2^32 * 4, stays inside 64 bits.
 constexpr int64_t kMaxStride = (int64_t)1 << 32;
-// Output elements: the smallest tile of a launch of more than 256 has 128 x 256 of them, so a launch has
-// at most 2^22 + 2^21 + 2^20 workgroups of 512 threads, less than the 2^32 threads a grid may have.
+// Output elements: more than a card holds, and few enough that the tiles of a launch (128 x 256 at least where
+// there are many; 768 threads each) stay in the 2^32 threads of a grid, which the launcher checks exactly.
 constexpr int64_t kMaxOutputs = (int64_t)1 << 37;
 
 bool far_rows(int64_t rows, int64_t ld) { return rows > 1 && ld > kMaxStride; }

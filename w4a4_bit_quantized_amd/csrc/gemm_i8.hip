@@ -782,6 +782,7 @@ template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int KG, int NL, bool 
 hipError_t run_tile(const GArgs& a) {
   using T = TileI8<WAVES_M, WAVES_N, FM, FN, S, KG, NL, SHIFT>;
   const int64_t tiles = (int64_t)((a.M + T::BM - 1) / T::BM) * ((a.N + T::BN - 1) / T::BN);
+  if (tiles * T::THREADS >= (int64_t)1 << 32) return hipErrorInvalidConfiguration;
   gemm_i8_kernel<WAVES_M, WAVES_N, FM, FN, S, KG, NL, SHIFT, YT><<<dim3((unsigned)tiles), T::THREADS, 0, a.stream>>>(
       a.qa, a.sa, a.qw, a.sw, a.bias, a.M, a.N, a.K, a.y, a.ldy);
   return hipGetLastError();
