@@ -491,7 +491,7 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
   if (st != W4A4_OK) return st;
   // y would be written while other workgroups of a one-launch call still read x
   if (x && x == y) return W4A4_ERR_SHAPE;
-  if (w4a4::linear_i8_one_launch && w4a4::linear_i8_one_launch(M, K)) {
+  if (w4a4::linear_i8_one_launch && w4a4::linear_i8_one_launch(M, N, K)) {
     (void)hipGetLastError();
     return from_hip(w4a4::launch_linear_i8_token(x, x_dtype, smooth_factor, hadamard_block,
                                                  rotation_norm(hadamard_block), qweight, wscales, bias, N, K, y, y_dtype,

@@ -604,8 +604,8 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
 // Each workgroup (KW waves, 16 NB channels) starts its weight rings, quantizes the token itself (it is in L2,
 // and its arithmetic hides behind the first weights' way from HBM) into codes in LDS, and goes on as the
 // streaming kernel above with the activation operand read from there.  Every workgroup repeats the
-// quantizer's work; what is saved is a launch and the wait between the two (2048 x 6144: 7.4 to 6.1 us,
-// 5120 x 13824: 15.9 to 15.0, and 3 us of the host's time; with two tokens 5120 x 13824 takes 17.2 us
+// quantizer's work; what is saved is a launch and the wait between the two (2048 x 6144: 7.2 to 5.2 us,
+// 5120 x 13824: 15.7 to 13.1, and 3 us of the host's time; with two tokens 5120 x 13824 takes 17.2 us
 // this way and 16.2 in two launches).  The codes are those of the quantizer kernel bit for bit.
 constexpr int TK_S = 3;
 
@@ -807,15 +807,14 @@ hipError_t run(const GArgs& a) {
   const char* forced = test_hook("W8A8_GEMM_TILE");
   auto is = [&](const char* s) { return forced && !strcmp(forced, s); };
   auto tiles = [&](int64_t bm, int64_t bn) { return (a.M + bm - 1) / bm * ((a.N + bn - 1) / bn); };
-  // Up to 32 rows: stream the weights (16 x 13824 x 5120: 13.6 us, 5.2 TB/s; 64-row tiles 17.6).  From 17
-  // rows on, past 256 workgroups, a ring of two K-steps lets two workgroups share a CU (32 x 13824 x
-  // 5120: 15.0 us, 16.9 with three).
-  // Up to 4096 channels, 16 of them and 8 waves per workgroup still make at most one per CU (16 x 1024 x
-  // 8192: 5.9 us, 7.2 with 32 and 4; 16 x 6144 x 2048: 7.0 and 5.2).
-  if (forced ? is("skinny") && a.M <= 32 : a.M <= 32) {
+  // Up to 32 rows and 4096 channels: stream the weights, 16 channels and 8 waves per workgroup (16 x 1024 x 8192:
+  // 5.9 us, 32 x 32 tiles 7.4; 2 x 4096 x 12288: 10.0 and 12.1).  Up to 8192 channels, 32 and 4 waves, as long as the
+  // weights are short (25 MB: 16 x 6144 x 2048 5.3 and 6.2, 16 x 6144 x 4096 equal, 16 x 6144 x 8192 13.8 and 11.0);
+  // past them the tiles below (16 x 28672 x 4096: 28.7 and 24.1; 16 x 13824 x 1040: 6.6 and 7.0).
+  const bool stream = a.M <= 32 && (a.N <= 4096 || (a.N <= 8192 && (int64_t)a.N * a.K <= 25000000));
+  if (forced ? is("skinny") && a.M <= 32 : stream) {
     if (a.N <= 4096) return a.M <= 16 ? run_skinny<1, 1, 8, 3, YT>(a) : run_skinny<2, 1, 8, 3, YT>(a);
-    if (a.M <= 16) return run_skinny<1, 2, 4, 3, YT>(a);
-    return a.N <= 8192 ? run_skinny<2, 2, 4, 3, YT>(a) : run_skinny<2, 2, 4, 2, YT>(a);
+    return a.M <= 16 ? run_skinny<1, 2, 4, 3, YT>(a) : run_skinny<2, 2, 4, 3, YT>(a);
   }
   // At most one tile per CU: the K loop's latency bounds the launch, and the smallest tile that still leaves
   // every CU at most one wins (128 x 2048 x 2048: 32 x 32 tiles 5.3 us, 64 x 32 6.0, 64 x 64 7.4; 128 x 4096 x
@@ -867,9 +866,11 @@ hipError_t launch_gemm_i8(const void* qact, const float* ascales, const void* qw
   }
 }
 
-bool linear_i8_one_launch(int64_t M, int64_t K) {
+bool linear_i8_one_launch(int64_t M, int64_t N, int64_t K) {
   const char* forced = test_hook("W8A8_ONE_LAUNCH");  // "0" keeps the two launches
-  return M == 1 && K <= 8192 && !(forced && forced[0] == '0');
+  // (past some 110 MB of weights the tiled kernel's loads gain more than the launch costs: 28672 x 8192 46 us in two
+  // launches, 51 in one; 13824 x 5120 15.7 and 13.1)
+  return M == 1 && K <= 8192 && N * K <= 110000000 && !(forced && forced[0] == '0');
 }
 
 hipError_t launch_linear_i8_token(const void* x, int xdtype, const void* lam, int block, float norm,

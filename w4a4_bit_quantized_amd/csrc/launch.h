@@ -87,7 +87,7 @@ hipError_t W4A4_KERNELS launch_gemm_i8(const void* qact, const float* ascales, c
                                        int64_t ldy, int ydtype, hipStream_t stream);
 
 // The whole layer for one token in one launch, for the sizes that linear_i8_one_launch accepts.
-bool W4A4_KERNELS linear_i8_one_launch(int64_t M, int64_t K);
+bool W4A4_KERNELS linear_i8_one_launch(int64_t M, int64_t N, int64_t K);
 hipError_t W4A4_KERNELS launch_linear_i8_token(const void* x, int xdtype, const void* lam, int block, float norm,
                                                const void* qweight, const float* wscales, const void* bias, int64_t N,
                                                int64_t K, void* y, int ydtype, hipStream_t stream);
