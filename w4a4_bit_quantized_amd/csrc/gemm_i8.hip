@@ -190,82 +190,36 @@ __device__ __forceinline__ void i8_interleave_q() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
+// 16 bytes at the alignment of an element.
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x4_t u32x4_a4 __attribute__((aligned(4)));
+
 // A wave's epilogue region (32 rows of FN * 32 elements of ES bytes; 16-byte chunk ch of row r at
-// (ch + r / 2) % CPR) to y rows m0 .., columns n0 ..: 16 bytes per lane where every row of y starts on
-// such a boundary, else 8, else the aligned dwords of each row with single elements at its ends (lanes on
-// consecutive addresses throughout; with eight single elements per lane 3332 x 7413 x 64 took 65 us).
+// (ch + r / 2) % CPR) to y rows m0 .., columns n0 ..: 16 bytes per lane, at any element (the hardware takes them;
+// the aligned dwords of each row, with single elements at its ends, took 2893 x 8595 x 272 51 us, this way 27, and
+// 2893 x 8600 x 272 26; 301 x 4099 x 1552 10.9 and 9.5; eight single elements per lane are slower still).
 template <int FN, int ES>
 __device__ __forceinline__ void store_region(const uint8_t* reg, int lane, uint8_t* y, int64_t ldy, int m0, int n0,
                                              int M, int N) {
   constexpr int RSB = FN * 32 * ES, CPR = RSB / 16;
-  const uint64_t mis = reinterpret_cast<uintptr_t>(y) | ((uint64_t)ldy * ES);
   auto at = [&](int r, int byte) { return reg + r * RSB + 16 * ((byte / 16 + (r >> 1)) % CPR) + byte % 16; };
-  if ((mis & 15) == 0) {
 #pragma unroll
-    for (int it = 0; it < CPR / 2; ++it) {
-      const int c = it * 64 + lane, r = c / CPR, b = 16 * (c % CPR);
-      const int m = m0 + r, n = n0 + b / ES;
-      if (m >= M || n >= N) continue;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(r, b));
-      uint8_t* dst = y + ((size_t)m * ldy + n) * ES;
-      if (n + 16 / ES <= N) {
-        *reinterpret_cast<u32x4_t*>(dst) = v;
-      } else {
+  for (int it = 0; it < CPR / 2; ++it) {
+    const int c = it * 64 + lane, r = c / CPR, b = 16 * (c % CPR);
+    const int m = m0 + r, n = n0 + b / ES;
+    if (m >= M || n >= N) continue;
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(at(r, b));
+    uint8_t* dst = y + ((size_t)m * ldy + n) * ES;
+    if (n + 16 / ES <= N) {
+      if constexpr (ES == 4) *reinterpret_cast<u32x4_a4*>(dst) = v;
+      else *reinterpret_cast<u32x4_a2*>(dst) = v;
+    } else {
 #pragma unroll
-        for (int e = 0; e < 16 / ES; ++e)
-          if (n + e < N) {
-            if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[e] = v[e];
-            else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-          }
-      }
-    }
-  } else if (ES == 2 && (mis & 7) == 0) {
-#pragma unroll 4
-    for (int it = 0; it < CPR; ++it) {
-      const int c = it * 64 + lane, r = c / (2 * CPR), b = 8 * (c % (2 * CPR));
-      const int m = m0 + r, n = n0 + b / 2;
-      if (m >= M || n >= N) continue;
-      const u32x2_t v = *reinterpret_cast<const u32x2_t*>(at(r, b));
-      uint8_t* dst = y + ((size_t)m * ldy + n) * ES;
-      if (n + 4 <= N) {
-        *reinterpret_cast<u32x2_t*>(dst) = v;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (n + e < N) reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-      }
-    }
-  } else {
-    constexpr int DPR = RSB / 4, LPR = DPR % 32 == 0 ? 32 : 16, RPI = 64 / LPR;  // dwords, lanes per row; rows at a time
-    const int r0 = lane / LPR, d0 = lane % LPR, cols = min(FN * 32, N - n0);
-    uint8_t* row = y + ((size_t)(m0 + r0) * ldy + n0) * ES;
-    const size_t step = (size_t)RPI * ldy * ES;
-#pragma unroll
-    for (int it = 0; it < 32 / RPI; ++it, row += step) {
-      const int r = it * RPI + r0;
-      if (m0 + r >= M) continue;
-      if constexpr (ES == 4) {
-#pragma unroll
-        for (int d = d0; d < DPR; d += LPR)
-          if (d < cols) reinterpret_cast<uint32_t*>(row)[d] = *reinterpret_cast<const uint32_t*>(at(r, 4 * d));
-      } else {
-        // elements e and e + 1 share an aligned dword of y; a row that starts inside one leaves its first
-        // element to the first lane
-        uint16_t* out = reinterpret_cast<uint16_t*>(row);
-        const int sh = (int)((reinterpret_cast<uintptr_t>(row) >> 1) & 1);
-        if (sh && d0 == 0 && cols > 0) out[0] = *reinterpret_cast<const uint16_t*>(at(r, 0));
-#pragma unroll
-        for (int d = d0; d < DPR; d += LPR) {
-          const int e = 2 * d + sh;
-          if (e + 1 < cols) {
-            const uint32_t lo = *reinterpret_cast<const uint16_t*>(at(r, 2 * e));
-            const uint32_t hi = *reinterpret_cast<const uint16_t*>(at(r, 2 * e + 2));
-            *reinterpret_cast<uint32_t*>(out + e) = lo | (hi << 16);
-          } else if (e < cols) {
-            out[e] = *reinterpret_cast<const uint16_t*>(at(r, 2 * e));
-          }
+      for (int e = 0; e < 16 / ES; ++e)
+        if (n + e < N) {
+          if constexpr (ES == 4) reinterpret_cast<uint32_t*>(dst)[e] = v[e];
+          else reinterpret_cast<uint16_t*>(dst)[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
         }
-      }
     }
   }
 }
