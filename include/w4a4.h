@@ -383,8 +383,8 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  * negative strides or more than 2^40, offsets past 2^60, outputs whose elements share an address, in
  * place with other strides),
  * W4A4_ERR_NULL, W4A4_ERR_ALIGN (element size).  tokens == 0 or no heads launches nothing.
- * 16-byte aligned pointers and strides, and in the split layouts axes of multiples of 8 elements,
- * take the vectorised path. */
+ * head_dim % 8 == 0, and in the split layouts axes of multiples of 8 elements, take the vectorised path
+ * (at any alignment). */
 #define W4A4_ROPE_INTERLEAVED 0
 #define W4A4_ROPE_HALF 1
 #define W4A4_ROPE_AXIS_HALF 2

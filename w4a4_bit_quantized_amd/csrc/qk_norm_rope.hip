@@ -36,7 +36,12 @@ constexpr int MAX_WGS = 1536;
 template <int DT>
 __device__ __forceinline__ constexpr int esize() { return DT == 2 ? 4 : 2; }
 
-// N consecutive elements (N = 1, 4 or 8; whole vectors are aligned to their size, at most 16 bytes).
+// Vectors at the alignment of an element, which the hardware takes.
+typedef u32x4_t u32x4_a2 __attribute__((aligned(2)));
+typedef u32x2_t u32x2_a2 __attribute__((aligned(2)));
+typedef float4_t float4_a4 __attribute__((aligned(4)));
+
+// N consecutive elements (N = 1, 4 or 8).
 template <int DT, int N>
 __device__ __forceinline__ void load_n(const uint8_t* p, float* v) {
   if constexpr (N == 1) {
@@ -46,18 +51,18 @@ __device__ __forceinline__ void load_n(const uint8_t* p, float* v) {
   } else if constexpr (DT == 2) {
 #pragma unroll
     for (int c = 0; c < N; c += 4) {
-      const float4_t f = *reinterpret_cast<const float4_t*>(p + 4 * c);
+      const float4_t f = *reinterpret_cast<const float4_a4*>(p + 4 * c);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[c + e] = f[e];
     }
   } else {
     uint32_t w[N / 2];
     if constexpr (N == 8) {
-      const u32x4_t f = *reinterpret_cast<const u32x4_t*>(p);
+      const u32x4_t f = *reinterpret_cast<const u32x4_a2*>(p);
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = f[e];
     } else {
-      const u32x2_t f = *reinterpret_cast<const u32x2_t*>(p);
+      const u32x2_t f = *reinterpret_cast<const u32x2_a2*>(p);
       w[0] = f[0];
       w[1] = f[1];
     }
@@ -96,12 +101,12 @@ __device__ __forceinline__ void store_n(uint8_t* p, const float* v) {
   } else if constexpr (DT == 2) {
 #pragma unroll
     for (int c = 0; c < N; c += 4)
-      *reinterpret_cast<float4_t*>(p + 4 * c) = float4_t{v[c], v[c + 1], v[c + 2], v[c + 3]};
+      *reinterpret_cast<float4_a4*>(p + 4 * c) = float4_t{v[c], v[c + 1], v[c + 2], v[c + 3]};
   } else if constexpr (N == 8) {
     __builtin_nontemporal_store(u32x4_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]),
-                                        pack2<DT>(v[6], v[7])}, reinterpret_cast<u32x4_t*>(p));
+                                        pack2<DT>(v[6], v[7])}, reinterpret_cast<u32x4_a2*>(p));
   } else {
-    __builtin_nontemporal_store(u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])}, reinterpret_cast<u32x2_t*>(p));
+    __builtin_nontemporal_store(u32x2_t{pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])}, reinterpret_cast<u32x2_a2*>(p));
   }
 }
 
@@ -149,11 +154,11 @@ __host__ __device__ constexpr int row_stride(int D) { return 2 * D + 16; }
 // INTER (V = 4): the lane's V pairs are 2 V consecutive elements; otherwise V consecutive elements at
 // e0 and V at e1.  IT: chunks of V pairs per lane; UN: items in flight.
 //
-// STAGED (V = 1, IT = 4, UN = 1, 16-bit types): for heads on 16-byte boundaries whose pairs are not.  A lane
-// group loads its head in 16-byte chunks into a row of its own in LDS, takes its pairs from there, puts the
+// STAGED (V = 1, IT = 4, UN = 1, 16-bit types): for heads of whole 16-byte chunks whose pairs are not in whole
+// chunks of 4.  A lane group loads its head in 16-byte chunks into a row of its own in LDS, takes its pairs from there, puts the
 // results in their places and stores the row in chunks again; no other wave touches the row.
 // 32760 tokens of 48 heads of 128, halves of axes of 44, 42 and 42: 178 us, element by element 283 (two items
-// in flight: 206, four: 219).  With 4-byte chunks, for heads of 66 on 4-byte boundaries, it loses: 57 against 52.
+// in flight: 206, four: 219).  In 4-byte chunks, for heads of 66, it loses: 57 against 52.
 template <int DT, int V, bool INTER, int IT, int UN, bool STAGED>
 __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
   static_assert(!STAGED || (DT != 2 && V == 1 && IT == 4 && UN == 1 && !INTER), "the staged form");
@@ -246,7 +251,7 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
         dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
                  (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
         if constexpr (STAGED) {
-          if (valid && has_chunk) *reinterpret_cast<u32x4_t*>(row + 16 * gl) = *reinterpret_cast<const u32x4_t*>(src + 16 * gl);
+          if (valid && has_chunk) *reinterpret_cast<u32x4_t*>(row + 16 * gl) = *reinterpret_cast<const u32x4_a2*>(src + 16 * gl);
           wave_lds_sync();
           src = row;
         }
@@ -318,7 +323,7 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
           wave_lds_sync();
           if (has_chunk)
             __builtin_nontemporal_store(*reinterpret_cast<const u32x4_t*>(row + 16 * gl),
-                                        reinterpret_cast<u32x4_t*>(dst[u] + 16 * gl));
+                                        reinterpret_cast<u32x4_a2*>(dst[u] + 16 * gl));
           wave_lds_sync();  // the row is written again
         }
       }
@@ -338,10 +343,10 @@ hipError_t run(const RopeArgs& a, hipStream_t st) {
 
 template <int DT>
 hipError_t run_dt(RopeArgs a, bool vec, bool staged, hipStream_t st) {
-  // Element-wise heads: 4 pairs per lane, or 2 of 2 items up to D = 128 where the lanes are still many
-  // (8000 tokens of 32 heads of 128, bf16: 53 us with 2, 60 with 4; 2071 tokens of 72 heads of 72, f16: 30 and
-  // 25; 16000 heads of 64, f32: 38 and 53; one pair per lane took 67, 39 and 39).
-  const bool two = !vec && !(staged && DT != 2) && a.D <= 128 && (a.D > 96 || DT == 2);
+  // Element-wise heads: 4 pairs per lane, in f32 with 49 to 64 of them 2 of 2 items (8000 tokens of 48 heads of 128,
+  // halves of axes of 44, 42 and 42, f32: 94 us with 2, 105 with 4; of 66, f32: 74 and 64; 40 heads of 126, bf16: 68
+  // and 67; 48 heads of 34, f16: 29 and 24).
+  const bool two = DT == 2 && !vec && a.D > 96 && a.D <= 128;
   const int lanes = vec ? a.D / 8 : two ? (a.D / 2 + 1) / 2 : (a.D / 2 + 3) / 4;
   a.log2g = 0;
   while ((1 << a.log2g) < lanes) ++a.log2g;
@@ -356,30 +361,25 @@ hipError_t run_dt(RopeArgs a, bool vec, bool staged, hipStream_t st) {
   a.tb = full < 1 ? 1 : full > 8 ? 8 : full;
   if (per < a.tb) a.tb = (int)per;
   if (vec) return a.layout == 0 ? run<DT, 4, true, 1, 2, false>(a, st) : run<DT, 4, false, 1, 2, false>(a, st);
-  if constexpr (DT != 2)
+  if constexpr (DT == 2) {
+    if (two) return run<DT, 1, false, 2, 2, false>(a, st);
+  } else {
     if (staged) return run<DT, 1, false, 4, 1, true>(a, st);
-  return two ? run<DT, 1, false, 2, 2, false>(a, st) : run<DT, 1, false, 4, 1, false>(a, st);
-}
-
-// The address bits of every element that a tensor's heads start at.
-uint64_t low_bits(const RopeHeads& h, int es) {
-  if (h.heads == 0) return 0;
-  return reinterpret_cast<uintptr_t>(h.x) | reinterpret_cast<uintptr_t>(h.y) |
-         ((uint64_t)(h.ts | h.hs | h.yts | h.yhs) * (uint64_t)es);
+  }
+  return run<DT, 1, false, 4, 1, false>(a, st);
 }
 
 }  // namespace
 
 hipError_t launch_qk_norm_rope(RopeArgs a, int dtype, hipStream_t stream) {
-  const int es = dtype == 2 ? 4 : 2;
-  // heads of whole 16-byte chunks on 16-byte boundaries; 4-pair vectors also need such weights, and in the
-  // split layouts whole chunks of 4 pairs in the span and in every slice
-  const bool chunks = a.D % 8 == 0 && ((low_bits(a.q, es) | low_bits(a.k, es)) & 15) == 0;
-  bool vec = chunks && ((reinterpret_cast<uintptr_t>(a.q.weight) | reinterpret_cast<uintptr_t>(a.k.weight)) & 15) == 0;
+  // 4-pair vectors need whole 8-element chunks of the head, and in the split layouts whole chunks of 4 pairs in
+  // the span and in every slice
+  bool vec = a.D % 8 == 0;
   if (a.layout == 1) vec = vec && a.rot2 % 4 == 0;
   if (a.layout == 2)
     for (int x = 0; x < a.axes; ++x) vec = vec && a.start[x + 1] % 4 == 0;
-  const bool staged = chunks && !vec;  // (16-bit types; one token of 40 heads: 5.1 us, element by element 4.6; 300 tokens: 6.6 and 7.2)
+  // (16-bit types; one token of 40 heads: 5.1 us, element by element 4.6; 300 tokens: 6.6 and 7.2)
+  const bool staged = a.D % 8 == 0 && !vec;
   switch (dtype) {
     case 0: return run_dt<0>(a, vec, staged, stream);
     case 1: return run_dt<1>(a, vec, staged, stream);
