@@ -604,10 +604,11 @@ def _dense(t, name, dtype, shape, dev):
 def _on(dev, call, *args):
     """``call(*args, stream)`` with ``dev`` current and its current stream (a stream launches on its own
     device only while that device is current)."""
-    torch = _torch()
+    torch = _TORCH
+    index = dev.index
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the stream's handle without a Stream object
-    stream = raw(dev.index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev.index:
+    stream = raw(index) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    if torch.cuda.current_device() == index:
         return call(*args, stream)
     with torch.cuda.device(dev):
         return call(*args, stream)
@@ -619,11 +620,11 @@ def _addr(t):
 
 def _w8a8_rows(t, name):
     """(rows, K, row stride, dtype code, device) of a quantizer input."""
+    if isinstance(t, _torch().Tensor) and t.is_cuda and t.dim() == 2 and t.is_contiguous():
+        rows, K = t.shape
+        return rows, K, K, _dtype_code(t.dtype, name), t.device
     dev = _device_tensor(t, name)
     code = _dtype_code(t.dtype, name)
-    shape = t.shape
-    if len(shape) == 2 and t.is_contiguous():
-        return shape[0], shape[1], shape[1], code, dev
     rows, K, ld = _rows_view(t, name)
     return rows, K, ld, code, dev
 
@@ -635,8 +636,8 @@ def _check_smooth(smooth_factor, K, dev):
 
 def _check_w8a8_weights(qweight, wscales, bias, K, dev):
     torch = _torch()
-    _device_tensor(qweight, "qweight")
-    if qweight.dim() != 2:
+    if not isinstance(qweight, torch.Tensor) or qweight.dim() != 2:
+        _device_tensor(qweight, "qweight")
         raise ValueError(f"qweight must be 2-D (N, K), got shape {tuple(qweight.shape)}")
     N = qweight.shape[0]
     _dense(qweight, "qweight", torch.int8, (N, K), dev)
@@ -646,12 +647,17 @@ def _check_w8a8_weights(qweight, wscales, bias, K, dev):
     return N
 
 
-def _w8a8_out(out, lead, M, N, out_dtype, default, dev):
-    """(y, its row stride, its dtype code): `out` checked, or a new tensor (*lead, N)."""
+def _w8a8_out(out, x, M, N, out_dtype, default, dev):
+    """(y, its row stride, its dtype code): `out` checked, or a new tensor with x's leading dimensions."""
     if out is None:
         dtype = default if out_dtype is None else out_dtype
         code = _dtype_code(dtype, "out_dtype")
-        return _torch().empty((*lead, N), dtype=dtype, device=dev), N, code
+        shape = (M, N) if x.dim() == 2 else (*x.shape[:-1], N)
+        return x.new_empty(shape) if dtype is x.dtype else x.new_empty(shape, dtype=dtype), N, code
+    if (isinstance(out, _torch().Tensor) and out.device == dev and out.shape == (M, N) and out.is_contiguous()
+            and (out_dtype is None or out.dtype is out_dtype)):
+        return out, N, _dtype_code(out.dtype, "out")
+    lead = x.shape[:-1]
     if _device_tensor(out, "out") != dev:
         raise ValueError(f"out is on {out.device}, expected {dev}")
     if out_dtype is not None and out.dtype != out_dtype:
@@ -708,7 +714,7 @@ def w8a8_gemm(qact, ascales, qweight, wscales, bias=None, out=None, out_dtype=No
     _dense(qact, "qact", torch.int8, (M, K), dev)
     _dense(ascales, "ascales", torch.float32, (M,), dev)
     N = _check_w8a8_weights(qweight, wscales, bias, K, dev)
-    y, ldy, code = _w8a8_out(out, (M,), M, N, out_dtype, torch.bfloat16, dev)
+    y, ldy, code = _w8a8_out(out, qact, M, N, out_dtype, torch.bfloat16, dev)
     st = _on(dev, lib.w8a8_gemm, qact.data_ptr(), ascales.data_ptr(), qweight.data_ptr(), wscales.data_ptr(),
              _addr(bias), M, N, K, y.data_ptr(), ldy, code)
     _check(st, "w8a8_gemm")
@@ -729,15 +735,18 @@ def w8a8_linear(x, layer, hadamard_block=0, workspace=None, out=None, out_dtype=
     _check_smooth(smooth, K, dev)
     qweight, wscales = layer["qweight"], layer["wscales"]
     N = _check_w8a8_weights(qweight, wscales, bias, K, dev)
-    y, ldy, ycode = _w8a8_out(out, x.shape[:-1], M, N, out_dtype, x.dtype, dev)
+    y, ldy, ycode = _w8a8_out(out, x, M, N, out_dtype, x.dtype, dev)
     need = lib.w8a8_linear_workspace_bytes(M, K)
     if workspace is None:
         workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
     else:
-        _dev(workspace, "workspace", (torch.uint8,), dev)
-        need = workspace.numel()
-        if need < lib.w8a8_linear_workspace_bytes(M, K):
-            raise ValueError(f"workspace holds {need} bytes, the call needs {lib.w8a8_linear_workspace_bytes(M, K)}")
+        if not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.device == dev
+                and workspace.is_contiguous()):
+            _dev(workspace, "workspace", (torch.uint8,), dev)
+        size = workspace.numel()
+        if size < need:
+            raise ValueError(f"workspace holds {size} bytes, the call needs {need}")
+        need = size
     st = _on(dev, lib.w8a8_linear, x.data_ptr(), ldx, code, qweight.data_ptr(), wscales.data_ptr(), _addr(smooth),
              _addr(bias), M, N, K, int(hadamard_block), y.data_ptr(), ldy, ycode, workspace.data_ptr(), need)
     _check(st, "w8a8_linear")
