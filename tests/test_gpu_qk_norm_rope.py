@@ -269,6 +269,43 @@ def test_empty_and_refused_calls(w4):
         w4.qk_norm_rope(torch.zeros((2, 8, 2, 64), device="cuda")[:, :2], None, p, [64])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D,dims", [(128, [44, 42, 42]), (64, [20, 2]), (96, [32, 64]), (90, [30, 60])])
+def test_every_alignment(w4, dtype, D, dims):
+    """Heads, strides, weights and outputs at element offsets 0 .. 8, in place too; the elements around the heads
+    stay as they were."""
+    import torch
+    rng = np.random.default_rng(D)
+    T, hq, hk = 9, 3, 2
+    q, k, wq, wk = make(rng, T, hq, D, dtype), make(rng, T, hk, D, dtype), weights(rng, D, dtype), weights(rng, D, dtype)
+    pos = rng.integers(0, 500, (T, len(dims)))
+    pt = torch.from_numpy(pos.astype(np.int32)).cuda()
+    for off in range(9):
+        pad = off % 3  # elements between the heads
+        big = torch.full((T + 1, off + (hq + hk) * (D + pad) + 1), 5.0, dtype=tdtype(dtype), device="cuda")
+        heads = big[:T, off:off + (hq + hk) * (D + pad)].unflatten(1, (hq + hk, D + pad))[..., :D]
+        heads[:, :hq], heads[:, hq:] = dev(q, dtype), dev(k, dtype)
+        w = torch.full((2 * D + 9,), 5.0, dtype=tdtype(dtype), device="cuda")
+        w[off:off + D], w[off + D:off + 2 * D] = dev(wq, dtype), dev(wk, dtype)
+        before = big.clone()
+        outs = torch.zeros_like(big)
+        to = outs[:T, off:off + (hq + hk) * (D + pad)].unflatten(1, (hq + hk, D + pad))[..., :D]
+        for layout in LAYOUTS:
+            big.copy_(before)
+            a, b = w4.qk_norm_rope(heads[:, :hq], heads[:, hq:], pt, dims, w[off:off + D], w[off + D:off + 2 * D],
+                                   layout=layout, q_out=to[:, :hq], k_out=to[:, hq:])
+            assert torch.equal(big, before)
+            check(a, q, pos, dims, dtype, wq, layout, what=f"q off {off}")
+            check(b, k, pos, dims, dtype, wk, layout, what=f"k off {off}")
+            w4.qk_norm_rope(heads[:, :hq], heads[:, hq:], pt, dims, w[off:off + D], w[off + D:off + 2 * D], layout=layout,
+                            inplace=True)
+            assert torch.equal(heads, to)
+            heads.copy_(before[:T, off:off + (hq + hk) * (D + pad)].unflatten(1, (hq + hk, D + pad))[..., :D])
+            assert torch.equal(big, before), "elements around the heads were written"
+        to.zero_()
+        assert not bool(outs.any()), "elements around the output heads were written"
+
+
 def test_one_tensor_as_q_and_k(w4):
     """One input for both (with different weights), broadcast tokens and heads, on two streams at once."""
     import torch
