@@ -317,6 +317,38 @@ def test_linear_one_token(w4, hooks, K, xd):
             same_bits(host(y), ref, f"K={K} N={N} {xd} {yd} one launch {mode}")
 
 
+@pytest.mark.parametrize("M", [2, 3, 4, 5])
+@pytest.mark.parametrize("K", [16, 400, 2048, 4112, 6144, 8192])
+def test_linear_few_tokens(w4, hooks, M, K):
+    """A few tokens (one launch up to 4): strided input and output rows, a zero row and a NaN row among them, with and
+    without smoothing, rotation and bias, against the oracle and the two-launch layer."""
+    import torch
+    rng = np.random.default_rng(M * K)
+    for N, block, xd, yd, smooth in ((37, 16, "bf16", "f32", True), (300, 128 if K % 128 == 0 else 0, "f16", "bf16", False),
+                                     (4099, 0, "f32", "f16", True)):
+        x, lam = rows(rng, M, K, xd), factors(rng, K)
+        xf = oh.to_f32(x, xd).copy()
+        xf[M // 2] = 0
+        if N == 37:
+            xf[M - 1, K // 3] = np.nan
+        x = oh.from_f32(xf, xd)
+        qw, sw = codes(rng, N, K), rng.uniform(0.001, 0.01, N).astype(np.float32)
+        b = oh.from_f32(rng.uniform(-1, 1, N).astype(np.float32), "bf16") if block else None
+        layer = dict(qweight=torch.from_numpy(qw).cuda(), wscales=torch.from_numpy(sw).cuda(),
+                     smooth_factor=dev(lam, "bf16") if smooth else None, bias=None if b is None else dev(b, "bf16"))
+        ref = oh.from_f32(ow.linear_f32(xf, qw, sw, oh.to_f32(lam, "bf16") if smooth else None,
+                                        None if b is None else oh.to_f32(b, "bf16"), block), yd)
+        wide = torch.zeros((M, K + 24), dtype=tdtype(xd), device="cuda")
+        wide[:, 8:8 + K] = dev(x, xd)
+        for mode in ("1", "0"):
+            hooks.setenv("W8A8_ONE_LAUNCH", mode)
+            big = torch.full((M + 1, N + 5), 7.0, dtype=tdtype(yd), device="cuda")
+            y = w4.w8a8_linear(wide[:, 8:8 + K], layer, hadamard_block=block, out=big[:M, 3:3 + N])
+            same_bits(host(y), ref, f"M={M} K={K} N={N} {xd} {yd} one launch {mode}")
+            big[:M, 3:3 + N] = 7.0
+            assert bool((big == 7.0).all()), "elements around the output were written"
+
+
 def test_linear_one_token_extreme_factors(w4):
     """Smoothing factors outside the two-part division's range, in the one-launch layer."""
     import torch

@@ -493,9 +493,9 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
   if (x && x == y) return W4A4_ERR_SHAPE;
   if (w4a4::linear_i8_one_launch && w4a4::linear_i8_one_launch(M, N, K)) {
     (void)hipGetLastError();
-    return from_hip(w4a4::launch_linear_i8_token(x, x_dtype, smooth_factor, hadamard_block,
-                                                 rotation_norm(hadamard_block), qweight, wscales, bias, N, K, y, y_dtype,
-                                                 static_cast<hipStream_t>(stream)));
+    return from_hip(w4a4::launch_linear_i8_token(x, ldx, x_dtype, smooth_factor, hadamard_block,
+                                                 rotation_norm(hadamard_block), qweight, wscales, bias, M, N, K, y, ldy,
+                                                 y_dtype, static_cast<hipStream_t>(stream)));
   }
   st = quantize_w8a8(true, x, ldx, x_dtype, smooth_factor, M, K, hadamard_block, ws, ascales, stream);
   if (st != W4A4_OK) return st;

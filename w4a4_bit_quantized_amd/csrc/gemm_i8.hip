@@ -554,13 +554,13 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
   }
 }
 
-// ---- one token: quantizer and weight streaming in one launch ---------------------------------------
-// Each workgroup (KW waves, 16 NB channels) starts its weight rings, quantizes the token itself (it is in L2,
-// and its arithmetic hides behind the first weights' way from HBM) into codes in LDS, and goes on as the
+// ---- up to four tokens: quantizer and weight streaming in one launch ---------------------------------
+// Each workgroup (KW waves, 16 NB channels) starts its weight rings, quantizes the tokens itself (they are in L2,
+// and the arithmetic hides behind the first weights' way from HBM) into codes in LDS, and goes on as the
 // streaming kernel above with the activation operand read from there.  Every workgroup repeats the
-// quantizer's work; what is saved is a launch and the wait between the two (2048 x 6144: 7.2 to 5.2 us,
-// 5120 x 13824: 15.7 to 13.1, and 3 us of the host's time; with two tokens 5120 x 13824 takes 17.2 us
-// this way and 16.2 in two launches).  The codes are those of the quantizer kernel bit for bit.
+// quantizer's work; what is saved is a launch and the wait between the two (1 x 6144 x 2048: 7.3 to 5.3 us, 4 x 4096 x
+// 4096: 8.4 to 7.5, 4 x 13824 x 5120: 15.9 to 15.3), and 3 us of the host's time.  The codes are those of the quantizer
+// kernel bit for bit.
 constexpr int TK_S = 3;
 
 struct TokenArgs {
@@ -571,8 +571,10 @@ struct TokenArgs {
   const uint8_t* qw;
   const float* sw;
   const uint16_t* bias;
+  int64_t ldx;
   int N, K, ydtype;
   void* y;
+  int64_t ldy;
 };
 
 template <int NB>
@@ -594,12 +596,12 @@ __device__ __forceinline__ void token_mma(i32x4_t (&acc)[NB], const i32x4_t (&a)
     for (int j = 0; j < NB; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][j], a[s], acc[j], 0, 0, 0);
 }
 
-// C: chunks of 8 columns per thread, 512 KW C >= K.
-template <int DT, bool ROT, int C, int NB, int KW>
+// C: chunks of 8 columns per thread, 512 KW C >= K; MT: tokens.
+template <int DT, bool ROT, int C, int NB, int KW, int MT>
 __global__ __launch_bounds__(64 * KW) void linear_i8_token_kernel(const TokenArgs p) {
   constexpr int STAGE = 2048 * NB, COLS = 512 * KW;  // bytes of a K-step's weight rows; columns of one chunk each
   extern __shared__ __attribute__((aligned(16))) uint8_t dyn[];
-  __shared__ uint32_t red[KW];
+  __shared__ uint32_t red[MT][KW];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int l16 = lane & 15, g = lane >> 4;
@@ -622,11 +624,16 @@ __global__ __launch_bounds__(64 * KW) void linear_i8_token_kernel(const TokenArg
   }
 
   const int tc = 8 * (ROT ? chunk_of(t) : t);
-  float v[C][8];
+  const size_t es = DT == 2 ? 4 : 2;
+  float v[MT][C][8];
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int k = COLS * c + tc;
-    widen8<DT>(k < K ? load_raw<DT>(p.x, k) : zero_raw<DT>(), v[c]);
+  for (int r = 0; r < MT; ++r) {
+    const uint8_t* xr = static_cast<const uint8_t*>(p.x) + (size_t)r * p.ldx * es;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int k = COLS * c + tc;
+      widen8<DT>(k < K ? load_raw<DT>(xr, k) : zero_raw<DT>(), v[r][c]);
+    }
   }
   if (p.lam != nullptr) {
 #pragma unroll
@@ -638,32 +645,44 @@ __global__ __launch_bounds__(64 * KW) void linear_i8_token_kernel(const TokenArg
       if (k < K) lambda8(p.lam, k, l);
       if (__all(reciprocals8(l, rh, rl))) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = fmaf(v[c][i], rh[i], v[c][i] * rl[i]);
+        for (int r = 0; r < MT; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[r][c][i] = fmaf(v[r][c][i], rh[i], v[r][c][i] * rl[i]);
       } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[c][i] = v[c][i] / l[i];
+        for (int r = 0; r < MT; ++r)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[r][c][i] = v[r][c][i] / l[i];
       }
     }
   }
-  if (ROT) rotate<C>(v, p.block, lane);
-  const uint32_t mx = chunk_max<C>(v), mw = wave_max2(mx, mx);
-  if (lane == 0) red[wave] = mw;
+  const int kp = (K + 127) / 128 * 128 + 16;  // bytes of a token's codes
+#pragma unroll
+  for (int r = 0; r < MT; ++r) {
+    if (ROT) rotate<C>(v[r], p.block, lane);
+    const uint32_t mx = chunk_max<C>(v[r]), mw = wave_max2(mx, mx);
+    if (lane == 0) red[r][wave] = mw;
+  }
   // (LDS only: the weights in flight are not waited for)
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  uint32_t bits = 0;
+  const float sign = ROT ? lane_sign(lane, p.block) : 1.0f;
 #pragma unroll
-  for (int w = 0; w < KW; ++w) bits = max(bits, red[w]);
-  const float inv = row_inv(bits, p.norm) * (ROT ? lane_sign(lane, p.block) : 1.0f);
+  for (int r = 0; r < MT; ++r) {
+    uint32_t bits = 0;
 #pragma unroll
-  for (int c = 0; c < C; ++c) {
-    const int k = COLS * c + tc;
-    if (k < K) *reinterpret_cast<u32x2_t*>(codes + k) = codes8(v[c], inv);
+    for (int w = 0; w < KW; ++w) bits = max(bits, red[r][w]);
+    const float inv = row_inv(bits, p.norm) * sign;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int k = COLS * c + tc;
+      if (k < K) *reinterpret_cast<u32x2_t*>(codes + r * kp + k) = codes8(v[r][c], inv);
+    }
   }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 
-  // all 16 activation rows of the instruction are the token (one column of the product is stored); columns
-  // past K, up to the K-step's end, meet zero weights
-  const uint8_t* arow = codes + 16 * g;
+  // the activation rows past the tokens repeat the last one and are not stored; columns past K, up to the
+  // K-step's end, meet zero weights
+  const uint8_t* arow = codes + min(l16, MT - 1) * kp + 16 * g;
   i32x4_t acc[NB];
 #pragma unroll
   for (int j = 0; j < NB; ++j) acc[j] = i32x4_t{0, 0, 0, 0};
@@ -691,33 +710,39 @@ __global__ __launch_bounds__(64 * KW) void linear_i8_token_kernel(const TokenArg
   int* part = reinterpret_cast<int*>(dyn);
 #pragma unroll
   for (int j = 0; j < NB; ++j)
-    if (l16 == 0) *reinterpret_cast<i32x4_t*>(part + wave * 16 * NB + 16 * j + 4 * g) = acc[j];
+    if (l16 < MT) *reinterpret_cast<i32x4_t*>(part + (wave * MT + l16) * 16 * NB + 16 * j + 4 * g) = acc[j];
   __syncthreads();
-  const int n = n0 + t;
-  if (t < 16 * NB && n < N) {
+  const int r = t / (16 * NB), n = n0 + t % (16 * NB);
+  if (r < MT && n < N) {
     int sum = 0;
+    uint32_t bits = 0;
 #pragma unroll
-    for (int w = 0; w < KW; ++w) sum += part[w * 16 * NB + t];
+    for (int w = 0; w < KW; ++w) {
+      sum += part[(w * MT + r) * 16 * NB + t % (16 * NB)];
+      bits = max(bits, red[r][w]);
+    }
     float f = ((float)sum * row_scale(bits, p.norm)) * p.sw[n];
     if (p.bias != nullptr) f += bf16_bits_to_f32(p.bias[n]);
-    if (p.ydtype == 2) store_one<2>(p.y, n, f);
-    else if (p.ydtype == 1) store_one<1>(p.y, n, f);
-    else store_one<0>(p.y, n, f);
+    const size_t at = (size_t)r * p.ldy + n;
+    if (p.ydtype == 2) store_one<2>(p.y, at, f);
+    else if (p.ydtype == 1) store_one<1>(p.y, at, f);
+    else store_one<0>(p.y, at, f);
   }
 }
 
-template <int DT, bool ROT, int C, int NB, int KW>
+template <int DT, bool ROT, int C, int NB, int KW, int MT>
 hipError_t run_token_c(const TokenArgs& a, hipStream_t stream) {
-  const size_t lds = KW * TK_S * 2048 * NB + (size_t)(a.K + 127) / 128 * 128;
-  linear_i8_token_kernel<DT, ROT, C, NB, KW><<<dim3((unsigned)((a.N + 16 * NB - 1) / (16 * NB))), 64 * KW, lds, stream>>>(a);
+  static_assert(MT * 16 * NB <= 64 * KW, "a thread for every output");
+  const size_t lds = KW * TK_S * 2048 * NB + MT * ((size_t)(a.K + 127) / 128 * 128 + 16);
+  linear_i8_token_kernel<DT, ROT, C, NB, KW, MT><<<dim3((unsigned)((a.N + 16 * NB - 1) / (16 * NB))), 64 * KW, lds, stream>>>(a);
   return hipGetLastError();
 }
 
-template <int DT, bool ROT>
+template <int DT, bool ROT, int MT>
 hipError_t run_token(const TokenArgs& a, hipStream_t stream) {
   // (the split of the streaming kernel: see run)
-  if (a.N <= 4096) return a.K <= 4096 ? run_token_c<DT, ROT, 1, 1, 8>(a, stream) : run_token_c<DT, ROT, 2, 1, 8>(a, stream);
-  return a.K <= 4096 ? run_token_c<DT, ROT, 2, 2, 4>(a, stream) : run_token_c<DT, ROT, 4, 2, 4>(a, stream);
+  if (a.N <= 4096) return a.K <= 4096 ? run_token_c<DT, ROT, 1, 1, 8, MT>(a, stream) : run_token_c<DT, ROT, 2, 1, 8, MT>(a, stream);
+  return a.K <= 4096 ? run_token_c<DT, ROT, 2, 2, 4, MT>(a, stream) : run_token_c<DT, ROT, 3, 2, 4, MT>(a, stream);
 }
 
 struct GArgs {
@@ -825,20 +850,31 @@ hipError_t launch_gemm_i8(const void* qact, const float* ascales, const void* qw
 
 bool linear_i8_one_launch(int64_t M, int64_t N, int64_t K) {
   const char* forced = test_hook("W8A8_ONE_LAUNCH");  // "0" keeps the two launches
-  // (past some 110 MB of weights the tiled kernel's loads gain more than the launch costs: 28672 x 8192 46 us in two
-  // launches, 51 in one; 13824 x 5120 15.7 and 13.1)
-  return M == 1 && K <= 8192 && N * K <= 110000000 && !(forced && forced[0] == '0');
+  // (with 32 channels per workgroup long rows cost more than the launch: 4 x 6144 x 5120 10.1 us in one launch and 11.3 in
+  // two, x 8192 15.8 and 13.7; the number of channels does not matter: 1 x 128256 x 2048 46.7 and 55.9)
+  const bool small = K <= (N <= 4096 ? 8192 : 6144);
+  return M <= 4 && small && !(forced && forced[0] == '0');
 }
 
-hipError_t launch_linear_i8_token(const void* x, int xdtype, const void* lam, int block, float norm,
-                                  const void* qweight, const float* wscales, const void* bias, int64_t N, int64_t K,
-                                  void* y, int ydtype, hipStream_t stream) {
-  const TokenArgs a{x, static_cast<const uint16_t*>(lam), block, norm, static_cast<const uint8_t*>(qweight),
-                    wscales, static_cast<const uint16_t*>(bias), (int)N, (int)K, ydtype, y};
+template <int MT>
+hipError_t run_token_m(const TokenArgs& a, int xdtype, hipStream_t stream) {
   switch (xdtype) {
-    case 0: return block ? run_token<0, true>(a, stream) : run_token<0, false>(a, stream);
-    case 1: return block ? run_token<1, true>(a, stream) : run_token<1, false>(a, stream);
-    default: return block ? run_token<2, true>(a, stream) : run_token<2, false>(a, stream);
+    case 0: return a.block ? run_token<0, true, MT>(a, stream) : run_token<0, false, MT>(a, stream);
+    case 1: return a.block ? run_token<1, true, MT>(a, stream) : run_token<1, false, MT>(a, stream);
+    default: return a.block ? run_token<2, true, MT>(a, stream) : run_token<2, false, MT>(a, stream);
+  }
+}
+
+hipError_t launch_linear_i8_token(const void* x, int64_t ldx, int xdtype, const void* lam, int block, float norm,
+                                  const void* qweight, const float* wscales, const void* bias, int64_t M, int64_t N,
+                                  int64_t K, void* y, int64_t ldy, int ydtype, hipStream_t stream) {
+  const TokenArgs a{x, static_cast<const uint16_t*>(lam), block, norm, static_cast<const uint8_t*>(qweight), wscales,
+                    static_cast<const uint16_t*>(bias), ldx, (int)N, (int)K, ydtype, y, ldy};
+  switch (M) {
+    case 1: return run_token_m<1>(a, xdtype, stream);
+    case 2: return run_token_m<2>(a, xdtype, stream);
+    case 3: return run_token_m<3>(a, xdtype, stream);
+    default: return run_token_m<4>(a, xdtype, stream);
   }
 }
 

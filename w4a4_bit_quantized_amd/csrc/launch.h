@@ -86,11 +86,12 @@ hipError_t W4A4_KERNELS launch_gemm_i8(const void* qact, const float* ascales, c
                                        const float* wscales, const void* bias, int64_t M, int64_t N, int64_t K, void* y,
                                        int64_t ldy, int ydtype, hipStream_t stream);
 
-// The whole layer for one token in one launch, for the sizes that linear_i8_one_launch accepts.
+// The whole layer for a few tokens in one launch, for the sizes that linear_i8_one_launch accepts.
 bool W4A4_KERNELS linear_i8_one_launch(int64_t M, int64_t N, int64_t K);
-hipError_t W4A4_KERNELS launch_linear_i8_token(const void* x, int xdtype, const void* lam, int block, float norm,
-                                               const void* qweight, const float* wscales, const void* bias, int64_t N,
-                                               int64_t K, void* y, int ydtype, hipStream_t stream);
+hipError_t W4A4_KERNELS launch_linear_i8_token(const void* x, int64_t ldx, int xdtype, const void* lam, int block,
+                                               float norm, const void* qweight, const float* wscales,
+                                               const void* bias, int64_t M, int64_t N, int64_t K, void* y, int64_t ldy,
+                                               int ydtype, hipStream_t stream);
 
 // Heads of one tensor of qk_norm_rope: element (token, head, d) at x + token ts + head hs + d.
 struct RopeHeads {
