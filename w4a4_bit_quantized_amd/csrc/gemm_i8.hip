@@ -767,7 +767,7 @@ hipError_t run_tile(const GArgs& a) {
   return hipGetLastError();
 }
 
-// S stages where rows are whole lines, S2 where they are not (unless lines are not to be looked at).
+// S stages where rows are whole 128-byte lines, S2 where they are not.
 template <int WAVES_M, int WAVES_N, int FM, int FN, int S, int S2, int KG, int YT>
 hipError_t run_lines(const GArgs& a, bool lines) {
   return lines ? run_tile<WAVES_M, WAVES_N, FM, FN, S, KG, 4, false, YT>(a)
