@@ -382,3 +382,41 @@ def test_projection_then_norm_and_rotation(w4):
     w4.hadamard_transform(qkv[:, :(hq + hk) * D], block=D, inplace=True)
     assert np.array_equal(host(qkv[:, :(hq + hk) * D]), oh.hadamard_transform(turned, D, "bf16"))
     assert torch.equal(qkv[:, (hq + hk) * D:], v)
+
+
+def turned_units(w4, dims, layout, theta, shared, pos, D, sin_cos):
+    """The rotation of (1, 0) and of (0, 1) in every pair, in f32: its outputs are the kernel's cosines and sines as
+    they are.  Each is checked against 64 bits within ``sin_cos(value, largest angle of the token)``."""
+    import torch
+    table = orope.pair_table(dims, layout, shared)
+    x = np.zeros((len(pos), 2, D), np.float32)
+    for e0, e1, _, _ in table:
+        x[:, 0, e0] = x[:, 1, e1] = 1.0
+    y = host(w4.qk_norm_rope(torch.from_numpy(x).cuda(), None, torch.from_numpy(pos).cuda(), dims, norm=False,
+                             theta=theta, layout=layout, shared_frequencies=shared)).astype(np.float64)
+    ref, _ = orope.norm_rope(x, pos, dims, theta=theta, layout=layout, shared=shared, norm=False)
+    far = np.zeros(len(pos))
+    for _, _, a, ex in table:
+        far = np.maximum(far, np.abs(pos[:, a].astype(np.float64)) * theta ** -ex)
+    off = np.abs(y - ref) / sin_cos(np.abs(ref), far[:, None, None])
+    at = np.unravel_index(np.argmax(off), off.shape)
+    assert off[at] <= 1, f"D={D} axes={dims} {layout} theta={theta}: {off[at]:.1f} times the bound at {at}: {y[at]} for {ref[at]}"
+
+
+# A cosine or sine of its own: sincospi 2 units in the last place (4 * 2^-24 of the value), the step from the argument
+# that sincospi gets, rounded to float32, to the whole one half a unit (2^-24 of the value).  That step is at most pi 2^-25
+# times the other of the two, whose own roundings and its square's half are below 4e-14.  The float64 angle: 6 * 2^-53
+# of the token's largest.
+def own_size(value, far):
+    return 5 * 2.0 ** -24 * value + 4e-14 + 6 * 2.0 ** -53 * far
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+def test_small_sines_and_cosines(w4, layout):
+    """Sines and cosines next to multiples of a quarter turn are as accurate as their own size asks for, which the
+    float32 rounding of the angle alone would not leave."""
+    pos = np.concatenate([np.arange(-1000, 1001), [31, 355, 710, 103993]]).astype(np.int32)[:, None]
+    for D, dims in ((64, [64]), (2, [2]), (34, [34]), (128, [126]), (512, [512])):
+        turned_units(w4, dims, layout, 10000.0, False, pos, D, own_size)
+    two = np.concatenate([pos, pos[::-1]], 1)
+    turned_units(w4, [44, 20], layout, 10000.0, True, two, 64, own_size)
