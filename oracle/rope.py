@@ -13,7 +13,8 @@ import numpy as np
 
 
 def pair_table(axis_dims, layout, shared):
-    """[(e0, e1, axis, exponent)] of every pair; the pair turns by pos[axis] * theta^-exponent."""
+    """[(e0, e1, axis, exponent)] of every pair; the pair turns by pos[axis] * theta^-exponent.  (The exponents in
+    extended precision too: rounded to float64, 2 i / 40 moves the angle by up to ln(theta) 2^-54 of itself.)"""
     rot = sum(axis_dims)
     out = []
     base = 0
@@ -22,7 +23,7 @@ def pair_table(axis_dims, layout, shared):
             p = base // 2 + i
             e0, e1 = {"interleaved": (2 * p, 2 * p + 1), "half": (p, p + rot // 2),
                       "axis_half": (base + i, base + i + d // 2)}[layout]
-            out.append((e0, e1, a, 2.0 * p / rot if shared else 2.0 * i / d))
+            out.append((e0, e1, a, np.longdouble(2 * p) / rot if shared else np.longdouble(2 * i) / d))
         base += d
     return out
 
@@ -41,7 +42,7 @@ def norm_rope(x, positions, axis_dims, weight=None, eps=1e-6, theta=10000.0, lay
         e0 = [t[0] for t in table]
         e1 = [t[1] for t in table]
         pos = np.asarray(positions).reshape(len(u), len(axis_dims)).astype(np.longdouble)
-        freq = np.array([np.longdouble(theta) ** -np.longdouble(t[3]) for t in table], np.longdouble)
+        freq = np.array([np.longdouble(theta) ** -t[3] for t in table], np.longdouble)
         ang = pos[:, [t[2] for t in table]] * freq[None, :]
         c = np.cos(ang).astype(np.float64)[:, None, :]
         s = np.sin(ang).astype(np.float64)[:, None, :]

@@ -70,3 +70,20 @@ def test_layouts_are_permutations_of_each_other():
             assert np.allclose(w[..., b[0]], y[..., a[0]]) and np.allclose(w[..., b[1]], y[..., a[1]])
     one = rope.pair_table([20], "half", False)
     assert one == rope.pair_table([20], "axis_half", False)
+
+
+def test_far_angles_in_extended_precision():
+    """Exponents that are no float64 (2 i / 40) and angles of about 1e12 against 60 digits: what extended precision loses
+    is the exponent's rounding times ln(theta) (15 * 2^-64), a power (2^-63) and a product (2^-64), below 20 * 2^-64."""
+    from decimal import Decimal as Dec, getcontext
+    getcontext().prec = 60
+    pi = Dec("3.14159265358979323846264338327950288419716939937510582097494")
+    for theta, pos in ((3e-7, 1234567), (1e4, 10 ** 12 + 39)):
+        x = np.zeros((1, 1, 40))
+        x[..., ::2] = 1.0
+        y, _ = rope.norm_rope(x, [[pos]], [40], theta=theta, norm=False)
+        for i in range(20):
+            angle = Dec(pos) * (-(Dec(theta).ln() * Dec(2 * i) / Dec(40))).exp()
+            r = float(angle % (2 * pi))
+            tol = float(angle) * 20 * 2.0 ** -64 + 4 * 2.0 ** -53 * 7
+            assert abs(y[0, 0, 2 * i] - math.cos(r)) < tol and abs(y[0, 0, 2 * i + 1] - math.sin(r)) < tol, (theta, i)
