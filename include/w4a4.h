@@ -357,10 +357,11 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  *   angle = positions[t, a] * theta^(-2 p / rot)         (with W4A4_ROPE_SHARED_FREQUENCIES)
  *   (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
  * Elements rot .. head_dim - 1 are normed only.  Angles are formed and reduced in float64 (to
- * within 6 * 2^-53 of the token's largest angle: from positions of about 2^28 on, this shows in
- * float32; positions past 2^53 are rounded to float64 first); each cosine and sine is then within a few
- * 2^-24 of its own size, also next to 0; the rest is float32 with one rounding to the tensors' type.  Squares that overflow float32 (|x| above about 2^63) give zeros; with
- * eps = 0, a head whose squares all underflow gives infinities, and one of zeros NaN.
+ * within 6 * 2^-53 of the token's largest angle, for any theta: from angles of about 2^28 on, this
+ * shows in float32; positions past 2^53 are rounded to float64 first); each cosine and sine is then
+ * within a few 2^-24 of its own size, also next to 0; the rest is float32 with one rounding to the
+ * tensors' type.  Squares that overflow float32 (|x| above about 2^63) give zeros; with eps = 0, a
+ * head whose squares all underflow gives infinities, and one of zeros NaN.
  *
  * Elements (e0, e1) of pair p, number i of axis a whose first pair is s_a:
  *   W4A4_ROPE_INTERLEAVED  (2 p, 2 p + 1)

@@ -420,3 +420,17 @@ def test_small_sines_and_cosines(w4, layout):
         turned_units(w4, dims, layout, 10000.0, False, pos, D, own_size)
     two = np.concatenate([pos, pos[::-1]], 1)
     turned_units(w4, [44, 20], layout, 10000.0, True, two, 64, own_size)
+
+
+@pytest.mark.parametrize("theta", [0.5, 1e-2, 1e-4, 3e-7, 1e-8, 1e-12])
+def test_theta_below_one(w4, theta):
+    """Ladders of rising frequencies: the float64 angle is within 6 * 2^-53 of the token's largest here too.  Positions
+    that put this bound, for the largest angle, at about 1e-3."""
+    rng = np.random.default_rng(13)
+    for D, dims, layout, shared in ((64, [64], "half", False), (48, [48], "interleaved", False), (80, [40, 32], "axis_half", False),
+                                    (64, [16, 24, 24], "half", True), (2, [2], "interleaved", False), (34, [34], "half", True)):
+        n = sum(dims) if shared else max(dims)
+        top = theta ** -(1 - 2 / n)  # the largest frequency
+        far = int(min(max(1e12 / top, 3), 2.0 ** 40))
+        pos = rng.integers(-far, far + 1, (300, len(dims)))
+        turned_units(w4, dims, layout, theta, shared, pos, D, own_size)

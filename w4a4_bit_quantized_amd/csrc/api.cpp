@@ -588,13 +588,18 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
   a.rot2 = (int)(rot / 2);
   a.layout = layout;
   a.norm = (flags & W4A4_ROPE_NORM) != 0;
-  a.shared = (flags & W4A4_ROPE_SHARED_FREQUENCIES) != 0;
   a.pos64 = (flags & W4A4_ROPE_POSITIONS_I64) != 0;
   a.eps = eps;
   a.inv_d = (float)(1.0 / head_dim);
   for (int x = 0; x < axes; ++x) {
-    const int pairs = a.shared ? a.rot2 : a.start[x + 1] - a.start[x];
-    a.step[x] = pairs > 0 ? std::log2(theta) / pairs : 0.0;
+    const bool shared = (flags & W4A4_ROPE_SHARED_FREQUENCIES) != 0, rising = theta < 1.0;
+    const int first = shared ? 0 : a.start[x], last = (shared ? a.rot2 : a.start[x + 1]) - 1, pairs = last + 1 - first;
+    if (pairs == 0) continue;
+    // (the highest of rising frequencies in 80-bit floats, rounded once)
+    a.ladder[x].top = rising ? (double)(std::pow((long double)theta, -(long double)(pairs - 1) / pairs) / 6.283185307179586477L)
+                             : 0.15915494309189535;  // 1 / (2 pi)
+    a.ladder[x].step = std::fabs(std::log2(theta)) / pairs;
+    a.ladder[x].origin = rising ? last : first;
   }
   if (!w4a4::launch_qk_norm_rope) return W4A4_ERR_HIP;
   (void)hipGetLastError();

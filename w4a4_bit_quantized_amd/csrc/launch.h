@@ -105,6 +105,14 @@ struct RopeHeads {
 
 constexpr int ROPE_MAX_AXES = 8;
 
+// The frequencies of one axis's pairs, in turns per position: top * 2^(-step |p - origin|) for pair p.  The pair
+// `origin` has the highest: the ladder's first pair, or its last where theta < 1.  (Axes that share one
+// ladder have the same record.)
+struct RopeLadder {
+  double top, step;
+  int origin;
+};
+
 struct RopeArgs {
   RopeHeads q, k;
   const void* pos;                // [tokens, axes], int32 or int64
@@ -112,9 +120,9 @@ struct RopeArgs {
   int rot2;                       // rotated pairs
   int start[ROPE_MAX_AXES + 1];   // first pair of every axis, then rot2
   int layout;                     // 0 interleaved, 1 halves of the span, 2 halves of each axis's slice
-  bool norm, shared, pos64;
+  bool norm, pos64;
   float eps, inv_d;
-  double step[ROPE_MAX_AXES];     // log2(theta) / pairs of each axis (shared: of the span, in the first)
+  RopeLadder ladder[ROPE_MAX_AXES];
   // set by the launcher: tokens and heads of a workgroup's pass, log2 of the lanes per head and of the pairs
   int tb, hb, log2g, log2p;
 };

@@ -11,11 +11,13 @@
 // rounded to float32 and passed to sincospi, and the rest d of the angle that the rounding dropped (at most
 // pi 2^-25) turns its result on, to (c - d s, s + d c): without it, a sine or cosine near 0 would be off by d,
 // thousands of times its own last place.  The square of d, below 2^-46, is left out.
-// (Two fused multiply-adds for a pair and token, which all its heads share: one token of 40 heads 3.9 us, 3.8 without
-// them, 1237 tokens of 16 heads of 80 in f32 6.95 and 6.86, 32760 tokens of 48 heads of 128 the same 154.)
+// (Two fused multiply-adds for a pair and token, which all its heads share: 0.1 us at one token of 40 heads and at 1237
+// tokens of 16 heads of 80 in f32, nothing at 32760 tokens of 48 heads of 128.)
+//
 // The float64 part is off by at most 6 * 2^-53 of the
-// largest angle (i step and its exp2: 2.5 roundings of an exponent e, so 2.5 e 2^-53 theta^.. <=
-// 2.5 / 2.7 of the first pair's angle; the two products, 1 / (2 pi) and exp2 itself: 4).
+// largest angle: each frequency is its ladder's highest (the first pair's, or the last's where theta < 1) times 2^-e,
+// with 2.5 roundings in e and so 2.5 ln2 e 2^-e <= 2.5 / 2.7 of the highest; the two products, the highest
+// and exp2 itself: 4.  (From the first pair up, e ln2 would not be bounded: 17 * 2^-53 at theta = 1e-8.)
 //
 // Bound: HBM (every element read and written once).  A group of G lanes (a power of two) holds one
 // head of one token, 2 V elements per lane: V pairs, so a rotation never leaves its lane and the only
@@ -182,8 +184,8 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
   int axis = 0;
   if (ap < a.rot2) {
     while (axis + 1 < a.axes && ap >= a.start[axis + 1]) ++axis;
-    const int i = a.shared ? ap : ap - a.start[axis];
-    freq = exp2(-(double)i * a.step[a.shared ? 0 : axis]) * 0.15915494309189535;  // 1 / (2 pi)
+    const RopeLadder& l = a.ladder[axis];
+    freq = exp2(-(double)abs(ap - l.origin) * l.step) * l.top;
   }
 
   // this lane's chunks: the same pairs for every item
