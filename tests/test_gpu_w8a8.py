@@ -492,3 +492,86 @@ def test_layer_object(w4):
     out = torch.empty((12, N), dtype=torch.float32, device="cuda")
     assert layer(dev(x, "bf16"), out=out) is out
     same_bits(host(out), ref)
+
+
+def special_rows(rng, K, dtype):
+    """Forty rows as stored: ordinary ones of several sizes, zeros, tiny, huge, non-finite, one element alone."""
+    xf = oh.to_f32(rows(rng, 40, K, dtype), dtype).copy()
+    xf[8:16] *= np.float32(2.0 ** -9)
+    xf[0] = 0
+    xf[1] = 2.0 ** -105  # (0 in f16)
+    xf[2, 3] = np.inf
+    xf[3, K - 1] = np.nan
+    xf[4] = 3e38 if dtype != "f16" else 65504.0
+    xf[5] = 0
+    xf[5, 7] = -5.0
+    xf[6, 1:] *= np.float32(2.0 ** -112)
+    xf[7, :-1] = 0
+    with np.errstate(over="ignore"):
+        return oh.from_f32(xf, dtype)
+
+
+def many_rows(w4, rng, x, dtype, lam, block, M, pad=0):
+    """M tokens drawn from the rows of ``x`` (in a matrix ``pad`` columns wider), quantized into the middle of larger
+    buffers: every row is its oracle row wherever it sits, and nothing around the outputs is written."""
+    import torch
+    K = x.shape[1]
+    idx = rng.integers(0, len(x), M)
+    assert all(set(idx[p::2]) >= set(range(8)) for p in (0, 1)), "special rows in both places of a pair"
+    wide = torch.empty((M, K + pad), dtype=tdtype(dtype), device="cuda")
+    xt = wide[:, :K]
+    xt.copy_(dev(x, dtype)[torch.from_numpy(idx).cuda()])
+    lt = None if lam is None else dev(lam, "bf16")
+    q = torch.full((M + 2, K), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((M + 2,), 77.0, device="cuda")
+    st = w4.load_library().w8a8_quantize_act(xt.data_ptr(), K + pad, DTYPES.index(dtype), None if lt is None else lt.data_ptr(),
+                                             M, K, block, q[1:].data_ptr(), s[1:].data_ptr(),
+                                             torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    what = f"{M}x{K} {dtype} B={block}"
+    qr, sr = ow.quantize_act(oh.to_f32(x, dtype), None if lam is None else oh.to_f32(lam, "bf16"), block)
+    got_q, got_s = host(q), host(s)
+    same_bits(got_s[1:-1], sr[idx], f"{what} scales")
+    same_bits(got_q[1:-1], qr[idx], f"{what} codes")
+    assert (got_q[[0, -1]] == 77).all() and (got_s[[0, -1]] == 77).all(), f"{what}: rows around the outputs were written"
+
+
+# from 2048 rows on a workgroup takes two rows per pass, one chunk of 8 columns per thread up to 8192 columns, two up to
+# 16384; 256 to 6144 workgroups, so that 4099 rows (20000 at 208 columns) are several passes for each
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("K", [208, 1040, 4224, 8192, 8208, 8320, 16384])
+def test_quantize_two_rows_per_pass(w4, K, dtype):
+    rng = np.random.default_rng(K)
+    x, lam = special_rows(rng, K, dtype), factors(rng, K)
+    print(f"\nK={K} {dtype}", flush=True)
+    for block in (0, 16, 32, 64, 128):
+        if block == 0 or K % block == 0:
+            for M in (2047, 2048, 2049):
+                many_rows(w4, rng, x, dtype, lam, block, M)
+    many_rows(w4, rng, x, dtype, None, 16, 4099, pad=24)
+    many_rows(w4, rng, x, dtype, lam, 0, 4099 if K > 208 else 20001)
+
+
+@pytest.mark.parametrize("K", [256, 8320])
+def test_quantize_two_rows_extreme_factors(w4, K):
+    """Smoothing factors outside the two-part division's range, zero, negative and non-finite ones, in two rows per pass."""
+    rng = np.random.default_rng(K)
+    x = special_rows(rng, K, "bf16")
+    for values in ([2.0 ** -40, 1.0], [2.0 ** 50, 2.0 ** 50], [-1.5, 0.75], [0.0, 1.0], [np.nan, 1.0], [np.inf, 2.0], [1e-39, 1.0]):
+        lam = oh.from_f32(np.resize(np.array(values, np.float32), K), "bf16")
+        many_rows(w4, rng, x, "bf16", lam, 0, 2049)
+        many_rows(w4, rng, x, "bf16", lam, 32, 2049)
+
+
+def test_linear_two_rows_per_pass(w4):
+    """The layer over the two-row quantizer: its row count is odd, and a workgroup takes several pairs."""
+    import torch
+    rng = np.random.default_rng(21)
+    M, K, N = 2051, 4224, 136
+    x, lam = rows(rng, M, K, "bf16"), factors(rng, K)
+    qw, sw = codes(rng, N, K), rng.uniform(0.001, 0.01, N).astype(np.float32)
+    y = w4.w8a8_linear(dev(x, "bf16"), dict(qweight=torch.from_numpy(qw).cuda(), wscales=torch.from_numpy(sw).cuda(),
+                                            smooth_factor=dev(lam, "bf16")), hadamard_block=128)
+    ref = ow.linear_f32(oh.to_f32(x, "bf16"), qw, sw, oh.to_f32(lam, "bf16"), None, 128)
+    same_bits(host(y), oh.from_f32(ref, "bf16"), "layer of 2051 tokens")
