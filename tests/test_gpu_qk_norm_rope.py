@@ -434,3 +434,64 @@ def test_theta_below_one(w4, theta):
         far = int(min(max(1e12 / top, 3), 2.0 ** 40))
         pos = rng.integers(-far, far + 1, (300, len(dims)))
         turned_units(w4, dims, layout, theta, shared, pos, D, own_size)
+
+
+def walked(w4, T, hq, hk, D, dims, dtype, layout):
+    """q and k partitions of T rows where workgroups make several passes: tokens next to every kind of border against
+    the oracle, all of them against calls of 500 tokens (one pass per workgroup), bit for bit, and in place."""
+    import torch
+    tokens = passes(T, hq + hk, D, dims, layout, dtype)
+    print(f"\nT={T} heads={hq}+{hk} D={D} axes={dims} {dtype} {layout}: {tokens} tokens per pass", flush=True)
+    assert -(-T // tokens) > 1536, "more blocks of tokens than workgroups"
+    rng = np.random.default_rng(T + D)
+    g = torch.Generator(device="cuda").manual_seed(T + D)
+    # a column before the heads and one behind them, a row behind the last token
+    big = torch.full((T + 1, (hq + hk) * D + 2), 5.0, dtype=tdtype(dtype), device="cuda")
+    big[:T, 1:-1] = torch.randn((T, (hq + hk) * D), generator=g, device="cuda") * 1.5
+    heads = big[:T, 1:-1].unflatten(1, (hq + hk, D))
+    q, k = heads[:, :hq], heads[:, hq:]
+    wq, wk = weights(rng, D, dtype), weights(rng, D, dtype)
+    pos = rng.integers(-500, 500, (T, len(dims)))
+    pt, wqt, wkt = torch.from_numpy(pos.astype(np.int32)).cuda(), dev(wq, dtype), dev(wk, dtype)
+    a, b = w4.qk_norm_rope(q, k, pt, dims, wqt, wkt, layout=layout)
+    step = 1536 * tokens
+    some = np.unique(np.clip(np.concatenate([np.arange(30), np.arange(step - 30, step + 30), np.arange(T - 30, T),
+                                             rng.integers(0, T, 100)]), 0, T - 1))
+    at = torch.from_numpy(some).cuda()
+    check(a[at], host(q[at]), pos[some], dims, dtype, wq, layout, what="q")
+    check(b[at], host(k[at]), pos[some], dims, dtype, wk, layout, what="k")
+    for t in range(0, T, 500):
+        c, d = w4.qk_norm_rope(q[t:t + 500], k[t:t + 500], pt[t:t + 500], dims, wqt, wkt, layout=layout)
+        assert torch.equal(c, a[t:t + 500]) and torch.equal(d, b[t:t + 500]), f"tokens {t} .. {t + 499}"
+    w4.qk_norm_rope(q, k, pt, dims, wqt, wkt, layout=layout, inplace=True)
+    assert torch.equal(q, a) and torch.equal(k, b)
+    assert bool((big[:, 0] == 5).all() and (big[:, -1] == 5).all() and (big[T] == 5).all())
+
+
+def passes(T, heads, D, dims, layout, dtype):
+    """Tokens per pass: about six (token, head) items for each of a workgroup's lane groups, 1 to 8."""
+    pairs = {"interleaved": [4], "half": [sum(dims) // 2], "axis_half": np.cumsum(dims) // 2}[layout]
+    vector = D % 8 == 0 and all(p % 4 == 0 for p in pairs)
+    lanes = D / 8 if vector else D / 4 if dtype == "f32" and 96 < D <= 128 else D / 8
+    groups = 256 >> int(np.ceil(np.log2(np.ceil(lanes))))
+    return min(max(6 * groups // heads, 1), 8, -(-T // 1536))
+
+
+WALKS = [(20011, 3, 1, 64, [20, 2], "axis_half"), (26001, 1, 1, 128, [44, 42, 42], "axis_half"), (5003, 60, 4, 64, [20, 24], "half"),
+         (13001, 24, 24, 24, [6, 10, 8], "axis_half"), (2003, 32, 2, 512, [250, 130], "half"), (8001, 8, 8, 256, [100, 152], "half")]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", WALKS, ids=str)
+def test_many_passes_of_staged_heads(w4, case, dtype):
+    """Heads of whole 16-byte chunks whose pairs are not in whole fours: through LDS in 16 bits, element by element in f32
+    (two items in flight where D is 128).  Passes of 8, 3 and 1 tokens."""
+    walked(w4, *case[:-1], dtype, case[-1])
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("case", [(20011, 3, 2, 66, [30, 20], "half"), (20001, 2, 1, 126, [60, 66], "interleaved"), (2003, 40, 40, 90, [30, 60], "axis_half"),
+                                  (13003, 3, 2, 64, [24, 40], "half"), (13001, 3, 1, 128, [44, 42, 42], "interleaved")], ids=str)
+def test_many_passes_of_other_heads(w4, case, dtype):
+    """The same for the element-wise forms and the vector path."""
+    walked(w4, *case[:-1], dtype, case[-1])
