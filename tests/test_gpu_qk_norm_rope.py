@@ -495,3 +495,30 @@ def test_many_passes_of_staged_heads(w4, case, dtype):
 def test_many_passes_of_other_heads(w4, case, dtype):
     """The same for the element-wise forms and the vector path."""
     walked(w4, *case[:-1], dtype, case[-1])
+
+
+@pytest.mark.parametrize("M", [5, 77])
+def test_4bit_projection_then_norm_and_rotation(w4, M):
+    """The chain of a fused q / k / v projection behind the 4-bit layer: its output against the oracle's gates, then q and
+    k of that output normed and rotated in place, then rotated per head by the block Hadamard transform."""
+    import torch
+    import helpers as H
+    from w4a4_bit_quantized_amd import synth
+    rng = np.random.default_rng(M)
+    K, hq, hk, D, dims = 512, 4, 2, 64, [16, 24, 24]
+    N, qk = (hq + 2 * hk) * D, (hq + hk) * D
+    lay = synth.make_layer("tiny", seed=M, M=M, K=K, N=N, R=32, B=64)
+    weight, scales = H.oracle_weights(lay)
+    qkv = w4.svdq_linear(H.to_dev_bf16(lay["x"]), H.device_layer(lay, weight, scales), hadamard_block=64)
+    H.assert_gates(H.from_dev_bf16_f64(qkv), H.oracle_linear_rows(lay, weight, scales)[1], "4-bit projection")
+    before = host(qkv)
+    q, k = qkv[:, :hq * D].unflatten(1, (hq, D)), qkv[:, hq * D:qk].unflatten(1, (hk, D))
+    pos = rng.integers(0, 64, (M, 3)).astype(np.int32)
+    wq, wk = weights(rng, D, "bf16"), weights(rng, D, "bf16")
+    w4.qk_norm_rope(q, k, torch.from_numpy(pos).cuda(), dims, dev(wq, "bf16"), dev(wk, "bf16"), inplace=True)
+    check(q, before[:, :hq * D].reshape(M, hq, D), pos, dims, "bf16", wq)
+    check(k, before[:, hq * D:qk].reshape(M, hk, D), pos, dims, "bf16", wk)
+    turned = host(qkv[:, :qk])
+    w4.hadamard_transform(qkv[:, :qk], block=D, inplace=True)
+    assert np.array_equal(host(qkv[:, :qk]), oh.hadamard_transform(turned, D, "bf16"))
+    assert np.array_equal(host(qkv[:, qk:]), before[:, qk:])
