@@ -555,12 +555,13 @@ __global__ __launch_bounds__(64 * KW) void gemm_i8_skinny_kernel(
 }
 
 // ---- up to four tokens: quantizer and weight streaming in one launch ---------------------------------
-// Each workgroup (KW waves, 16 NB channels) starts its weight rings, quantizes the tokens itself (they are in L2,
-// and the arithmetic hides behind the first weights' way from HBM) into codes in LDS, and goes on as the
-// streaming kernel above with the activation operand read from there.  Every workgroup repeats the
-// quantizer's work; what is saved is a launch and the wait between the two (1 x 6144 x 2048: 7.3 to 5.3 us, 4 x 4096 x
-// 4096: 8.4 to 7.5, 4 x 13824 x 5120: 15.9 to 15.3), and 3 us of the host's time.  The codes are those of the quantizer
-// kernel bit for bit.
+// Each workgroup (KW waves, 16 NB channels) starts its weight rings, quantizes the tokens itself (they are in L2)
+// into codes in LDS, and goes on as the streaming kernel above with the activation operand read from there.  Every
+// workgroup repeats the quantizer's work; what is saved is a launch and the wait between the two (1 x 6144 x 2048:
+// 7.3 to 5.3 us, 4 x 4096 x 4096: 8.4 to 7.5, 4 x 13824 x 5120: 15.9 to 15.3), and 3 us of the host's time.  Loads
+// complete in order and x is asked for after the rings' first two K-steps, the smoothing factors after x, so the
+// quantizer starts when those K-steps have landed: they cover the way of x, but not the quantizer's arithmetic,
+// during which no load is in flight.  The codes are those of the quantizer kernel bit for bit.
 constexpr int TK_S = 3;
 
 struct TokenArgs {
@@ -663,7 +664,7 @@ __global__ __launch_bounds__(64 * KW) void linear_i8_token_kernel(const TokenArg
     const uint32_t mx = chunk_max<C>(v[r]), mw = wave_max2(mx, mx);
     if (lane == 0) red[r][wave] = mw;
   }
-  // (LDS only: the weights in flight are not waited for)
+  // (LDS only: every load so far had landed before the values were there)
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
   const float sign = ROT ? lane_sign(lane, p.block) : 1.0f;
 #pragma unroll
