@@ -356,6 +356,9 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  *   angle = positions[t, a] * theta^(-2 i / axis_dims[a])
  *   angle = positions[t, a] * theta^(-2 p / rot)         (with W4A4_ROPE_SHARED_FREQUENCIES)
  *   (u0, u1) -> (u0 cos - u1 sin, u0 sin + u1 cos)
+ * These powers of theta are the only frequencies: ladders scaled per pair (a table of frequencies, a factor on
+ * the cosines and sines) and axes that take the pairs in turn instead of in runs are not covered.  (One factor
+ * on all of a ladder's frequencies cannot be given either; positions are integers.)
  * Elements rot .. head_dim - 1 are normed only.  Angles are formed and reduced in float64 (to
  * within 6 * 2^-53 of the token's largest angle, for any theta: from angles of about 2^28 on, this
  * shows in float32; positions past 2^53 are rounded to float64 first); each cosine and sine is then

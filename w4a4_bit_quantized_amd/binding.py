@@ -810,9 +810,10 @@ def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1
     a rotates axis_dims[a] elements, further elements are only normed.  ``layout``: "interleaved"
     pairs (2p, 2p + 1), "half" (p, p + rot / 2), "axis_half" (halves of each axis's slice).
     ``shared_frequencies``: one ladder theta^(-2p / rot) over all pairs instead of one per axis.
+    Frequencies are powers of theta only (no table of frequencies, no scaled ladders), axes take pairs in runs.
     norm=False only rotates.  q and k may be one tensor, but not ``inplace``: outputs share no element
-    with each other, or with an input that is not theirs.  Returns (q_out, k_out), or q_out when k is None; new contiguous tensors
-    unless ``inplace`` or given."""
+    with each other, or with an input that is not theirs.  Returns (q_out, k_out), or q_out when k is None; new
+    contiguous tensors unless ``inplace`` or given."""
     torch = _torch()
     lib = load_library()
     dev = _device_tensor(q, "q")
