@@ -9,7 +9,8 @@
 // practical ceiling the GEMMs are compared against.  HBM: a 2 GiB read (16 bytes per lane,
 // summed so nothing is optimised away), a 1 GiB -> 1 GiB copy and a 1 GiB write, each timed with
 // HIP events over 5 repetitions after a warm-up (buffers far larger than the 256 MB Infinity
-// Cache).  LDS: every CU runs one workgroup of 256, 512 or 1024 threads reading 16 bytes per lane
+// Cache); copies of 54, 128 and 336 MiB by resident workgroups with non-temporal stores over three
+// pairs of buffers in turn, the manner of the streaming kernels.  LDS: every CU runs one workgroup of 256, 512 or 1024 threads reading 16 bytes per lane
 // per instruction from a 64 KB buffer, consecutive lanes on consecutive 16-byte chunks (no bank
 // conflicts), timed with HIP events.  L2 -> LDS: every CU runs one 1024-thread workgroup that
 // streams 32 KB per step from its own 64 KB window (resident in L2 after the first pass) through
@@ -34,7 +35,9 @@ typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef _Float16 half8_t __attribute__((ext_vector_type(8)));
 
-enum Kind { FP4_32x32x64 = 0, FP4_16x16x128 = 1, FP8_32x32x64 = 2, F16_32x32x16 = 3, FP8_GROUP16 = 4 };
+typedef int i32x16_t __attribute__((ext_vector_type(16)));
+
+enum Kind { FP4_32x32x64 = 0, FP4_16x16x128 = 1, FP8_32x32x64 = 2, F16_32x32x16 = 3, FP8_GROUP16 = 4, I8_32x32x32 = 5 };
 
 // FP8_GROUP16 is the inner loop of the rejected route for 16-wide e4m3 scales: the E2M1 codes as
 // fp8 (exact), one fp8 32x32x16 instruction per 16-column group into a zeroed accumulator, then
@@ -56,11 +59,14 @@ __global__ __launch_bounds__(256) void probe(const int* in, float* out, unsigned
   float sa[16];  // per-element activation scales of the lane's 16 rows (one per group in the real loop)
   for (int r = 0; r < 16; ++r) sa[r] = 1.0f + (float)((in[l + r] >> 8) & 7) * 0.125f;
   float sw = 1.0f + (float)(in[l] & 7) * 0.125f;  // the lane's column scale, changed every group
+  const i32x4_t b4 = {in[l + 4], in[l + 5], in[l + 6], in[l + 7]};
   f32x16_t c[8];
   f32x4_t d[8];
+  i32x16_t n[8];
   for (int i = 0; i < 8; ++i) {
     c[i] = f32x16_t{};
     d[i] = f32x4_t{};
+    n[i] = i32x16_t{};
   }
   __syncthreads();
   const unsigned long long t0 = clock64();
@@ -71,6 +77,7 @@ __global__ __launch_bounds__(256) void probe(const int* in, float* out, unsigned
       if (KIND == FP4_16x16x128) d[i] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, d[i], 4, 4, 0, s, 0, s);
       if (KIND == FP8_32x32x64) c[i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, a8, c[i], 0, 0, 0, s, 0, s);
       if (KIND == F16_32x32x16) c[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(h8, h8, c[i], 0, 0, 0);
+      if (KIND == I8_32x32x32) n[i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(a4, b4, n[i], 0, 0, 0);
       if (KIND == FP8_GROUP16) {
         const f32x16_t p = __builtin_amdgcn_mfma_f32_32x32x16_fp8_fp8(a64 ^ (long)i, b64, f32x16_t{}, 0, 0, 0);
 #pragma unroll
@@ -82,7 +89,7 @@ __global__ __launch_bounds__(256) void probe(const int* in, float* out, unsigned
   const unsigned long long t1 = clock64();
   float acc = 0.f;
   for (int i = 0; i < 8; ++i) {
-    for (int r = 0; r < 16; ++r) acc += c[i][r];
+    for (int r = 0; r < 16; ++r) acc += c[i][r] + (float)n[i][r];
     for (int r = 0; r < 4; ++r) acc += d[i][r];
   }
   out[blockIdx.x * 256 + threadIdx.x] = acc;
@@ -99,6 +106,21 @@ __global__ __launch_bounds__(256) void hbm_read(const u32x4_t* __restrict__ src,
 
 __global__ __launch_bounds__(256) void hbm_copy(const u32x4_t* __restrict__ src, u32x4_t* __restrict__ dst, size_t n) {
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) dst[i] = src[i];
+}
+
+// Copy as the streaming kernels do it: resident workgroups, U chunks of 16 bytes in flight per lane, non-temporal stores.
+template <int U>
+__global__ __launch_bounds__(256) void hbm_copy_nt(const u32x4_t* __restrict__ src, u32x4_t* __restrict__ dst, size_t n) {
+  const size_t stride = (size_t)gridDim.x * 256 * U;
+  for (size_t i = (size_t)blockIdx.x * 256 * U + threadIdx.x; i < n; i += stride) {
+    u32x4_t v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * 256 < n) v[u] = src[i + u * 256];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (i + u * 256 < n) __builtin_nontemporal_store(v[u], dst + i + u * 256);
+  }
 }
 
 __global__ __launch_bounds__(256) void hbm_write(u32x4_t* __restrict__ dst, size_t n) {
@@ -207,6 +229,7 @@ bool run(const char* name, const int* in, float* out, unsigned long long* cyc, i
   const double n = (double)iters * 8;
   const double flops = KIND == FP4_16x16x128                          ? 2.0 * 16 * 16 * 128
                        : (KIND == F16_32x32x16 || KIND == FP8_GROUP16) ? 2.0 * 32 * 32 * 16
+                       : KIND == I8_32x32x32                           ? 2.0 * 32 * 32 * 32
                                                                        : 2.0 * 32 * 32 * 64;
   std::printf("%-26s %5.1f cycles/instr/wave  %7.3f ms  %8.1f TFLOP/s  clock %.2f GHz\n", name, avg / n, ms,
               flops * n * 4 * blocks / (ms * 1e-3) / 1e12, avg / (ms * 1e-3) / 1e9);
@@ -246,6 +269,7 @@ int main(int argc, char** argv) {
         !run<FP4_16x16x128>("fp4 16x16x128 (scaled)", in, out, cyc, blocks, iters) ||
         !run<FP8_32x32x64>("fp8 32x32x64 (scaled)", in, out, cyc, blocks, iters) ||
         !run<F16_32x32x16>("f16 32x32x16", in, out, cyc, blocks, iters) ||
+        !run<I8_32x32x32>("i8 32x32x32", in, out, cyc, blocks, iters) ||
         !run<FP8_GROUP16>("fp8 32x32x16 + f32 rescale", in, out, cyc, blocks, iters))
       return 1;
   }
@@ -281,6 +305,31 @@ int main(int argc, char** argv) {
     float ms = 0.f;
     (void)hipEventElapsedTime(&ms, e0, e1);
     std::printf("%-26s %8.3f ms per pass  %7.0f GB/s\n", c.name, ms / 5, c.bytes / (ms / 5 * 1e-3) / 1e9);
+  }
+  // The same in the streaming kernels' manner, over three pairs of buffers in turn (a is 2 GiB, b 1 GiB; the pairs
+  // are 3 n <= 1 GiB of each), 24 launches.
+  std::printf("HBM copies, 3 pairs of buffers in turn, non-temporal stores (GB/s of reads and writes)\n");
+  for (size_t mib : {54, 128, 336}) {
+    const size_t n = mib * (1 << 20) / 16;
+    for (int wgs : {1536, 2048, 4096, 16384}) {
+      double gbs[2];
+      for (int u = 0; u < 2; ++u) {
+        auto launch = [&](int p) {
+          if (u == 0) hipLaunchKernelGGL(hbm_copy_nt<2>, dim3(wgs), block, 0, 0, a + p * n, b + p * n, n);
+          else hipLaunchKernelGGL(hbm_copy_nt<4>, dim3(wgs), block, 0, 0, a + p * n, b + p * n, n);
+        };
+        for (int r = 0; r < 3; ++r) launch(r);
+        if (!ok(hipDeviceSynchronize(), "copy warm-up")) return 1;
+        (void)hipEventRecord(e0);
+        for (int r = 0; r < 24; ++r) launch(r % 3);
+        (void)hipEventRecord(e1);
+        if (!ok(hipEventSynchronize(e1), "copy run")) return 1;
+        float ms = 0.f;
+        (void)hipEventElapsedTime(&ms, e0, e1);
+        gbs[u] = 2.0 * n * 16 * 24 / (ms * 1e-3) / 1e9;
+      }
+      std::printf("%3zu MiB each, %5d workgroups   2 chunks in flight %6.0f   4 chunks %6.0f\n", mib, wgs, gbs[0], gbs[1]);
+    }
   }
   (void)hipFree(a);
   (void)hipFree(b);
