@@ -809,11 +809,12 @@ hipError_t run(const GArgs& a) {
   // (four stages from about K = 2048: 256 x 5120 x 5120 16.9 us, 17.8 with three; 301 x 4099 x 1552 11.6 and 11.2)
   if (forced ? is("64x128s4") : tiles(64, 128) <= 256 && a.K >= 2048) return run_lines<2, 4, 1, 1, 4, 5, 1, YT>(a, lines);
   if (forced ? is("64x128") : tiles(64, 128) <= 256) return run_lines<2, 4, 1, 1, 3, 4, 1, YT>(a, lines);
-  // Otherwise, in rounds of 256 tiles, the shape with the least time: rounds by the measured times (10 ns) of a
-  // round's first loads and stores and of its 128-column K-steps.  A last round that is mostly empty then costs
-  // little (4096 x 2560 x 12288: 137 us in 224 tiles of 256 x 192, 144 in 160 of 256 x 256; 300 x 13824 x 5120: 33 in 216 of
-  // 128 x 192, 36 in 162 of 128 x 256; 1021 x 2050 x 4096: 19 in 136 of 128 x 128, 29 in 88 of 128 x 192).  Over 150 drawn
-  // shapes the rule is 0.3 % behind the best of the five, and at most 7 %.
+  // Otherwise, in rounds of 256 tiles, the shape with the least time: rounds by the times (10 ns) of a round's
+  // first loads and stores and of its 128-column K-steps, fitted to measured products of whole 128 columns.  A last round
+  // that is mostly empty then costs little (4096 x 2560 x 12288: 137 us in 224 tiles of 256 x 192, 144 in 160 of 256 x 256;
+  // 300 x 13824 x 5120: 33 in 216 of 128 x 192, 36 in 162 of 128 x 256; 1021 x 2050 x 4096: 19 in 136 of 128 x 128, 29 in 88 of
+  // 128 x 192).  Over 300 drawn shapes with such K the rule is 0.1 % behind the best of the five on average and 8 % at
+  // most, over 300 with any K 0.35 % and 11 % (297 x 11451 x 192: 9.8 us in 128 x 192 tiles, 8.8 in 128 x 256).
   struct { const char* name; int64_t bm, bn, round, step; } const shapes[] = {{"128", 128, 128, 400, 50},
                                                                               {"128x192", 128, 192, 520, 69},
                                                                               {"128x256", 128, 256, 530, 86},
