@@ -575,3 +575,18 @@ def test_linear_two_rows_per_pass(w4):
                                             smooth_factor=dev(lam, "bf16")), hadamard_block=128)
     ref = ow.linear_f32(oh.to_f32(x, "bf16"), qw, sw, oh.to_f32(lam, "bf16"), None, 128)
     same_bits(host(y), oh.from_f32(ref, "bf16"), "layer of 2051 tokens")
+
+
+def test_numbers_past_32_bits_are_refused(w4):
+    """A block or an axis that only fits after its upper bits are lost is no valid one."""
+    import torch
+    x = torch.ones((4, 64), dtype=torch.bfloat16, device="cuda")
+    layer = dict(qweight=torch.ones((8, 64), dtype=torch.int8, device="cuda"), wscales=torch.ones(8, device="cuda"))
+    q = torch.ones((4, 2, 64), dtype=torch.bfloat16, device="cuda")
+    pos = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    for far in (2 ** 32, -2 ** 32, 2 ** 40):
+        for call in (lambda: w4.w8a8_quantize_act(x, hadamard_block=far + 64), lambda: w4.w8a8_quantize_weight(x, hadamard_block=far),
+                     lambda: w4.w8a8_linear(x, layer, hadamard_block=far + 16), lambda: w4.hadamard_transform(x, block=far + 64),
+                     lambda: w4.qk_norm_rope(q, None, pos, [far + 32, 32]), lambda: w4.qk_norm_rope(q, None, pos, [32, far])):
+            with pytest.raises((ValueError, w4.W4A4Error)):
+                call()

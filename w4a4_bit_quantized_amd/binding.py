@@ -112,6 +112,14 @@ def load_library():
     return _LIB
 
 
+def _i32(value, name):
+    """``value`` as an int that the C interface's int32 holds (ctypes drops the bits above without a word)."""
+    value = int(value)
+    if not -0x80000000 <= value <= 0x7FFFFFFF:
+        raise ValueError(f"{name} = {value} is out of range")
+    return value
+
+
 def _check(status, what):
     if status != 0:
         name = STATUS_NAMES.get(status, str(status))
@@ -249,7 +257,8 @@ def svdq_quantize_act(x, smooth_factor, proj_down, hadamard_block=0):
     qact = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
     ascales = torch.empty((K // 16, M), dtype=torch.uint8, device=dev)
     lora = torch.empty((M, R), dtype=torch.float32, device=dev)
-    st = lib.svdq_quantize_act(_ptr(x), _ptr(smooth_factor), _ptr(proj_down), M, K, R, int(hadamard_block),
+    st = lib.svdq_quantize_act(_ptr(x), _ptr(smooth_factor), _ptr(proj_down), M, K, R,
+                               _i32(hadamard_block, "hadamard_block"),
                                _ptr(qact), _ptr(ascales), _ptr(lora), _stream(dev))
     _check(st, "svdq_quantize_act")
     return qact, ascales, lora
@@ -266,7 +275,7 @@ def svdq_quantize_weight(w, smooth_factor, hadamard_block=0):
     _shape(smooth_factor, "smooth_factor", (K,))
     qweight = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
     wscales = torch.empty((K // 16, N), dtype=torch.uint8, device=dev)
-    st = lib.svdq_quantize_weight(_ptr(w), _ptr(smooth_factor), N, K, int(hadamard_block),
+    st = lib.svdq_quantize_weight(_ptr(w), _ptr(smooth_factor), N, K, _i32(hadamard_block, "hadamard_block"),
                                   _ptr(qweight), _ptr(wscales), _stream(dev))
     _check(st, "svdq_quantize_weight")
     return qweight, wscales
@@ -338,7 +347,7 @@ def svdq_linear(x, layer, hadamard_block=0, workspace=None, out=None):
     _dev(y, "y", (torch.bfloat16,), dev)
     common = (_ptr(x2), _ptr(t["qweight"]), _ptr(t["wscales"]), _ptr(t["proj_down"]), _ptr(t["proj_up"]),
               _ptr(t["smooth_factor"]), _ptr(t["wcscales"]), _ptr(t["wtscale"]))
-    tail = (M, N, K, R, int(hadamard_block), _ptr(y), _ptr(workspace), workspace.numel(), _stream(dev))
+    tail = (M, N, K, R, _i32(hadamard_block, "hadamard_block"), _ptr(y), _ptr(workspace), workspace.numel(), _stream(dev))
     bias = layer.get("bias")
     if bias is None:
         st = lib.svdq_linear(*common, *tail)
@@ -375,7 +384,7 @@ def svdq_linear_noalloc(x, layer, hadamard_block=0, out=None):
     _dev(y, "y", (torch.bfloat16,), dev)
     st = lib.svdq_linear_noalloc(_ptr(x2), _ptr(t["qweight"]), _ptr(t["wscales"]), _ptr(t["proj_down"]),
                                  _ptr(t["proj_up"]), _ptr(t["smooth_factor"]), _ptr(t["wcscales"]), _ptr(t["wtscale"]),
-                                 _ptr(bias), M, N, K, R, int(hadamard_block), _ptr(y), _stream(dev))
+                                 _ptr(bias), M, N, K, R, _i32(hadamard_block, "hadamard_block"), _ptr(y), _stream(dev))
     _check(st, "svdq_linear_noalloc")
     return y.reshape(*lead, N)
 
@@ -404,7 +413,8 @@ def svdq_quantize_act_mx(x, smooth_factor, proj_down, hadamard_block=32):
     qact = torch.empty((M, K // 2), dtype=torch.uint8, device=dev)
     ascales = torch.empty((K // 32, mx_scale_rows(M)), dtype=torch.uint8, device=dev)
     lora = torch.empty((M, R), dtype=torch.float32, device=dev)
-    st = lib.svdq_quantize_act_mx(_ptr(x), _ptr(smooth_factor), _ptr(proj_down), M, K, R, int(hadamard_block),
+    st = lib.svdq_quantize_act_mx(_ptr(x), _ptr(smooth_factor), _ptr(proj_down), M, K, R,
+                                  _i32(hadamard_block, "hadamard_block"),
                                   _ptr(qact), _ptr(ascales), _ptr(lora), _stream(dev))
     _check(st, "svdq_quantize_act_mx")
     return qact, ascales, lora
@@ -421,7 +431,7 @@ def svdq_quantize_weight_mx(w, smooth_factor, hadamard_block=32):
     _shape(smooth_factor, "smooth_factor", (K,))
     qweight = torch.empty((N, K // 2), dtype=torch.uint8, device=dev)
     wscales = torch.empty((K // 32, N), dtype=torch.uint8, device=dev)
-    st = lib.svdq_quantize_weight_mx(_ptr(w), _ptr(smooth_factor), N, K, int(hadamard_block),
+    st = lib.svdq_quantize_weight_mx(_ptr(w), _ptr(smooth_factor), N, K, _i32(hadamard_block, "hadamard_block"),
                                      _ptr(qweight), _ptr(wscales), _stream(dev))
     _check(st, "svdq_quantize_weight_mx")
     return qweight, wscales
@@ -486,7 +496,7 @@ def svdq_linear_mx(x, layer, hadamard_block=32, workspace=None, out=None):
     _dev(y, "y", (torch.bfloat16,), dev)
     common = (_ptr(x2), _ptr(t["qweight"]), _ptr(t["wscales"]), _ptr(t["proj_down"]), _ptr(t["proj_up"]),
               _ptr(t["smooth_factor"]), _ptr(t["wcscales"]), _ptr(t["wtscale"]))
-    tail = (M, N, K, R, int(hadamard_block), _ptr(y), _ptr(workspace), workspace.numel(), _stream(dev))
+    tail = (M, N, K, R, _i32(hadamard_block, "hadamard_block"), _ptr(y), _ptr(workspace), workspace.numel(), _stream(dev))
     bias = layer.get("bias")
     if bias is None:
         st = lib.svdq_linear_mx(*common, *tail)
@@ -529,7 +539,7 @@ def hadamard_transform(x, block=None, inplace=False, out=None):
     if x.dtype not in codes:
         raise TypeError(f"x must be bf16, f16 or f32, got {x.dtype}")
     rows, cols, ldx = _rows_view(x, "x")
-    block = int(cols if block is None else block)
+    block = _i32(cols if block is None else block, "block")
     if inplace:
         y = x
     else:
@@ -678,8 +688,8 @@ def _w8a8_quantize(call, x, name, smooth_factor, hadamard_block):
     _check_smooth(smooth_factor, K, dev)
     q = torch.empty((rows, K), dtype=torch.int8, device=dev)
     scales = torch.empty((rows,), dtype=torch.float32, device=dev)
-    st = _on(dev, call, x.data_ptr(), ld, code, _addr(smooth_factor), rows, K, int(hadamard_block), q.data_ptr(),
-             scales.data_ptr())
+    st = _on(dev, call, x.data_ptr(), ld, code, _addr(smooth_factor), rows, K, _i32(hadamard_block, "hadamard_block"),
+             q.data_ptr(), scales.data_ptr())
     return st, q, scales
 
 
@@ -748,7 +758,8 @@ def w8a8_linear(x, layer, hadamard_block=0, workspace=None, out=None, out_dtype=
             raise ValueError(f"workspace holds {size} bytes, the call needs {need}")
         need = size
     st = _on(dev, lib.w8a8_linear, x.data_ptr(), ldx, code, qweight.data_ptr(), wscales.data_ptr(), _addr(smooth),
-             _addr(bias), M, N, K, int(hadamard_block), y.data_ptr(), ldy, ycode, workspace.data_ptr(), need)
+             _addr(bias), M, N, K, _i32(hadamard_block, "hadamard_block"), y.data_ptr(), ldy, ycode,
+             workspace.data_ptr(), need)
     _check(st, "w8a8_linear")
     return y
 
@@ -856,7 +867,9 @@ def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1
     array = _I32_ARRAYS.get(n)
     if array is None:
         array = _I32_ARRAYS[n] = ctypes.c_int32 * n
-    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ks, pos, T, D, n, array(*axis_dims), layout_code, flags,
-             theta, eps, code)
+    dims = array(*axis_dims)
+    if dims[:] != [*axis_dims]:  # (see _i32)
+        raise ValueError(f"axis_dims {list(axis_dims)} are out of range")
+    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ks, pos, T, D, n, dims, layout_code, flags, theta, eps, code)
     _check(st, "w4a4_qk_norm_rope")
     return q_out if k is None else (q_out, k_out)
