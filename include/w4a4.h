@@ -375,7 +375,7 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  * element (t, h, d) is at x + t x_token_stride + h x_head_stride + d, so partitions of a fused
  * projection's output and head-major outputs are addressed as they lie; q and k may have different
  * head counts.  x == y (with equal strides) works in place; any other overlap of an input and an
- * output, or of the two outputs, is undefined (q's y == k's y is refused).  Only the addressed
+ * output, or of the two outputs, is undefined (one's y == the other's y or x is refused).  Only the addressed
  * elements are written.
  *   positions  [tokens, axes] int32 (int64 with W4A4_ROPE_POSITIONS_I64), dense; NULL when rot == 0
  *   axis_dims  HOST array of `axes` even sizes (0 allowed), sum at most head_dim; axes 0 ..

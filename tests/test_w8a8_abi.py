@@ -205,3 +205,16 @@ def test_check_layer_w8a8():
                 dict(t, qweight=torch.zeros(8, dtype=torch.int8))):
         with pytest.raises(c.ContractError):
             c.check_layer_w8a8(bad)
+
+
+def test_rope_output_on_the_other_input(lib):
+    """q's output where k's input starts, or the reverse, would be written while other workgroups still read it."""
+    far, odd = P + 0x200000, P + 1
+    q, k = dict(x=P, y=P + 0x100000, w=odd), dict(x=far, y=far + 0x100000, w=odd)
+    r = lambda a, b: _rope(lib, q=_heads(**{**q, **a}), k=_heads(**{**k, **b}))
+    assert r({}, {}) == ERR_ALIGN                                  # apart: on to the alignment check
+    assert r(dict(y=far), {}) == ERR_SHAPE and r({}, dict(y=P)) == ERR_SHAPE
+    assert r(dict(y=far), dict(y=P)) == ERR_SHAPE                  # swapped
+    assert r(dict(x=P, y=P), dict(x=P)) == ERR_SHAPE               # one input, q in place
+    assert r(dict(x=P, y=P), dict(x=far, y=far)) == ERR_ALIGN      # both in place
+    assert _rope(lib, q=_heads(**{**q, "y": far}), k=_heads(**{**k, "heads": 0})) == ERR_ALIGN  # no heads: not read

@@ -571,7 +571,9 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
     if (st != W4A4_OK) return st;
   }
   if (tokens == 0 || q->heads + kk.heads == 0) return W4A4_OK;
-  if (q->heads > 0 && kk.heads > 0 && q->y && q->y == kk.y) return W4A4_ERR_SHAPE;
+  // an output on the other output, or on the other input, which other workgroups read at any time
+  if (q->heads > 0 && kk.heads > 0 && ((q->y && (q->y == kk.y || q->y == kk.x)) || (kk.y && kk.y == q->x)))
+    return W4A4_ERR_SHAPE;
   if (rot > 0 && !positions) return W4A4_ERR_NULL;
   const uintptr_t es = dtype == W4A4_DTYPE_F32 ? 4 : 2;
   for (const w4a4_heads* h : {q, &kk})
