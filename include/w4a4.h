@@ -324,7 +324,8 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
  * row n, the same rotation and codes; qweight and wscales are the layer's checkpoint tensors.
  * w8a8_linear is w8a8_quantize_act into the workspace (at least w8a8_linear_workspace_bytes(M, K)
  * bytes, 256-byte aligned, contents overwritten), then w8a8_gemm; projections of one input may
- * share one w8a8_quantize_act instead.  Results do not depend on the batch a row is in (only the
+ * share one w8a8_quantize_act instead.  (Few tokens may be quantized and multiplied in one launch, which
+ * leaves the workspace as it was: same results, but no codes to read there.)  Results do not depend on the batch a row is in (only the
  * quotients below 2^-110 of a smoothing factor outside [2^-32, 2^32] may round otherwise).
  * Outputs and the workspace share no element with an input or with each other (y == x is
  * refused); a call on another stream at the same time takes another workspace.
