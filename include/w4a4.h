@@ -324,9 +324,10 @@ w4a4_status w4a4_hadamard_transform(const void* x, int64_t ldx, void* y, int64_t
  * row n, the same rotation and codes; qweight and wscales are the layer's checkpoint tensors.
  * w8a8_linear is w8a8_quantize_act into the workspace (at least w8a8_linear_workspace_bytes(M, K)
  * bytes, 256-byte aligned, contents overwritten), then w8a8_gemm; projections of one input may
- * share one w8a8_quantize_act instead.  (Few tokens may be quantized and multiplied in one launch, which
- * leaves the workspace as it was: same results, but no codes to read there.)  Results do not depend on the batch a row is in (only the
- * quotients below 2^-110 of a smoothing factor outside [2^-32, 2^32] may round otherwise).
+ * share one w8a8_quantize_act instead.  (Few tokens may be quantized and multiplied in one launch,
+ * which leaves the workspace as it was: the same results, but no codes to read there.)  Results do
+ * not depend on the batch a row is in (only the quotients below 2^-110 of a smoothing factor outside
+ * [2^-32, 2^32] may round otherwise).
  * Outputs and the workspace share no element with an input or with each other (y == x is
  * refused); a call on another stream at the same time takes another workspace.
  * Errors: W4A4_ERR_UNSUPPORTED (hadamard_block, dtype, K > W8A8_MAX_K), W4A4_ERR_SHAPE (sizes,
@@ -363,8 +364,8 @@ w4a4_status w8a8_linear(const void* x, int64_t ldx, int32_t x_dtype, const void*
  * Elements rot .. head_dim - 1 are normed only.  Angles are formed and reduced in float64 (to
  * within 6 * 2^-53 of the token's largest angle, for any theta: from angles of about 2^28 on, this
  * shows in float32; positions past 2^53 are rounded to float64 first); each cosine and sine is then
- * within a few 2^-24 of its own size, also next to 0; the rest is float32 with one rounding to the
- * tensors' type.  Squares that overflow float32 (|x| above about 2^63) give zeros; with eps = 0, a
+ * within a few 2^-24 of its own size, next to 0 too (or within 4e-14); the rest is float32 with one
+ * rounding to the tensors' type.  Squares that overflow float32 (|x| above about 2^63) give zeros; with eps = 0, a
  * head whose squares all underflow gives infinities, and one of zeros NaN.
  *
  * Elements (e0, e1) of pair p, number i of axis a whose first pair is s_a:

@@ -9,8 +9,9 @@
 // practical ceiling the GEMMs are compared against.  HBM: a 2 GiB read (16 bytes per lane,
 // summed so nothing is optimised away), a 1 GiB -> 1 GiB copy and a 1 GiB write, each timed with
 // HIP events over 5 repetitions after a warm-up (buffers far larger than the 256 MB Infinity
-// Cache); copies of 54, 128 and 336 MiB by resident workgroups with non-temporal stores over three
-// pairs of buffers in turn, the manner of the streaming kernels.  LDS: every CU runs one workgroup of 256, 512 or 1024 threads reading 16 bytes per lane
+// Cache); copies of 54, 128 and 336 MiB with non-temporal stores by workgroups that walk three pairs of
+// buffers in turn, the manner of the streaming kernels.
+// LDS: every CU runs one workgroup of 256, 512 or 1024 threads reading 16 bytes per lane
 // per instruction from a 64 KB buffer, consecutive lanes on consecutive 16-byte chunks (no bank
 // conflicts), timed with HIP events.  L2 -> LDS: every CU runs one 1024-thread workgroup that
 // streams 32 KB per step from its own 64 KB window (resident in L2 after the first pass) through
@@ -108,7 +109,7 @@ __global__ __launch_bounds__(256) void hbm_copy(const u32x4_t* __restrict__ src,
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (size_t)gridDim.x * 256) dst[i] = src[i];
 }
 
-// Copy as the streaming kernels do it: resident workgroups, U chunks of 16 bytes in flight per lane, non-temporal stores.
+// Copy as the streaming kernels do it: workgroups that walk the buffer, U chunks of 16 bytes in flight per lane, non-temporal stores.
 template <int U>
 __global__ __launch_bounds__(256) void hbm_copy_nt(const u32x4_t* __restrict__ src, u32x4_t* __restrict__ dst, size_t n) {
   const size_t stride = (size_t)gridDim.x * 256 * U;
