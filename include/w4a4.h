@@ -411,6 +411,104 @@ w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* k, const vo
                               int32_t head_dim, int32_t axes, const int32_t* axis_dims, int32_t layout, int32_t flags,
                               double theta, float eps, int32_t dtype, void* stream);
 
+/* ---- Paged key / value cache -------------------------------------------------------------------
+ * A pool of `pages` pages of `page_size` tokens each holds the keys and values of all sequences: element
+ * (page, token of the page, head, d) of the keys is at k + page k_page_stride + token k_token_stride
+ * + head k_head_stride + d, the values' likewise (strides in elements, the last dimension dense), so pools that
+ * keep a page's tokens or its heads together, and pools whose k and v are one tensor, are addressed as they
+ * lie.  16-bit elements. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t pages, page_size, heads;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+} w4a4_kv_cache;
+
+/* ---- Appending to the cache -----------------------------------------------------------------------
+ * w4a4_qk_norm_rope with k's result and v (as it is) stored in the cache instead, in the same one pass: q goes to
+ * its y; token t's k and v go to slot slots[t] = page * page_size + token of the page.  Tokens whose slot is
+ * negative or past the pool (a padded batch) are not stored; of two tokens with one slot, either's elements
+ * are (element by element).
+ *   q      as for w4a4_qk_norm_rope (in place too); NULL or no heads: only k and v are stored
+ *   k, v   inputs as there, of the cache's head count; their y and y strides are not read, nor is v's weight
+ *   slots  [tokens] int32 (int64 with W4A4_KV_SLOTS_I64), dense
+ *   flags  W4A4_ROPE_* and W4A4_KV_SLOTS_I64
+ *   dtype  W4A4_DTYPE_BF16 or _F16, of the cache too
+ * NaNs of v may come back as other NaNs.  Only the addressed elements are written; the cache shares none with an input or
+ * with q's output.  Errors as there; the cache's elements must not share an address, and its strides are at
+ * most 2^40, pages and page_size at most 2^31 - 1, with offsets below 2^60 (W4A4_ERR_SHAPE).  A pool of no pages
+ * stores nothing. */
+#define W4A4_KV_SLOTS_I64 8
+w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_heads* v, const void* positions,
+                           int64_t tokens, int32_t head_dim, int32_t axes, const int32_t* axis_dims, int32_t layout,
+                           int32_t flags, double theta, float eps, int32_t dtype, const void* slots,
+                           const w4a4_kv_cache* cache, void* stream);
+
+/* ---- Attention over the cache ---------------------------------------------------------------------
+ * For every sequence b of `batch`, with l = kv_lens[b] keys (its queries' own among them) in the pages that row b of
+ * page_table names, and n = q_starts[b + 1] - q_starts[b] queries (rows q_starts[b] .. of q and out):
+ *   query i is at position p = l - n + i and sees the keys j <= p with j > p - window or j < sinks
+ *   out = sum_j softmax_j(scale q . k_j) v_j  over the keys j that it sees;  zeros if it sees none
+ * Key j is at token j % page_size of page page_table[b, j / page_size].  Query head h reads key / value head
+ * h / (heads / cache heads).
+ *
+ * w4a4_tree_attention: the last n keys are the queries' own, drafted, tokens, nodes of a tree: query i sees the keys
+ * l - n + j with tree_mask[q_starts[b] + i, j] != 0 (j < n; columns past the mask's width are not seen) and the
+ * keys before l - n, all of them or, with a window, those with j > p - window or j < sinks, where
+ * p = positions[row], taken as l - n where it is less.  The mask alone rules the drafted tokens, the query's own too.
+ *
+ *   q, out      [tokens, heads, head_dim], element (t, h, d) at x + t token_stride + h head_stride + d; out's
+ *               rows past the last sequence, and all rows of no sequence, are left as they were
+ *   page_table  [batch, table_width] int32, row b at + b table_stride; entries that no key seen by anybody
+ *               needs are not used (pages that a window has left may be given to others); an entry that
+ *               names no page of the pool holds no keys: nobody sees them
+ *   kv_lens     [batch] int32, taken as 0 where negative, and as table_width * page_size where more
+ *   q_starts    [batch + 1] int32, rising, within [0, tokens]; NULL: tokens / batch queries per sequence
+ *   max_q       at least the largest n: it chooses the kernel (any other value costs time only)
+ *   window      0: none; otherwise the number of keys up to the query's own that are seen
+ *   sinks       first keys that stay seen behind the window (no effect without one)
+ *   scale       positive and finite
+ *   head_dim    a multiple of 8, 8 .. W4A4_ATTENTION_MAX_HEAD_DIM; dtype W4A4_DTYPE_BF16 or _F16, of q, the
+ *               cache and out alike
+ *   q, out, k, v  16-byte aligned, with strides that are multiples of 8 elements
+ *   tree_mask   [tokens, mask_width] bytes, row t at + t mask_stride
+ *   positions   [tokens] int32, read with a window only
+ * Keys and values that nobody sees are not read into the sums: what they hold (a page's end behind the last
+ * token, pages that the window has left) does not matter.  Scores, softmax statistics and sums are float32; the probabilities are
+ * rounded to dtype for the second product.  A row whose scores are all -infinity gives zeros; a NaN or +infinity
+ * among them gives NaN.  Results do not depend on the stream's other work or on earlier calls, and two calls on the
+ * same data give the same bits; those of one sequence may depend, in the order of their sums, on the batch it is in.
+ *
+ * workspace: at least w4a4_attention_workspace_bytes(a, cache) bytes, 256-byte aligned, contents overwritten and
+ * nothing kept there between calls: calls that may overlap (other streams) take one each, captured graphs that
+ * run one after another may share one.  The sizes depend on head_dim, tokens, heads, batch and max_q only.
+ * Errors: W4A4_ERR_UNSUPPORTED (dtype, head_dim above the maximum), W4A4_ERR_SHAPE (sizes; head_dim % 8;
+ * heads % cache heads; strides negative, above 2^40 or not multiples of 8; out's elements sharing an address;
+ * tokens * heads above 2^31 - 1; without q_starts, tokens % batch; scale; workspace too small; out == q
+ * or in the cache's place), W4A4_ERR_NULL, W4A4_ERR_ALIGN.  tokens == 0 or batch == 0 launches nothing. */
+#define W4A4_ATTENTION_MAX_HEAD_DIM 256
+typedef struct {
+  const void* q;
+  int64_t q_token_stride, q_head_stride;
+  void* out;
+  int64_t out_token_stride, out_head_stride;
+  int64_t tokens, heads;
+  const void* page_table;
+  int64_t table_stride, table_width;
+  const void* kv_lens;
+  const void* q_starts;
+  int64_t batch, max_q, window, sinks;
+  float scale;
+  int32_t head_dim, dtype;
+} w4a4_attention;
+size_t w4a4_attention_workspace_bytes(const w4a4_attention* a, const w4a4_kv_cache* cache);
+w4a4_status w4a4_paged_attention(const w4a4_attention* a, const w4a4_kv_cache* cache, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+w4a4_status w4a4_tree_attention(const w4a4_attention* a, const w4a4_kv_cache* cache, const void* tree_mask,
+                                int64_t mask_stride, int64_t mask_width, const void* positions, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -12,9 +12,12 @@ __version__ = "0.1.0"
 
 from .binding import (  # noqa: F401
     W4A4Error,
+    attention_workspace_bytes,
     hadamard_transform,
+    kv_append,
     library_path,
     load_library,
+    paged_attention,
     qk_norm_rope,
     svdq_gemm_lowrank,
     svdq_linear,
@@ -28,6 +31,7 @@ from .binding import (  # noqa: F401
     svdq_lowrank_split,
     svdq_quantize_act_mx,
     svdq_quantize_weight_mx,
+    tree_attention,
     w8a8_gemm,
     w8a8_linear,
     w8a8_linear_workspace_bytes,

@@ -26,6 +26,23 @@ class Heads(ctypes.Structure):
                 ("weight", _c_p), ("y", _c_p), ("y_token_stride", _c_i64), ("y_head_stride", _c_i64)]
 
 
+class KvCache(ctypes.Structure):
+    """w4a4_kv_cache: a paged key / value cache."""
+    _fields_ = [("k", _c_p), ("v", _c_p), ("pages", _c_i64), ("page_size", _c_i64), ("heads", _c_i64),
+                ("k_page_stride", _c_i64), ("k_token_stride", _c_i64), ("k_head_stride", _c_i64),
+                ("v_page_stride", _c_i64), ("v_token_stride", _c_i64), ("v_head_stride", _c_i64)]
+
+
+class Attention(ctypes.Structure):
+    """w4a4_attention: the arguments that w4a4_paged_attention and w4a4_tree_attention share."""
+    _fields_ = [("q", _c_p), ("q_token_stride", _c_i64), ("q_head_stride", _c_i64),
+                ("out", _c_p), ("out_token_stride", _c_i64), ("out_head_stride", _c_i64),
+                ("tokens", _c_i64), ("heads", _c_i64), ("page_table", _c_p), ("table_stride", _c_i64),
+                ("table_width", _c_i64), ("kv_lens", _c_p), ("q_starts", _c_p), ("batch", _c_i64), ("max_q", _c_i64),
+                ("window", _c_i64), ("sinks", _c_i64), ("scale", ctypes.c_float), ("head_dim", _c_i32),
+                ("dtype", _c_i32)]
+
+
 # name -> (restype, argtypes), mirroring include/w4a4.h
 SIGNATURES = {
     "w4a4_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -68,6 +85,14 @@ SIGNATURES = {
     "w4a4_qk_norm_rope": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(Heads), _c_p, _c_i64, _c_i32, _c_i32,
                                          ctypes.POINTER(ctypes.c_int32), _c_i32, _c_i32, ctypes.c_double,
                                          ctypes.c_float, _c_i32, _c_p]),
+    "w4a4_kv_append": (ctypes.c_int, [ctypes.POINTER(Heads), ctypes.POINTER(Heads), ctypes.POINTER(Heads), _c_p, _c_i64,
+                                      _c_i32, _c_i32, ctypes.POINTER(ctypes.c_int32), _c_i32, _c_i32, ctypes.c_double,
+                                      ctypes.c_float, _c_i32, _c_p, ctypes.POINTER(KvCache), _c_p]),
+    "w4a4_attention_workspace_bytes": (ctypes.c_size_t, [ctypes.POINTER(Attention), ctypes.POINTER(KvCache)]),
+    "w4a4_paged_attention": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.POINTER(KvCache), _c_p, ctypes.c_size_t,
+                                            _c_p]),
+    "w4a4_tree_attention": (ctypes.c_int, [ctypes.POINTER(Attention), ctypes.POINTER(KvCache), _c_p, _c_i64, _c_i64,
+                                           _c_p, _c_p, ctypes.c_size_t, _c_p]),
 }
 
 # storage type codes of w4a4_hadamard_transform, the w8a8 entry points and w4a4_qk_norm_rope
@@ -147,7 +172,7 @@ def _ptr(t):
     return ctypes.c_void_p(t.data_ptr()) if t is not None else ctypes.c_void_p(0)
 
 
-def _dev(t, name, dtypes, device=None):
+def _dev(t, name, dtypes, device=None, dense=True):
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
@@ -157,7 +182,7 @@ def _dev(t, name, dtypes, device=None):
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must have dtype in {dtypes}, got {t.dtype}")
-    if not t.is_contiguous():
+    if dense and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
 
@@ -811,6 +836,40 @@ def _rope_side(x, view, out, weight, name, dtype, dev):
     return Heads(x.data_ptr(), ts, hs, h, _addr(weight), out.data_ptr(), yts, yhs), out
 
 
+def _matching_view(t, name, like, dtype, dev):
+    """The view of a tensor with the tokens and head_dim of the view ``like``."""
+    if _device_tensor(t, name) != dev or t.dtype != dtype:
+        raise ValueError(f"q, k and v must match in dtype and device, {name} is {t.dtype} on {t.device}")
+    view = _heads_view(t, name)
+    if view[0] != like[0] or view[2] != like[2]:
+        raise ValueError(f"{name} has {view[0]} tokens and head_dim {view[2]}, expected {like[0]} and {like[2]}")
+    return view
+
+
+def _rope_positions(positions, axis_dims, T, lead, dev):
+    """(address or None, axis_dims as a C array, axes, flag of their type) of T tokens' checked positions."""
+    n = len(axis_dims)
+    pos, flag = None, 0
+    if n:
+        torch = _torch()
+        if not isinstance(positions, torch.Tensor) or positions.device != dev or not positions.is_contiguous() or (
+                positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
+            _dev(positions, "positions", (torch.int32, torch.int64), dev)
+        shape = positions.shape
+        if shape != (T, n) and shape != (*lead, n) and not (n == 1 and (shape == (T,) or shape == lead)):
+            raise ValueError(f"positions has shape {tuple(shape)}, expected {(T, n)}")
+        if positions.dtype is torch.int64:
+            flag = ROPE_POSITIONS_I64
+        pos = positions.data_ptr()
+    array = _I32_ARRAYS.get(n)
+    if array is None:
+        array = _I32_ARRAYS[n] = ctypes.c_int32 * n
+    dims = array(*axis_dims)
+    if dims[:] != [*axis_dims]:  # (see _i32)
+        raise ValueError(f"axis_dims {list(axis_dims)} are out of range")
+    return pos, dims, n, flag
+
+
 def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1e-6, theta=10000.0,
                  layout="interleaved", shared_frequencies=False, norm=True, inplace=False, q_out=None, k_out=None):
     """RMS norm of each head of q and k and the rotary rotation by one or more position axes, in one pass.
@@ -842,34 +901,202 @@ def qk_norm_rope(q, k, positions, axis_dims, q_weight=None, k_weight=None, eps=1
     if k is None and (k_out is not None or k_weight is not None):
         raise ValueError("k_out and k_weight need k")
     flags = (ROPE_NORM if norm else 0) | (ROPE_SHARED_FREQUENCIES if shared_frequencies else 0)
-    n = len(axis_dims)
-    pos = None
-    if n:
-        if not isinstance(positions, torch.Tensor) or positions.device != dev or not positions.is_contiguous() or (
-                positions.dtype is not torch.int32 and positions.dtype is not torch.int64):
-            _dev(positions, "positions", (torch.int32, torch.int64), dev)
-        shape = positions.shape
-        if shape != (T, n) and shape != (*q.shape[:-2], n) and not (n == 1 and (shape == (T,) or shape == q.shape[:-2])):
-            raise ValueError(f"positions has shape {tuple(shape)}, expected {(T, n)}")
-        if positions.dtype is torch.int64:
-            flags |= ROPE_POSITIONS_I64
-        pos = positions.data_ptr()
+    pos, dims, n, pos_flag = _rope_positions(positions, axis_dims, T, q.shape[:-2], dev)
     qs, q_out = _rope_side(q, view, q_out, q_weight, "q", dtype, dev)
     ks = None
     if k is not None:
-        if _device_tensor(k, "k") != dev or k.dtype != dtype:
-            raise ValueError("k must match q in dtype and device")
-        kview = _heads_view(k, "k")
-        if kview[0] != T or kview[2] != D:
-            raise ValueError(f"k has {kview[0]} tokens and head_dim {kview[2]}, expected {T} and {D}")
-        ks, k_out = _rope_side(k, kview, k_out, k_weight, "k", dtype, dev)
+        ks, k_out = _rope_side(k, _matching_view(k, "k", view, dtype, dev), k_out, k_weight, "k", dtype, dev)
         ks = ctypes.byref(ks)
-    array = _I32_ARRAYS.get(n)
-    if array is None:
-        array = _I32_ARRAYS[n] = ctypes.c_int32 * n
-    dims = array(*axis_dims)
-    if dims[:] != [*axis_dims]:  # (see _i32)
-        raise ValueError(f"axis_dims {list(axis_dims)} are out of range")
-    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ks, pos, T, D, n, dims, layout_code, flags, theta, eps, code)
+    st = _on(dev, lib.w4a4_qk_norm_rope, ctypes.byref(qs), ks, pos, T, D, n, dims, layout_code, flags | pos_flag, theta, eps,
+             code)
     _check(st, "w4a4_qk_norm_rope")
     return q_out if k is None else (q_out, k_out)
+
+
+# ---- paged key / value cache -----------------------------------------------------------------
+
+KV_SLOTS_I64 = 8
+ATTENTION_MAX_HEAD_DIM = 256
+
+
+def _kv_cache(k_cache, v_cache, dtype, dev):
+    """The descriptor of a cache of two (pages, page_size, heads, head_dim) tensors of this dtype and device."""
+    Tensor = _torch().Tensor
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if not (isinstance(t, Tensor) and t.dtype is dtype and t.device == dev):
+            _dev(t, name, (dtype,), dev, dense=False)
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
+        raise ValueError(f"k_cache and v_cache must both be (pages, page_size, heads, head_dim), got shapes "
+                         f"{tuple(shape)} and {tuple(v_cache.shape)}")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if (ks[3] != 1 or vs[3] != 1) and shape[3] > 1:
+        raise ValueError("k_cache and v_cache must have a dense last dimension")
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), shape[0], shape[1], shape[2], *ks[:3], *vs[:3]), shape
+
+
+def kv_append(q, k, v, positions, axis_dims, slots, k_cache, v_cache, q_weight=None, k_weight=None, eps=1e-6,
+              theta=10000.0, layout="interleaved", shared_frequencies=False, norm=True, inplace=False, q_out=None):
+    """``qk_norm_rope`` with k's result, and v as it is, stored in a paged cache, in one pass; returns q's result.
+
+    q (T, Hq, D) or None, k and v (T, Hk, D), or (B, S, H, D): bf16 or f16, partitions of a fused projection's output
+    are fine.  k_cache and v_cache (pages, page_size, Hk, D) may have any strides with a dense last dimension, whose
+    elements do not overlap.  slots (T,) or (B, S) int32 or int64, contiguous: token t goes to page slots[t] // page_size,
+    place slots[t] % page_size; a negative slot, or one past the pool, is not stored.  No two tokens have one
+    slot.  The other arguments are ``qk_norm_rope``'s."""
+    torch = _torch()
+    lib = load_library()
+    dev = _device_tensor(k, "k")
+    dtype = k.dtype
+    code = _dtype_code(dtype, "k")
+    layout_code = ROPE_LAYOUTS.get(layout)
+    if layout_code is None:
+        raise ValueError(f"layout must be one of {sorted(ROPE_LAYOUTS)}, got {layout!r}")
+    view = _heads_view(k, "k")
+    T, h, D, ts, hs = view
+    cache, shape = _kv_cache(k_cache, v_cache, dtype, dev)
+    if shape[2] != h or shape[3] != D:
+        raise ValueError(f"the cache holds {shape[2]} heads of {shape[3]}, k has {h} of {D}")
+    if k_weight is not None:
+        _dense(k_weight, "k_weight", dtype, (D,), dev)
+    ks = Heads(k.data_ptr(), ts, hs, h, _addr(k_weight), None, 0, 0)
+    vv = _matching_view(v, "v", view, dtype, dev)
+    if vv[1] != h:
+        raise ValueError(f"v has {vv[1]} heads, expected {h}")
+    vs = Heads(v.data_ptr(), vv[3], vv[4], h, None, None, 0, 0)
+    lead = k.shape[:-2]
+    if not (isinstance(slots, torch.Tensor) and slots.device == dev and slots.is_contiguous()
+            and (slots.dtype is torch.int64 or slots.dtype is torch.int32)):
+        _dev(slots, "slots", (torch.int32, torch.int64), dev)
+    if slots.shape != (T,) and slots.shape != lead:
+        raise ValueError(f"slots has shape {tuple(slots.shape)}, expected {(T,)}")
+    flags = (ROPE_NORM if norm else 0) | (ROPE_SHARED_FREQUENCIES if shared_frequencies else 0)
+    if slots.dtype is torch.int64:
+        flags |= KV_SLOTS_I64
+    pos, dims, n, pos_flag = _rope_positions(positions, axis_dims, T, lead, dev)
+    qs = None
+    if q is not None:
+        if inplace:
+            if q_out is not None:
+                raise ValueError("inplace takes no outputs")
+            q_out = q
+        qs, q_out = _rope_side(q, _matching_view(q, "q", view, dtype, dev), q_out, q_weight, "q", dtype, dev)
+        qs = ctypes.byref(qs)
+    elif q_out is not None or q_weight is not None or inplace:
+        raise ValueError("q_out, q_weight and inplace need q")
+    st = _on(dev, lib.w4a4_kv_append, qs, ctypes.byref(ks), ctypes.byref(vs), pos, T, D, n, dims, layout_code,
+             flags | pos_flag, theta, eps, code, slots.data_ptr(), ctypes.byref(cache))
+    _check(st, "w4a4_kv_append")
+    return q_out
+
+
+def _attention(name, q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, scale, window, sinks, workspace, out,
+               tree):
+    torch = _torch()
+    Tensor = torch.Tensor
+    lib = load_library()
+    dev = _device_tensor(q, "q")
+    dtype = q.dtype
+    code = _dtype_code(dtype, "q")
+    T, H, D, ts, hs = _heads_view(q, "q")
+    cache, shape = _kv_cache(k_cache, v_cache, dtype, dev)
+    if shape[3] != D or shape[2] == 0 or H % shape[2] != 0:
+        raise ValueError(f"q has {H} heads of {D}, the cache {shape[2]} of {shape[3]}")
+    if not (isinstance(page_table, Tensor) and page_table.dtype is torch.int32 and page_table.device == dev):
+        _dev(page_table, "page_table", (torch.int32,), dev, dense=False)
+    if page_table.dim() != 2 or (page_table.stride(1) != 1 and page_table.shape[1] > 1):
+        raise ValueError("page_table must be (batch, pages of a sequence) with a dense last dimension")
+    B, width = page_table.shape
+    _dense(kv_lens, "kv_lens", torch.int32, (B,), dev)
+    if q_starts is not None:
+        _dense(q_starts, "q_starts", torch.int32, (B + 1,), dev)
+        most = T if max_q is None else int(max_q)
+    else:
+        if (B and T % B) or (T and not B):
+            raise ValueError(f"{T} queries are not the same number for each of {B} sequences (pass q_starts)")
+        if q.dim() == 4 and q.shape[0] != B:
+            raise ValueError(f"q holds {q.shape[0]} sequences, page_table {B}")
+        most = T // B if B else 0
+        if max_q is not None and int(max_q) < most:
+            raise ValueError(f"max_q = {max_q}, but every sequence has {most} queries")
+    if most < 0:
+        raise ValueError(f"max_q = {max_q} is negative")
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        ots, ohs = H * D, D
+    else:
+        if not isinstance(out, Tensor) or out.shape != q.shape or out.dtype is not dtype or out.device != dev:
+            raise ValueError("out must match q in shape, dtype and device")
+        _, _, _, ots, ohs = _heads_view(out, "out")
+    a = Attention(q.data_ptr(), ts, hs, out.data_ptr(), ots, ohs, T, H, page_table.data_ptr(), page_table.stride(0), width,
+                  kv_lens.data_ptr(), _addr(q_starts), B, most, window, sinks, D ** -0.5 if scale is None else scale, D, code)
+    ra, rc = ctypes.byref(a), ctypes.byref(cache)
+    need = lib.w4a4_attention_workspace_bytes(ra, rc)
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=dev)
+    else:
+        if not (isinstance(workspace, Tensor) and workspace.dtype is torch.uint8 and workspace.device == dev
+                and workspace.is_contiguous()):
+            _dev(workspace, "workspace", (torch.uint8,), dev)
+        size = workspace.numel()
+        if size < need:
+            raise ValueError(f"workspace holds {size} bytes, the call needs {need}")
+        need = size
+    if tree is None:
+        st = _on(dev, lib.w4a4_paged_attention, ra, rc, workspace.data_ptr(), need)
+    else:
+        mask, positions = tree
+        if not (isinstance(mask, Tensor) and mask.device == dev and (mask.dtype is torch.bool or mask.dtype is torch.uint8)):
+            _dev(mask, "tree_mask", (torch.bool, torch.uint8), dev, dense=False)
+        if mask.dim() != 2 or mask.shape[0] != T or (mask.stride(1) != 1 and mask.shape[1] > 1):
+            raise ValueError(f"tree_mask must be ({T}, drafted tokens) with a dense last dimension, got shape "
+                             f"{tuple(mask.shape)}")
+        if positions is not None:
+            if not (isinstance(positions, Tensor) and positions.numel() == T):
+                raise ValueError(f"positions must have {T} elements")
+            _dense(positions, "positions", torch.int32, positions.shape, dev)
+        elif window:
+            raise ValueError("a window needs the drafted tokens' positions")
+        st = _on(dev, lib.w4a4_tree_attention, ra, rc, mask.data_ptr(), mask.stride(0), mask.shape[1], _addr(positions),
+                 workspace.data_ptr(), need)
+    _check(st, name)
+    return out
+
+
+def attention_workspace_bytes(q, k_cache, v_cache, batch, max_q=None):
+    """Bytes of workspace of ``paged_attention`` and ``tree_attention`` for q and a cache of these shapes."""
+    T, H, D, ts, hs = _heads_view(q, "q")
+    cache, _ = _kv_cache(k_cache, v_cache, q.dtype, q.device)
+    a = Attention(None, ts, hs, None, H * D, D, T, H, None, 0, 0, None, 1, batch, T if max_q is None else max_q, 0, 0, 1.0, D,
+                  _dtype_code(q.dtype, "q"))
+    return int(load_library().w4a4_attention_workspace_bytes(ctypes.byref(a), ctypes.byref(cache)))
+
+
+def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max_q=None, scale=None, window=0, sinks=0,
+                    workspace=None, out=None):
+    """Causal attention over a paged cache; a query at position p sees the keys j <= p, with a window only those with
+    j > p - window or j < sinks.
+
+    q (T, Hq, D) or (B, S, Hq, D): bf16 or f16, D a multiple of 8 up to 256, Hq a multiple of the cache's heads.
+    k_cache, v_cache (pages, page_size, Hk, D) of q's dtype, any strides with a dense last dimension, 16-byte aligned rows.
+    page_table (B, width) int32: key j of sequence b is in page page_table[b, j // page_size].  kv_lens (B,)
+    int32: a sequence's keys, its queries' own (already appended) among them.  q_starts (B + 1,) int32: sequence b's
+    queries, the last of its keys, are rows q_starts[b] .. q_starts[b + 1] - 1 of q; without it, every sequence has
+    T / B.  max_q: at least the largest number of queries of a sequence (default T); it chooses the kernel.  scale
+    defaults to D ** -0.5.  window 0 is none.  Rows that see no key, and sequences without keys, give zeros; rows of
+    no sequence are not written.  ``workspace`` (u8, attention_workspace_bytes) and ``out`` may be passed to avoid
+    allocation; calls that may overlap take a workspace each."""
+    return _attention("w4a4_paged_attention", q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, scale, window,
+                      sinks, workspace, out, None)
+
+
+def tree_attention(q, k_cache, v_cache, page_table, kv_lens, tree_mask, q_starts=None, max_q=None, positions=None,
+                   scale=None, window=0, sinks=0, workspace=None, out=None):
+    """Attention of drafted tokens over a paged cache that holds them as its last keys.
+
+    Query i of sequence b sees drafted token j of the same sequence where tree_mask[q_starts[b] + i, j] is set ((T, widest
+    tree) bool or uint8; the token's own bit counts too), and all keys before them: with a window those with
+    j > p - window or j < sinks, where p is the query's entry of positions (T elements, int32; not less than the number of
+    keys before the tree).  The other arguments are ``paged_attention``'s."""
+    return _attention("w4a4_tree_attention", q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, scale, window,
+                      sinks, workspace, out, (tree_mask, positions))

@@ -13,7 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["csrc/api.cpp", "csrc/quantize.hip", "csrc/gemm.hip", "csrc/gemm_skinny.hip", "csrc/hadamard.hip",
            "csrc/lowrank_split.cpp", "csrc/noalloc.hip", "csrc/gemm_mx.hip",
-           "csrc/quantize_i8.hip", "csrc/gemm_i8.hip", "csrc/qk_norm_rope.hip"]
+           "csrc/quantize_i8.hip", "csrc/gemm_i8.hip", "csrc/qk_norm_rope.hip", "csrc/attn_stream.hip"]
 # Sources whose kernel choice reads the path-forcing test hooks (see csrc/launch.h).
 HOOKED = ("csrc/gemm.hip", "csrc/gemm_skinny.hip", "csrc/gemm_mx.hip", "csrc/gemm_i8.hip")
 TEST_LIB = "libw4a4_test.so"

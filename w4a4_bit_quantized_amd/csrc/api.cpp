@@ -4,8 +4,10 @@
 
 #include <hip/hip_runtime_api.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <utility>
 
 #include "launch.h"
 
@@ -542,20 +544,15 @@ w4a4::RopeHeads rope_heads(const w4a4_heads& h, bool norm) {
           h.y, h.y_token_stride, h.y_head_stride};
 }
 
-}  // namespace
-
-extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* k, const void* positions,
-                                         int64_t tokens, int32_t head_dim, int32_t axes, const int32_t* axis_dims,
-                                         int32_t layout, int32_t flags, double theta, float eps, int32_t dtype,
-                                         void* stream) {
-  if (dtype < W4A4_DTYPE_BF16 || dtype > W4A4_DTYPE_F32) return W4A4_ERR_UNSUPPORTED;
+// What w4a4_qk_norm_rope and w4a4_kv_append check and derive from the arguments that they share.
+w4a4_status rope_sizes(int64_t tokens, int32_t head_dim, int32_t axes, const int32_t* axis_dims, int32_t layout,
+                       int32_t flags, double theta, float eps, w4a4::RopeArgs& a) {
   if (layout < W4A4_ROPE_INTERLEAVED || layout > W4A4_ROPE_AXIS_HALF) return W4A4_ERR_UNSUPPORTED;
   if ((flags & ~(W4A4_ROPE_NORM | W4A4_ROPE_SHARED_FREQUENCIES | W4A4_ROPE_POSITIONS_I64)) != 0) return W4A4_ERR_UNSUPPORTED;
   if (head_dim > W4A4_ROPE_MAX_HEAD_DIM || axes > W4A4_ROPE_MAX_AXES) return W4A4_ERR_UNSUPPORTED;
   if (tokens < 0 || tokens > kMaxDim || head_dim < 2 || head_dim % 2 != 0 || axes < 0) return W4A4_ERR_SHAPE;
   if (axes > 0 && !axis_dims) return W4A4_ERR_NULL;
   if (!(theta > 0.0) || !std::isfinite(theta) || !(eps >= 0.0f) || !std::isfinite(eps)) return W4A4_ERR_SHAPE;
-  w4a4::RopeArgs a{};
   int64_t rot = 0;
   for (int x = 0; x < axes; ++x) {
     if (axis_dims[x] < 0 || axis_dims[x] % 2 != 0 || axis_dims[x] > head_dim) return W4A4_ERR_SHAPE;
@@ -563,27 +560,6 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
     a.start[x + 1] = (int)(rot / 2);
   }
   if (rot > head_dim) return W4A4_ERR_SHAPE;
-  if (!q) return W4A4_ERR_NULL;
-  const w4a4_heads none{};
-  const w4a4_heads& kk = k ? *k : none;
-  for (const w4a4_heads* h : {q, &kk}) {
-    w4a4_status st = check_heads(*h, tokens, head_dim);
-    if (st != W4A4_OK) return st;
-  }
-  if (tokens == 0 || q->heads + kk.heads == 0) return W4A4_OK;
-  // an output on the other output, or on the other input, which other workgroups read at any time
-  if (q->heads > 0 && kk.heads > 0 && ((q->y && (q->y == kk.y || q->y == kk.x)) || (kk.y && kk.y == q->x)))
-    return W4A4_ERR_SHAPE;
-  if (rot > 0 && !positions) return W4A4_ERR_NULL;
-  const uintptr_t es = dtype == W4A4_DTYPE_F32 ? 4 : 2;
-  for (const w4a4_heads* h : {q, &kk})
-    if (h->heads > 0 && (!h->x || !h->y)) return W4A4_ERR_NULL;
-  for (const w4a4_heads* h : {q, &kk})
-    if (h->heads > 0 && (!aligned(h->x, es) || !aligned(h->y, es) || !aligned(h->weight, es))) return W4A4_ERR_ALIGN;
-  if (rot > 0 && !aligned(positions, (flags & W4A4_ROPE_POSITIONS_I64) ? 8 : 4)) return W4A4_ERR_ALIGN;
-  a.q = rope_heads(*q, (flags & W4A4_ROPE_NORM) != 0);
-  a.k = rope_heads(kk, (flags & W4A4_ROPE_NORM) != 0);
-  a.pos = positions;
   a.tokens = (int)tokens;
   a.D = head_dim;
   a.axes = axes;
@@ -603,7 +579,269 @@ extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* 
     a.ladder[x].step = std::fabs(std::log2(theta)) / pairs;
     a.ladder[x].origin = rising ? last : first;
   }
+  return W4A4_OK;
+}
+
+}  // namespace
+
+extern "C" w4a4_status w4a4_qk_norm_rope(const w4a4_heads* q, const w4a4_heads* k, const void* positions,
+                                         int64_t tokens, int32_t head_dim, int32_t axes, const int32_t* axis_dims,
+                                         int32_t layout, int32_t flags, double theta, float eps, int32_t dtype,
+                                         void* stream) {
+  if (dtype < W4A4_DTYPE_BF16 || dtype > W4A4_DTYPE_F32) return W4A4_ERR_UNSUPPORTED;
+  w4a4::RopeArgs a{};
+  w4a4_status st = rope_sizes(tokens, head_dim, axes, axis_dims, layout, flags, theta, eps, a);
+  if (st != W4A4_OK) return st;
+  if (!q) return W4A4_ERR_NULL;
+  const w4a4_heads none{};
+  const w4a4_heads& kk = k ? *k : none;
+  for (const w4a4_heads* h : {q, &kk}) {
+    st = check_heads(*h, tokens, head_dim);
+    if (st != W4A4_OK) return st;
+  }
+  if (tokens == 0 || q->heads + kk.heads == 0) return W4A4_OK;
+  // an output on the other output, or on the other input, which other workgroups read at any time
+  if (q->heads > 0 && kk.heads > 0 && ((q->y && (q->y == kk.y || q->y == kk.x)) || (kk.y && kk.y == q->x)))
+    return W4A4_ERR_SHAPE;
+  if (a.rot2 > 0 && !positions) return W4A4_ERR_NULL;
+  const uintptr_t es = dtype == W4A4_DTYPE_F32 ? 4 : 2;
+  for (const w4a4_heads* h : {q, &kk})
+    if (h->heads > 0 && (!h->x || !h->y)) return W4A4_ERR_NULL;
+  for (const w4a4_heads* h : {q, &kk})
+    if (h->heads > 0 && (!aligned(h->x, es) || !aligned(h->y, es) || !aligned(h->weight, es))) return W4A4_ERR_ALIGN;
+  if (a.rot2 > 0 && !aligned(positions, (flags & W4A4_ROPE_POSITIONS_I64) ? 8 : 4)) return W4A4_ERR_ALIGN;
+  a.q = rope_heads(*q, a.norm);
+  a.k = rope_heads(kk, a.norm);
+  a.pos = positions;
   if (!w4a4::launch_qk_norm_rope) return W4A4_ERR_HIP;
   (void)hipGetLastError();
-  return from_hip(w4a4::launch_qk_norm_rope(a, dtype, static_cast<hipStream_t>(stream)));
+  return from_hip(w4a4::launch_qk_norm_rope(a, nullptr, dtype, static_cast<hipStream_t>(stream)));
 }
+
+// ---- Paged key / value cache -------------------------------------------------------------------
+
+namespace {
+
+// One of the cache's two tensors: strides in range, and (`apart`) no two elements at one address: taken from the
+// smallest stride up, each steps past all that the smaller ones reach.
+w4a4_status check_pool(const w4a4_kv_cache& c, int64_t page, int64_t token, int64_t head, int64_t D, bool apart) {
+  struct { int64_t n, s; } d[3] = {{c.pages, page}, {c.page_size, token}, {c.heads, head}};
+  for (auto& x : d)
+    if (x.s < 0 || x.s > (int64_t)1 << 40) return W4A4_ERR_SHAPE;
+  for (int i : {0, 1, 0})
+    if (d[i].s > d[i + 1].s) std::swap(d[i], d[i + 1]);
+  __int128 reach = D;
+  for (auto& x : d) {
+    if (x.n <= 1) continue;
+    if (apart && x.s < reach) return W4A4_ERR_SHAPE;
+    reach += (__int128)(x.n - 1) * x.s;
+  }
+  return reach > (int64_t)1 << 60 ? W4A4_ERR_SHAPE : W4A4_OK;
+}
+
+w4a4_status check_cache(const w4a4_kv_cache& c, int64_t D, bool apart) {
+  if (c.pages < 0 || c.pages > kMaxDim || c.page_size < 1 || c.page_size > kMaxDim || c.heads < 0 || c.heads > kMaxHeads)
+    return W4A4_ERR_SHAPE;
+  if (c.pages == 0 || c.heads == 0) return W4A4_OK;
+  w4a4_status st = check_pool(c, c.k_page_stride, c.k_token_stride, c.k_head_stride, D, apart);
+  return st != W4A4_OK ? st : check_pool(c, c.v_page_stride, c.v_token_stride, c.v_head_stride, D, apart);
+}
+
+}  // namespace
+
+extern "C" w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_heads* v,
+                                      const void* positions, int64_t tokens, int32_t head_dim, int32_t axes,
+                                      const int32_t* axis_dims, int32_t layout, int32_t flags, double theta, float eps,
+                                      int32_t dtype, const void* slots, const w4a4_kv_cache* cache, void* stream) {
+  if (dtype != W4A4_DTYPE_BF16 && dtype != W4A4_DTYPE_F16) return W4A4_ERR_UNSUPPORTED;
+  w4a4::RopeArgs a{};
+  w4a4_status st = rope_sizes(tokens, head_dim, axes, axis_dims, layout, flags & ~W4A4_KV_SLOTS_I64, theta, eps, a);
+  if (st != W4A4_OK) return st;
+  if (!k || !v || !cache) return W4A4_ERR_NULL;
+  const w4a4_heads none{};
+  const w4a4_heads& qq = q ? *q : none;
+  // (their outputs' places are the cache's)
+  w4a4_heads kk = *k, vv = *v;
+  for (w4a4_heads* h : {&kk, &vv}) {
+    h->y = nullptr;
+    h->y_head_stride = head_dim;
+    h->y_token_stride = h->heads > 0 && h->heads <= kMaxHeads ? h->heads * head_dim : 0;
+  }
+  vv.weight = nullptr;
+  for (const w4a4_heads* h : {&qq, (const w4a4_heads*)&kk, (const w4a4_heads*)&vv}) {
+    st = check_heads(*h, tokens, head_dim);
+    if (st != W4A4_OK) return st;
+  }
+  if (kk.heads != cache->heads || vv.heads != cache->heads) return W4A4_ERR_SHAPE;
+  st = check_cache(*cache, head_dim, true);
+  if (st != W4A4_OK) return st;
+  if (cache->pages == 0) kk.heads = vv.heads = 0;  // nothing is stored
+  if (tokens == 0 || qq.heads + kk.heads == 0) return W4A4_OK;
+  const bool stores = kk.heads > 0;
+  const void *inputs[] = {qq.heads > 0 ? qq.x : nullptr, stores ? kk.x : nullptr, stores ? vv.x : nullptr};
+  // an output on another one, or on an input that other workgroups read at any time
+  if (stores) {
+    for (const void* to : {(const void*)cache->k, (const void*)cache->v})
+      for (const void* x : inputs)
+        if (to && to == x) return W4A4_ERR_SHAPE;
+    if (cache->k && cache->k == cache->v) return W4A4_ERR_SHAPE;
+  }
+  if (qq.heads > 0 && qq.y && stores && (qq.y == kk.x || qq.y == vv.x || qq.y == cache->k || qq.y == cache->v))
+    return W4A4_ERR_SHAPE;
+  if (a.rot2 > 0 && !positions) return W4A4_ERR_NULL;
+  if (qq.heads > 0 && (!qq.x || !qq.y)) return W4A4_ERR_NULL;
+  if (stores && (!kk.x || !vv.x || !cache->k || !cache->v || !slots)) return W4A4_ERR_NULL;
+  if (qq.heads > 0 && (!aligned(qq.x, 2) || !aligned(qq.y, 2) || !aligned(qq.weight, 2))) return W4A4_ERR_ALIGN;
+  if (stores && (!aligned(kk.x, 2) || !aligned(kk.weight, 2) || !aligned(vv.x, 2) || !aligned(cache->k, 2) ||
+                 !aligned(cache->v, 2) || !aligned(slots, (flags & W4A4_KV_SLOTS_I64) ? 8 : 4)))
+    return W4A4_ERR_ALIGN;
+  if (a.rot2 > 0 && !aligned(positions, (flags & W4A4_ROPE_POSITIONS_I64) ? 8 : 4)) return W4A4_ERR_ALIGN;
+  kk.y = cache->k;
+  kk.y_head_stride = cache->k_head_stride;
+  vv.y = cache->v;
+  vv.y_head_stride = cache->v_head_stride;
+  a.q = rope_heads(qq, a.norm);
+  a.k = rope_heads(kk, a.norm);
+  a.pos = positions;
+  const w4a4::CacheArgs c = {rope_heads(vv, false), slots, (flags & W4A4_KV_SLOTS_I64) != 0, cache->pages,
+                             cache->page_size, cache->k_page_stride, cache->k_token_stride, cache->v_page_stride,
+                             cache->v_token_stride};
+  if (!w4a4::launch_qk_norm_rope) return W4A4_ERR_HIP;
+  (void)hipGetLastError();
+  return from_hip(w4a4::launch_qk_norm_rope(a, &c, dtype, static_cast<hipStream_t>(stream)));
+}
+
+// ---- Attention over the cache --------------------------------------------------------------------
+
+namespace {
+
+struct TreeMask {
+  const void* mask;
+  int64_t stride, width;
+  const void* positions;
+};
+
+// Everything but pointers, in `a` for the kernels.
+w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, const TreeMask* tree, w4a4::AttnArgs& a) {
+  if (p.dtype != W4A4_DTYPE_BF16 && p.dtype != W4A4_DTYPE_F16) return W4A4_ERR_UNSUPPORTED;
+  if (p.head_dim > W4A4_ATTENTION_MAX_HEAD_DIM) return W4A4_ERR_UNSUPPORTED;
+  if (p.head_dim < 8 || p.head_dim % 8 != 0) return W4A4_ERR_SHAPE;
+  if (p.tokens < 0 || p.batch < 0 || p.batch > kMaxDim - 1 || p.heads < 1 || p.heads > kMaxHeads || c.heads < 1 ||
+      p.heads % c.heads != 0 || p.tokens > kMaxDim / p.heads)
+    return W4A4_ERR_SHAPE;
+  if (p.table_width < 0 || p.table_width > kMaxDim || p.table_stride < 0 || p.table_stride > (int64_t)1 << 40 ||
+      p.window < 0 || p.sinks < 0 || p.max_q < 0)
+    return W4A4_ERR_SHAPE;
+  if (!(p.scale > 0.0f) || !std::isfinite(p.scale)) return W4A4_ERR_SHAPE;
+  if (!p.q_starts && p.batch > 0 && p.tokens % p.batch != 0) return W4A4_ERR_SHAPE;
+  if (tree && (tree->stride < 0 || tree->stride > (int64_t)1 << 40 || tree->width < 0 || tree->width > kMaxDim))
+    return W4A4_ERR_SHAPE;
+  // q and out as the heads of one tensor
+  const w4a4_heads h = {nullptr, p.q_token_stride, p.q_head_stride, p.heads, nullptr, nullptr, p.out_token_stride,
+                        p.out_head_stride};
+  w4a4_status st = check_heads(h, p.tokens, p.head_dim);
+  if (st != W4A4_OK) return st;
+  st = check_cache(c, p.head_dim, false);
+  if (st != W4A4_OK) return st;
+  // (the stride of a dimension of one does not matter)
+  const struct { int64_t n, s; } strides[] = {
+      {p.tokens, p.q_token_stride}, {p.heads, p.q_head_stride}, {p.tokens, p.out_token_stride}, {p.heads, p.out_head_stride},
+      {c.pages, c.k_page_stride}, {c.page_size, c.k_token_stride}, {c.heads, c.k_head_stride},
+      {c.pages, c.v_page_stride}, {c.page_size, c.v_token_stride}, {c.heads, c.v_head_stride}};
+  for (const auto& x : strides)
+    if (x.n > 1 && x.s % 8 != 0) return W4A4_ERR_SHAPE;
+  a.q_ts = p.q_token_stride;
+  a.q_hs = p.q_head_stride;
+  a.o_ts = p.out_token_stride;
+  a.o_hs = p.out_head_stride;
+  a.k_page = c.k_page_stride;
+  a.k_token = c.k_token_stride;
+  a.k_head = c.k_head_stride;
+  a.v_page = c.v_page_stride;
+  a.v_token = c.v_token_stride;
+  a.v_head = c.v_head_stride;
+  a.table_stride = p.table_stride;
+  a.tokens = (int)p.tokens;
+  a.batch = (int)p.batch;
+  a.each = p.batch > 0 ? (int)(p.tokens / p.batch) : 0;
+  a.heads = (int)p.heads;
+  a.kv_heads = (int)c.heads;
+  a.group = (int)(p.heads / c.heads);
+  a.D = p.head_dim;
+  a.max_len = (int)std::min<int64_t>(p.table_width * c.page_size, kMaxDim - 64);  // (block ends stay in 32 bits)
+  a.pages = (uint32_t)c.pages;
+  a.page_size = (int)c.page_size;
+  // x / d = (x m) >> (31 + l) for x < 2^31, with l = ceil(log2 d) and m = ceil(2^(31 + l) / d): m d exceeds 2^(31 + l) by
+  // less than d <= 2^l, so x (m d - 2^(31 + l)) < 2^(31 + l), which keeps the quotient below the next integer
+  int l = 0;
+  while (((int64_t)1 << l) < c.page_size) ++l;
+  a.page_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + c.page_size - 1) / c.page_size);
+  a.page_shift = 31 + l;
+  a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
+  a.window = (int)std::min<int64_t>(p.window, kMaxDim);
+  a.sinks = (int)std::min<int64_t>(p.sinks, kMaxDim);
+  if (tree) {
+    a.mask_stride = tree->stride;
+    a.mask_width = (int)tree->width;
+  }
+  return W4A4_OK;
+}
+
+w4a4_status attention(const w4a4_attention* p, const w4a4_kv_cache* c, const TreeMask* tree, void* workspace,
+                      size_t workspace_bytes, void* stream) {
+  if (!p || !c) return W4A4_ERR_NULL;
+  w4a4::AttnArgs a{};
+  const w4a4_status st = attention_sizes(*p, *c, tree, a);
+  if (st != W4A4_OK) return st;
+  if (p->tokens == 0 || p->batch == 0) return W4A4_OK;
+  if (workspace && workspace_bytes < w4a4_attention_workspace_bytes(p, c)) return W4A4_ERR_SHAPE;
+  const bool keys = c->pages > 0 && a.max_len > 0;
+  // out would be written while other workgroups read q or the cache
+  if (p->out && (p->out == p->q || (keys && (p->out == c->k || p->out == c->v)))) return W4A4_ERR_SHAPE;
+  if (!p->q || !p->out || !p->kv_lens || !workspace || (tree && !tree->mask)) return W4A4_ERR_NULL;
+  if (keys && (!c->k || !c->v || !p->page_table)) return W4A4_ERR_NULL;
+  if (tree && p->window > 0 && !tree->positions) return W4A4_ERR_NULL;
+  if (!aligned(p->q, 16) || !aligned(p->out, 16) || !aligned(p->kv_lens, 4) || !aligned(p->q_starts, 4) ||
+      !aligned(workspace, 256) || (keys && (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(p->page_table, 4))) ||
+      (tree && !aligned(tree->positions, 4)))
+    return W4A4_ERR_ALIGN;
+  a.q = static_cast<const uint8_t*>(p->q);
+  a.out = static_cast<uint8_t*>(p->out);
+  a.k = static_cast<const uint8_t*>(c->k);
+  a.v = static_cast<const uint8_t*>(c->v);
+  a.table = static_cast<const int32_t*>(p->page_table);
+  a.lens = static_cast<const int32_t*>(p->kv_lens);
+  a.starts = static_cast<const int32_t*>(p->q_starts);
+  if (tree) {
+    a.mask = static_cast<const uint8_t*>(tree->mask);
+    a.pos = p->window > 0 ? static_cast<const int32_t*>(tree->positions) : nullptr;
+  }
+  if (!w4a4::launch_attention) return W4A4_ERR_HIP;
+  (void)hipGetLastError();
+  return from_hip(w4a4::launch_attention(a, p->dtype, std::min(p->max_q, p->tokens), workspace,
+                                         static_cast<hipStream_t>(stream)));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t w4a4_attention_workspace_bytes(const w4a4_attention* p, const w4a4_kv_cache* c) {
+  w4a4::AttnArgs a{};
+  if (!p || !c || attention_sizes(*p, *c, nullptr, a) != W4A4_OK || !w4a4::attention_workspace_bytes) return 0;
+  return align256(w4a4::attention_workspace_bytes(a, std::min(p->max_q, p->tokens)));
+}
+
+w4a4_status w4a4_paged_attention(const w4a4_attention* a, const w4a4_kv_cache* cache, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  return attention(a, cache, nullptr, workspace, workspace_bytes, stream);
+}
+
+w4a4_status w4a4_tree_attention(const w4a4_attention* a, const w4a4_kv_cache* cache, const void* tree_mask,
+                                int64_t mask_stride, int64_t mask_width, const void* positions, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+  const TreeMask t = {tree_mask, mask_stride, mask_width, positions};
+  return attention(a, cache, &t, workspace, workspace_bytes, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,189 @@
+// What the attention kernels over the paged cache share (gfx950).
+//
+// Rows.  The query heads of one key / value head (a group) and all queries of a sequence share its keys: row
+// r = i group + g of the pair (sequence, key / value head) is query i's head g of the group, and tiles are made of
+// consecutive rows.
+//
+// Scores are formed transposed, S^T = K Q^T, so that a lane holds one row's scores (a column of the matrix
+// instruction's result) for 4 keys in 4, 8 or 16: maxima and sums stay in the lane but for one or two exchanges, the
+// factor that rescales a row's sums is the lane's own, and the probabilities are already where the second product,
+// O^T = V^T P^T, takes them (its keys are summed in whatever order both operands share).  V's operand comes from
+// the row-major LDS tile through the transposing LDS read.
+//
+// Rounding: scores, maxima, sums and outputs are float32.  The probabilities (at most 1) are rounded to the
+// tensors' 16-bit type for the matrix instruction, half a step each (2^-8 of the value in bf16, 2^-11 in f16, which
+// leaves 2^-25 for what is below 2^-14): less than the output's own rounding on average, and the sums
+// below the fraction are of the unrounded ones.
+#pragma once
+
+#include "device_common.h"
+#include "launch.h"
+
+namespace w4a4 {
+
+typedef __attribute__((address_space(3))) void attn_lds_void;
+typedef short attn_short4_t __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) attn_short4_t attn_lds_s4;
+
+struct Bf16 {
+  typedef bf16x8_t x8;
+  static __device__ __forceinline__ float4_t mma16(x8 a, x8 b, float4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float16_t mma32(x8 a, x8 b, float16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {  // round to nearest even
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf16x2_t));
+  }
+};
+
+struct F16 {
+  typedef half8_t x8;
+  static __device__ __forceinline__ float4_t mma16(x8 a, x8 b, float4_t c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ float16_t mma32(x8 a, x8 b, float16_t c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack2(float a, float b) {
+    return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
+  }
+};
+
+// One sequence, as the device's arrays describe it, with everything clamped to what the arguments hold.
+struct AttnSeq {
+  int token0, nq;  // its queries
+  int len, ctx;    // its keys, and those before its queries (negative: more queries than keys)
+};
+
+__device__ __forceinline__ AttnSeq attn_seq(const AttnArgs& a, int s) {
+  AttnSeq q;
+  if (a.starts != nullptr) {
+    q.token0 = min(max(a.starts[s], 0), a.tokens);
+    q.nq = min(max(a.starts[s + 1], q.token0), a.tokens) - q.token0;
+  } else {
+    q.token0 = s * a.each;
+    q.nq = a.each;
+  }
+  q.len = min(max(a.lens[s], 0), a.max_len);
+  q.ctx = q.len - q.nq;
+  return q;
+}
+
+// The keys that the queries from number i0 on may see: [lo, hi), and below lo the sinks, in blocks of BN keys.
+// Block b of the list is block b of the cache below `sink_blocks`, and b + skip from there on.
+struct AttnSpan {
+  int lo, hi, sinks;  // keys below `sinks` are seen too
+  int sink_blocks, skip, blocks;
+};
+
+template <int BN>
+__device__ __forceinline__ AttnSpan attn_span(const AttnArgs& a, const AttnSeq& q, int i0, int hi) {
+  AttnSpan s;
+  s.hi = max(hi, 0);
+  // (a tree's nodes lie at or behind the tree's start)
+  const int first = a.mask != nullptr ? q.ctx : q.ctx + i0;
+  s.lo = a.window > 0 && first >= a.window ? min(first - a.window + 1, s.hi) : 0;
+  s.sinks = a.window > 0 ? min(a.sinks, s.lo) : 0;
+  const int b0 = s.lo / BN;
+  s.sink_blocks = min((s.sinks + BN - 1) / BN, b0);
+  s.skip = b0 - s.sink_blocks;
+  s.blocks = max((s.hi + BN - 1) / BN - s.skip, 1);
+  return s;
+}
+
+// What one row sees: keys below hi from lo on, or below a.sinks.
+struct AttnRow {
+  int hi, lo;
+};
+
+__device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, const AttnSeq& q, int i, bool valid) {
+  AttnRow r;
+  r.hi = 0;
+  r.lo = 0;
+  if (valid) {
+    int p = q.ctx + i;
+    r.hi = min(p + 1, q.len);
+    if (a.mask != nullptr) {
+      r.hi = q.ctx;
+      p = a.pos != nullptr ? max(a.pos[q.token0 + i], q.ctx) : q.ctx;
+    }
+    if (a.window > 0 && p >= a.window) r.lo = p - a.window + 1;
+  }
+  return r;
+}
+
+__device__ __forceinline__ int attn_page(const AttnArgs& a, int key) {  // key / page_size
+  return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift);
+}
+
+// The place of a key in the cache, elements from the head's first one; -1: none (nothing there is seen).
+struct AttnPlace {
+  int64_t k, v;
+};
+
+__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int key, uint32_t page, bool ok) {
+  AttnPlace p;
+  p.k = p.v = -1;
+  if (ok && page < a.pages) {
+    const int64_t in = key - attn_page(a, key) * a.page_size;
+    p.k = (int64_t)page * a.k_page + in * a.k_token;
+    p.v = (int64_t)page * a.v_page + in * a.v_token;
+  }
+  return p;
+}
+
+// Chunk (16 bytes) c of row r of an LDS tile with DP / 8 chunks a row lies at c ^ swizzle(r): 16 consecutive
+// rows reading one chunk touch all banks.
+template <int DP>
+__device__ __forceinline__ int attn_swizzle(int row) {
+  return DP == 64 ? (row >> 1) & 7 : row & 15;
+}
+
+// 16 bytes per lane from `src` to LDS at dst + 16 lane (dst is the wave's).
+__device__ __forceinline__ void attn_load16(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)dst, 16, 0, 0);
+}
+
+template <int N>
+__device__ __forceinline__ void attn_vm_wait() {  // all but the last N of the wave's memory operations are done
+  static_assert(N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+}
+
+__device__ __forceinline__ float attn_max32(float v) {  // with the lane 32 further
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float attn_max16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+}
+__device__ __forceinline__ float attn_sum32(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+__device__ __forceinline__ float attn_sum16(float v) {
+  const uint32_t u = __float_as_uint(v);
+  const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return __uint_as_float(s[0]) + __uint_as_float(s[1]);
+}
+
+// Two rows' 8 bytes of V at `a` and `b` (this lane's part of 4 keys x 16 columns each), transposed: the lane's
+// column of both.
+template <class T>
+__device__ __forceinline__ typename T::x8 attn_read_vt(const uint8_t* a, const uint8_t* b) {
+  const attn_short4_t t0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4*)a);
+  const attn_short4_t t1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4*)b);
+  const u32x2_t w0 = __builtin_bit_cast(u32x2_t, t0), w1 = __builtin_bit_cast(u32x2_t, t1);
+  return __builtin_bit_cast(typename T::x8, u32x4_t{w0[0], w0[1], w1[0], w1[1]});
+}
+
+constexpr float ATTN_NONE = -__builtin_inff();
+
+}  // namespace w4a4

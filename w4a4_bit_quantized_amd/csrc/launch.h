@@ -127,8 +127,43 @@ struct RopeArgs {
   int tb, hb, log2g, log2p;
 };
 
-// RMS norm and rotary rotation of q and k heads; dtype 0 bf16, 1 f16, 2 f32.
-hipError_t W4A4_KERNELS launch_qk_norm_rope(RopeArgs args, int dtype, hipStream_t stream);
+// Where w4a4_kv_append stores k and v: element (page, token of the page, head, d) of k at
+// k.y + page k_page + token k_token + head k.yhs + d (k.yts is not used); v alike.
+struct CacheArgs {
+  RopeHeads v;
+  const void* slots;  // [tokens], int32 or int64: page page_size + token of the page
+  bool slots64;
+  int64_t pages, page_size, k_page, k_token, v_page, v_token;
+};
+
+// RMS norm and rotary rotation of q and k heads; dtype 0 bf16, 1 f16, 2 f32.  With `cache` (16-bit types), k's
+// results and v as it is go into a paged cache.
+hipError_t W4A4_KERNELS launch_qk_norm_rope(RopeArgs args, const CacheArgs* cache, int dtype, hipStream_t stream);
+
+// Attention over a paged cache (see w4a4_paged_attention).  Strides in elements; max_len = keys that the page
+// table has room for; key / page_size = (key * page_mul) >> page_shift for 0 <= key < 2^31.
+struct AttnArgs {
+  const uint8_t* q;
+  uint8_t* out;
+  const uint8_t *k, *v;
+  int64_t q_ts, q_hs, o_ts, o_hs;
+  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+  const int32_t *table, *lens, *starts, *pos;  // starts NULL: `each` queries per sequence
+  const uint8_t* mask;                         // NULL: causal
+  int64_t table_stride, mask_stride;
+  int tokens, batch, each, heads, kv_heads, group, D, max_len, mask_width;
+  uint32_t pages, page_mul;
+  int page_size, page_shift;
+  float scale_log2;  // scale * log2(e)
+  int window, sinks;
+  // set by the launcher: sequences of more than rows_from and at most rows_to rows are this launch's
+  int rows_from, rows_to, least, pieces;
+  int32_t* desc;
+  float *stats, *part;
+};
+
+size_t W4A4_KERNELS attention_workspace_bytes(const AttnArgs& a, int64_t max_q);
+hipError_t W4A4_KERNELS launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream);
 
 // Device address of the static workspace of svdq_linear_noalloc on the current device (looked up
 // once per device), or NULL when the lookup fails.

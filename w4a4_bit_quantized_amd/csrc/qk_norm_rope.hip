@@ -40,6 +40,7 @@ constexpr int RT = 256;  // threads per workgroup
 // strides of the whole launch (2048 of them: 180 us at 32760 tokens of 48 heads of 128, 1536: 159;
 // a contiguous run of tokens for each: 172; one pass per workgroup: 169).
 constexpr int MAX_WGS = 1536;
+constexpr int MAX_TB = 8;  // tokens of a workgroup's pass
 
 template <int DT>
 __device__ __forceinline__ constexpr int esize() { return DT == 2 ? 4 : 2; }
@@ -167,14 +168,19 @@ __host__ __device__ constexpr int row_stride(int D) { return 2 * D + 16; }
 // results in their places and stores the row in chunks again; no other wave touches the row.
 // 32760 tokens of 48 heads of 128, halves of axes of 44, 42 and 42: 178 us, element by element 283 (two items
 // in flight: 206, four: 219).  In 4-byte chunks, for heads of 66, it loses: 57 against 52.
-template <int DT, int V, bool INTER, int IT, int UN, bool STAGED>
-__global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
+//
+// CACHE: the heads of v follow those of k.  k and v go to the token's place in a paged cache, v as it is; each
+// pass's threads find the places while the angles are formed (a 64-bit division per token), and items of tokens
+// that have none store nothing.
+template <int DT, int V, bool INTER, int IT, int UN, bool STAGED, bool CACHE>
+__global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a, const CacheArgs cache) {
   static_assert(!STAGED || (DT != 2 && V == 1 && IT == 4 && UN == 1 && !INTER), "the staged form");
   // two halves of [tb][D / 2] cosines, then sines; then (STAGED) a row for every lane group
   extern __shared__ __attribute__((aligned(16))) float trig[];
+  __shared__ int64_t place[CACHE ? 2 : 1][CACHE ? MAX_TB : 1][2];  // (CACHE) of every token's k and v, or -1
   const int t = threadIdx.x;
   const int D2 = a.D / 2, G = 1 << a.log2g;
-  const int heads = a.q.heads + a.k.heads;
+  const int heads = a.q.heads + a.k.heads + (CACHE ? cache.v.heads : 0);
   const int h0 = blockIdx.y * a.hb, nh = min(a.hb, heads - h0);
   constexpr int ES = esize<DT>();
 
@@ -241,6 +247,21 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
         cos_t[tk * D2 + ap] = c;
         sin_t[tk * D2 + ap] = s;
       }
+    if constexpr (CACHE) {
+      if (t >= RT - nt) {  // (the last wave, which has the fewest angles)
+        const int tk = RT - 1 - t;
+        const int64_t slot = cache.slots64 ? static_cast<const int64_t*>(cache.slots)[t0 + tk]
+                                           : static_cast<const int32_t*>(cache.slots)[t0 + tk];
+        int64_t kp = -1, vp = -1;
+        if (slot >= 0 && slot < cache.pages * cache.page_size) {
+          const int64_t page = slot / cache.page_size, in_page = slot - page * cache.page_size;
+          kp = page * cache.k_page + in_page * cache.k_token;
+          vp = page * cache.v_page + in_page * cache.v_token;
+        }
+        place[half][tk][0] = kp;
+        place[half][tk][1] = vp;
+      }
+    }
     __syncthreads();  // (the other half is rewritten only after the next one)
 
     int tok = 0, head = grp;  // item of this group: token t0 + tok, head h0 + head
@@ -248,7 +269,7 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
     while (tok < nt) {
       float v[UN][IT][2 * V];
       int it_tok[UN];
-      bool it_q[UN];
+      bool it_q[UN], it_v[UN];
       uint8_t* dst[UN];
 #pragma unroll
       for (int u = 0; u < UN; ++u) {
@@ -259,10 +280,23 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
         it_q[u] = isq;
         const int hh = isq ? hd : hd - a.q.heads;
         const int64_t tt = t0 + tok;
-        const uint8_t* src = static_cast<const uint8_t*>(isq ? a.q.x : a.k.x) +
-                             (tt * (isq ? a.q.ts : a.k.ts) + hh * (isq ? a.q.hs : a.k.hs)) * ES;
-        dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
-                 (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
+        const uint8_t* src;
+        it_v[u] = false;
+        if constexpr (CACHE) {
+          const bool isv = hh >= a.k.heads && !isq;
+          it_v[u] = isv;
+          const RopeHeads& x = isq ? a.q : isv ? cache.v : a.k;
+          const int hx = isv ? hh - a.k.heads : hh;
+          src = static_cast<const uint8_t*>(x.x) + (tt * x.ts + hx * x.hs) * ES;
+          const int64_t at = isq || !valid ? 0 : place[half][tok][isv];
+          if (at < 0) it_tok[u] = -1;
+          dst[u] = static_cast<uint8_t*>(x.y) + ((isq ? tt * x.yts : at) + hx * x.yhs) * ES;
+        } else {
+          src = static_cast<const uint8_t*>(isq ? a.q.x : a.k.x) +
+                (tt * (isq ? a.q.ts : a.k.ts) + hh * (isq ? a.q.hs : a.k.hs)) * ES;
+          dst[u] = static_cast<uint8_t*>(isq ? a.q.y : a.k.y) +
+                   (tt * (isq ? a.q.yts : a.k.yts) + hh * (isq ? a.q.yhs : a.k.yhs)) * ES;
+        }
         if constexpr (STAGED) {
           if (valid && has_chunk) *reinterpret_cast<u32x4_t*>(row + 16 * gl) = *reinterpret_cast<const u32x4_a2*>(src + 16 * gl);
           wave_lds_sync();
@@ -302,7 +336,8 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
           if (!in[c]) continue;
           float o[2 * V];
 #pragma unroll
-          for (int i = 0; i < 2 * V; ++i) o[i] = a.norm ? (v[u][c][i] * r) * (it_q[u] ? wq[c][i] : wk[c][i]) : v[u][c][i];
+          for (int i = 0; i < 2 * V; ++i)
+            o[i] = a.norm && !it_v[u] ? (v[u][c][i] * r) * (it_q[u] ? wq[c][i] : wk[c][i]) : v[u][c][i];
           const int at = it_tok[u] * D2 + (gl + c * G) * V;
           float cs[V], sn[V];
           if constexpr (V == 4) {
@@ -319,7 +354,7 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const int i0 = INTER ? 2 * i : i, i1 = INTER ? 2 * i + 1 : V + i;
-            const bool turn = (gl + c * G) * V + i < a.rot2;
+            const bool turn = (gl + c * G) * V + i < a.rot2 && !it_v[u];
             const float x0 = o[i0], x1 = o[i1];
             o[i0] = turn ? fmaf(x0, cs[i], -(x1 * sn[i])) : x0;
             o[i1] = turn ? fmaf(x0, sn[i], x1 * cs[i]) : x1;
@@ -345,17 +380,23 @@ __global__ __launch_bounds__(RT) void qk_norm_rope_kernel(const RopeArgs a) {
 }
 
 template <int DT, int V, bool INTER, int IT, int UN, bool STAGED>
-hipError_t run(const RopeArgs& a, hipStream_t st) {
-  const int heads = a.q.heads + a.k.heads;
+hipError_t run(const RopeArgs& a, const CacheArgs* cache, hipStream_t st) {
+  const int heads = a.q.heads + a.k.heads + (cache ? cache->v.heads : 0);
   const int64_t blocks = ((int64_t)a.tokens + a.tb - 1) / a.tb;
   const dim3 grid((unsigned)(blocks < MAX_WGS ? blocks : MAX_WGS), (unsigned)((heads + a.hb - 1) / a.hb));
   const size_t lds = 2 * (size_t)a.tb * a.D * sizeof(float) + (STAGED ? (size_t)(RT >> a.log2g) * row_stride(a.D) : 0);
-  qk_norm_rope_kernel<DT, V, INTER, IT, UN, STAGED><<<grid, RT, lds, st>>>(a);
+  if constexpr (DT != 2) {  // (a cache holds 16-bit elements)
+    if (cache) {
+      qk_norm_rope_kernel<DT, V, INTER, IT, UN, STAGED, true><<<grid, RT, lds, st>>>(a, *cache);
+      return hipGetLastError();
+    }
+  }
+  qk_norm_rope_kernel<DT, V, INTER, IT, UN, STAGED, false><<<grid, RT, lds, st>>>(a, CacheArgs{});
   return hipGetLastError();
 }
 
 template <int DT>
-hipError_t run_dt(RopeArgs a, bool vec, bool staged, hipStream_t st) {
+hipError_t run_dt(RopeArgs a, const CacheArgs* cache, bool vec, bool staged, hipStream_t st) {
   // Element-wise heads: 4 pairs per lane, in f32 with 49 to 64 of them 2 of 2 items (8000 tokens of 48 heads of 128,
   // halves of axes of 44, 42 and 42, f32: 94 us with 2, 105 with 4; of 66, f32: 74 and 64; 40 heads of 126, bf16: 68
   // and 67; 48 heads of 34, f16: 29 and 24).
@@ -363,7 +404,7 @@ hipError_t run_dt(RopeArgs a, bool vec, bool staged, hipStream_t st) {
   const int lanes = vec ? a.D / 8 : two ? (a.D / 2 + 1) / 2 : (a.D / 2 + 3) / 4;
   a.log2g = 0;
   while ((1 << a.log2g) < lanes) ++a.log2g;
-  const int ng = RT >> a.log2g, heads = a.q.heads + a.k.heads;
+  const int ng = RT >> a.log2g, heads = a.q.heads + a.k.heads + (cache ? cache->v.heads : 0);
   a.log2p = 0;
   while ((1 << a.log2p) < a.D / 2) ++a.log2p;
   // few tokens: one pass per workgroup, heads split over workgroups; many: several tokens each
@@ -371,20 +412,20 @@ hipError_t run_dt(RopeArgs a, bool vec, bool staged, hipStream_t st) {
   // tokens per pass: about six items for every lane group, so that a pass is worth its angles and its barrier
   const int64_t per = ((int64_t)a.tokens + MAX_WGS - 1) / MAX_WGS;  // (fewer where not every workgroup has a pass)
   const int full = heads > 0 ? 6 * ng / heads : 1;
-  a.tb = full < 1 ? 1 : full > 8 ? 8 : full;
+  a.tb = full < 1 ? 1 : full > MAX_TB ? MAX_TB : full;
   if (per < a.tb) a.tb = (int)per;
-  if (vec) return a.layout == 0 ? run<DT, 4, true, 1, 2, false>(a, st) : run<DT, 4, false, 1, 2, false>(a, st);
+  if (vec) return a.layout == 0 ? run<DT, 4, true, 1, 2, false>(a, cache, st) : run<DT, 4, false, 1, 2, false>(a, cache, st);
   if constexpr (DT == 2) {
-    if (two) return run<DT, 1, false, 2, 2, false>(a, st);
+    if (two) return run<DT, 1, false, 2, 2, false>(a, cache, st);
   } else {
-    if (staged) return run<DT, 1, false, 4, 1, true>(a, st);
+    if (staged) return run<DT, 1, false, 4, 1, true>(a, cache, st);
   }
-  return run<DT, 1, false, 4, 1, false>(a, st);
+  return run<DT, 1, false, 4, 1, false>(a, cache, st);
 }
 
 }  // namespace
 
-hipError_t launch_qk_norm_rope(RopeArgs a, int dtype, hipStream_t stream) {
+hipError_t launch_qk_norm_rope(RopeArgs a, const CacheArgs* cache, int dtype, hipStream_t stream) {
   // 4-pair vectors need whole 8-element chunks of the head, and in the split layouts whole chunks of 4 pairs in
   // the span and in every slice
   bool vec = a.D % 8 == 0;
@@ -394,9 +435,9 @@ hipError_t launch_qk_norm_rope(RopeArgs a, int dtype, hipStream_t stream) {
   // (16-bit types; one token of 40 heads: 5.1 us, element by element 4.6; 300 tokens: 6.6 and 7.2)
   const bool staged = a.D % 8 == 0 && !vec;
   switch (dtype) {
-    case 0: return run_dt<0>(a, vec, staged, stream);
-    case 1: return run_dt<1>(a, vec, staged, stream);
-    default: return run_dt<2>(a, vec, staged, stream);
+    case 0: return run_dt<0>(a, cache, vec, staged, stream);
+    case 1: return run_dt<1>(a, cache, vec, staged, stream);
+    default: return run_dt<2>(a, cache, vec, staged, stream);
   }
 }
 
