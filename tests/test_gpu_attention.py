@@ -157,3 +157,22 @@ def test_few_queries_and_trees(w4, shape, dtype):
     b.check(b.run_tree(w4, m, pos, window=33, sinks=2), "tree, window", mask=m, positions=pos, window=33, sinks=2)
     m[::3] = False  # rows that see no drafted token
     b.check(b.run_tree(w4, m, pos), "tree with empty rows", mask=m)
+
+
+MANY = [([(70, 70)], 4, 1, 64, 16), ([(200, 200), (3, 50), (129, 300)], 2, 2, 128, 16), ([(40, 700), (90, 95)], 8, 1, 80, 24),
+        ([(1, 400), (150, 150), (0, 7), (2, 2)], 4, 2, 256, 32), ([(65, 30)], 3, 3, 8, 1), ([(300, 1000)], 2, 1, 128, 256)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", MANY, ids=names)
+def test_prompts_and_large_trees(w4, shape, dtype):
+    both, hq, hk, D, page = shape
+    print(f"\n{shape} {dtype}", flush=True)
+    b = Batch(3, both, hq, hk, D, page, dtype, tail=3, heads_first=hq == 2)
+    b.check(b.run(w4), "causal")
+    b.check(b.run(w4, window=60, sinks=5), "window", window=60, sinks=5)
+    b.check(b.run(w4, max_q=1), "another kernel")
+    m, pos = b.tree()
+    b.check(b.run_tree(w4, m, pos), "tree", mask=m)
+    m[::5] = False
+    b.check(b.run_tree(w4, m, pos, window=75, sinks=70), "tree, window", mask=m, positions=pos, window=75, sinks=70)

@@ -13,9 +13,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SOURCES = ["csrc/api.cpp", "csrc/quantize.hip", "csrc/gemm.hip", "csrc/gemm_skinny.hip", "csrc/hadamard.hip",
            "csrc/lowrank_split.cpp", "csrc/noalloc.hip", "csrc/gemm_mx.hip",
-           "csrc/quantize_i8.hip", "csrc/gemm_i8.hip", "csrc/qk_norm_rope.hip", "csrc/attn_stream.hip"]
+           "csrc/quantize_i8.hip", "csrc/gemm_i8.hip", "csrc/qk_norm_rope.hip", "csrc/attn_stream.hip",
+           "csrc/attn_tile.hip"]
 # Sources whose kernel choice reads the path-forcing test hooks (see csrc/launch.h).
 HOOKED = ("csrc/gemm.hip", "csrc/gemm_skinny.hip", "csrc/gemm_mx.hip", "csrc/gemm_i8.hip")
+# Matrix instructions' results in vector registers: the attention kernels scale their accumulators between the
+# products, which from accumulation registers costs two moves per value and block.
+VGPR_FORM = ("csrc/attn_stream.hip", "csrc/attn_tile.hip")
 TEST_LIB = "libw4a4_test.so"
 ARCH = os.environ.get("W4A4_ARCH", "gfx950")
 
@@ -61,7 +65,8 @@ def build(verbose=False, out=None, test_lib=True, jobs=None):
     for s in SOURCES:
         obj = os.path.join(objdir, os.path.basename(s) + ".o")
         objs.append(obj)
-        cmds.append([hipcc()] + base + ["-c", os.path.join(HERE, s), "-o", obj])
+        extra = ["-mllvm", "-amdgpu-mfma-vgpr-form=1"] if s in VGPR_FORM else []
+        cmds.append([hipcc()] + base + extra + ["-c", os.path.join(HERE, s), "-o", obj])
         if test_lib and s in HOOKED:
             tobj = os.path.join(objdir, os.path.basename(s) + ".hooks.o")
             tobjs.append(tobj)

@@ -721,13 +721,22 @@ struct TreeMask {
   const void* positions;
 };
 
+// x / d = (x m) >> (31 + l) for x < 2^31, with l = ceil(log2 d) and m = ceil(2^(31 + l) / d): m d exceeds 2^(31 + l) by
+// less than d <= 2^l, so x (m d - 2^(31 + l)) < 2^(31 + l), which keeps the quotient below the next integer.
+void divisor(int64_t d, uint32_t& mul, int& shift) {
+  int l = 0;
+  while (((int64_t)1 << l) < d) ++l;
+  mul = (uint32_t)((((uint64_t)1 << (31 + l)) + d - 1) / d);
+  shift = 31 + l;
+}
+
 // Everything but pointers, in `a` for the kernels.
 w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, const TreeMask* tree, w4a4::AttnArgs& a) {
   if (p.dtype != W4A4_DTYPE_BF16 && p.dtype != W4A4_DTYPE_F16) return W4A4_ERR_UNSUPPORTED;
   if (p.head_dim > W4A4_ATTENTION_MAX_HEAD_DIM) return W4A4_ERR_UNSUPPORTED;
   if (p.head_dim < 8 || p.head_dim % 8 != 0) return W4A4_ERR_SHAPE;
   if (p.tokens < 0 || p.batch < 0 || p.batch > kMaxDim - 1 || p.heads < 1 || p.heads > kMaxHeads || c.heads < 1 ||
-      p.heads % c.heads != 0 || p.tokens > kMaxDim / p.heads)
+      p.heads % c.heads != 0 || p.tokens > ((int64_t)1 << 30) / p.heads)
     return W4A4_ERR_SHAPE;
   if (p.table_width < 0 || p.table_width > kMaxDim || p.table_stride < 0 || p.table_stride > (int64_t)1 << 40 ||
       p.window < 0 || p.sinks < 0 || p.max_q < 0)
@@ -771,12 +780,8 @@ w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, con
   a.max_len = (int)std::min<int64_t>(p.table_width * c.page_size, kMaxDim - 64);  // (block ends stay in 32 bits)
   a.pages = (uint32_t)c.pages;
   a.page_size = (int)c.page_size;
-  // x / d = (x m) >> (31 + l) for x < 2^31, with l = ceil(log2 d) and m = ceil(2^(31 + l) / d): m d exceeds 2^(31 + l) by
-  // less than d <= 2^l, so x (m d - 2^(31 + l)) < 2^(31 + l), which keeps the quotient below the next integer
-  int l = 0;
-  while (((int64_t)1 << l) < c.page_size) ++l;
-  a.page_mul = (uint32_t)((((uint64_t)1 << (31 + l)) + c.page_size - 1) / c.page_size);
-  a.page_shift = 31 + l;
+  divisor(c.page_size, a.page_mul, a.page_shift);
+  divisor(a.group, a.group_mul, a.group_shift);
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
   a.window = (int)std::min<int64_t>(p.window, kMaxDim);
   a.sinks = (int)std::min<int64_t>(p.sinks, kMaxDim);

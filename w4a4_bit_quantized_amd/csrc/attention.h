@@ -16,8 +16,11 @@
 // below the fraction are of the unrounded ones.
 #pragma once
 
+#include <algorithm>
+
 #include "device_common.h"
 #include "launch.h"
+#include "w4a4.h"
 
 namespace w4a4 {
 
@@ -115,25 +118,72 @@ __device__ __forceinline__ AttnRow attn_row(const AttnArgs& a, const AttnSeq& q,
   return r;
 }
 
+// x / d for 0 <= x < 2^52, d > 0: the float64 quotient is off by one at most.
+__device__ __forceinline__ int64_t attn_div(int64_t x, int64_t d) {
+  int64_t q = (int64_t)((double)x / (double)d);
+  const int64_t r = x - q * d;
+  return r < 0 ? q - 1 : r >= d ? q + 1 : q;
+}
+
+__device__ __forceinline__ int attn_query(const AttnArgs& a, int row) {  // row / group
+  return (int)(((uint64_t)(uint32_t)row * a.group_mul) >> a.group_shift);
+}
 __device__ __forceinline__ int attn_page(const AttnArgs& a, int key) {  // key / page_size
   return (int)(((uint64_t)(uint32_t)key * a.page_mul) >> a.page_shift);
 }
 
-// The place of a key in the cache, elements from the head's first one; -1: none (nothing there is seen).
+// Where a key's row and its value's start in the cache; keys that are not there (behind the last one, out of
+// everybody's window, on a page that the pool does not have) start at attn_zeros: what nobody sees is zero, whatever
+// the cache holds in its place.
 struct AttnPlace {
-  int64_t k, v;
+  const uint8_t *k, *v;
 };
 
-__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, int key, uint32_t page, bool ok) {
+static __device__ const u32x4_t attn_zeros[2 * W4A4_ATTENTION_MAX_HEAD_DIM / 16] = {};
+
+__device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, const uint8_t* k, const uint8_t* v, int key,
+                                                uint32_t page, bool ok) {
+  const int64_t in = key - attn_page(a, key) * a.page_size;
   AttnPlace p;
-  p.k = p.v = -1;
-  if (ok && page < a.pages) {
-    const int64_t in = key - attn_page(a, key) * a.page_size;
-    p.k = (int64_t)page * a.k_page + in * a.k_token;
-    p.v = (int64_t)page * a.v_page + in * a.v_token;
-  }
+  p.k = k + 2 * ((int64_t)page * a.k_page + in * a.k_token);
+  p.v = v + 2 * ((int64_t)page * a.v_page + in * a.v_token);
+  const uint8_t* z = reinterpret_cast<const uint8_t*>(attn_zeros);
+  if (!ok) p.k = p.v = z;
   return p;
 }
+
+// src + 16 c, or zeros for a chunk past the head's last element (none if EXACT).
+template <bool EXACT>
+__device__ __forceinline__ const uint8_t* attn_chunk(const uint8_t* src, int c, int D) {
+  if constexpr (EXACT) return src + 16 * c;
+  uint64_t x = reinterpret_cast<uint64_t>(src) + 16 * c, z = reinterpret_cast<uint64_t>(attn_zeros);
+  asm("" : "+v"(x), "+v"(z));  // (a select of two addresses: a branch would split the load in two)
+  return reinterpret_cast<const uint8_t*>(8 * c < D ? x : z);
+}
+
+__device__ __forceinline__ int64_t uniform(int64_t x) {  // one value of the whole wave
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x), hi = __builtin_amdgcn_readfirstlane((int)(x >> 32));
+  return (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Sums over the lanes up to each (6 steps within the vector registers).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int64_t attn_scan_step(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_update_dpp(0, (int)x, CTRL, ROWS, 0xF, false);
+  const uint32_t hi = __builtin_amdgcn_update_dpp(0, (int)(x >> 32), CTRL, ROWS, 0xF, false);
+  return x + (int64_t)(((uint64_t)hi << 32) | lo);
+}
+__device__ __forceinline__ int64_t attn_scan(int64_t x) {
+  x = attn_scan_step<0x111, 0xF>(x);  // row_shr 1, 2, 4, 8
+  x = attn_scan_step<0x112, 0xF>(x);
+  x = attn_scan_step<0x114, 0xF>(x);
+  x = attn_scan_step<0x118, 0xF>(x);
+  x = attn_scan_step<0x142, 0xA>(x);  // row_bcast 15, 31
+  return attn_scan_step<0x143, 0xC>(x);
+}
+
+__device__ __forceinline__ float attn_exp2(float x) { return __builtin_amdgcn_exp2f(x); }  // (results below 2^-126: 0)
 
 // Chunk (16 bytes) c of row r of an LDS tile with DP / 8 chunks a row lies at c ^ swizzle(r): 16 consecutive
 // rows reading one chunk touch all banks.
@@ -147,10 +197,17 @@ __device__ __forceinline__ void attn_load16(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)dst, 16, 0, 0);
 }
 
+// All but the last N of the wave's memory operations are done.  (In the loops' assembly: a wait that the compiler
+// counts itself it would make one for all direct loads, before the LDS is read.)
 template <int N>
-__device__ __forceinline__ void attn_vm_wait() {  // all but the last N of the wave's memory operations are done
-  static_assert(N < 64, "vmcnt range");
-  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | 0x0F70);
+__device__ __forceinline__ void attn_vm_wait() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+// All of them, and the compiler knows.
+__device__ __forceinline__ void attn_vm_drain() {
+  __builtin_amdgcn_s_waitcnt(0x0F70);
+  __builtin_amdgcn_wave_barrier();
 }
 
 __device__ __forceinline__ float attn_max32(float v) {  // with the lane 32 further
@@ -175,9 +232,10 @@ __device__ __forceinline__ float attn_sum16(float v) {
 }
 
 // Two rows' 8 bytes of V at `a` and `b` (this lane's part of 4 keys x 16 columns each), transposed: the lane's
-// column of both.
+// column of both.  (restrict gives the reads an alias scope; without one the compiler waits for every direct load
+// before each of them.)
 template <class T>
-__device__ __forceinline__ typename T::x8 attn_read_vt(const uint8_t* a, const uint8_t* b) {
+__device__ __forceinline__ typename T::x8 attn_read_vt(const uint8_t* __restrict__ a, const uint8_t* __restrict__ b) {
   const attn_short4_t t0 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4*)a);
   const attn_short4_t t1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4*)b);
   const u32x2_t w0 = __builtin_bit_cast(u32x2_t, t0), w1 = __builtin_bit_cast(u32x2_t, t1);
@@ -185,5 +243,8 @@ __device__ __forceinline__ typename T::x8 attn_read_vt(const uint8_t* a, const u
 }
 
 constexpr float ATTN_NONE = -__builtin_inff();
+// The reference that exponents are taken against is raised to a row's maximum only when that has passed it by more
+// than this (in powers of two): probabilities up to 2^8 lose nothing, and rescaling becomes rare.
+constexpr float ATTN_SLACK = 8.0f;
 
 }  // namespace w4a4

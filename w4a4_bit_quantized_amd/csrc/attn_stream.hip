@@ -26,55 +26,59 @@ struct Stream {
   static constexpr int STAGE = 2 * HALF;
 };
 
-// A lane without a key, or past the head's last element, loads this instead: what nobody sees is zero, so
-// whatever the cache holds there stays out of the sums.
-__device__ const u32x4_t attn_zeros = {0, 0, 0, 0};
-
-struct Desc {  // of a cut triple, where its first piece is
-  int pieces, seq, head, tile;
-};
-
-template <int DP, int NQ, class T>
+template <int DP, bool EXACT, int NQ, class T>
 __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
   using S = Stream<DP>;
   constexpr int BM = 16 * NQ, KS = DP / 32, ND = DP / 16;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[2 * S::STAGE];
-  __shared__ __attribute__((aligned(16))) AttnPlace places[KB];
+  // two stages, the places of a block's keys, and the pages of four blocks' keys (key lane % 32 of 64)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::STAGE + KB * sizeof(AttnPlace) + 4 * 256];
+  uint8_t* const ring = lds;
+  AttnPlace* const places = reinterpret_cast<AttnPlace*>(lds + 2 * S::STAGE);
+  uint8_t* const pages = lds + 2 * S::STAGE + KB * sizeof(AttnPlace);
   const int lane = threadIdx.x, c16 = lane & 15, qd = lane >> 4;
   const int w = blockIdx.x;
 
-  // blocks of a tile of sequence s, and its tiles (0: not this launch's)
-  auto tiles_of = [&](const AttnSeq& q) {
-    const int64_t rows = (int64_t)q.nq * a.group;
-    return rows > a.rows_from && rows <= a.rows_to ? (int)((rows + BM - 1) / BM) : 0;
+  // this wave's run [u0, u1) of all blocks, and the sequence that u0 is in.  A lane sums the blocks of a strip of
+  // sequences; with at most 64 of them, it keeps its one for later.
+  auto tiles_of = [&](const AttnSeq& q) {  // (0: not this launch's)
+    const int rows = q.nq * a.group;       // (at most tokens x group, which was checked to fit)
+    return rows > a.rows_from && rows <= a.rows_to ? (rows + BM - 1) / BM : 0;
   };
-  auto units_of = [&](int s) {
-    const AttnSeq q = attn_seq(a, s);
+  auto units_of = [&](const AttnSeq& q) {
     const int tiles = tiles_of(q);
     return tiles ? (int64_t)tiles * a.kv_heads * attn_span<KB>(a, q, 0, q.len).blocks : (int64_t)0;
   };
-  // this wave's run [u0, u1) of all blocks, and the sequence that u0 is in
   const int strip = (a.batch + 63) / 64;
+  AttnSeq own = {0, 0, 0, 0};
   int64_t mine = 0;
-  for (int s = lane * strip; s < min((lane + 1) * strip, a.batch); ++s) mine += units_of(s);
-  int64_t upto = mine;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const int64_t x = __shfl_up(upto, d);
-    if (lane >= d) upto += x;
+#pragma unroll 1
+  for (int s = lane * strip; s < min((lane + 1) * strip, a.batch); ++s) {
+    own = attn_seq(a, s);
+    mine += units_of(own);
   }
-  const int64_t total = __shfl(upto, 63);
-  const int64_t run = max((total + gridDim.x - 1) / gridDim.x, (int64_t)a.least);
+  auto seq_at = [&](int s) {
+    int many = strip;
+    asm volatile("" : "+s"(many));  // (a condition that the loop around it does not get a second copy for)
+    if (many > 1) return attn_seq(a, s);
+    return AttnSeq{__builtin_amdgcn_readlane(own.token0, s), __builtin_amdgcn_readlane(own.nq, s),
+                   __builtin_amdgcn_readlane(own.len, s), __builtin_amdgcn_readlane(own.ctx, s)};
+  };
+  const int64_t upto = attn_scan(mine);
+  auto lane_of = [](int64_t x, int l) {
+    const uint32_t lo = __builtin_amdgcn_readlane((int)x, l), hi = __builtin_amdgcn_readlane((int)(x >> 32), l);
+    return (int64_t)(((uint64_t)hi << 32) | lo);
+  };
+  const int64_t total = lane_of(upto, 63);
+  const int64_t run = max((total + gridDim.x - 1) >> a.log2_waves, (int64_t)a.least);
   const int64_t u0 = w * run, u1 = min(u0 + run, total);
   if (lane == 0) a.desc[4 * w] = 0;
   if (u0 >= u1) return;
-  const int at = __ffsll(__ballot(upto > u0)) - 1;
-  int64_t u = u0, before = __shfl(upto - mine, at);
-  int seq = __builtin_amdgcn_readfirstlane(at * strip);
+  const int at = uniform(__ffsll(__ballot(upto > u0)) - 1);
+  int64_t u = u0, before = lane_of(upto - mine, at);
 
-  const float sc = a.scale_log2;
-  for (; u < u1; ++seq) {
-    const AttnSeq sq = attn_seq(a, seq);
+#pragma unroll 1
+  for (int seq = at * strip; u < u1; ++seq) {
+    const AttnSeq sq = seq_at(seq);
     const int tiles = tiles_of(sq);
     if (tiles == 0) continue;
     const AttnSpan sp = attn_span<KB>(a, sq, 0, sq.len);
@@ -84,27 +88,27 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
       continue;
     }
     const int32_t* table = a.table + (int64_t)seq * a.table_stride;
-    while (u < u1 && u < before + units) {
-      const int64_t r = u - before;
-      const int pair = (int)(r / sp.blocks), head = pair / tiles, tile = pair % tiles;
-      const int b0 = (int)(r - (int64_t)pair * sp.blocks), b1 = (int)min((int64_t)sp.blocks, b0 + (u1 - u));
+    const int rows = sq.nq * a.group;
+    int64_t pair = uniform(attn_div(u - before, sp.blocks));  // head * tiles + tile
+    int b0 = (int)(u - before - pair * sp.blocks);
+    int head = uniform((int)attn_div(pair, tiles)), tile = (int)(pair - (int64_t)head * tiles);
+#pragma unroll 1
+    while (u < u1 && head < a.kv_heads) {
+      const int b1 = (int)min((int64_t)sp.blocks, b0 + (u1 - u));
       u += b1 - b0;
       const uint8_t* kh = a.k + 2 * (head * a.k_head);
       const uint8_t* vh = a.v + 2 * (head * a.v_head);
-      const int rows = sq.nq * a.group;  // (at most tokens x group: checked to fit)
 
       // the tile's rows: what each lane's sees, and its operands
       AttnRow row[NQ];
-      int64_t mrow[NQ];
       typename T::x8 qf[NQ][KS];
       int low_hi = 0x7FFFFFFF, top_lo = 0;
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const int rr = tile * BM + n * 16 + c16;
         const bool valid = rr < rows;
-        const int i = valid ? rr / a.group : 0, g = valid ? rr - i * a.group : 0;
+        const int i = valid ? attn_query(a, rr) : 0, g = valid ? rr - i * a.group : 0;
         row[n] = attn_row(a, sq, i, valid);
-        mrow[n] = (int64_t)(sq.token0 + i) * a.mask_stride;
         if (valid) {
           low_hi = min(low_hi, row[n].hi);
           top_lo = max(top_lo, row[n].lo);
@@ -123,35 +127,16 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         low_hi = min(low_hi, __shfl_xor(low_hi, d));
         top_lo = max(top_lo, __shfl_xor(top_lo, d));
       }
-      low_hi = __builtin_amdgcn_readfirstlane(low_hi);
-      top_lo = __builtin_amdgcn_readfirstlane(top_lo);
+      low_hi = uniform(low_hi);
+      top_lo = uniform(top_lo);
 
       auto key0 = [&](int b) { return (b < sp.sink_blocks ? b : b + sp.skip) * KB; };
       auto seen_by_any = [&](int key) { return key < sp.hi && (key >= sp.lo || key < sp.sinks); };
-      // page of this lane's key (lane % 32) of block b
-      auto page_of = [&](int b) {
+      // starts the load of the pages of block b's keys (of zeros where there is no such key)
+      auto load_pages = [&](int b) {
         const int key = key0(b) + (lane & 31);
-        return b < b1 && seen_by_any(key) ? (uint32_t)table[attn_page(a, key)] : 0xFFFFFFFFu;
-      };
-      // starts block b's loads into stage b % 2; returns which of its keys are there
-      auto issue = [&](int b, uint32_t page) {
-        const int key = key0(b) + (lane & 31);
-        const AttnPlace p = attn_place(a, key, page, seen_by_any(key));
-        wave_lds_sync();
-        if (lane < KB) places[lane] = p;
-        wave_lds_sync();
-        uint8_t* stage = ring + (b & 1) * S::STAGE;
-#pragma unroll
-        for (int n = 0; n < S::NI; ++n) {
-          const int lr = n * S::RPI + lane / S::CPR;
-          const int c = (lane % S::CPR) ^ attn_swizzle<DP>(lr);
-          const AttnPlace pl = places[lr];
-          const bool none = pl.k < 0 || 8 * c >= a.D;
-          const uint8_t* z = reinterpret_cast<const uint8_t*>(&attn_zeros);
-          attn_load16(none ? z : kh + 2 * pl.k + 16 * c, stage + n * 1024);
-          attn_load16(none ? z : vh + 2 * pl.v + 16 * c, stage + S::HALF + n * 1024);
-        }
-        return (uint32_t)__ballot(p.k >= 0);
+        const void* src = b < b1 && seen_by_any(key) ? (const void*)(table + attn_page(a, key)) : attn_zeros;
+        __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)(pages + (b & 3) * 256), 4, 0, 0);
       };
 
       float m[NQ], l[NQ];
@@ -163,54 +148,102 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[n][d] = float4_t{0, 0, 0, 0};
       }
-      wave_lds_sync();
-      uint32_t there[2];
-      there[0] = issue(b0, page_of(b0));
-      there[1] = 0;
-      uint32_t next = page_of(b0 + 1);
-      for (int b = b0; b < b1; ++b) {
-        const uint32_t here = there[0];
-        if (b + 1 < b1) {
-          there[1] = issue(b + 1, next);
-          next = page_of(b + 2);
-          attn_vm_wait<2 * S::NI>();  // (the page's load is one more, after them)
-        } else {
-          attn_vm_wait<0>();
-        }
-        __builtin_amdgcn_wave_barrier();
+      // Pass b works on block b and starts the loads of block b + 2: those of K as soon as this block's
+      // scores are formed, those of V at its end, so that one and a half blocks are on their way while the wave
+      // computes and two while it waits.  Past the run, zeros are loaded: every wait counts the same.  The pages are
+      // loaded two passes ahead of their use, into LDS too: for a register the compiler would wait by itself, for all loads.
+      // In the order of their issue: pages b + 2, K b, V b, pages b + 3, K b + 1, V b + 1, pages b + 4, K b + 2.
+      constexpr int AHEAD = 3 * S::NI + 2;
+      uint32_t here = 0, there = 0, later = 0;  // which keys of blocks b, b + 1, b + 2 are there
+      load_pages(b0);
+      load_pages(b0 + 1);
+      attn_vm_drain();
+#pragma unroll 1
+      for (int b = b0 - 2; b < b1; ++b) {
+        here = there;
+        there = later;
+        load_pages(b + 4);
+        const bool work = b >= b0;
         const uint8_t* ks = ring + (b & 1) * S::STAGE;
         const uint8_t* vs = ks + S::HALF;
         const int j0 = key0(b);
+        uint8_t* stage = ring + (b & 1) * S::STAGE;
 
         float4_t s[NQ][2];
+        if (work) {
+        attn_vm_wait<AHEAD>();
+      
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) s[n][t] = float4_t{0, 0, 0, 0};
+          typename T::x8 kf[KS];
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             const int lr = 16 * t + c16;
-            const auto kf = __builtin_bit_cast(typename T::x8, *reinterpret_cast<const u32x4_t*>(
+            kf[k] = __builtin_bit_cast(typename T::x8, *reinterpret_cast<const u32x4_t*>(
                 ks + lr * S::ROW + 16 * ((4 * k + qd) ^ attn_swizzle<DP>(lr))));
+          }
 #pragma unroll
-            for (int n = 0; n < NQ; ++n) s[n][t] = T::mma16(kf, qf[n][k], s[n][t]);
+          for (int n = 0; n < NQ; ++n) {
+            s[n][t] = float4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int k = 0; k < KS; ++k) s[n][t] = T::mma16(kf[k], qf[n][k], s[n][t]);
           }
         }
+        }
+        const int key = key0(b + 2) + (lane & 31);
+        const uint32_t page = *reinterpret_cast<const uint32_t*>(pages + (b + 2 & 3) * 256 + 4 * lane);
+        const bool ok = b + 2 < b1 && seen_by_any(key) && page < a.pages;
+        later = (uint32_t)__ballot(ok);
+        wave_lds_sync();
+        if (lane < KB) places[lane] = attn_place(a, kh, vh, key, page, ok);
+        wave_lds_sync();
+#pragma unroll
+        for (int n = 0; n < S::NI; ++n) {
+          const int lr = n * S::RPI + lane / S::CPR;
+          attn_load16(attn_chunk<EXACT>(places[lr].k, (lane % S::CPR) ^ attn_swizzle<DP>(lr), a.D), stage + n * 1024);
+        }
+        auto load_v = [&]() {
+#pragma unroll
+          for (int n = 0; n < S::NI; ++n) {
+            const int lr = n * S::RPI + lane / S::CPR;
+            attn_load16(attn_chunk<EXACT>(places[lr].v, (lane % S::CPR) ^ attn_swizzle<DP>(lr), a.D),
+                        stage + S::HALF + n * 1024);
+          }
+        };
+        if (work) {
         if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
+          // element (t, i) is key j0 + 4 qd + 16 t + i
+          const uint32_t mine = here >> (4 * qd);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n)
+          for (int n = 0; n < NQ; ++n) {
+            uint32_t bits = 0;  // (bit 16 t + i)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+            for (int e = 0; e < 8; ++e) {
+              const int in = 16 * (e >> 2) + (e & 3), j = j0 + 4 * qd + in;
+              bits |= (j < row[n].hi && (j >= row[n].lo || j < a.sinks) ? 1u : 0u) << in;
+            }
+            if (a.mask != nullptr && j0 + KB > sq.ctx && a.mask_width > 0) {
+              const int rr = tile * BM + n * 16 + c16;
+              const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
+              const int node = j0 + 4 * qd - sq.ctx;
+              uint32_t set[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int in = 16 * t + 4 * qd + i, j = j0 + in;
-                bool seen = j < row[n].hi && (j >= row[n].lo || j < a.sinks);
-                if (a.mask != nullptr && j >= sq.ctx) {
-                  const int node = j - sq.ctx;
-                  if (node < a.mask_width) seen = a.mask[mrow[n] + node] != 0;
-                }
-                if (!seen || !((here >> in) & 1)) s[n][t][i] = ATTN_NONE;
+              for (int e = 0; e < 8; ++e) set[e] = of[min(max(node + 16 * (e >> 2) + (e & 3), 0), a.mask_width - 1)];
+              attn_vm_drain();  // (with one for each, the loop's waits would wait for every load)
+              uint32_t tree = 0, nodes = 0;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const int in = 16 * (e >> 2) + (e & 3);
+                tree |= (set[e] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
+                nodes |= (node + in >= 0 ? 1u : 0u) << in;
               }
+              bits = (bits & ~nodes) | (tree & nodes);
+            }
+            bits &= mine;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (!((bits >> (16 * (e >> 2) + (e & 3))) & 1)) s[n][e >> 2][e & 3] = ATTN_NONE;
+          }
         }
 
         typename T::x8 p[NQ];
@@ -218,24 +251,26 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         for (int n = 0; n < NQ; ++n) {
           float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
                             fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-          top = fmaxf(m[n], attn_max16(attn_max32(top)) * sc);
-          const float ref = top == ATTN_NONE ? 0.0f : top;
-          if (__any(top > m[n])) {
-            const float f = exp2f(m[n] - ref);
+          top = attn_max16(attn_max32(top)) * a.scale_log2;
+          if (__any(top > m[n] + ATTN_SLACK)) {
+            const float to = fmaxf(m[n], top), f = attn_exp2(m[n] - (to == ATTN_NONE ? 0.0f : to));
             l[n] *= f;
 #pragma unroll
             for (int d = 0; d < ND; ++d) o[n][d] *= f;
-            m[n] = top;
+            m[n] = to;
           }
+          const float ref = m[n] == ATTN_NONE ? 0.0f : m[n];
           float e[8];
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[4 * t + i] = exp2f(fmaf(s[n][t][i], sc, -ref));
+            for (int i = 0; i < 4; ++i) e[4 * t + i] = attn_exp2(fmaf(s[n][t][i], a.scale_log2, -ref));
           l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
           p[n] = __builtin_bit_cast(typename T::x8, u32x4_t{T::pack2(e[0], e[1]), T::pack2(e[2], e[3]),
                                                            T::pack2(e[4], e[5]), T::pack2(e[6], e[7])});
         }
+        attn_vm_wait<AHEAD>();
+      
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
           const int r0 = 4 * qd + (c16 >> 2), r1 = r0 + 16, ch = 2 * d + ((c16 & 3) >> 1), half = 8 * (c16 & 1);
@@ -244,15 +279,15 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
           for (int n = 0; n < NQ; ++n) o[n][d] = T::mma16(vf, p[n], o[n][d]);
         }
-        there[0] = there[1];
+        wave_lds_sync();  // (the stage is read)
+        }
+        load_v();
       }
 
       // finished, or a piece: the first of a triple in slot 1 of the wave, any other in slot 0
       const bool whole = b0 == 0 && b1 == sp.blocks;
-      if (b0 == 0 && !whole && lane == 0) {
-        *reinterpret_cast<int4*>(a.desc + 4 * w) =
-            int4{1 + (int)((sp.blocks - b1 + run - 1) / run), seq, head, tile};
-      }
+      if (b0 == 0 && !whole && lane == 0)
+        *reinterpret_cast<int4*>(a.desc + 4 * w) = int4{1 + (int)attn_div(sp.blocks - b1 + run - 1, run), seq, head, tile};
       const int64_t slot = 2 * (int64_t)w + (b0 == 0 ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
@@ -261,7 +296,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         if (rr >= rows) continue;
         if (whole) {
           const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int i = rr / a.group, g = rr - i * a.group;
+          const int i = attn_query(a, rr), g = rr - i * a.group;
           uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs);
 #pragma unroll
           for (int d = 0; d < ND; ++d) {
@@ -277,64 +312,113 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
           for (int d = 0; d < ND; ++d) *reinterpret_cast<float4_t*>(a.part + at * DP + 16 * d + 4 * qd) = o[n][d];
         }
       }
+      b0 = 0;
+      if (++tile == tiles) {
+        tile = 0;
+        ++head;
+      }
     }
     before += units;
   }
+  attn_vm_drain();  // (nothing arrives in the LDS of an ended wave)
 }
 
-// Joins the pieces of the triple that starts in run blockIdx.x and is cut.  A thread takes 4 columns of a row.
+// Joins the pieces of the triple that starts in run blockIdx.x and is cut, one row at a time: lines of DP / 4 threads
+// take the pieces in turn, four at a time, and their sums meet in LDS.
 template <int DP, int BM, class T>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-  const int w = blockIdx.x;
+  constexpr int PER = DP / 4;
+  const int w = blockIdx.x, t = threadIdx.x;
   const int4 d = *reinterpret_cast<const int4*>(a.desc + 4 * w);
   if (d.x == 0) return;
   const AttnSeq sq = attn_seq(a, d.y);
-  const int rows = min(BM, sq.nq * a.group - d.w * BM), per = a.D / 4;
-  for (int x = threadIdx.x; x < rows * per; x += 256) {
-    const int r = x / per, e = 4 * (x - r * per);
-    auto at = [&](int p) { return (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * BM + r; };
-    float top = ATTN_NONE;
-    for (int p = 0; p < d.x; ++p) top = fmaxf(top, a.stats[2 * at(p)]);
-    const float ref = top == ATTN_NONE ? 0.0f : top;
-    float sum = 0.0f;
+  const int rows = min(BM, sq.nq * a.group - d.w * BM);
+  // piece p of row r
+  auto at = [&](int p, int r) { return (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * BM + r; };
+  __shared__ float4_t sums[256];
+  __shared__ float tops[256 / PER + 1], ls[256 / PER + 1];
+  constexpr int LINES = 256 / PER;  // lines of threads that each cover a row's columns
+  const int line = t / PER, e = 4 * (t % PER);
+  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+    // every line takes each LINES-th piece, with a maximum of its own
+    float top = ATTN_NONE, sum = 0.0f;
     float4_t o = {0, 0, 0, 0};
-    for (int p = 0; p < d.x; ++p) {
-      const float2_t st = *reinterpret_cast<const float2_t*>(a.stats + 2 * at(p));
-      const float f = exp2f(st[0] - ref);
-      sum = fmaf(st[1], f, sum);
-      const float4_t v = *reinterpret_cast<const float4_t*>(a.part + at(p) * DP + e);
+    for (int p0 = line; p0 < d.x; p0 += 4 * LINES) {
+      float2_t st[4];
+      float4_t v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[i] = fmaf(v[i], f, o[i]);
+      for (int i = 0; i < 4; ++i) {
+        const int64_t x = at(min(p0 + i * LINES, d.x - 1), r);
+        st[i] = *reinterpret_cast<const float2_t*>(a.stats + 2 * x);
+        v[i] = *reinterpret_cast<const float4_t*>(a.part + x * DP + e);
+        if (p0 + i * LINES >= d.x) st[i] = float2_t{ATTN_NONE, 0.0f};
+      }
+      const float to = fmaxf(fmaxf(fmaxf(st[0][0], st[1][0]), fmaxf(st[2][0], st[3][0])), top);
+      const float ref = to == ATTN_NONE ? 0.0f : to, keep = attn_exp2(top - ref);
+      sum *= keep;
+      o *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (p0 + i * LINES >= d.x) continue;  // (not even times 0: it may hold anything)
+        const float f = attn_exp2(st[i][0] - ref);
+        sum = fmaf(st[i][1], f, sum);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[i][c], f, o[c]);
+      }
+      top = to;
     }
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = d.w * BM + r, i = rr / a.group, g = rr - i * a.group;
-    uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(d.z * a.group + g) * a.o_hs + e);
-    *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{T::pack2(o[0] * f, o[1] * f), T::pack2(o[2] * f, o[3] * f)};
+    __syncthreads();
+    sums[t] = o;
+    if (e == 0) {
+      tops[line] = top;
+      ls[line] = sum;
+    }
+    __syncthreads();
+    if (line == 0 && e < a.D) {
+      float all = ATTN_NONE;
+#pragma unroll
+      for (int i = 0; i < LINES; ++i) all = fmaxf(all, tops[i]);
+      const float ref = all == ATTN_NONE ? 0.0f : all;
+      sum = 0.0f;
+      o = float4_t{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < LINES; ++i) {
+        const float f = attn_exp2(tops[i] - ref);
+        sum = fmaf(ls[i], f, sum);
+        const float4_t v = sums[i * PER + t];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], f, o[c]);
+      }
+      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+      const int rr = d.w * BM + r, i = attn_query(a, rr), g = rr - i * a.group;
+      uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(d.z * a.group + g) * a.o_hs + e);
+      *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{T::pack2(o[0] * f, o[1] * f), T::pack2(o[2] * f, o[3] * f)};
+    }
   }
 }
 
 // Waves of a launch: as many as the GPU's 256 CUs hold by their LDS.
-constexpr int waves_of(int DP) { return DP == 64 ? 2048 : DP == 128 ? 1024 : 512; }
+constexpr int log2_waves(int DP) { return DP == 64 ? 11 : DP == 128 ? 10 : 9; }
 
 template <int DP, int NQ, class T>
 hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
-  constexpr int W = waves_of(DP), BM = 16 * NQ;
+  constexpr int W = 1 << log2_waves(DP), BM = 16 * NQ;
   a.desc = static_cast<int32_t*>(workspace);
   a.stats = reinterpret_cast<float*>(a.desc + 4 * W);
   a.part = a.stats + (size_t)2 * W * BM * 2;
+  a.log2_waves = log2_waves(DP);
   a.least = 4;
-  attn_stream_kernel<DP, NQ, T><<<W, 64, 0, st>>>(a);
+  if (a.D == DP) attn_stream_kernel<DP, true, NQ, T><<<W, 64, 0, st>>>(a);
+  else attn_stream_kernel<DP, false, NQ, T><<<W, 64, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_join_kernel<DP, BM, T><<<W, 256, 0, st>>>(a);
+  attn_join_kernel<DP, BM, T><<<dim3(W, 4), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
 template <int DP, class T>
 hipError_t run_rows(const AttnArgs& a, int64_t rows, void* workspace, hipStream_t st) {
   if (rows <= 16) return run<DP, 1, T>(a, workspace, st);
-  if (rows <= 32) return run<DP, 2, T>(a, workspace, st);
-  if constexpr (DP <= 128) return run<DP, 4, T>(a, workspace, st);
   return run<DP, 2, T>(a, workspace, st);
 }
 
@@ -347,17 +431,31 @@ hipError_t run_dim(const AttnArgs& a, int64_t rows, void* workspace, hipStream_t
 
 }  // namespace
 
+// Sequences of at most this many rows are streamed; longer ones go to the tiles.
+constexpr int STREAM_ROWS = 32;
+
 size_t attention_workspace_bytes(const AttnArgs& a, int64_t max_q) {
   const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
-  const size_t W = waves_of(DP), BM = DP <= 128 ? 64 : 32;
-  return W * 16 + 2 * W * BM * 8 + 2 * W * BM * DP * 4;
+  const size_t W = 1 << log2_waves(DP), BM = STREAM_ROWS;
+  const size_t stream = W * 16 + 2 * W * BM * 8 + 2 * W * BM * DP * 4;
+  return max_q * a.group <= STREAM_ROWS ? stream : std::max(stream, attention_tile_bytes(a));
 }
 
 hipError_t launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream) {
   a.rows_from = 0;
   a.rows_to = 0x7FFFFFFF;
   const int64_t rows = max_q * a.group;
-  return dtype == 0 ? run_dim<Bf16>(a, rows, workspace, stream) : run_dim<F16>(a, rows, workspace, stream);
+  if (rows > STREAM_ROWS) {
+    // (queries that come to batch * max_q are max_q of every sequence)
+    const bool all = (int64_t)a.batch * max_q == a.tokens;
+    if (!all) a.rows_from = STREAM_ROWS;
+    hipError_t e = launch_attention_tile(a, dtype, workspace, stream);
+    if (e != hipSuccess || all) return e;
+    a.rows_from = 0;
+    a.rows_to = STREAM_ROWS;
+  }
+  return dtype == 0 ? run_dim<Bf16>(a, std::min<int64_t>(rows, STREAM_ROWS), workspace, stream)
+                    : run_dim<F16>(a, std::min<int64_t>(rows, STREAM_ROWS), workspace, stream);
 }
 
 }  // namespace w4a4

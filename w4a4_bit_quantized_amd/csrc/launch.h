@@ -141,7 +141,7 @@ struct CacheArgs {
 hipError_t W4A4_KERNELS launch_qk_norm_rope(RopeArgs args, const CacheArgs* cache, int dtype, hipStream_t stream);
 
 // Attention over a paged cache (see w4a4_paged_attention).  Strides in elements; max_len = keys that the page
-// table has room for; key / page_size = (key * page_mul) >> page_shift for 0 <= key < 2^31.
+// table has room for; x / page_size = (x * page_mul) >> page_shift for 0 <= x < 2^31, x / group alike.
 struct AttnArgs {
   const uint8_t* q;
   uint8_t* out;
@@ -152,18 +152,22 @@ struct AttnArgs {
   const uint8_t* mask;                         // NULL: causal
   int64_t table_stride, mask_stride;
   int tokens, batch, each, heads, kv_heads, group, D, max_len, mask_width;
-  uint32_t pages, page_mul;
-  int page_size, page_shift;
+  uint32_t pages, page_mul, group_mul;
+  int page_size, page_shift, group_shift;
   float scale_log2;  // scale * log2(e)
   int window, sinks;
   // set by the launcher: sequences of more than rows_from and at most rows_to rows are this launch's
-  int rows_from, rows_to, least, pieces;
+  int rows_from, rows_to, least, log2_waves, pieces;
   int32_t* desc;
   float *stats, *part;
 };
 
 size_t W4A4_KERNELS attention_workspace_bytes(const AttnArgs& a, int64_t max_q);
 hipError_t W4A4_KERNELS launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream);
+
+// Its kernel for many rows per sequence (called by launch_attention).
+size_t attention_tile_bytes(const AttnArgs& a);
+hipError_t launch_attention_tile(const AttnArgs& a, int dtype, void* workspace, hipStream_t stream);
 
 // Device address of the static workspace of svdq_linear_noalloc on the current device (looked up
 // once per device), or NULL when the lookup fails.
