@@ -176,3 +176,19 @@ def test_prompts_and_large_trees(w4, shape, dtype):
     b.check(b.run_tree(w4, m, pos), "tree", mask=m)
     m[::5] = False
     b.check(b.run_tree(w4, m, pos, window=75, sinks=70), "tree, window", mask=m, positions=pos, window=75, sinks=70)
+
+
+@pytest.mark.parametrize("shape", [([(500, 600), (512, 900)], 16, 2, 128, 128), ([(1, 5000)], 8, 1, 128, 16), ([(9, 700), (3, 80)], 8, 2, 64, 16),
+                                   ([(100, 150), (1, 900), (0, 3)], 4, 1, 256, 16)], ids=names)
+def test_workspace_of_exactly_its_size(w4, shape):
+    """Nothing is written behind the workspace, or behind the output's last sequence; what they held before does not matter."""
+    import torch
+    b = Batch(4, *shape, "bf16", tail=5)
+    for kw in (dict(), dict(max_q=None)):
+        need = w4.attention_workspace_bytes(b.dq, b.dk, b.dv, len(b.both), kw.get("max_q", b.max_q))
+        ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        out = torch.full_like(b.dq, 7.0)
+        b.check(b.run(w4, workspace=ws[:need], out=out, **kw))
+        assert (ws[need:] == 0xFF).all() and (out[int(b.starts[-1]):] == 7).all()
+        with pytest.raises(ValueError, match="workspace holds"):
+            b.run(w4, workspace=ws[:need - 1], **kw)

@@ -43,10 +43,10 @@ struct TileOf {
 };
 template <int BM>
 __device__ __forceinline__ TileOf tile_at(const AttnArgs& a, int slot) {
-  if (a.starts == nullptr) {
+  if (a.starts == nullptr) {  // (fewer slots than that; the last ones are past the batch)
     const int per = (int)(((int64_t)a.each * a.group + BM - 1) / BM);
     const int s = slot / per;
-    return {s, slot - s * per};
+    return {min(s, a.batch - 1), s < a.batch ? slot - s * per : -1};
   }
   auto first = [&](int s) { return min(max(a.starts[s], 0), a.tokens) * a.group / BM + s; };
   int lo = 0, hi = a.batch;  // first(lo) <= slot < first(hi)
@@ -346,16 +346,23 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(const AttnArgs a, c
   }
 }
 
-// Tile slots of a launch, and how many pieces each tile's keys are cut into.
+#ifndef VQ
+#define VQ 1
+#define VS 2
+#endif
+// The tiles of a call: rows of one, how many slots they take (see tile_at; without `starts`, sequence by sequence,
+// they take no more), and into how many pieces each tile's keys are cut.
 struct TilePlan {
+  int rows;
   int64_t slots;
   int pieces;
 };
-TilePlan plan(const AttnArgs& a, int BM) {
-  const int64_t rows = (int64_t)a.tokens * a.group;
+TilePlan plan(const AttnArgs& a) {
   TilePlan p;
-  p.slots = a.starts != nullptr ? rows / BM + a.batch : a.batch * (((int64_t)a.each * a.group + BM - 1) / BM);
-  const int64_t tiles = std::max<int64_t>(1, rows / BM) * a.kv_heads;
+  p.rows = a.D <= 64 ? 128 : a.D <= 128 ? 128 * VQ : 128;
+  const int64_t rows = (int64_t)a.tokens * a.group;
+  p.slots = rows / p.rows + a.batch;
+  const int64_t tiles = std::max<int64_t>(1, rows / p.rows) * a.kv_heads;
   p.pieces = (int)std::min<int64_t>(16, std::max<int64_t>(1, 512 / tiles));
   return p;
 }
@@ -363,7 +370,8 @@ TilePlan plan(const AttnArgs& a, int BM) {
 template <int DP, int NQ, int WAVES, int S, class T>
 hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
   using L = Tile<DP, NQ, WAVES, S>;
-  const TilePlan p = plan(a, L::BM);
+  const TilePlan p = plan(a);
+  if (p.rows != L::BM) return hipErrorInvalidValue;
   const int64_t wgs = p.slots * a.kv_heads * p.pieces;
   if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
   a.pieces = p.pieces;
@@ -380,16 +388,16 @@ hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
 template <class T>
 hipError_t run_dim(const AttnArgs& a, void* workspace, hipStream_t st) {
   if (a.D <= 64) return run<64, 1, 4, 2, T>(a, workspace, st);
-  if (a.D <= 128) return run<128, 1, 4, 2, T>(a, workspace, st);
+  if (a.D <= 128) return run<128, VQ, 4, VS, T>(a, workspace, st);
   return run<256, 1, 4, 2, T>(a, workspace, st);
 }
 
 }  // namespace
 
 size_t attention_tile_bytes(const AttnArgs& a) {
-  const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256, BM = 128;
-  const TilePlan p = plan(a, BM);
-  return p.pieces == 1 ? 0 : (size_t)p.slots * a.kv_heads * p.pieces * BM * (2 + DP) * sizeof(float);
+  const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
+  const TilePlan p = plan(a);
+  return p.pieces == 1 ? 0 : (size_t)p.slots * a.kv_heads * p.pieces * p.rows * (2 + DP) * sizeof(float);
 }
 
 hipError_t launch_attention_tile(const AttnArgs& a, int dtype, void* workspace, hipStream_t stream) {
