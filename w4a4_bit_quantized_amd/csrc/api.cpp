@@ -753,21 +753,25 @@ w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, con
   st = check_cache(c, p.head_dim, false);
   if (st != W4A4_OK) return st;
   // (the stride of a dimension of one does not matter)
-  const struct { int64_t n, s; } strides[] = {
+  struct Stride { int64_t n, s; };
+  const Stride strides[] = {
       {p.tokens, p.q_token_stride}, {p.heads, p.q_head_stride}, {p.tokens, p.out_token_stride}, {p.heads, p.out_head_stride},
       {c.pages, c.k_page_stride}, {c.page_size, c.k_token_stride}, {c.heads, c.k_head_stride},
       {c.pages, c.v_page_stride}, {c.page_size, c.v_token_stride}, {c.heads, c.v_head_stride}};
   for (const auto& x : strides)
     if (x.n > 1 && x.s % 8 != 0) return W4A4_ERR_SHAPE;
+  // (the kernels multiply a page's or token's number by its stride in 32 x 32 bits; the sums have 64)
+  for (const auto& x : {strides[4], strides[5], strides[7], strides[8]})
+    if (x.n > 1 && x.s > (int64_t)1 << 31) return W4A4_ERR_SHAPE;
   a.q_ts = p.q_token_stride;
   a.q_hs = p.q_head_stride;
   a.o_ts = p.out_token_stride;
   a.o_hs = p.out_head_stride;
-  a.k_page = c.k_page_stride;
-  a.k_token = c.k_token_stride;
+  a.k_page = (uint32_t)c.k_page_stride;
+  a.k_token = (uint32_t)c.k_token_stride;
   a.k_head = c.k_head_stride;
-  a.v_page = c.v_page_stride;
-  a.v_token = c.v_token_stride;
+  a.v_page = (uint32_t)c.v_page_stride;
+  a.v_token = (uint32_t)c.v_token_stride;
   a.v_head = c.v_head_stride;
   a.table_stride = p.table_stride;
   a.tokens = (int)p.tokens;

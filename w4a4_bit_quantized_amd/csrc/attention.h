@@ -40,6 +40,11 @@ struct Bf16 {
     typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf16x2_t));
   }
+  static __device__ __forceinline__ float sum2(uint32_t p, float c) {  // c + both values of p
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p), __builtin_bit_cast(bf16x2_t, 0x3F803F80u), c,
+                                           false);
+  }
 };
 
 struct F16 {
@@ -52,6 +57,9 @@ struct F16 {
   }
   static __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
+  }
+  static __device__ __forceinline__ float sum2(uint32_t p, float c) {
+    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, p), half2_t{(_Float16)1, (_Float16)1}, c, false);
   }
 };
 
@@ -143,10 +151,10 @@ static __device__ const u32x4_t attn_zeros[2 * W4A4_ATTENTION_MAX_HEAD_DIM / 16]
 
 __device__ __forceinline__ AttnPlace attn_place(const AttnArgs& a, const uint8_t* k, const uint8_t* v, int key,
                                                 uint32_t page, bool ok) {
-  const int64_t in = key - attn_page(a, key) * a.page_size;
+  const uint32_t in = key - attn_page(a, key) * a.page_size;
   AttnPlace p;
-  p.k = k + 2 * ((int64_t)page * a.k_page + in * a.k_token);
-  p.v = v + 2 * ((int64_t)page * a.v_page + in * a.v_token);
+  p.k = k + 2 * ((uint64_t)page * a.k_page + (uint64_t)in * a.k_token);
+  p.v = v + 2 * ((uint64_t)page * a.v_page + (uint64_t)in * a.v_token);
   const uint8_t* z = reinterpret_cast<const uint8_t*>(attn_zeros);
   if (!ok) p.k = p.v = z;
   return p;

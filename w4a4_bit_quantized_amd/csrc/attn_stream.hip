@@ -197,19 +197,14 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         wave_lds_sync();
         if (lane < KB) places[lane] = attn_place(a, kh, vh, key, page, ok);
         wave_lds_sync();
+        const uint8_t* from[S::NI];  // (all read before the first load: the compiler keeps their order)
+#pragma unroll
+        for (int n = 0; n < S::NI; ++n) from[n] = places[n * S::RPI + lane / S::CPR].k;
 #pragma unroll
         for (int n = 0; n < S::NI; ++n) {
-          const int lr = n * S::RPI + lane / S::CPR;
-          attn_load16(attn_chunk<EXACT>(places[lr].k, (lane % S::CPR) ^ attn_swizzle<DP>(lr), a.D), stage + n * 1024);
+          const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
+          attn_load16(attn_chunk<EXACT>(from[n], c, a.D), stage + n * 1024);
         }
-        auto load_v = [&]() {
-#pragma unroll
-          for (int n = 0; n < S::NI; ++n) {
-            const int lr = n * S::RPI + lane / S::CPR;
-            attn_load16(attn_chunk<EXACT>(places[lr].v, (lane % S::CPR) ^ attn_swizzle<DP>(lr), a.D),
-                        stage + S::HALF + n * 1024);
-          }
-        };
         if (work) {
         if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
           // element (t, i) is key j0 + 4 qd + 16 t + i
@@ -281,7 +276,13 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         }
         wave_lds_sync();  // (the stage is read)
         }
-        load_v();
+#pragma unroll
+        for (int n = 0; n < S::NI; ++n) from[n] = places[n * S::RPI + lane / S::CPR].v;
+#pragma unroll
+        for (int n = 0; n < S::NI; ++n) {
+          const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
+          attn_load16(attn_chunk<EXACT>(from[n], c, a.D), stage + S::HALF + n * 1024);
+        }
       }
 
       // finished, or a piece: the first of a triple in slot 1 of the wave, any other in slot 0

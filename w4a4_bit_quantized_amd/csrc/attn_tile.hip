@@ -8,25 +8,26 @@
 // v_mfma_f32_32x32x16: lane l holds row l % 32 of 32, keys 8 (i / 4) + 4 (l / 32) + i % 4 of 32.
 #include "attention.h"
 
+#include <type_traits>
+
 namespace w4a4 {
 
 namespace {
 
 constexpr int BN = 64;  // keys of a block
 
-template <int DP, int NQ, int WAVES, int S>
+template <int DP, int WAVES>
 struct Tile {
-  static constexpr int BM = 32 * NQ * WAVES;
+  static constexpr int BM = 32 * WAVES;
   static constexpr int ROW = 2 * DP, CPR = DP / 8;  // bytes and 16-byte chunks of an LDS row
   static constexpr int RPI = 64 / CPR;              // rows of a direct load
   static constexpr int RW = BN / WAVES;             // rows of a block that one wave loads
   static constexpr int NI = RW / RPI;               // its direct loads of K, or of V
-  static constexpr int HALF = BN * ROW, STAGE = 2 * HALF;
-  // stages; per wave the places of its rows and four blocks' pages
-  static constexpr int OWN = RW * (int)sizeof(AttnPlace) + 4 * 256;
-  static constexpr int LDS = S * STAGE + WAVES * OWN;
+  static constexpr int BLOCK = BN * ROW;            // two of K, then two of V
+  // per wave the places of its rows' keys, and values (of two blocks), and four blocks' pages
+  static constexpr int OWN = 3 * RW * 8 + 4 * 256;
+  static constexpr int LDS = 4 * BLOCK + WAVES * OWN;
   static_assert(LDS <= 160 * 1024, "LDS of one CU");
-  static_assert(S <= 3, "four blocks' pages");
 };
 
 // V's chunks are placed for the transposing reads, which take 64 bytes of 8 rows at once: 4 rows in a row
@@ -58,9 +59,9 @@ __device__ __forceinline__ TileOf tile_at(const AttnArgs& a, int slot) {
   return {lo, slot - first(lo)};
 }
 
-template <int DP, bool EXACT, int NQ, int WAVES, int S, class T>
-__global__ __launch_bounds__(64 * WAVES) void attn_tile_kernel(const AttnArgs a, const int slots) {
-  using L = Tile<DP, NQ, WAVES, S>;
+template <int DP, bool EXACT, int WAVES, class T>
+__global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kernel(const AttnArgs a, const int slots) {
+  using L = Tile<DP, WAVES>;
   constexpr int BM = L::BM, KS = DP / 16, ND = DP / 32;
   extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
@@ -79,47 +80,33 @@ __global__ __launch_bounds__(64 * WAVES) void attn_tile_kernel(const AttnArgs a,
   const int32_t* table = a.table + (int64_t)at.seq * a.table_stride;
   const uint8_t* kh = a.k + 2 * (head * a.k_head);
   const uint8_t* vh = a.v + 2 * (head * a.v_head);
-  const int my0 = row0 + wave * 32 * NQ;  // this wave's first row
 
-  AttnRow row[NQ];
-  typename T::x8 qf[NQ][KS];
-  int low_hi = 0x7FFFFFFF, top_hi = 0, top_lo = 0, low_lo = 0x7FFFFFFF;
-#pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const int rr = my0 + n * 32 + l32;
-    const bool valid = rr < rows;
-    const int i = valid ? attn_query(a, rr) : 0, g = valid ? rr - i * a.group : 0;
-    row[n] = attn_row(a, sq, i, valid);
-    if (valid) {
-      low_hi = min(low_hi, row[n].hi);
-      top_hi = max(top_hi, row[n].hi);
-      top_lo = max(top_lo, row[n].lo);
-      low_lo = min(low_lo, row[n].lo);
-    }
-    const uint8_t* src = a.q + 2 * ((int64_t)(sq.token0 + i) * a.q_ts + (int64_t)(head * a.group + g) * a.q_hs);
+  const int rr = row0 + wave * 32 + l32;  // this lane's row
+  const bool valid = rr < rows;
+  const int qi = valid ? attn_query(a, rr) : 0, qg = valid ? rr - qi * a.group : 0;
+  const AttnRow row = attn_row(a, sq, qi, valid);
+  typename T::x8 qf[KS];
+  {
+    const uint8_t* src = a.q + 2 * ((int64_t)(sq.token0 + qi) * a.q_ts + (int64_t)(head * a.group + qg) * a.q_hs);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const int d = 16 * k + 8 * h;
       u32x4_t x = {0, 0, 0, 0};
       if (valid && d < a.D) x = *reinterpret_cast<const u32x4_t*>(src + 2 * d);
-      qf[n][k] = __builtin_bit_cast(typename T::x8, x);
+      qf[k] = __builtin_bit_cast(typename T::x8, x);
     }
   }
+  int low_hi = valid ? row.hi : 0x7FFFFFFF, top_lo = row.lo;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     low_hi = min(low_hi, __shfl_xor(low_hi, d));
-    top_hi = max(top_hi, __shfl_xor(top_hi, d));
     top_lo = max(top_lo, __shfl_xor(top_lo, d));
-    low_lo = min(low_lo, __shfl_xor(low_lo, d));
   }
   low_hi = uniform(low_hi);
-  top_hi = a.mask != nullptr ? sp.hi : uniform(top_hi);
   top_lo = uniform(top_lo);
-  low_lo = uniform(low_lo);
-  if (my0 >= rows) top_hi = 0;
 
-  uint8_t* const places = lds + S * L::STAGE + wave * L::OWN;
-  uint8_t* const pages = places + L::RW * sizeof(AttnPlace);
+  uint8_t* const places = lds + 4 * L::BLOCK + wave * L::OWN;
+  uint8_t* const pages = places + 3 * L::RW * 8;
   auto key0 = [&](int b) { return (b < sp.sink_blocks ? b : b + sp.skip) * BN; };
   auto seen_by_any = [&](int key) { return key < sp.hi && (key >= sp.lo || key < sp.sinks); };
   // starts the load of the pages of block b's 64 keys (of zeros where there is no such key)
@@ -128,187 +115,227 @@ __global__ __launch_bounds__(64 * WAVES) void attn_tile_kernel(const AttnArgs a,
     const void* src = b < b1 && seen_by_any(key) ? (const void*)(table + attn_page(a, key)) : attn_zeros;
     __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)(pages + (b & 3) * 256), 4, 0, 0);
   };
-  // starts this wave's share of block b's loads (of zeros past the run); returns which of the block's keys are there
-  auto load_block = [&](int b, int stage) {
+  // starts this wave's share of the loads of block b's keys (of zeros past the run), and keeps the places of its values;
+  // returns which of the block's keys are there
+  auto load_k = [&](int b, int odd) {
     const int key = key0(b) + lane;
     const uint32_t page = *reinterpret_cast<const uint32_t*>(pages + (b & 3) * 256 + 4 * lane);
     const bool ok = b < b1 && seen_by_any(key) && page < a.pages;
     const AttnPlace p = attn_place(a, kh, vh, key, page, ok);
-    if (lane / L::RW == wave) *reinterpret_cast<AttnPlace*>(places + (lane % L::RW) * sizeof(AttnPlace)) = p;
+    if (lane / L::RW == wave) {
+      *reinterpret_cast<const uint8_t**>(places + (lane % L::RW) * 8) = p.k;
+      *reinterpret_cast<const uint8_t**>(places + ((1 + odd) * L::RW + lane % L::RW) * 8) = p.v;
+    }
     wave_lds_sync();
-    uint8_t* to = lds + stage * L::STAGE + wave * L::RW * L::ROW;
+    uint8_t* to = lds + odd * L::BLOCK + wave * L::RW * L::ROW;
+    const uint8_t* from[L::NI];  // (all read before the first load: the compiler keeps their order)
+#pragma unroll
+    for (int n = 0; n < L::NI; ++n) from[n] = *reinterpret_cast<const uint8_t**>(places + (n * L::RPI + lane / L::CPR) * 8);
 #pragma unroll
     for (int n = 0; n < L::NI; ++n) {
-      const int r = n * L::RPI + lane / L::CPR, lr = wave * L::RW + r;
-      const AttnPlace pl = *reinterpret_cast<const AttnPlace*>(places + r * sizeof(AttnPlace));
-      attn_load16(attn_chunk<EXACT>(pl.k, (lane % L::CPR) ^ attn_swizzle<DP>(lr), a.D), to + n * 1024);
-      attn_load16(attn_chunk<EXACT>(pl.v, (lane % L::CPR) ^ swizzle_v<DP>(lr), a.D), to + L::HALF + n * 1024);
+      const int r = n * L::RPI + lane / L::CPR;
+      attn_load16(attn_chunk<EXACT>(from[n], (lane % L::CPR) ^ attn_swizzle<DP>(wave * L::RW + r), a.D), to + n * 1024);
     }
     return (uint64_t)__ballot(ok);
   };
-
-  float m[NQ], l[NQ];
-  float16_t o[NQ][ND];
+  auto load_v = [&](int odd) {
+    uint8_t* to = lds + (2 + odd) * L::BLOCK + wave * L::RW * L::ROW;
+    const uint8_t* from[L::NI];
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    m[n] = ATTN_NONE;
-    l[n] = 0.0f;
+    for (int n = 0; n < L::NI; ++n)
+      from[n] = *reinterpret_cast<const uint8_t**>(places + ((1 + odd) * L::RW + n * L::RPI + lane / L::CPR) * 8);
 #pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) o[n][d][i] = 0.0f;
-  }
-
-  // In the order of their issue: pages b + S - 1, block b + S - 2, pages b + S, block b + S - 1.  A pass waits for all but
-  // the blocks after b, so for the pages of block b + S - 1 too.
-  for (int j = 0; j < S; ++j) load_pages(b0 + j);
-  attn_vm_drain();
-  uint64_t there[S];
-#pragma unroll
-  for (int j = 0; j < S - 1; ++j) there[j] = load_block(b0 + j, j);
-  int stage = 0;
-#pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    // block b has landed, here and in the other waves, and block b - 1's stage is read
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"((S - 2) * 2 * L::NI) : "memory");
-    load_pages(b + S);
-    there[S - 1] = load_block(b + S - 1, stage == 0 ? S - 1 : stage - 1);
-    const uint64_t here = there[0];
-#pragma unroll
-    for (int j = 0; j < S - 1; ++j) there[j] = there[j + 1];
-    const uint8_t* ks = lds + stage * L::STAGE;
-    const uint8_t* vs = ks + L::HALF;
-    stage = stage == S - 1 ? 0 : stage + 1;
-    const int j0 = key0(b);
-    if (j0 >= top_hi || (j0 + BN <= low_lo && j0 >= a.sinks)) continue;  // no row of this wave sees the block
-
-    float16_t s[NQ][2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int n = 0; n < NQ; ++n)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[n][t][i] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        const int lr = 32 * t + l32;
-        const auto kf = __builtin_bit_cast(typename T::x8, *reinterpret_cast<const u32x4_t*>(
-            ks + lr * L::ROW + 16 * ((2 * k + h) ^ attn_swizzle<DP>(lr))));
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) s[n][t] = T::mma32(kf, qf[n][k], s[n][t]);
-      }
+    for (int n = 0; n < L::NI; ++n) {
+      const int r = n * L::RPI + lane / L::CPR;
+      attn_load16(attn_chunk<EXACT>(from[n], (lane % L::CPR) ^ swizzle_v<DP>(wave * L::RW + r), a.D), to + n * 1024);
     }
+  };
+  // Operands in LDS, 16 bytes a lane.  Of K: keys 32 t + l32, elements 16 k + 8 h ..; of V: this lane's column of 32 d ..,
+  // keys 16 u + 4 h .. + 3 and 8 further.  What the swizzles move depends on the lane and on the low bits of k and d
+  // only, the rest is a constant of the instruction.
+  constexpr int KO = KS < 8 ? KS : 8, VO = ND < 4 ? ND : 4;
+  const uint8_t *kat[KO], *vat[VO];
+#pragma unroll
+  for (int k = 0; k < KO; ++k) kat[k] = lds + l32 * L::ROW + 16 * ((2 * k + h) ^ attn_swizzle<DP>(l32));
+  {
+    const int c16 = lane & 15, r = 4 * h + (c16 >> 2), c = 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1);
+#pragma unroll
+    for (int d = 0; d < VO; ++d)
+      vat[d] = lds + 2 * L::BLOCK + r * L::ROW + 16 * ((4 * d + c) ^ swizzle_v<DP>(r)) + 8 * (c16 & 1);
+  }
+  auto fetch_k = [&](int odd, int t, int k) {
+    return __builtin_bit_cast(typename T::x8, *reinterpret_cast<const u32x4_t*>(
+        kat[k % KO] + odd * L::BLOCK + 32 * t * L::ROW + k / KO * 256));
+  };
+  auto fetch_v = [&](int odd, int u, int d) {
+    const uint8_t* p = vat[d % VO] + odd * L::BLOCK + 16 * u * L::ROW + d / VO * 256;
+    return attn_read_vt<T>(p, p + 8 * L::ROW);
+  };
 
+  float m = ATTN_NONE, l = 0.0f;
+  float16_t o[ND];
+#pragma unroll
+  for (int d = 0; d < ND; ++d)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
+
+  // Pass b: softmax of block b's scores and the product with its values, and, among their instructions, the
+  // scores of block b + 1; meanwhile the keys of block b + 2 and the values of block b + 1 are loaded.
+  uint64_t here, there;
+  load_pages(b0);
+  load_pages(b0 + 1);
+  load_pages(b0 + 2);
+  attn_vm_drain();
+  here = load_k(b0, 0);
+  load_v(0);
+  there = load_k(b0 + 1, 1);
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  float16_t sa[2], sb[2], zero;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int k = 0; k < KS; ++k) sa[t] = T::mma32(fetch_k(0, t, k), qf[k], k == 0 ? zero : sa[t]);
+  auto larger = [](float top, const float16_t& s, int i) { return fmaxf(fmaxf(top, s[2 * i]), s[2 * i + 1]); };
+  float top = fmaxf(sa[0][0], sa[0][1]);
+#pragma unroll
+  for (int i = 1; i < 16; ++i) top = larger(top, sa[i >> 3], i & 7);
+
+  auto pass = [&](auto parity, int b, float16_t (&s)[2], float16_t (&next)[2]) {
+    constexpr int ODD = decltype(parity)::value;
+    // keys b + 1 and values b have landed, here and in the other waves; keys b and values b - 1 are read
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    load_pages(b + 3);
+    const uint64_t later = load_k(b + 2, ODD);
+    load_v(1 - ODD);
+    const int j0 = key0(b);
     if (here != ~0ull || j0 + BN > low_hi || (j0 < top_lo && j0 + BN > a.sinks)) {
       // element (t, i) is key j0 + 4 h + 32 t + 8 (i / 4) + i % 4
 #pragma unroll
-      for (int n = 0; n < NQ; ++n)
+      for (int t = 0; t < 2; ++t) {
+        const uint32_t mine = (uint32_t)(here >> (32 * t)) >> (4 * h);
+        uint32_t bits = 0;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t mine = (uint32_t)(here >> (32 * t)) >> (4 * h);
-          uint32_t bits = 0;
+        for (int i = 0; i < 16; ++i) {
+          const int in = 8 * (i >> 2) + (i & 3), j = j0 + 32 * t + 4 * h + in;
+          bits |= (j < row.hi && (j >= row.lo || j < a.sinks) ? 1u : 0u) << in;
+        }
+        if (a.mask != nullptr && j0 + 32 * t + 32 > sq.ctx && a.mask_width > 0) {
+          const uint8_t* of = a.mask + (int64_t)(sq.token0 + qi) * a.mask_stride;
+          const int node = j0 + 32 * t + 4 * h - sq.ctx;
+          uint32_t set[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) set[i] = of[min(max(node + 8 * (i >> 2) + (i & 3), 0), a.mask_width - 1)];
+          attn_vm_drain();
+          uint32_t tree = 0, nodes = 0;
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            const int in = 8 * (i >> 2) + (i & 3), j = j0 + 32 * t + 4 * h + in;
-            bits |= (j < row[n].hi && (j >= row[n].lo || j < a.sinks) ? 1u : 0u) << in;
+            const int in = 8 * (i >> 2) + (i & 3);
+            tree |= (set[i] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
+            nodes |= (node + in >= 0 ? 1u : 0u) << in;
           }
-          if (a.mask != nullptr && j0 + 32 * t + 32 > sq.ctx && a.mask_width > 0) {
-            const int rr = my0 + n * 32 + l32;
-            const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
-            const int node = j0 + 32 * t + 4 * h - sq.ctx;
-            uint32_t set[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) set[i] = of[min(max(node + 8 * (i >> 2) + (i & 3), 0), a.mask_width - 1)];
-            attn_vm_drain();
-            uint32_t tree = 0, nodes = 0;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const int in = 8 * (i >> 2) + (i & 3);
-              tree |= (set[i] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
-              nodes |= (node + in >= 0 ? 1u : 0u) << in;
-            }
-            bits = (bits & ~nodes) | (tree & nodes);
-          }
-          bits &= mine;
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (!((bits >> (8 * (i >> 2) + (i & 3))) & 1)) s[n][t][i] = ATTN_NONE;
+          bits = (bits & ~nodes) | (tree & nodes);
         }
-    }
-
-    typename T::x8 p[NQ][4];
+        bits &= mine;
 #pragma unroll
-    for (int n = 0; n < NQ; ++n) {
-      float top = fmaxf(s[n][0][0], s[n][1][0]);
-#pragma unroll
-      for (int i = 1; i < 16; ++i) top = fmaxf(fmaxf(top, s[n][0][i]), s[n][1][i]);
-      top = attn_max32(top) * a.scale_log2;
-      if (__any(top > m[n] + ATTN_SLACK)) {
-        const float to = fmaxf(m[n], top), f = attn_exp2(m[n] - (to == ATTN_NONE ? 0.0f : to));
-        l[n] *= f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) o[n][d] *= f;
-        m[n] = to;
+        for (int i = 0; i < 16; ++i)
+          if (!((bits >> (8 * (i >> 2) + (i & 3))) & 1)) s[t][i] = ATTN_NONE;
       }
-      const float ref = m[n] == ATTN_NONE ? 0.0f : m[n];
-      float sum = 0.0f;
+      top = fmaxf(s[0][0], s[0][1]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int i = 1; i < 16; ++i) top = larger(top, s[i >> 3], i & 7);
+    }
+    top = attn_max32(top) * a.scale_log2;
+    if (__any(top > m + ATTN_SLACK)) {
+      const float to = fmaxf(m, top), f = attn_exp2(m - (to == ATTN_NONE ? 0.0f : to));
+      l *= f;
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          float e[8];
+      for (int d = 0; d < ND; ++d) o[d] *= f;
+      m = to;
+    }
+    const float ref = m == ATTN_NONE ? 0.0f : m, sc = a.scale_log2;
+
+    // Step i: matrix instruction i (2 KS of the next block's scores, then 4 ND products, 16 keys after 16 keys), the
+    // LDS reads of the one PRE further, and its share of the vector work: the 16 pairs of exponentials end
+    // before the products that need them (a pair's rounding a step after its exponentials), and the next
+    // block's maximum follows its scores.  The barriers keep the compiler from gathering each kind again.
+    constexpr int N1 = 2 * KS, N = N1 + 4 * ND, PRE = 3, LAST = N1 + 3 * ND - 1;
+    typename T::x8 f[PRE + 1];
+    float e[16][2];
+    u32x4_t p[4];
+    auto fetch = [&](int i) {
+      f[i % (PRE + 1)] = i < N1 ? fetch_k(1 - ODD, i / KS, i % KS) : fetch_v(ODD, (i - N1) / ND, (i - N1) % ND);
+    };
+    float over = ATTN_NONE;
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) e[i] = attn_exp2(fmaf(s[n][t][8 * u + i], a.scale_log2, -ref));
-          sum += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-          p[n][2 * t + u] = __builtin_bit_cast(typename T::x8, u32x4_t{T::pack2(e[0], e[1]), T::pack2(e[2], e[3]),
-                                                                      T::pack2(e[4], e[5]), T::pack2(e[6], e[7])});
+    for (int i = 0; i < PRE; ++i) fetch(i);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i + PRE < N) fetch(i + PRE);
+      const auto& op = f[i % (PRE + 1)];
+      if (i < N1) {
+        next[i / KS] = T::mma32(op, qf[i % KS], i % KS == 0 ? zero : next[i / KS]);
+      } else {
+        o[(i - N1) % ND] = T::mma32(op, __builtin_bit_cast(typename T::x8, p[(i - N1) / ND]), o[(i - N1) % ND]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {  // pair j: exponentials in step j LAST / 16, rounding in the next one
+        const int j1 = (16 * (i - 1) + LAST - 1) / LAST + x, j = (16 * i + LAST - 1) / LAST + x;
+        if (i > 0 && j1 < 16 && j1 * LAST / 16 == i - 1) {
+          p[j1 / 4][j1 % 4] = T::pack2(e[j1][0], e[j1][1]);
+          l = T::sum2(p[j1 / 4][j1 % 4], l);
         }
-      l[n] += sum;
-    }
-
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-      for (int d = 0; d < ND; ++d) {
-        const int c16 = lane & 15;
-        const int r0 = 16 * u + 4 * h + (c16 >> 2), r1 = r0 + 8;
-        const int ch = 4 * d + 2 * ((lane >> 4) & 1) + ((c16 & 3) >> 1), half = 8 * (c16 & 1);
-        const auto vf = attn_read_vt<T>(vs + r0 * L::ROW + 16 * (ch ^ swizzle_v<DP>(r0)) + half,
-                                        vs + r1 * L::ROW + 16 * (ch ^ swizzle_v<DP>(r1)) + half);
-#pragma unroll
-        for (int n = 0; n < NQ; ++n) o[n][d] = T::mma32(vf, p[n][u], o[n][d]);
+        if (j < 16 && j * LAST / 16 == i) {
+          e[j][0] = attn_exp2(fmaf(s[j >> 3][2 * (j & 7)], sc, -ref));
+          e[j][1] = attn_exp2(fmaf(s[j >> 3][2 * (j & 7) + 1], sc, -ref));
+        }
       }
+      // (a score's last matrix instruction is two steps ahead)
+      if (i >= KS + 2 && i < KS + 10) over = larger(over, next[0], i - KS - 2);
+      if (i >= N1 + 2 && i < N1 + 6) {
+        over = larger(over, next[1], 2 * (i - N1 - 2));
+        over = larger(over, next[1], 2 * (i - N1 - 2) + 1);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    asm volatile("" : "+v"(over), "+v"(l));  // (not moved out of the steps and behind them)
+    top = over;
+    here = there;
+    there = later;
+  };
+#pragma unroll 1
+  for (int b = b0; b < b1; b += 2) {
+    pass(std::integral_constant<int, 0>{}, b, sa, sb);
+    if (b + 1 < b1) pass(std::integral_constant<int, 1>{}, b + 1, sb, sa);
   }
-  attn_vm_drain();  // (nothing arrives in the LDS of an ended wave)
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (nothing arrives in the LDS of an ended wave)
 
+  const float sum = attn_sum32(l);
+  if (!valid) return;
+  if (a.pieces == 1) {
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + qi) * a.o_ts + (int64_t)(head * a.group + qg) * a.o_hs);
 #pragma unroll
-  for (int n = 0; n < NQ; ++n) {
-    const float sum = attn_sum32(l[n]);
-    const int rr = my0 + n * 32 + l32;
-    if (rr >= rows) continue;
-    if (a.pieces == 1) {
-      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int i = attn_query(a, rr), g = rr - i * a.group;
-      uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs);
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
+      for (int q = 0; q < 4; ++q) {
+        const int e = 32 * d + 8 * q + 4 * h;
+        if (e < a.D)
+          *reinterpret_cast<u32x2_t*>(dst + 2 * e) = u32x2_t{T::pack2(o[d][4 * q] * f, o[d][4 * q + 1] * f),
+                                                            T::pack2(o[d][4 * q + 2] * f, o[d][4 * q + 3] * f)};
+      }
+  } else {
+    const int64_t to = (((int64_t)slot * a.kv_heads + head) * a.pieces + piece) * BM + (rr - row0);
+    if (h == 0) *reinterpret_cast<float2_t*>(a.stats + 2 * to) = float2_t{m, sum};
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int e = 32 * d + 8 * q + 4 * h;
-          if (e < a.D)
-            *reinterpret_cast<u32x2_t*>(dst + 2 * e) = u32x2_t{T::pack2(o[n][d][4 * q] * f, o[n][d][4 * q + 1] * f),
-                                                              T::pack2(o[n][d][4 * q + 2] * f, o[n][d][4 * q + 3] * f)};
-        }
-    } else {
-      const int64_t to = (((int64_t)slot * a.kv_heads + head) * a.pieces + piece) * BM + (rr - row0);
-      if (h == 0) *reinterpret_cast<float2_t*>(a.stats + 2 * to) = float2_t{m[n], sum};
+    for (int d = 0; d < ND; ++d)
 #pragma unroll
-      for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<float4_t*>(a.part + to * DP + 32 * d + 8 * q + 4 * h) =
-              float4_t{o[n][d][4 * q], o[n][d][4 * q + 1], o[n][d][4 * q + 2], o[n][d][4 * q + 3]};
-    }
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<float4_t*>(a.part + to * DP + 32 * d + 8 * q + 4 * h) =
+            float4_t{o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
   }
 }
 
@@ -346,10 +373,6 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(const AttnArgs a, c
   }
 }
 
-#ifndef VQ
-#define VQ 1
-#define VS 2
-#endif
 // The tiles of a call: rows of one, how many slots they take (see tile_at; without `starts`, sequence by sequence,
 // they take no more), and into how many pieces each tile's keys are cut.
 struct TilePlan {
@@ -359,7 +382,7 @@ struct TilePlan {
 };
 TilePlan plan(const AttnArgs& a) {
   TilePlan p;
-  p.rows = a.D <= 64 ? 128 : a.D <= 128 ? 128 * VQ : 128;
+  p.rows = 128;
   const int64_t rows = (int64_t)a.tokens * a.group;
   p.slots = rows / p.rows + a.batch;
   const int64_t tiles = std::max<int64_t>(1, rows / p.rows) * a.kv_heads;
@@ -367,9 +390,9 @@ TilePlan plan(const AttnArgs& a) {
   return p;
 }
 
-template <int DP, int NQ, int WAVES, int S, class T>
+template <int DP, int WAVES, class T>
 hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
-  using L = Tile<DP, NQ, WAVES, S>;
+  using L = Tile<DP, WAVES>;
   const TilePlan p = plan(a);
   if (p.rows != L::BM) return hipErrorInvalidValue;
   const int64_t wgs = p.slots * a.kv_heads * p.pieces;
@@ -377,8 +400,8 @@ hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
   a.pieces = p.pieces;
   a.stats = static_cast<float*>(workspace);
   a.part = a.stats + (size_t)wgs * L::BM * 2;
-  if (a.D == DP) attn_tile_kernel<DP, true, NQ, WAVES, S, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
-  else attn_tile_kernel<DP, false, NQ, WAVES, S, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
+  if (a.D == DP) attn_tile_kernel<DP, true, WAVES, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
+  else attn_tile_kernel<DP, false, WAVES, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.pieces == 1) return e;
   attn_tile_join_kernel<DP, L::BM, T><<<dim3((unsigned)(p.slots * a.kv_heads), 8), 256, 0, st>>>(a, (int)p.slots);
@@ -387,9 +410,9 @@ hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
 
 template <class T>
 hipError_t run_dim(const AttnArgs& a, void* workspace, hipStream_t st) {
-  if (a.D <= 64) return run<64, 1, 4, 2, T>(a, workspace, st);
-  if (a.D <= 128) return run<128, VQ, 4, VS, T>(a, workspace, st);
-  return run<256, 1, 4, 2, T>(a, workspace, st);
+  if (a.D <= 64) return run<64, 4, T>(a, workspace, st);
+  if (a.D <= 128) return run<128, 4, T>(a, workspace, st);
+  return run<256, 4, T>(a, workspace, st);
 }
 
 }  // namespace

@@ -147,7 +147,8 @@ struct AttnArgs {
   uint8_t* out;
   const uint8_t *k, *v;
   int64_t q_ts, q_hs, o_ts, o_hs;
-  int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+  int64_t k_head, v_head;
+  uint32_t k_page, k_token, v_page, v_token;
   const int32_t *table, *lens, *starts, *pos;  // starts NULL: `each` queries per sequence
   const uint8_t* mask;                         // NULL: causal
   int64_t table_stride, mask_stride;
