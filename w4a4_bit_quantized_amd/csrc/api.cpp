@@ -784,6 +784,7 @@ w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, con
   a.max_len = (int)std::min<int64_t>(p.table_width * c.page_size, kMaxDim - 64);  // (block ends stay in 32 bits)
   a.pages = (uint32_t)c.pages;
   a.page_size = (int)c.page_size;
+  a.page_rows = c.page_size % 16 == 0 && c.k_token_stride <= 1 << 26 && c.v_token_stride <= 1 << 26;
   divisor(c.page_size, a.page_mul, a.page_shift);
   divisor(a.group, a.group_mul, a.group_shift);
   a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);

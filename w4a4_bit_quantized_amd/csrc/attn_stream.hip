@@ -16,6 +16,16 @@ namespace w4a4 {
 namespace {
 
 constexpr int KB = 32;  // keys of a block
+// What a triple costs before its first block (its queries, pages and first keys follow one another), in blocks: runs
+// are equal in blocks and starts.
+// (64 sequences of 37 to 8191 keys: 190 us with 0, 183, 184, 180 and 184 with 1 to 4)
+constexpr int START = 3;
+
+// 16 bytes per lane from `src` to LDS at dst + 16 lane, not kept in the caches: nobody reads them again (64 sequences of
+// 4096 keys, 8 heads of 128: 172 us, 191 with ordinary loads).
+__device__ __forceinline__ void load16(const uint8_t* src, uint8_t* dst) {
+  __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)dst, 16, 0, 2);
+}
 
 template <int DP>
 struct Stream {
@@ -46,7 +56,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
   };
   auto units_of = [&](const AttnSeq& q) {
     const int tiles = tiles_of(q);
-    return tiles ? (int64_t)tiles * a.kv_heads * attn_span<KB>(a, q, 0, q.len).blocks : (int64_t)0;
+    return tiles ? (int64_t)tiles * a.kv_heads * (attn_span<KB>(a, q, 0, q.len).blocks + START) : (int64_t)0;
   };
   const int strip = (a.batch + 63) / 64;
   AttnSeq own = {0, 0, 0, 0};
@@ -71,7 +81,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
   const int64_t total = lane_of(upto, 63);
   const int64_t run = max((total + gridDim.x - 1) >> a.log2_waves, (int64_t)a.least);
   const int64_t u0 = w * run, u1 = min(u0 + run, total);
-  if (lane == 0) a.desc[4 * w] = 0;
+  if (lane == 0) a.desc[8 * w] = 0;
   if (u0 >= u1) return;
   const int at = uniform(__ffsll(__ballot(upto > u0)) - 1);
   int64_t u = u0, before = lane_of(upto - mine, at);
@@ -82,20 +92,23 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
     const int tiles = tiles_of(sq);
     if (tiles == 0) continue;
     const AttnSpan sp = attn_span<KB>(a, sq, 0, sq.len);
-    const int64_t units = (int64_t)tiles * a.kv_heads * sp.blocks;
+    const int each = sp.blocks + START;  // units of a triple
+    const int64_t units = (int64_t)tiles * a.kv_heads * each;
     if (before + units <= u) {
       before += units;
       continue;
     }
     const int32_t* table = a.table + (int64_t)seq * a.table_stride;
     const int rows = sq.nq * a.group;
-    int64_t pair = uniform(attn_div(u - before, sp.blocks));  // head * tiles + tile
-    int b0 = (int)(u - before - pair * sp.blocks);
-    int head = uniform((int)attn_div(pair, tiles)), tile = (int)(pair - (int64_t)head * tiles);
+    const int pair = uniform(attn_div(u - before, each));            // head * tiles + tile
+    int u_in = (int)(u - before - (int64_t)pair * each);  // this run's first unit of the triple
+    int head = tiles == 1 ? pair : uniform(attn_div(pair, tiles)), tile = pair - head * tiles;
 #pragma unroll 1
     while (u < u1 && head < a.kv_heads) {
-      const int b1 = (int)min((int64_t)sp.blocks, b0 + (u1 - u));
-      u += b1 - b0;
+      const int u_end = (int)min((int64_t)each, u_in + (u1 - u));
+      const int b0 = max(u_in - START, 0), b1 = max(u_end - START, 0);
+      const bool first = u_in == 0, whole = first && u_end == each;
+      u += u_end - u_in;
       const uint8_t* kh = a.k + 2 * (head * a.k_head);
       const uint8_t* vh = a.v + 2 * (head * a.v_head);
 
@@ -203,7 +216,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < S::NI; ++n) {
           const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
-          attn_load16(attn_chunk<EXACT>(from[n], c, a.D), stage + n * 1024);
+          load16(attn_chunk<EXACT>(from[n], c, a.D), stage + n * 1024);
         }
         if (work) {
         if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
@@ -281,15 +294,17 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
         for (int n = 0; n < S::NI; ++n) {
           const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
-          attn_load16(attn_chunk<EXACT>(from[n], c, a.D), stage + S::HALF + n * 1024);
+          load16(attn_chunk<EXACT>(from[n], c, a.D), stage + S::HALF + n * 1024);
         }
       }
 
       // finished, or a piece: the first of a triple in slot 1 of the wave, any other in slot 0
-      const bool whole = b0 == 0 && b1 == sp.blocks;
-      if (b0 == 0 && !whole && lane == 0)
-        *reinterpret_cast<int4*>(a.desc + 4 * w) = int4{1 + (int)attn_div(sp.blocks - b1 + run - 1, run), seq, head, tile};
-      const int64_t slot = 2 * (int64_t)w + (b0 == 0 ? 1 : 0);
+      if (first && !whole && lane == 0) {  // pieces, sequence's first row of q, rows of the tile and the first of them, head
+        const int pieces = 1 + (run >= each ? 1 : attn_div(each - u_end + run - 1, (int)run));
+        *reinterpret_cast<int4*>(a.desc + 8 * w) = int4{pieces, sq.token0, min(BM, rows - tile * BM), tile * BM};
+        a.desc[8 * w + 4] = head;
+      }
+      const int64_t slot = 2 * (int64_t)w + (first ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
         const float sum = attn_sum16(attn_sum32(l[n]));
@@ -313,7 +328,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
           for (int d = 0; d < ND; ++d) *reinterpret_cast<float4_t*>(a.part + at * DP + 16 * d + 4 * qd) = o[n][d];
         }
       }
-      b0 = 0;
+      u_in = 0;
       if (++tile == tiles) {
         tile = 0;
         ++head;
@@ -324,24 +339,20 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
   attn_vm_drain();  // (nothing arrives in the LDS of an ended wave)
 }
 
-// Joins the pieces of the triple that starts in run blockIdx.x and is cut, one row at a time: lines of DP / 4 threads
-// take the pieces in turn, four at a time, and their sums meet in LDS.
+// Joins the pieces of the triple that starts in run blockIdx.x and is cut, every gridDim.y-th row of it: lines of DP / 4
+// threads take the row's pieces in turn, four at a time, and their sums meet in LDS.
 template <int DP, int BM, class T>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-  constexpr int PER = DP / 4;
-  const int w = blockIdx.x, t = threadIdx.x;
-  const int4 d = *reinterpret_cast<const int4*>(a.desc + 4 * w);
-  if (d.x == 0) return;
-  const AttnSeq sq = attn_seq(a, d.y);
-  const int rows = min(BM, sq.nq * a.group - d.w * BM);
-  // piece p of row r
-  auto at = [&](int p, int r) { return (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * BM + r; };
+  constexpr int PER = DP / 4, LINES = 256 / PER;
   __shared__ float4_t sums[256];
-  __shared__ float tops[256 / PER + 1], ls[256 / PER + 1];
-  constexpr int LINES = 256 / PER;  // lines of threads that each cover a row's columns
-  const int line = t / PER, e = 4 * (t % PER);
-  for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-    // every line takes each LINES-th piece, with a maximum of its own
+  __shared__ float2_t tops[LINES];
+  const int w = blockIdx.x, t = threadIdx.x, line = t / PER, e = 4 * (t % PER);
+  const int4 d = *reinterpret_cast<const int4*>(a.desc + 8 * w);
+  const int head = a.desc[8 * w + 4];
+  if (d.x == 0) return;
+  for (int r = blockIdx.y; r < d.z; r += gridDim.y) {
+    // piece p of row r
+    auto at = [&](int p) { return (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * BM + r; };
     float top = ATTN_NONE, sum = 0.0f;
     float4_t o = {0, 0, 0, 0};
     for (int p0 = line; p0 < d.x; p0 += 4 * LINES) {
@@ -349,7 +360,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
       float4_t v[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int64_t x = at(min(p0 + i * LINES, d.x - 1), r);
+        const int64_t x = at(min(p0 + i * LINES, d.x - 1));
         st[i] = *reinterpret_cast<const float2_t*>(a.stats + 2 * x);
         v[i] = *reinterpret_cast<const float4_t*>(a.part + x * DP + e);
         if (p0 + i * LINES >= d.x) st[i] = float2_t{ATTN_NONE, 0.0f};
@@ -360,7 +371,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
       o *= keep;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (p0 + i * LINES >= d.x) continue;  // (not even times 0: it may hold anything)
+        if (p0 + i * LINES >= d.x) continue;  // (not even times 0: a NaN would count twice)
         const float f = attn_exp2(st[i][0] - ref);
         sum = fmaf(st[i][1], f, sum);
 #pragma unroll
@@ -370,29 +381,26 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
     }
     __syncthreads();
     sums[t] = o;
-    if (e == 0) {
-      tops[line] = top;
-      ls[line] = sum;
-    }
+    if (e == 0) tops[line] = float2_t{top, sum};
     __syncthreads();
     if (line == 0 && e < a.D) {
-      float all = ATTN_NONE;
+      top = ATTN_NONE;
 #pragma unroll
-      for (int i = 0; i < LINES; ++i) all = fmaxf(all, tops[i]);
-      const float ref = all == ATTN_NONE ? 0.0f : all;
+      for (int i = 0; i < LINES; ++i) top = fmaxf(top, tops[i][0]);
+      const float ref = top == ATTN_NONE ? 0.0f : top;
       sum = 0.0f;
       o = float4_t{0, 0, 0, 0};
 #pragma unroll
       for (int i = 0; i < LINES; ++i) {
-        const float f = attn_exp2(tops[i] - ref);
-        sum = fmaf(ls[i], f, sum);
+        const float f = attn_exp2(tops[i][0] - ref);
+        sum = fmaf(tops[i][1], f, sum);
         const float4_t v = sums[i * PER + t];
 #pragma unroll
         for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], f, o[c]);
       }
       const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int rr = d.w * BM + r, i = attn_query(a, rr), g = rr - i * a.group;
-      uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(d.z * a.group + g) * a.o_hs + e);
+      const int rr = d.w + r, i = attn_query(a, rr), g = rr - i * a.group;
+      uint8_t* dst = a.out + 2 * ((int64_t)(d.y + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs + e);
       *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{T::pack2(o[0] * f, o[1] * f), T::pack2(o[2] * f, o[3] * f)};
     }
   }
@@ -405,10 +413,10 @@ template <int DP, int NQ, class T>
 hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
   constexpr int W = 1 << log2_waves(DP), BM = 16 * NQ;
   a.desc = static_cast<int32_t*>(workspace);
-  a.stats = reinterpret_cast<float*>(a.desc + 4 * W);
+  a.stats = reinterpret_cast<float*>(a.desc + 8 * W);
   a.part = a.stats + (size_t)2 * W * BM * 2;
   a.log2_waves = log2_waves(DP);
-  a.least = 4;
+  a.least = 4;  // (one sequence of 4096 keys, 8 heads: 16.0 us with 4, 2 and 3: 16.4 and 17.6, 6: 19)
   if (a.D == DP) attn_stream_kernel<DP, true, NQ, T><<<W, 64, 0, st>>>(a);
   else attn_stream_kernel<DP, false, NQ, T><<<W, 64, 0, st>>>(a);
   hipError_t e = hipGetLastError();
@@ -438,7 +446,7 @@ constexpr int STREAM_ROWS = 32;
 size_t attention_workspace_bytes(const AttnArgs& a, int64_t max_q) {
   const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
   const size_t W = 1 << log2_waves(DP), BM = STREAM_ROWS;
-  const size_t stream = W * 16 + 2 * W * BM * 8 + 2 * W * BM * DP * 4;
+  const size_t stream = W * 32 + 2 * W * BM * 8 + 2 * W * BM * DP * 4;
   return max_q * a.group <= STREAM_ROWS ? stream : std::max(stream, attention_tile_bytes(a));
 }
 
@@ -447,8 +455,9 @@ hipError_t launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspac
   a.rows_to = 0x7FFFFFFF;
   const int64_t rows = max_q * a.group;
   if (rows > STREAM_ROWS) {
-    // (queries that come to batch * max_q are max_q of every sequence)
-    const bool all = (int64_t)a.batch * max_q == a.tokens;
+    // Of a batch whose sequences have half of max_q queries on average, the tiles take the short ones too; in one of
+    // prompts among single tokens, the second launch is worth its time (a few us).
+    const bool all = (int64_t)a.batch * max_q <= 2 * (int64_t)a.tokens;
     if (!all) a.rows_from = STREAM_ROWS;
     hipError_t e = launch_attention_tile(a, dtype, workspace, stream);
     if (e != hipSuccess || all) return e;

@@ -37,6 +37,15 @@ __device__ __forceinline__ int swizzle_v(int row) {
   return DP == 64 ? (row & 2) << 1 : (row & 3) << 2;
 }
 
+// f(0), f(1), ..., f(N - 1), each with its number as a constant.
+template <int N, int I = 0, class F>
+__device__ __forceinline__ void each(F&& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>{});
+    each<N, I + 1>(f);
+  }
+}
+
 // Tile slots.  Sequence s's tiles are slots first(s), first(s) + 1, ..., with first(s) = token0(s) group / BM + s:
 // they are at least as many as its tiles (a slot of no tile has a number below 0 or past its sequence's rows).
 struct TileOf {
@@ -115,11 +124,31 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
     const void* src = b < b1 && seen_by_any(key) ? (const void*)(table + attn_page(a, key)) : attn_zeros;
     __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)(pages + (b & 3) * 256), 4, 0, 0);
   };
+  // Rows of one wave that lie in one page, all of them seen: their addresses are one scalar each and an offset of
+  // the lane, which the swizzles change in bits that a load's number sets alone.
+  const uint32_t k_row = lane / L::CPR * 2 * a.k_token, v_row = lane / L::CPR * 2 * a.v_token;
+  const uint32_t k_chunk = 16 * ((lane % L::CPR) ^ attn_swizzle<DP>(wave * L::RW + lane / L::CPR));
+  const uint32_t v_chunk = 16 * ((lane % L::CPR) ^ swizzle_v<DP>(wave * L::RW + lane / L::CPR));
+  auto load_rows = [&](const uint8_t* from, uint32_t token, uint32_t row, uint32_t chunk, uint8_t* to, auto swizzle) {
+#pragma unroll
+    for (int n = 0; n < L::NI; ++n)
+      attn_load16(from + (uint64_t)n * L::RPI * 2 * token + ((chunk ^ (16 * swizzle(n * L::RPI))) + row), to + n * 1024);
+  };
+  auto page_of = [&](int b) { return *reinterpret_cast<const uint32_t*>(pages + (b & 3) * 256 + 4 * lane); };
+  const uint8_t *v_at[2];  // the first row of the values of the block of each parity, NULL: see their places
   // starts this wave's share of the loads of block b's keys (of zeros past the run), and keeps the places of its values;
-  // returns which of the block's keys are there
-  auto load_k = [&](int b, int odd) {
-    const int key = key0(b) + lane;
-    const uint32_t page = *reinterpret_cast<const uint32_t*>(pages + (b & 3) * 256 + 4 * lane);
+  // returns which of the block's keys are there.  `page`: of the lane's key
+  auto load_k = [&](int b, int odd, uint32_t page) {
+    const int j0 = key0(b);
+    const uint32_t of = __builtin_amdgcn_readlane(page, wave * L::RW);
+    if (EXACT && a.page_rows && b < b1 && j0 + BN <= sp.hi && (j0 >= sp.lo || j0 + BN <= sp.sinks) && of < a.pages) {
+      const AttnPlace p = attn_place(a, kh, vh, j0 + wave * L::RW, of, true);
+      v_at[odd] = p.v;
+      load_rows(p.k, a.k_token, k_row, k_chunk, lds + odd * L::BLOCK + wave * L::RW * L::ROW, attn_swizzle<DP>);
+      return (uint64_t)__ballot(page < a.pages);  // (the other waves' rows too)
+    }
+    v_at[odd] = nullptr;
+    const int key = j0 + lane;
     const bool ok = b < b1 && seen_by_any(key) && page < a.pages;
     const AttnPlace p = attn_place(a, kh, vh, key, page, ok);
     if (lane / L::RW == wave) {
@@ -140,6 +169,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   };
   auto load_v = [&](int odd) {
     uint8_t* to = lds + (2 + odd) * L::BLOCK + wave * L::RW * L::ROW;
+    if (v_at[odd] != nullptr) {
+      load_rows(v_at[odd], a.v_token, v_row, v_chunk, to, swizzle_v<DP>);
+      return;
+    }
     const uint8_t* from[L::NI];
 #pragma unroll
     for (int n = 0; n < L::NI; ++n)
@@ -185,10 +218,12 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   load_pages(b0);
   load_pages(b0 + 1);
   load_pages(b0 + 2);
+  load_pages(b0 + 3);
   attn_vm_drain();
-  here = load_k(b0, 0);
+  here = load_k(b0, 0, page_of(b0));
   load_v(0);
-  there = load_k(b0 + 1, 1);
+  there = load_k(b0 + 1, 1, page_of(b0 + 1));
+  uint32_t page = page_of(b0 + 2);
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
   float16_t sa[2], sb[2], zero;
 #pragma unroll
@@ -206,9 +241,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
     constexpr int ODD = decltype(parity)::value;
     // keys b + 1 and values b have landed, here and in the other waves; keys b and values b - 1 are read
     asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-    load_pages(b + 3);
-    const uint64_t later = load_k(b + 2, ODD);
+    const uint64_t later = load_k(b + 2, ODD, page);
     load_v(1 - ODD);
+    load_pages(b + 4);
+    page = page_of(b + 3);
     const int j0 = key0(b);
     if (here != ~0ull || j0 + BN > low_hi || (j0 < top_lo && j0 + BN > a.sinks)) {
       // element (t, i) is key j0 + 4 h + 32 t + 8 (i / 4) + i % 4
@@ -268,39 +304,43 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
       f[i % (PRE + 1)] = i < N1 ? fetch_k(1 - ODD, i / KS, i % KS) : fetch_v(ODD, (i - N1) / ND, (i - N1) % ND);
     };
     float over = ATTN_NONE;
+    __builtin_amdgcn_s_setprio(1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 0; i < PRE; ++i) fetch(i);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i + PRE < N) fetch(i + PRE);
+    each<N>([&](auto step) __attribute__((always_inline)) {
+      constexpr int i = decltype(step)::value;
+      if constexpr (i + PRE < N) fetch(i + PRE);
       const auto& op = f[i % (PRE + 1)];
-      if (i < N1) {
+      if constexpr (i < N1) {
         next[i / KS] = T::mma32(op, qf[i % KS], i % KS == 0 ? zero : next[i / KS]);
       } else {
-        o[(i - N1) % ND] = T::mma32(op, __builtin_bit_cast(typename T::x8, p[(i - N1) / ND]), o[(i - N1) % ND]);
+        constexpr int u = (i - N1) / ND, d = (i - N1) % ND;
+        o[d] = T::mma32(op, __builtin_bit_cast(typename T::x8, p[u]), o[d]);
       }
       __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {  // pair j: exponentials in step j LAST / 16, rounding in the next one
-        const int j1 = (16 * (i - 1) + LAST - 1) / LAST + x, j = (16 * i + LAST - 1) / LAST + x;
-        if (i > 0 && j1 < 16 && j1 * LAST / 16 == i - 1) {
+      each<2>([&](auto y) __attribute__((always_inline)) {
+        // pair j: exponentials in step j LAST / 16, rounding in the next one
+        constexpr int j1 = (16 * (i - 1) + LAST - 1) / LAST + decltype(y)::value;
+        constexpr int j0 = (16 * i + LAST - 1) / LAST + decltype(y)::value;
+        if constexpr (i > 0 && j1 < 16 && j1 * LAST / 16 == i - 1) {
           p[j1 / 4][j1 % 4] = T::pack2(e[j1][0], e[j1][1]);
           l = T::sum2(p[j1 / 4][j1 % 4], l);
         }
-        if (j < 16 && j * LAST / 16 == i) {
-          e[j][0] = attn_exp2(fmaf(s[j >> 3][2 * (j & 7)], sc, -ref));
-          e[j][1] = attn_exp2(fmaf(s[j >> 3][2 * (j & 7) + 1], sc, -ref));
+        if constexpr (j0 < 16 && j0 * LAST / 16 == i) {
+          e[j0][0] = attn_exp2(fmaf(s[j0 >> 3][2 * (j0 & 7)], sc, -ref));
+          e[j0][1] = attn_exp2(fmaf(s[j0 >> 3][2 * (j0 & 7) + 1], sc, -ref));
         }
-      }
+      });
       // (a score's last matrix instruction is two steps ahead)
-      if (i >= KS + 2 && i < KS + 10) over = larger(over, next[0], i - KS - 2);
-      if (i >= N1 + 2 && i < N1 + 6) {
+      if constexpr (i >= KS + 2 && i < KS + 10) over = larger(over, next[0], i - KS - 2);
+      if constexpr (i >= N1 + 2 && i < N1 + 6) {
         over = larger(over, next[1], 2 * (i - N1 - 2));
         over = larger(over, next[1], 2 * (i - N1 - 2) + 1);
       }
       __builtin_amdgcn_sched_barrier(0);
-    }
+    });
+    __builtin_amdgcn_s_setprio(0);
     asm volatile("" : "+v"(over), "+v"(l));  // (not moved out of the steps and behind them)
     top = over;
     here = there;

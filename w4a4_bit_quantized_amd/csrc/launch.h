@@ -155,6 +155,7 @@ struct AttnArgs {
   int tokens, batch, each, heads, kv_heads, group, D, max_len, mask_width;
   uint32_t pages, page_mul, group_mul;
   int page_size, page_shift, group_shift;
+  bool page_rows;  // 16 keys from a multiple of 16 on lie in one page, less than 2^31 bytes apart
   float scale_log2;  // scale * log2(e)
   int window, sinks;
   // set by the launcher: sequences of more than rows_from and at most rows_to rows are this launch's
