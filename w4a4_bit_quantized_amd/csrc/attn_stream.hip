@@ -34,6 +34,7 @@ struct Stream {
   static constexpr int NI = KB / RPI;               // direct loads of K, or of V, per block
   static constexpr int HALF = KB * ROW;             // K of a stage, then V
   static constexpr int STAGE = 2 * HALF;
+  static constexpr int LDS = 2 * STAGE + KB * (int)sizeof(AttnPlace) + 4 * 256;
 };
 
 template <int DP, bool EXACT, int NQ, class T>
@@ -41,10 +42,9 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
   using S = Stream<DP>;
   constexpr int BM = 16 * NQ, KS = DP / 32, ND = DP / 16;
   // two stages, the places of a block's keys, and the pages of four blocks' keys (key lane % 32 of 64)
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * S::STAGE + KB * sizeof(AttnPlace) + 4 * 256];
-  uint8_t* const ring = lds;
-  AttnPlace* const places = reinterpret_cast<AttnPlace*>(lds + 2 * S::STAGE);
-  uint8_t* const pages = lds + 2 * S::STAGE + KB * sizeof(AttnPlace);
+  __shared__ __attribute__((aligned(16))) uint8_t ring[S::LDS];
+  AttnPlace* const places = reinterpret_cast<AttnPlace*>(ring + 2 * S::STAGE);
+  uint8_t* const pages = ring + 2 * S::STAGE + KB * sizeof(AttnPlace);
   const int lane = threadIdx.x, c16 = lane & 15, qd = lane >> 4;
   const int w = blockIdx.x;
 
@@ -161,12 +161,20 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
         for (int d = 0; d < ND; ++d) o[n][d] = float4_t{0, 0, 0, 0};
       }
+      // 16 keys that lie in one page, all of them seen: their rows' addresses are one scalar and an offset of the lane,
+      // which the swizzle changes in bits that a load's number sets alone.
+      const uint32_t k_row = lane / S::CPR * 2 * a.k_token, v_row = lane / S::CPR * 2 * a.v_token;
+      const uint32_t chunk = 16 * ((lane % S::CPR) ^ attn_swizzle<DP>(lane / S::CPR));
+      auto load_row = [&](const uint8_t* from, uint32_t token, uint32_t row, uint8_t* to, int n) {  // (from: of row n RPI & ~15)
+        load16(from + (uint64_t)(n * S::RPI % 16) * 2 * token + ((chunk ^ (16 * attn_swizzle<DP>(n * S::RPI))) + row), to + n * 1024);
+      };
+
       // Pass b works on block b and starts the loads of block b + 2: those of K as soon as this block's
       // scores are formed, those of V at its end, so that one and a half blocks are on their way while the wave
-      // computes and two while it waits.  Past the run, zeros are loaded: every wait counts the same.  The pages are
-      // loaded two passes ahead of their use, into LDS too: for a register the compiler would wait by itself, for all loads.
-      // In the order of their issue: pages b + 2, K b, V b, pages b + 3, K b + 1, V b + 1, pages b + 4, K b + 2.
-      constexpr int AHEAD = 3 * S::NI + 2;
+      // computes and two while it waits.  The pages are loaded two passes ahead of their use, into LDS too: for a register the
+      // compiler would wait by itself, for all loads.  In the order of their issue: pages b + 2, K b, V b, pages b + 3, K b + 1,
+      // V b + 1, pages b + 4, K b + 2, with no K and V past the run; the waits count what may be on its way behind.
+      constexpr int NI = S::NI;
       uint32_t here = 0, there = 0, later = 0;  // which keys of blocks b, b + 1, b + 2 are there
       load_pages(b0);
       load_pages(b0 + 1);
@@ -176,47 +184,63 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         here = there;
         there = later;
         load_pages(b + 4);
-        const bool work = b >= b0;
-        const uint8_t* ks = ring + (b & 1) * S::STAGE;
-        const uint8_t* vs = ks + S::HALF;
-        const int j0 = key0(b);
+        const bool work = b >= b0, more = b + 2 < b1;
         uint8_t* stage = ring + (b & 1) * S::STAGE;
+        const uint8_t *ks = stage, *vs = stage + S::HALF;
+        const int j0 = key0(b);
+        if (work) {
+          if (b + 1 < b1) attn_vm_wait<3 * NI + 2>();
+          else attn_vm_wait<NI + 2>();
+        }
+        const uint32_t page = *reinterpret_cast<const uint32_t*>(pages + (b + 2 & 3) * 256 + 4 * lane);
 
         float4_t s[NQ][2];
         if (work) {
-        attn_vm_wait<AHEAD>();
-      
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          typename T::x8 kf[KS];
+          for (int t = 0; t < 2; ++t) {
+            typename T::x8 kf[KS];
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const int lr = 16 * t + c16;
-            kf[k] = __builtin_bit_cast(typename T::x8, *reinterpret_cast<const u32x4_t*>(
-                ks + lr * S::ROW + 16 * ((4 * k + qd) ^ attn_swizzle<DP>(lr))));
-          }
+            for (int k = 0; k < KS; ++k) {
+              const int lr = 16 * t + c16;
+              kf[k] = __builtin_bit_cast(typename T::x8, *reinterpret_cast<const u32x4_t*>(
+                  ks + lr * S::ROW + 16 * ((4 * k + qd) ^ attn_swizzle<DP>(lr))));
+            }
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            s[n][t] = float4_t{0, 0, 0, 0};
+            for (int n = 0; n < NQ; ++n) {
+              s[n][t] = float4_t{0, 0, 0, 0};
 #pragma unroll
-            for (int k = 0; k < KS; ++k) s[n][t] = T::mma16(kf[k], qf[n][k], s[n][t]);
+              for (int k = 0; k < KS; ++k) s[n][t] = T::mma16(kf[k], qf[n][k], s[n][t]);
+            }
           }
         }
-        }
-        const int key = key0(b + 2) + (lane & 31);
-        const uint32_t page = *reinterpret_cast<const uint32_t*>(pages + (b + 2 & 3) * 256 + 4 * lane);
-        const bool ok = b + 2 < b1 && seen_by_any(key) && page < a.pages;
-        later = (uint32_t)__ballot(ok);
-        wave_lds_sync();
-        if (lane < KB) places[lane] = attn_place(a, kh, vh, key, page, ok);
-        wave_lds_sync();
-        const uint8_t* from[S::NI];  // (all read before the first load: the compiler keeps their order)
+        // block b + 2
+        const int n0 = key0(b + 2);
+        const bool whole_rows = EXACT && a.page_rows && n0 + KB <= sp.hi && (n0 >= sp.lo || n0 + KB <= sp.sinks);
+        later = 0;
+        const uint8_t *v0 = nullptr, *v1 = nullptr;
+        if (more) {
+          const bool ok = seen_by_any(n0 + (lane & 31)) && page < a.pages;
+          later = (uint32_t)__ballot(ok);
+          wave_lds_sync();  // (this block's keys are read)
+          if (whole_rows && later == 0xFFFFFFFFu) {
+            const AttnPlace p0 = attn_place(a, kh, vh, n0, __builtin_amdgcn_readlane(page, 0), true);
+            const AttnPlace p1 = attn_place(a, kh, vh, n0 + 16, __builtin_amdgcn_readlane(page, 16), true);
+            v0 = p0.v;
+            v1 = p1.v;
 #pragma unroll
-        for (int n = 0; n < S::NI; ++n) from[n] = places[n * S::RPI + lane / S::CPR].k;
+            for (int n = 0; n < NI; ++n) load_row(n < NI / 2 ? p0.k : p1.k, a.k_token, k_row, stage, n);
+          } else {
+            if (lane < KB) places[lane] = attn_place(a, kh, vh, n0 + lane, page, ok);
+            wave_lds_sync();
+            const uint8_t* from[NI];  // (all read before the first load: the compiler keeps their order)
 #pragma unroll
-        for (int n = 0; n < S::NI; ++n) {
-          const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
-          load16(attn_chunk<EXACT>(from[n], c, a.D), stage + n * 1024);
+            for (int n = 0; n < NI; ++n) from[n] = places[n * S::RPI + lane / S::CPR].k;
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+              const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
+              load16(attn_chunk<EXACT>(from[n], c, a.D), stage + n * 1024);
+            }
+          }
         }
         if (work) {
         if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
@@ -277,7 +301,9 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
           p[n] = __builtin_bit_cast(typename T::x8, u32x4_t{T::pack2(e[0], e[1]), T::pack2(e[2], e[3]),
                                                            T::pack2(e[4], e[5]), T::pack2(e[6], e[7])});
         }
-        attn_vm_wait<AHEAD>();
+        if (more) attn_vm_wait<3 * NI + 2>();
+        else if (b + 1 < b1) attn_vm_wait<2 * NI + 2>();
+        else attn_vm_wait<2>();
       
 #pragma unroll
         for (int d = 0; d < ND; ++d) {
@@ -289,15 +315,26 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         }
         wave_lds_sync();  // (the stage is read)
         }
+        if (more) {
+          if (v0 != nullptr) {
 #pragma unroll
-        for (int n = 0; n < S::NI; ++n) from[n] = places[n * S::RPI + lane / S::CPR].v;
+            for (int n = 0; n < NI; ++n) load_row(n < NI / 2 ? v0 : v1, a.v_token, v_row, stage + S::HALF, n);
+          } else {
+            const uint8_t* from[NI];
 #pragma unroll
-        for (int n = 0; n < S::NI; ++n) {
-          const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
-          load16(attn_chunk<EXACT>(from[n], c, a.D), stage + S::HALF + n * 1024);
+            for (int n = 0; n < NI; ++n) from[n] = places[n * S::RPI + lane / S::CPR].v;
+#pragma unroll
+            for (int n = 0; n < NI; ++n) {
+              const int c = (lane % S::CPR) ^ attn_swizzle<DP>(n * S::RPI + lane / S::CPR);
+              load16(attn_chunk<EXACT>(from[n], c, a.D), stage + S::HALF + n * 1024);
+            }
+          }
         }
       }
 
+      float sum[NQ];
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) sum[n] = attn_sum16(attn_sum32(l[n]));
       // finished, or a piece: the first of a triple in slot 1 of the wave, any other in slot 0
       if (first && !whole && lane == 0) {  // pieces, sequence's first row of q, rows of the tile and the first of them, head
         const int pieces = 1 + (run >= each ? 1 : attn_div(each - u_end + run - 1, (int)run));
@@ -307,25 +344,22 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
       const int64_t slot = 2 * (int64_t)w + (first ? 1 : 0);
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const float sum = attn_sum16(attn_sum32(l[n]));
         const int rr = tile * BM + n * 16 + c16;
         if (rr >= rows) continue;
-        if (whole) {
-          const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-          const int i = attn_query(a, rr), g = rr - i * a.group;
-          uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs);
+        const int i = attn_query(a, rr), g = rr - i * a.group;
+        uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs);
+        const int64_t at = slot * BM + n * 16 + c16;
+        if (!whole && qd == 0) *reinterpret_cast<float2_t*>(a.stats + 2 * at) = float2_t{m[n], sum[n]};
+        const float f = sum[n] == 0.0f ? 0.0f : 1.0f / sum[n];
 #pragma unroll
-          for (int d = 0; d < ND; ++d) {
-            const int e = 16 * d + 4 * qd;
-            if (e < a.D)
-              *reinterpret_cast<u32x2_t*>(dst + 2 * e) = u32x2_t{T::pack2(o[n][d][0] * f, o[n][d][1] * f),
-                                                                T::pack2(o[n][d][2] * f, o[n][d][3] * f)};
+        for (int d = 0; d < ND; ++d) {
+          const int e = 16 * d + 4 * qd;
+          if (!whole) {
+            *reinterpret_cast<float4_t*>(a.part + at * DP + e) = o[n][d];
+          } else if (e < a.D) {
+            *reinterpret_cast<u32x2_t*>(dst + 2 * e) = u32x2_t{T::pack2(o[n][d][0] * f, o[n][d][1] * f),
+                                                              T::pack2(o[n][d][2] * f, o[n][d][3] * f)};
           }
-        } else {
-          const int64_t at = slot * BM + n * 16 + c16;
-          if (qd == 0) *reinterpret_cast<float2_t*>(a.stats + 2 * at) = float2_t{m[n], sum};
-#pragma unroll
-          for (int d = 0; d < ND; ++d) *reinterpret_cast<float4_t*>(a.part + at * DP + 16 * d + 4 * qd) = o[n][d];
         }
       }
       u_in = 0;
@@ -416,12 +450,12 @@ hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
   a.stats = reinterpret_cast<float*>(a.desc + 8 * W);
   a.part = a.stats + (size_t)2 * W * BM * 2;
   a.log2_waves = log2_waves(DP);
-  a.least = 4;  // (one sequence of 4096 keys, 8 heads: 16.0 us with 4, 2 and 3: 16.4 and 17.6, 6: 19)
+  a.least = 4;  // (one sequence of 4096 keys, 8 heads: 16.0 us with 4, 3: 16.5, 5: 17.0)
   if (a.D == DP) attn_stream_kernel<DP, true, NQ, T><<<W, 64, 0, st>>>(a);
   else attn_stream_kernel<DP, false, NQ, T><<<W, 64, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_join_kernel<DP, BM, T><<<dim3(W, 4), 256, 0, st>>>(a);
+  attn_join_kernel<DP, BM, T><<<dim3(W, 8), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
