@@ -192,3 +192,39 @@ def test_workspace_of_exactly_its_size(w4, shape):
         assert (ws[need:] == 0xFF).all() and (out[int(b.starts[-1]):] == 7).all()
         with pytest.raises(ValueError, match="workspace holds"):
             b.run(w4, workspace=ws[:need - 1], **kw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf], ids=str)
+@pytest.mark.parametrize("shape", [([(5, 100), (4, 4)], 4, 2, 64, 16), ([(20, 200)], 2, 1, 128, 16), ([(40, 40)], 4, 1, 128, 24), ([(9, 130)], 8, 1, 256, 16),
+                                   ([(200, 260)], 2, 2, 64, 16), ([(150, 150)], 1, 1, 80, 32)], ids=names)
+def test_values_that_some_rows_see(w4, shape, bad, dtype):
+    """An infinity or NaN among the values or keys of one position reaches the rows that see it and no other."""
+    import torch
+    both, hq, hk, D, page = shape
+    b = Batch(5, both, hq, hk, D, page, dtype)
+    n, l = both[0]
+    at = l - n + n // 2                                  # a position that the later half of the queries sees
+    b.vc[b.table[0, at // page], at % page, 0, 3] = oh.from_f32(np.array([bad], np.float32), dtype)[0]
+    b.vc[b.table[0, at // page], at % page, 0, D - 1] = oh.from_f32(np.array([-bad], np.float32), dtype)[0]
+    b.dv = dev(b.vc, dtype)
+    window = n // 3 + 1
+    m, pos = b.tree()
+    m[: n] = np.tril(np.ones((n, b.max_q), bool))        # every second node sees its chain, the others only themselves
+    m[1:n:2] = np.eye(n, b.max_q, dtype=bool)[1::2]
+    for what, got, kw in (("causal", b.run(w4), {}), ("window", b.run(w4, window=window), dict(window=window)),
+                          ("tree", b.run_tree(w4, m, pos), dict(mask=m))):
+        with np.errstate(invalid="ignore"):
+            res = b.expected(**kw)
+        g, o = oh.to_f32(host(got), dtype).astype(np.float64), res[0]
+        assert (np.isfinite(g) == np.isfinite(o)).all(), what
+        assert (np.isnan(g) == np.isnan(o)).all() and (g[np.isinf(g)] == o[np.isinf(o)]).all(), what
+        fine = np.isfinite(o)
+        with np.errstate(invalid="ignore"):
+            assert (np.abs(g - o)[fine] <= limit(res, dtype, D, l)[fine]).all(), what
+    b.kc[b.table[0, at // page], at % page, 0, 1] = oh.from_f32(np.array([np.nan], np.float32), dtype)[0]
+    b.dk = dev(b.kc, dtype)
+    g = oh.to_f32(host(b.run(w4)), dtype)
+    group = hq // hk
+    assert np.isfinite(g[:n // 2]).all() and np.isnan(g[n // 2:n, :group]).all()
+    assert np.isfinite(g[n:]).all() and (hk == 1 or np.isfinite(g[:n, group:]).all())

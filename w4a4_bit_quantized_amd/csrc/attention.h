@@ -30,6 +30,8 @@ typedef __attribute__((address_space(3))) attn_short4_t attn_lds_s4;
 
 struct Bf16 {
   typedef bf16x8_t x8;
+  static constexpr uint32_t EXP = 0x7F80;  // the exponent of infinities and NaNs
+  static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
   static __device__ __forceinline__ float4_t mma16(x8 a, x8 b, float4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
   }
@@ -49,6 +51,11 @@ struct Bf16 {
 
 struct F16 {
   typedef half8_t x8;
+  static constexpr uint32_t EXP = 0x7C00;
+  static __device__ __forceinline__ float value(uint32_t bits) {
+    const uint16_t b = (uint16_t)bits;
+    return (float)__builtin_bit_cast(_Float16, b);
+  }
   static __device__ __forceinline__ float4_t mma16(x8 a, x8 b, float4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
   }
@@ -250,6 +257,64 @@ __device__ __forceinline__ typename T::x8 attn_read_vt(const uint8_t* __restrict
   const attn_short4_t t1 = __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn_lds_s4*)b);
   const u32x2_t w0 = __builtin_bit_cast(u32x2_t, t0), w1 = __builtin_bit_cast(u32x2_t, t1);
   return __builtin_bit_cast(typename T::x8, u32x4_t{w0[0], w0[1], w1[0], w1[1]});
+}
+
+// Infinities and NaNs among the values of keys that some of a tile's rows see and others do not.  In the product, the
+// others' probability 0 times such a value would be a NaN.  So in a block that a mask cuts, the values are looked
+// through first; those rows that see such a value get it added (their probability is positive), and it is set to 0 for the product.
+// A lane looks at 16 bytes of every 1024 of the tile.
+template <class T>
+__device__ __forceinline__ uint32_t attn_odd(uint32_t w) {  // the halves of w that are infinite or NaN, as masks
+  constexpr uint32_t E = T::EXP;
+  return ((w & E) == E ? 0xFFFFu : 0u) | ((w >> 16 & E) == E ? 0xFFFF0000u : 0u);
+}
+template <class T, int BYTES>
+__device__ __forceinline__ bool attn_any_odd(const uint8_t* tile, int lane) {
+  typedef unsigned short ushort2_t __attribute__((ext_vector_type(2)));
+  constexpr uint32_t E = T::EXP | T::EXP << 16;
+  ushort2_t least = {0xFFFF, 0xFFFF};
+#pragma unroll 4
+  for (int n = 0; n < BYTES / 1024; ++n) {
+    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(tile + n * 1024 + lane * 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) least = __builtin_elementwise_min(least, __builtin_bit_cast(ushort2_t, ~x[c] & E));
+  }
+  return __any(least[0] == 0 || least[1] == 0);
+}
+// The rows (a bit each) that have such values, looked for in chunks of 16 bytes, CPR of a row.
+template <class T, int CPR, int ROWS>
+__device__ __forceinline__ uint64_t attn_odd_rows(const uint8_t* tile, int lane) {
+  uint64_t odd = 0;
+#pragma unroll 1
+  for (int n = 0; n < ROWS * CPR / 64; ++n) {
+    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(tile + n * 1024 + lane * 16);
+    const uint64_t has = __ballot((attn_odd<T>(x[0]) | attn_odd<T>(x[1]) | attn_odd<T>(x[2]) | attn_odd<T>(x[3])) != 0);
+    for (int r = 0; r < 64 / CPR; ++r)
+      if ((has >> (r * CPR)) & (((uint64_t)1 << CPR) - 1)) odd |= (uint64_t)1 << (n * (64 / CPR) + r);
+  }
+  return odd;
+}
+template <class T, int CPR, int ROWS>
+__device__ __forceinline__ void attn_clear_odd(uint8_t* tile, int lane) {
+#pragma unroll 1
+  for (int n = 0; n < ROWS * CPR / 64; ++n) {
+    u32x4_t* at = reinterpret_cast<u32x4_t*>(tile + n * 1024 + lane * 16);
+    u32x4_t x = *at;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) x[c] &= ~attn_odd<T>(x[c]);
+    *at = x;
+  }
+}
+// What a row that sees a key (or not) gets of 4 of its values in this way.
+template <class T>
+__device__ __forceinline__ void attn_add_odd(const uint8_t* values, bool seen, float* o) {
+  const u32x2_t x = *reinterpret_cast<const u32x2_t*>(values);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    const uint32_t w = seen ? x[c] & attn_odd<T>(x[c]) : 0u;
+    o[2 * c] += T::value(w & 0xFFFFu);
+    o[2 * c + 1] += T::value(w >> 16);
+  }
 }
 
 constexpr float ATTN_NONE = -__builtin_inff();

@@ -242,8 +242,11 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
             }
           }
         }
+        uint32_t seen[NQ];  // (of a cut block: bit 16 t + i)
+        bool cut = false;
         if (work) {
         if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
+          cut = true;
           // element (t, i) is key j0 + 4 qd + 16 t + i
           const uint32_t mine = here >> (4 * qd);
 #pragma unroll
@@ -272,6 +275,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
               bits = (bits & ~nodes) | (tree & nodes);
             }
             bits &= mine;
+            seen[n] = bits;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
               if (!((bits >> (16 * (e >> 2) + (e & 3))) & 1)) s[n][e >> 2][e & 3] = ATTN_NONE;
@@ -304,6 +308,29 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         if (more) attn_vm_wait<3 * NI + 2>();
         else if (b + 1 < b1) attn_vm_wait<2 * NI + 2>();
         else attn_vm_wait<2>();
+        if (cut) {
+          if (attn_any_odd<T, S::HALF>(vs, lane)) {
+            uint32_t odd = (uint32_t)attn_odd_rows<T, S::CPR, KB>(vs, lane);
+            while (odd != 0) {
+              const int j = __ffs(odd) - 1;
+              odd &= odd - 1;
+#pragma unroll
+              for (int n = 0; n < NQ; ++n) {
+                const bool sees = (__shfl(seen[n], c16 + 16 * ((j >> 2) & 3)) >> (16 * (j >> 4) + (j & 3))) & 1;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                  const uint8_t* at = vs + j * S::ROW + 16 * ((2 * d + (qd >> 1)) ^ attn_swizzle<DP>(j)) + 8 * (qd & 1);
+                  float x[4] = {o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]};
+                  attn_add_odd<T>(at, sees, x);
+                  o[n][d] = float4_t{x[0], x[1], x[2], x[3]};
+                }
+              }
+            }
+            wave_lds_sync();
+            attn_clear_odd<T, S::CPR, KB>(stage + S::HALF, lane);
+            wave_lds_sync();
+          }
+        }
       
 #pragma unroll
         for (int d = 0; d < ND; ++d) {

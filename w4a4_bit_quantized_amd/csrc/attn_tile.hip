@@ -90,13 +90,25 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   const uint8_t* kh = a.k + 2 * (head * a.k_head);
   const uint8_t* vh = a.v + 2 * (head * a.v_head);
 
-  const int rr = row0 + wave * 32 + l32;  // this lane's row
-  const bool valid = rr < rows;
-  const int qi = valid ? attn_query(a, rr) : 0, qg = valid ? rr - qi * a.group : 0;
-  const AttnRow row = attn_row(a, sq, qi, valid);
+  // this lane's row, its query and head of the group.  (What is used seldom is formed again or lies in LDS: every
+  // register of the passes counts, and a spilled one would be waited for together with all loads.)
+  auto row_of = [&]() {
+    int l = l32;
+    asm volatile("" : "+v"(l));
+    return row0 + wave * 32 + l;
+  };
+  __shared__ AttnRow seen_by[WAVES][32];
+  int low_hi = 0x7FFFFFFF, top_lo = 0;
   typename T::x8 qf[KS];
   {
-    const uint8_t* src = a.q + 2 * ((int64_t)(sq.token0 + qi) * a.q_ts + (int64_t)(head * a.group + qg) * a.q_hs);
+    const int rr = row_of();
+    const bool valid = rr < rows;
+    const int i = valid ? attn_query(a, rr) : 0, g = valid ? rr - i * a.group : 0;
+    const AttnRow row = attn_row(a, sq, i, valid);
+    if (h == 0) seen_by[wave][l32] = row;
+    if (valid) low_hi = row.hi;
+    top_lo = row.lo;
+    const uint8_t* src = a.q + 2 * ((int64_t)(sq.token0 + i) * a.q_ts + (int64_t)(head * a.group + g) * a.q_hs);
 #pragma unroll
     for (int k = 0; k < KS; ++k) {
       const int d = 16 * k + 8 * h;
@@ -105,11 +117,22 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
       qf[k] = __builtin_bit_cast(typename T::x8, x);
     }
   }
-  int low_hi = valid ? row.hi : 0x7FFFFFFF, top_lo = row.lo;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
     low_hi = min(low_hi, __shfl_xor(low_hi, d));
     top_lo = max(top_lo, __shfl_xor(top_lo, d));
+  }
+  // (of the whole tile: its waves take the same blocks as cut)
+  __shared__ int ends[2][WAVES];
+  if (lane == 0) {
+    ends[0][wave] = low_hi;
+    ends[1][wave] = top_lo;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < WAVES; ++i) {
+    low_hi = min(low_hi, ends[0][i]);
+    top_lo = max(top_lo, ends[1][i]);
   }
   low_hi = uniform(low_hi);
   top_lo = uniform(top_lo);
@@ -126,10 +149,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   };
   // Rows of one wave that lie in one page, all of them seen: their addresses are one scalar each and an offset of
   // the lane, which the swizzles change in bits that a load's number sets alone.
-  const uint32_t k_row = lane / L::CPR * 2 * a.k_token, v_row = lane / L::CPR * 2 * a.v_token;
-  const uint32_t k_chunk = 16 * ((lane % L::CPR) ^ attn_swizzle<DP>(wave * L::RW + lane / L::CPR));
-  const uint32_t v_chunk = 16 * ((lane % L::CPR) ^ swizzle_v<DP>(wave * L::RW + lane / L::CPR));
-  auto load_rows = [&](const uint8_t* from, uint32_t token, uint32_t row, uint32_t chunk, uint8_t* to, auto swizzle) {
+  auto load_rows = [&](const uint8_t* from, uint32_t token, uint8_t* to, auto swizzle) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const uint32_t row = l / L::CPR * 2 * token, chunk = 16 * ((l % L::CPR) ^ swizzle(wave * L::RW + l / L::CPR));
 #pragma unroll
     for (int n = 0; n < L::NI; ++n)
       attn_load16(from + (uint64_t)n * L::RPI * 2 * token + ((chunk ^ (16 * swizzle(n * L::RPI))) + row), to + n * 1024);
@@ -144,7 +167,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
     if (EXACT && a.page_rows && b < b1 && j0 + BN <= sp.hi && (j0 >= sp.lo || j0 + BN <= sp.sinks) && of < a.pages) {
       const AttnPlace p = attn_place(a, kh, vh, j0 + wave * L::RW, of, true);
       v_at[odd] = p.v;
-      load_rows(p.k, a.k_token, k_row, k_chunk, lds + odd * L::BLOCK + wave * L::RW * L::ROW, attn_swizzle<DP>);
+      load_rows(p.k, a.k_token, lds + odd * L::BLOCK + wave * L::RW * L::ROW, attn_swizzle<DP>);
       return (uint64_t)__ballot(page < a.pages);  // (the other waves' rows too)
     }
     v_at[odd] = nullptr;
@@ -156,31 +179,35 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
       *reinterpret_cast<const uint8_t**>(places + ((1 + odd) * L::RW + lane % L::RW) * 8) = p.v;
     }
     wave_lds_sync();
+    int l = lane;
+    asm volatile("" : "+v"(l));
     uint8_t* to = lds + odd * L::BLOCK + wave * L::RW * L::ROW;
     const uint8_t* from[L::NI];  // (all read before the first load: the compiler keeps their order)
 #pragma unroll
-    for (int n = 0; n < L::NI; ++n) from[n] = *reinterpret_cast<const uint8_t**>(places + (n * L::RPI + lane / L::CPR) * 8);
+    for (int n = 0; n < L::NI; ++n) from[n] = *reinterpret_cast<const uint8_t**>(places + (n * L::RPI + l / L::CPR) * 8);
 #pragma unroll
     for (int n = 0; n < L::NI; ++n) {
-      const int r = n * L::RPI + lane / L::CPR;
-      attn_load16(attn_chunk<EXACT>(from[n], (lane % L::CPR) ^ attn_swizzle<DP>(wave * L::RW + r), a.D), to + n * 1024);
+      const int r = n * L::RPI + l / L::CPR;
+      attn_load16(attn_chunk<EXACT>(from[n], (l % L::CPR) ^ attn_swizzle<DP>(wave * L::RW + r), a.D), to + n * 1024);
     }
     return (uint64_t)__ballot(ok);
   };
   auto load_v = [&](int odd) {
+    int l = lane;
+    asm volatile("" : "+v"(l));
     uint8_t* to = lds + (2 + odd) * L::BLOCK + wave * L::RW * L::ROW;
     if (v_at[odd] != nullptr) {
-      load_rows(v_at[odd], a.v_token, v_row, v_chunk, to, swizzle_v<DP>);
+      load_rows(v_at[odd], a.v_token, to, swizzle_v<DP>);
       return;
     }
     const uint8_t* from[L::NI];
 #pragma unroll
     for (int n = 0; n < L::NI; ++n)
-      from[n] = *reinterpret_cast<const uint8_t**>(places + ((1 + odd) * L::RW + n * L::RPI + lane / L::CPR) * 8);
+      from[n] = *reinterpret_cast<const uint8_t**>(places + ((1 + odd) * L::RW + n * L::RPI + l / L::CPR) * 8);
 #pragma unroll
     for (int n = 0; n < L::NI; ++n) {
-      const int r = n * L::RPI + lane / L::CPR;
-      attn_load16(attn_chunk<EXACT>(from[n], (lane % L::CPR) ^ swizzle_v<DP>(wave * L::RW + r), a.D), to + n * 1024);
+      const int r = n * L::RPI + l / L::CPR;
+      attn_load16(attn_chunk<EXACT>(from[n], (l % L::CPR) ^ swizzle_v<DP>(wave * L::RW + r), a.D), to + n * 1024);
     }
   };
   // Operands in LDS, 16 bytes a lane.  Of K: keys 32 t + l32, elements 16 k + 8 h ..; of V: this lane's column of 32 d ..,
@@ -237,6 +264,13 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
 #pragma unroll
   for (int i = 1; i < 16; ++i) top = larger(top, sa[i >> 3], i & 7);
 
+  auto raise = [&](float top) {
+    const float to = fmaxf(m, top), f = attn_exp2(m - (to == ATTN_NONE ? 0.0f : to));
+    l *= f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d) o[d] *= f;
+    m = to;
+  };
   auto pass = [&](auto parity, int b, float16_t (&s)[2], float16_t (&next)[2]) {
     constexpr int ODD = decltype(parity)::value;
     // keys b + 1 and values b have landed, here and in the other waves; keys b and values b - 1 are read
@@ -247,6 +281,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
     page = page_of(b + 3);
     const int j0 = key0(b);
     if (here != ~0ull || j0 + BN > low_hi || (j0 < top_lo && j0 + BN > a.sinks)) {
+      uint32_t seen[2];
+      const AttnRow row = seen_by[wave][l32];
       // element (t, i) is key j0 + 4 h + 32 t + 8 (i / 4) + i % 4
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -258,7 +294,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
           bits |= (j < row.hi && (j >= row.lo || j < a.sinks) ? 1u : 0u) << in;
         }
         if (a.mask != nullptr && j0 + 32 * t + 32 > sq.ctx && a.mask_width > 0) {
-          const uint8_t* of = a.mask + (int64_t)(sq.token0 + qi) * a.mask_stride;
+          const int rr = row_of();
+          const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
           const int node = j0 + 32 * t + 4 * h - sq.ctx;
           uint32_t set[16];
 #pragma unroll
@@ -274,6 +311,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
           bits = (bits & ~nodes) | (tree & nodes);
         }
         bits &= mine;
+        seen[t] = bits;
 #pragma unroll
         for (int i = 0; i < 16; ++i)
           if (!((bits >> (8 * (i >> 2) + (i & 3))) & 1)) s[t][i] = ATTN_NONE;
@@ -281,15 +319,32 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
       top = fmaxf(s[0][0], s[0][1]);
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = larger(top, s[i >> 3], i & 7);
+      uint8_t* const values = lds + (2 + ODD) * L::BLOCK;
+      if (attn_any_odd<T, L::BLOCK>(values, lane)) {  // (the same in all waves)
+        raise(attn_max32(top) * a.scale_log2);        // (nothing is scaled by 0 afterwards)
+        uint64_t odd = attn_odd_rows<T, L::CPR, BN>(values, lane);
+        while (odd != 0) {
+          const int j = __ffsll((unsigned long long)odd) - 1;
+          odd &= odd - 1;
+          const uint32_t of = __shfl(j >= 32 ? seen[1] : seen[0], l32 + 8 * (j & 4));
+          const bool sees = (of >> (8 * (j >> 3 & 3) + (j & 3))) & 1;
+#pragma unroll
+          for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              float x[4] = {o[d][4 * q], o[d][4 * q + 1], o[d][4 * q + 2], o[d][4 * q + 3]};
+              attn_add_odd<T>(values + j * L::ROW + 16 * ((4 * d + q) ^ swizzle_v<DP>(j)) + 8 * h, sees, x);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) o[d][4 * q + c] = x[c];
+            }
+        }
+        __syncthreads();  // every wave has read them
+        attn_clear_odd<T, L::CPR, BN / WAVES>(values + wave * L::RW * L::ROW, lane);
+        __syncthreads();
+      }
     }
     top = attn_max32(top) * a.scale_log2;
-    if (__any(top > m + ATTN_SLACK)) {
-      const float to = fmaxf(m, top), f = attn_exp2(m - (to == ATTN_NONE ? 0.0f : to));
-      l *= f;
-#pragma unroll
-      for (int d = 0; d < ND; ++d) o[d] *= f;
-      m = to;
-    }
+    if (__any(top > m + ATTN_SLACK)) raise(top);
     const float ref = m == ATTN_NONE ? 0.0f : m, sc = a.scale_log2;
 
     // Step i: matrix instruction i (2 KS of the next block's scores, then 4 ND products, 16 keys after 16 keys), the
@@ -354,10 +409,12 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // (nothing arrives in the LDS of an ended wave)
 
   const float sum = attn_sum32(l);
-  if (!valid) return;
+  const int rr = row_of();
+  if (rr >= rows) return;
   if (a.pieces == 1) {
     const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + qi) * a.o_ts + (int64_t)(head * a.group + qg) * a.o_hs);
+    const int i = attn_query(a, rr), g = rr - i * a.group;
+    uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs);
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
