@@ -482,11 +482,12 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  *
  * workspace: at least w4a4_attention_workspace_bytes(a, cache) bytes, 256-byte aligned, contents overwritten and
  * nothing kept there between calls: calls that may overlap (other streams) take one each, captured graphs that
- * run one after another may share one.  The sizes depend on head_dim, tokens, heads, batch and max_q only.
+ * run one after another may share one.  Its size depends on head_dim, tokens, heads, the cache's heads, batch and
+ * max_q only.
  * Errors: W4A4_ERR_UNSUPPORTED (dtype, head_dim above the maximum), W4A4_ERR_SHAPE (sizes; head_dim % 8;
  * heads % cache heads; strides negative, above 2^40 (a pool's page and
  * token strides: 2^31) or not multiples of 8; out's elements sharing an address;
- * tokens * heads above 2^30; without q_starts, tokens % batch; scale; workspace too small; out == q
+ * tokens * heads or batch above 2^30; without q_starts, tokens % batch; scale; workspace too small; out == q
  * or in the cache's place), W4A4_ERR_NULL, W4A4_ERR_ALIGN.  tokens == 0 or batch == 0 launches nothing. */
 #define W4A4_ATTENTION_MAX_HEAD_DIM 256
 typedef struct {

@@ -100,6 +100,7 @@ def test_attention_validation(lib):
         assert r(scale=scale) == ERR_SHAPE
     assert r(starts=None, T=7) == ERR_SHAPE                               # 7 queries of 2 sequences
     assert r(T=(1 << 28) + 1, qt=256, ot=256) == ERR_SHAPE                # tokens x heads past 2^30
+    assert r(B=(1 << 30) + 1) == ERR_SHAPE and r(scale=3.4e38, lens=P + 1) == ERR_ALIGN
     assert r(T=0, q=None, out=None, lens=None, ws=None) == OK and r(B=0, T=0, lens=None) == OK
     for k in ("q", "out", "lens", "table"):
         assert r(**{k: None}) == ERR_NULL

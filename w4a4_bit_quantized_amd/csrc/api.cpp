@@ -7,6 +7,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <limits>
 #include <utility>
 
 #include "launch.h"
@@ -735,7 +736,7 @@ w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, con
   if (p.dtype != W4A4_DTYPE_BF16 && p.dtype != W4A4_DTYPE_F16) return W4A4_ERR_UNSUPPORTED;
   if (p.head_dim > W4A4_ATTENTION_MAX_HEAD_DIM) return W4A4_ERR_UNSUPPORTED;
   if (p.head_dim < 8 || p.head_dim % 8 != 0) return W4A4_ERR_SHAPE;
-  if (p.tokens < 0 || p.batch < 0 || p.batch > kMaxDim - 1 || p.heads < 1 || p.heads > kMaxHeads || c.heads < 1 ||
+  if (p.tokens < 0 || p.batch < 0 || p.batch > (int64_t)1 << 30 || p.heads < 1 || p.heads > kMaxHeads || c.heads < 1 ||
       p.heads % c.heads != 0 || p.tokens > ((int64_t)1 << 30) / p.heads)
     return W4A4_ERR_SHAPE;
   if (p.table_width < 0 || p.table_width > kMaxDim || p.table_stride < 0 || p.table_stride > (int64_t)1 << 40 ||
@@ -787,7 +788,7 @@ w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, con
   a.page_rows = c.page_size % 16 == 0 && c.k_token_stride <= 1 << 26 && c.v_token_stride <= 1 << 26;
   divisor(c.page_size, a.page_mul, a.page_shift);
   divisor(a.group, a.group_mul, a.group_shift);
-  a.scale_log2 = (float)((double)p.scale * 1.4426950408889634);
+  a.scale_log2 = (float)std::min((double)p.scale * 1.4426950408889634, (double)std::numeric_limits<float>::max());
   a.window = (int)std::min<int64_t>(p.window, kMaxDim);
   a.sinks = (int)std::min<int64_t>(p.sinks, kMaxDim);
   if (tree) {

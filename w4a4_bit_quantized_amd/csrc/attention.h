@@ -322,4 +322,72 @@ constexpr float ATTN_NONE = -__builtin_inff();
 // than this (in powers of two): probabilities up to 2^8 lose nothing, and rescaling becomes rare.
 constexpr float ATTN_SLACK = 8.0f;
 
+// The second kernels' work: joins `pieces` pieces of rows 0 .. rows - 1 of a tile, whose first is row row0 of its sequence
+// and head; piece p lies in slot slot(p) of BM rows.  A row is `split` lines of DP / 4 threads, which take its pieces in
+// turn, four at a time, and whose sums meet in LDS; more rows at once where there are few pieces.  Workgroups (of 256) with
+// other blockIdx.y take other rows.
+template <int DP, int BM, class T, class Slot>
+__device__ __forceinline__ void attn_join(const AttnArgs& a, int pieces, int rows, int row0, int token0, int head,
+                                          Slot slot) {
+  constexpr int PER = DP / 4, LINES = 256 / PER;
+  __shared__ float4_t sums[256];
+  __shared__ float2_t tops[LINES];
+  const int t = threadIdx.x, line = t / PER, e = 4 * (t % PER);
+  int log2_split = 0;
+  while ((1 << log2_split) < LINES && (4 << log2_split) < pieces) ++log2_split;
+  const int split = 1 << log2_split, at_once = LINES >> log2_split, part = line & (split - 1);
+  for (int r0 = blockIdx.y * at_once; r0 < rows; r0 += gridDim.y * at_once) {
+    const int r = r0 + (line >> log2_split), in = min(r, rows - 1);
+    float top = ATTN_NONE, sum = 0.0f;
+    float4_t o = {0, 0, 0, 0};
+    for (int p0 = part; p0 < pieces; p0 += 4 * split) {
+      float2_t st[4];
+      float4_t v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t x = slot(min(p0 + i * split, pieces - 1)) * BM + in;
+        st[i] = *reinterpret_cast<const float2_t*>(a.stats + 2 * x);
+        v[i] = *reinterpret_cast<const float4_t*>(a.part + x * DP + e);
+        if (p0 + i * split >= pieces) st[i] = float2_t{ATTN_NONE, 0.0f};
+      }
+      const float to = fmaxf(fmaxf(fmaxf(st[0][0], st[1][0]), fmaxf(st[2][0], st[3][0])), top);
+      const float ref = to == ATTN_NONE ? 0.0f : to, keep = attn_exp2(top - ref);
+      sum *= keep;
+      o *= keep;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (p0 + i * split >= pieces) continue;  // (not even times 0: a NaN would count twice)
+        const float f = attn_exp2(st[i][0] - ref);
+        sum = fmaf(st[i][1], f, sum);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[i][c], f, o[c]);
+      }
+      top = to;
+    }
+    if (split > 1) {
+      __syncthreads();
+      sums[t] = o;
+      if (e == 0) tops[line] = float2_t{top, sum};
+      __syncthreads();
+      if (part != 0) continue;
+      for (int i = 0; i < split; ++i) top = fmaxf(top, tops[line + i][0]);
+      const float ref = top == ATTN_NONE ? 0.0f : top;
+      sum = 0.0f;
+      o = float4_t{0, 0, 0, 0};
+      for (int i = 0; i < split; ++i) {
+        const float f = attn_exp2(tops[line + i][0] - ref);
+        sum = fmaf(tops[line + i][1], f, sum);
+        const float4_t v = sums[i * PER + t];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], f, o[c]);
+      }
+    }
+    if (r >= rows || e >= a.D) continue;
+    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const int rr = row0 + r, i = attn_query(a, rr), g = rr - i * a.group;
+    uint8_t* dst = a.out + 2 * ((int64_t)(token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs + e);
+    *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{T::pack2(o[0] * f, o[1] * f), T::pack2(o[2] * f, o[3] * f)};
+  }
+}
+
 }  // namespace w4a4

@@ -100,8 +100,8 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
     }
     const int32_t* table = a.table + (int64_t)seq * a.table_stride;
     const int rows = sq.nq * a.group;
-    const int pair = uniform(attn_div(u - before, each));            // head * tiles + tile
-    int u_in = (int)(u - before - (int64_t)pair * each);  // this run's first unit of the triple
+    const int pair = uniform(attn_div(u - before, each));  // head * tiles + tile
+    int u_in = (int)(u - before - (int64_t)pair * each);   // this run's first unit of the triple
     int head = tiles == 1 ? pair : uniform(attn_div(pair, tiles)), tile = pair - head * tiles;
 #pragma unroll 1
     while (u < u1 && head < a.kv_heads) {
@@ -165,15 +165,17 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
       // which the swizzle changes in bits that a load's number sets alone.
       const uint32_t k_row = lane / S::CPR * 2 * a.k_token, v_row = lane / S::CPR * 2 * a.v_token;
       const uint32_t chunk = 16 * ((lane % S::CPR) ^ attn_swizzle<DP>(lane / S::CPR));
-      auto load_row = [&](const uint8_t* from, uint32_t token, uint32_t row, uint8_t* to, int n) {  // (from: of row n RPI & ~15)
-        load16(from + (uint64_t)(n * S::RPI % 16) * 2 * token + ((chunk ^ (16 * attn_swizzle<DP>(n * S::RPI))) + row), to + n * 1024);
+      auto load_row = [&](const uint8_t* from, uint32_t token, uint32_t row, uint8_t* to, int n) {
+        from += (uint64_t)(n * S::RPI % 16) * 2 * token;  // (`from`: of the first of the 16)
+        load16(from + ((chunk ^ (16 * attn_swizzle<DP>(n * S::RPI))) + row), to + n * 1024);
       };
 
       // Pass b works on block b and starts the loads of block b + 2: those of K as soon as this block's
       // scores are formed, those of V at its end, so that one and a half blocks are on their way while the wave
-      // computes and two while it waits.  The pages are loaded two passes ahead of their use, into LDS too: for a register the
-      // compiler would wait by itself, for all loads.  In the order of their issue: pages b + 2, K b, V b, pages b + 3, K b + 1,
-      // V b + 1, pages b + 4, K b + 2, with no K and V past the run; the waits count what may be on its way behind.
+      // computes and two while it waits.  The pages are loaded two passes ahead of their use, into LDS too: for a
+      // register the compiler would wait by itself, for all loads.  In the order of their issue: pages b + 2, K b,
+      // V b, pages b + 3, K b + 1, V b + 1, pages b + 4, K b + 2, with no K and V past the run; the waits count what
+      // may be on its way behind.
       constexpr int NI = S::NI;
       uint32_t here = 0, there = 0, later = 0;  // which keys of blocks b, b + 1, b + 2 are there
       load_pages(b0);
@@ -245,102 +247,101 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
         uint32_t seen[NQ];  // (of a cut block: bit 16 t + i)
         bool cut = false;
         if (work) {
-        if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
-          cut = true;
-          // element (t, i) is key j0 + 4 qd + 16 t + i
-          const uint32_t mine = here >> (4 * qd);
+          if (here != 0xFFFFFFFFu || j0 + KB > low_hi || (j0 < top_lo && j0 + KB > a.sinks)) {
+            cut = true;
+            // element (t, i) is key j0 + 4 qd + 16 t + i
+            const uint32_t mine = here >> (4 * qd);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            uint32_t bits = 0;  // (bit 16 t + i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const int in = 16 * (e >> 2) + (e & 3), j = j0 + 4 * qd + in;
-              bits |= (j < row[n].hi && (j >= row[n].lo || j < a.sinks) ? 1u : 0u) << in;
-            }
-            if (a.mask != nullptr && j0 + KB > sq.ctx && a.mask_width > 0) {
-              const int rr = tile * BM + n * 16 + c16;
-              const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
-              const int node = j0 + 4 * qd - sq.ctx;
-              uint32_t set[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) set[e] = of[min(max(node + 16 * (e >> 2) + (e & 3), 0), a.mask_width - 1)];
-              attn_vm_drain();  // (with one for each, the loop's waits would wait for every load)
-              uint32_t tree = 0, nodes = 0;
+            for (int n = 0; n < NQ; ++n) {
+              uint32_t bits = 0;  // (bit 16 t + i)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
-                const int in = 16 * (e >> 2) + (e & 3);
-                tree |= (set[e] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
-                nodes |= (node + in >= 0 ? 1u : 0u) << in;
+                const int in = 16 * (e >> 2) + (e & 3), j = j0 + 4 * qd + in;
+                bits |= (j < row[n].hi && (j >= row[n].lo || j < a.sinks) ? 1u : 0u) << in;
               }
-              bits = (bits & ~nodes) | (tree & nodes);
+              if (a.mask != nullptr && j0 + KB > sq.ctx && a.mask_width > 0) {
+                const int rr = tile * BM + n * 16 + c16;
+                const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
+                const int node = j0 + 4 * qd - sq.ctx;
+                uint32_t set[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) set[e] = of[min(max(node + 16 * (e >> 2) + (e & 3), 0), a.mask_width - 1)];
+                attn_vm_drain();  // (with one for each, the loop's waits would wait for every load)
+                uint32_t tree = 0, nodes = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  const int in = 16 * (e >> 2) + (e & 3);
+                  tree |= (set[e] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
+                  nodes |= (node + in >= 0 ? 1u : 0u) << in;
+                }
+                bits = (bits & ~nodes) | (tree & nodes);
+              }
+              bits &= mine;
+              seen[n] = bits;
+#pragma unroll
+              for (int e = 0; e < 8; ++e)
+                if (!((bits >> (16 * (e >> 2) + (e & 3))) & 1)) s[n][e >> 2][e & 3] = ATTN_NONE;
             }
-            bits &= mine;
-            seen[n] = bits;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (!((bits >> (16 * (e >> 2) + (e & 3))) & 1)) s[n][e >> 2][e & 3] = ATTN_NONE;
           }
-        }
 
-        typename T::x8 p[NQ];
+          typename T::x8 p[NQ];
 #pragma unroll
-        for (int n = 0; n < NQ; ++n) {
-          float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
-                            fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-          top = attn_max16(attn_max32(top)) * a.scale_log2;
-          if (__any(top > m[n] + ATTN_SLACK)) {
-            const float to = fmaxf(m[n], top), f = attn_exp2(m[n] - (to == ATTN_NONE ? 0.0f : to));
-            l[n] *= f;
+          for (int n = 0; n < NQ; ++n) {
+            float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
+                              fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
+            top = attn_max16(attn_max32(top)) * a.scale_log2;
+            if (__any(top > m[n] + ATTN_SLACK)) {
+              const float to = fmaxf(m[n], top), f = attn_exp2(m[n] - (to == ATTN_NONE ? 0.0f : to));
+              l[n] *= f;
 #pragma unroll
-            for (int d = 0; d < ND; ++d) o[n][d] *= f;
-            m[n] = to;
+              for (int d = 0; d < ND; ++d) o[n][d] *= f;
+              m[n] = to;
+            }
+            const float ref = m[n] == ATTN_NONE ? 0.0f : m[n];
+            float e[8];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e[4 * t + i] = attn_exp2(fmaf(s[n][t][i], a.scale_log2, -ref));
+            l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+            p[n] = __builtin_bit_cast(typename T::x8, u32x4_t{T::pack2(e[0], e[1]), T::pack2(e[2], e[3]),
+                                                             T::pack2(e[4], e[5]), T::pack2(e[6], e[7])});
           }
-          const float ref = m[n] == ATTN_NONE ? 0.0f : m[n];
-          float e[8];
+          if (more) attn_vm_wait<3 * NI + 2>();
+          else if (b + 1 < b1) attn_vm_wait<2 * NI + 2>();
+          else attn_vm_wait<2>();
+          if (cut) {
+            if (attn_any_odd<T, S::HALF>(vs, lane)) {
+              uint32_t odd = (uint32_t)attn_odd_rows<T, S::CPR, KB>(vs, lane);
+              while (odd != 0) {
+                const int j = __ffs(odd) - 1;
+                odd &= odd - 1;
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+                for (int n = 0; n < NQ; ++n) {
+                  const bool sees = (__shfl(seen[n], c16 + 16 * ((j >> 2) & 3)) >> (16 * (j >> 4) + (j & 3))) & 1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[4 * t + i] = attn_exp2(fmaf(s[n][t][i], a.scale_log2, -ref));
-          l[n] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-          p[n] = __builtin_bit_cast(typename T::x8, u32x4_t{T::pack2(e[0], e[1]), T::pack2(e[2], e[3]),
-                                                           T::pack2(e[4], e[5]), T::pack2(e[6], e[7])});
-        }
-        if (more) attn_vm_wait<3 * NI + 2>();
-        else if (b + 1 < b1) attn_vm_wait<2 * NI + 2>();
-        else attn_vm_wait<2>();
-        if (cut) {
-          if (attn_any_odd<T, S::HALF>(vs, lane)) {
-            uint32_t odd = (uint32_t)attn_odd_rows<T, S::CPR, KB>(vs, lane);
-            while (odd != 0) {
-              const int j = __ffs(odd) - 1;
-              odd &= odd - 1;
-#pragma unroll
-              for (int n = 0; n < NQ; ++n) {
-                const bool sees = (__shfl(seen[n], c16 + 16 * ((j >> 2) & 3)) >> (16 * (j >> 4) + (j & 3))) & 1;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                  const uint8_t* at = vs + j * S::ROW + 16 * ((2 * d + (qd >> 1)) ^ attn_swizzle<DP>(j)) + 8 * (qd & 1);
-                  float x[4] = {o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]};
-                  attn_add_odd<T>(at, sees, x);
-                  o[n][d] = float4_t{x[0], x[1], x[2], x[3]};
+                  for (int d = 0; d < ND; ++d) {
+                    const uint8_t* at = vs + j * S::ROW + 16 * ((2 * d + (qd >> 1)) ^ attn_swizzle<DP>(j)) + 8 * (qd & 1);
+                    float x[4] = {o[n][d][0], o[n][d][1], o[n][d][2], o[n][d][3]};
+                    attn_add_odd<T>(at, sees, x);
+                    o[n][d] = float4_t{x[0], x[1], x[2], x[3]};
+                  }
                 }
               }
+              wave_lds_sync();
+              attn_clear_odd<T, S::CPR, KB>(stage + S::HALF, lane);
+              wave_lds_sync();
             }
-            wave_lds_sync();
-            attn_clear_odd<T, S::CPR, KB>(stage + S::HALF, lane);
-            wave_lds_sync();
           }
-        }
-      
 #pragma unroll
-        for (int d = 0; d < ND; ++d) {
-          const int r0 = 4 * qd + (c16 >> 2), r1 = r0 + 16, ch = 2 * d + ((c16 & 3) >> 1), half = 8 * (c16 & 1);
-          const auto vf = attn_read_vt<T>(vs + r0 * S::ROW + 16 * (ch ^ attn_swizzle<DP>(r0)) + half,
-                                          vs + r1 * S::ROW + 16 * (ch ^ attn_swizzle<DP>(r1)) + half);
+          for (int d = 0; d < ND; ++d) {
+            const int r0 = 4 * qd + (c16 >> 2), r1 = r0 + 16, ch = 2 * d + ((c16 & 3) >> 1), half = 8 * (c16 & 1);
+            const auto vf = attn_read_vt<T>(vs + r0 * S::ROW + 16 * (ch ^ attn_swizzle<DP>(r0)) + half,
+                                            vs + r1 * S::ROW + 16 * (ch ^ attn_swizzle<DP>(r1)) + half);
 #pragma unroll
-          for (int n = 0; n < NQ; ++n) o[n][d] = T::mma16(vf, p[n], o[n][d]);
-        }
-        wave_lds_sync();  // (the stage is read)
+            for (int n = 0; n < NQ; ++n) o[n][d] = T::mma16(vf, p[n], o[n][d]);
+          }
+          wave_lds_sync();  // (the stage is read)
         }
         if (more) {
           if (v0 != nullptr) {
@@ -363,7 +364,8 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
       for (int n = 0; n < NQ; ++n) sum[n] = attn_sum16(attn_sum32(l[n]));
       // finished, or a piece: the first of a triple in slot 1 of the wave, any other in slot 0
-      if (first && !whole && lane == 0) {  // pieces, sequence's first row of q, rows of the tile and the first of them, head
+      if (first && !whole && lane == 0) {
+        // pieces, the sequence's first row of q, rows of the tile and the first of them, head
         const int pieces = 1 + (run >= each ? 1 : attn_div(each - u_end + run - 1, (int)run));
         *reinterpret_cast<int4*>(a.desc + 8 * w) = int4{pieces, sq.token0, min(BM, rows - tile * BM), tile * BM};
         a.desc[8 * w + 4] = head;
@@ -400,71 +402,14 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
   attn_vm_drain();  // (nothing arrives in the LDS of an ended wave)
 }
 
-// Joins the pieces of the triple that starts in run blockIdx.x and is cut, every gridDim.y-th row of it: lines of DP / 4
-// threads take the row's pieces in turn, four at a time, and their sums meet in LDS.
+// Joins the pieces of the triple that starts in run blockIdx.x and is cut.
 template <int DP, int BM, class T>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-  constexpr int PER = DP / 4, LINES = 256 / PER;
-  __shared__ float4_t sums[256];
-  __shared__ float2_t tops[LINES];
-  const int w = blockIdx.x, t = threadIdx.x, line = t / PER, e = 4 * (t % PER);
+  const int w = blockIdx.x;
   const int4 d = *reinterpret_cast<const int4*>(a.desc + 8 * w);
   const int head = a.desc[8 * w + 4];
   if (d.x == 0) return;
-  for (int r = blockIdx.y; r < d.z; r += gridDim.y) {
-    // piece p of row r
-    auto at = [&](int p) { return (p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p)) * BM + r; };
-    float top = ATTN_NONE, sum = 0.0f;
-    float4_t o = {0, 0, 0, 0};
-    for (int p0 = line; p0 < d.x; p0 += 4 * LINES) {
-      float2_t st[4];
-      float4_t v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t x = at(min(p0 + i * LINES, d.x - 1));
-        st[i] = *reinterpret_cast<const float2_t*>(a.stats + 2 * x);
-        v[i] = *reinterpret_cast<const float4_t*>(a.part + x * DP + e);
-        if (p0 + i * LINES >= d.x) st[i] = float2_t{ATTN_NONE, 0.0f};
-      }
-      const float to = fmaxf(fmaxf(fmaxf(st[0][0], st[1][0]), fmaxf(st[2][0], st[3][0])), top);
-      const float ref = to == ATTN_NONE ? 0.0f : to, keep = attn_exp2(top - ref);
-      sum *= keep;
-      o *= keep;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (p0 + i * LINES >= d.x) continue;  // (not even times 0: a NaN would count twice)
-        const float f = attn_exp2(st[i][0] - ref);
-        sum = fmaf(st[i][1], f, sum);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[i][c], f, o[c]);
-      }
-      top = to;
-    }
-    __syncthreads();
-    sums[t] = o;
-    if (e == 0) tops[line] = float2_t{top, sum};
-    __syncthreads();
-    if (line == 0 && e < a.D) {
-      top = ATTN_NONE;
-#pragma unroll
-      for (int i = 0; i < LINES; ++i) top = fmaxf(top, tops[i][0]);
-      const float ref = top == ATTN_NONE ? 0.0f : top;
-      sum = 0.0f;
-      o = float4_t{0, 0, 0, 0};
-#pragma unroll
-      for (int i = 0; i < LINES; ++i) {
-        const float f = attn_exp2(tops[i][0] - ref);
-        sum = fmaf(tops[i][1], f, sum);
-        const float4_t v = sums[i * PER + t];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], f, o[c]);
-      }
-      const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-      const int rr = d.w + r, i = attn_query(a, rr), g = rr - i * a.group;
-      uint8_t* dst = a.out + 2 * ((int64_t)(d.y + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs + e);
-      *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{T::pack2(o[0] * f, o[1] * f), T::pack2(o[2] * f, o[3] * f)};
-    }
-  }
+  attn_join<DP, BM, T>(a, d.x, d.z, d.w, d.y, head, [&](int p) { return p == 0 ? 2 * (int64_t)w + 1 : 2 * (int64_t)(w + p); });
 }
 
 // Waves of a launch: as many as the GPU's 256 CUs hold by their LDS.
@@ -482,7 +427,7 @@ hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
   else attn_stream_kernel<DP, false, NQ, T><<<W, 64, 0, st>>>(a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  attn_join_kernel<DP, BM, T><<<dim3(W, 8), 256, 0, st>>>(a);
+  attn_join_kernel<DP, BM, T><<<dim3(W, 8 * NQ), 256, 0, st>>>(a);
   return hipGetLastError();
 }
 
@@ -501,32 +446,37 @@ hipError_t run_dim(const AttnArgs& a, int64_t rows, void* workspace, hipStream_t
 
 }  // namespace
 
-// Sequences of at most this many rows are streamed; longer ones go to the tiles.
+// Sequences of at most this many rows are streamed; longer ones go to the tiles.  (One batch of each kind, us:
+// 16 sequences of 4096 keys, 8 heads: 32 rows 61 streamed, 77 in tiles; 48 rows 112 and 78.  With few (sequence, head) pairs
+// the tiles are faster from 17 rows on, as they cut them into fewer pieces: one sequence, 32 rows: 27 and 19; two: 31 and 25;
+// four: 35 and 38.)
 constexpr int STREAM_ROWS = 32;
+static int stream_rows(const AttnArgs& a) { return (int64_t)a.batch * a.kv_heads <= 16 ? 16 : STREAM_ROWS; }
 
 size_t attention_workspace_bytes(const AttnArgs& a, int64_t max_q) {
   const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
   const size_t W = 1 << log2_waves(DP), BM = STREAM_ROWS;
   const size_t stream = W * 32 + 2 * W * BM * 8 + 2 * W * BM * DP * 4;
-  return max_q * a.group <= STREAM_ROWS ? stream : std::max(stream, attention_tile_bytes(a));
+  return max_q * a.group <= stream_rows(a) ? stream : std::max(stream, attention_tile_bytes(a, max_q));
 }
 
 hipError_t launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream) {
   a.rows_from = 0;
   a.rows_to = 0x7FFFFFFF;
-  const int64_t rows = max_q * a.group;
-  if (rows > STREAM_ROWS) {
+  int64_t rows = max_q * a.group;
+  const int few = stream_rows(a);
+  if (rows > few) {
     // Of a batch whose sequences have half of max_q queries on average, the tiles take the short ones too; in one of
-    // prompts among single tokens, the second launch is worth its time (a few us).
+    // prompts among single tokens, the second launch is worth its time (4096 keys each, us: 512 queries and 63
+    // sequences of one 241, 265 by the tiles alone; 12 sequences of 64 and 4 of 4 90, 111 by both).
     const bool all = (int64_t)a.batch * max_q <= 2 * (int64_t)a.tokens;
-    if (!all) a.rows_from = STREAM_ROWS;
-    hipError_t e = launch_attention_tile(a, dtype, workspace, stream);
+    if (!all) a.rows_from = few;
+    hipError_t e = launch_attention_tile(a, dtype, max_q, workspace, stream);
     if (e != hipSuccess || all) return e;
     a.rows_from = 0;
-    a.rows_to = STREAM_ROWS;
+    a.rows_to = rows = few;
   }
-  return dtype == 0 ? run_dim<Bf16>(a, std::min<int64_t>(rows, STREAM_ROWS), workspace, stream)
-                    : run_dim<F16>(a, std::min<int64_t>(rows, STREAM_ROWS), workspace, stream);
+  return dtype == 0 ? run_dim<Bf16>(a, rows, workspace, stream) : run_dim<F16>(a, rows, workspace, stream);
 }
 
 }  // namespace w4a4

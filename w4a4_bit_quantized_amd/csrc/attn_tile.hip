@@ -68,6 +68,16 @@ __device__ __forceinline__ TileOf tile_at(const AttnArgs& a, int slot) {
   return {lo, slot - first(lo)};
 }
 
+template <int BM>
+__device__ __forceinline__ AttnSpan span_of(const AttnArgs& a, const AttnSeq& sq, int row0, int rows) {
+  const int i0 = attn_query(a, row0), i1 = attn_query(a, min(row0 + BM, rows) - 1);
+  return attn_span<BN>(a, sq, i0, a.mask != nullptr ? sq.len : min(sq.len, sq.ctx + i1 + 1));
+}
+// Into how many of the at most a.pieces a tile is cut (a.piece_gain: see the launcher).
+__device__ __forceinline__ int pieces_of(const AttnArgs& a, const AttnSpan& sp) {
+  return max(min(min(a.pieces, sp.blocks / 2), (int)sqrtf((float)sp.blocks * a.piece_gain)), 1);
+}
+
 template <int DP, bool EXACT, int WAVES, class T>
 __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kernel(const AttnArgs a, const int slots) {
   using L = Tile<DP, WAVES>;
@@ -83,9 +93,10 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   const AttnSeq sq = attn_seq(a, at.seq);
   const int rows = sq.nq * a.group, row0 = at.tile * BM;
   if (at.tile < 0 || row0 >= rows || rows <= a.rows_from || rows > a.rows_to) return;
-  const int i0 = attn_query(a, row0), i1 = attn_query(a, min(row0 + BM, rows) - 1);
-  const AttnSpan sp = attn_span<BN>(a, sq, i0, a.mask != nullptr ? sq.len : min(sq.len, sq.ctx + i1 + 1));
-  const int b0 = (int)((int64_t)sp.blocks * piece / a.pieces), b1 = (int)((int64_t)sp.blocks * (piece + 1) / a.pieces);
+  const AttnSpan sp = span_of<BM>(a, sq, row0, rows);
+  const int pieces = pieces_of(a, sp);
+  if (piece >= pieces) return;
+  const int b0 = (int)((int64_t)sp.blocks * piece / pieces), b1 = (int)((int64_t)sp.blocks * (piece + 1) / pieces);
   const int32_t* table = a.table + (int64_t)at.seq * a.table_stride;
   const uint8_t* kh = a.k + 2 * (head * a.k_head);
   const uint8_t* vh = a.v + 2 * (head * a.v_head);
@@ -184,7 +195,8 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
     uint8_t* to = lds + odd * L::BLOCK + wave * L::RW * L::ROW;
     const uint8_t* from[L::NI];  // (all read before the first load: the compiler keeps their order)
 #pragma unroll
-    for (int n = 0; n < L::NI; ++n) from[n] = *reinterpret_cast<const uint8_t**>(places + (n * L::RPI + l / L::CPR) * 8);
+    for (int n = 0; n < L::NI; ++n)
+      from[n] = *reinterpret_cast<const uint8_t**>(places + (n * L::RPI + l / L::CPR) * 8);
 #pragma unroll
     for (int n = 0; n < L::NI; ++n) {
       const int r = n * L::RPI + l / L::CPR;
@@ -411,7 +423,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   const float sum = attn_sum32(l);
   const int rr = row_of();
   if (rr >= rows) return;
-  if (a.pieces == 1) {
+  if (pieces == 1) {
     const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
     const int i = attn_query(a, rr), g = rr - i * a.group;
     uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs);
@@ -436,92 +448,77 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
   }
 }
 
-// Joins the pieces of a tile: a thread takes 4 columns of a row.
+// Joins the pieces of a tile.
 template <int DP, int BM, class T>
 __global__ __launch_bounds__(256) void attn_tile_join_kernel(const AttnArgs a, const int slots) {
-  constexpr int PER = DP / 4;
   const int head = blockIdx.x % a.kv_heads, slot = blockIdx.x / a.kv_heads;
   const TileOf at = tile_at<BM>(a, slot);
   const AttnSeq sq = attn_seq(a, at.seq);
   const int rows = sq.nq * a.group, row0 = at.tile * BM;
   if (at.tile < 0 || row0 >= rows || rows <= a.rows_from || rows > a.rows_to) return;
-  const int e = 4 * (threadIdx.x % PER);
-  if (e >= a.D) return;
-  for (int r = blockIdx.y * (256 / PER) + threadIdx.x / PER; r < min(BM, rows - row0); r += gridDim.y * (256 / PER)) {
-    const int64_t first = ((int64_t)slot * a.kv_heads + head) * a.pieces * BM + r;
-    float top = ATTN_NONE, sum = 0.0f;
-    float4_t o = {0, 0, 0, 0};
-    for (int p = 0; p < a.pieces; ++p) top = fmaxf(top, a.stats[2 * (first + (int64_t)p * BM)]);
-    const float ref = top == ATTN_NONE ? 0.0f : top;
-#pragma unroll 4
-    for (int p = 0; p < a.pieces; ++p) {
-      const int64_t x = first + (int64_t)p * BM;
-      const float2_t st = *reinterpret_cast<const float2_t*>(a.stats + 2 * x);
-      const float4_t v = *reinterpret_cast<const float4_t*>(a.part + x * DP + e);
-      const float f = attn_exp2(st[0] - ref);
-      sum = fmaf(st[1], f, sum);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) o[c] = fmaf(v[c], f, o[c]);
-    }
-    const float f = sum == 0.0f ? 0.0f : 1.0f / sum;
-    const int rr = row0 + r, i = attn_query(a, rr), g = rr - i * a.group;
-    uint8_t* dst = a.out + 2 * ((int64_t)(sq.token0 + i) * a.o_ts + (int64_t)(head * a.group + g) * a.o_hs + e);
-    *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{T::pack2(o[0] * f, o[1] * f), T::pack2(o[2] * f, o[3] * f)};
-  }
+  const int pieces = pieces_of(a, span_of<BM>(a, sq, row0, rows));
+  if (pieces == 1) return;
+  const int64_t first = ((int64_t)slot * a.kv_heads + head) * a.pieces;
+  attn_join<DP, BM, T>(a, pieces, min(BM, rows - row0), row0, sq.token0, head, [&](int p) { return first + p; });
 }
 
 // The tiles of a call: rows of one, how many slots they take (see tile_at; without `starts`, sequence by sequence,
-// they take no more), and into how many pieces each tile's keys are cut.
+// they take no more), and into how many pieces each tile's keys are cut at most: so many that all tiles' pieces are
+// about the 512 workgroups that the GPU holds (sequences' last tiles are half full on average).
 struct TilePlan {
   int rows;
   int64_t slots;
   int pieces;
 };
-TilePlan plan(const AttnArgs& a) {
+TilePlan plan(const AttnArgs& a, int64_t max_q) {
   TilePlan p;
   p.rows = 128;
-  const int64_t rows = (int64_t)a.tokens * a.group;
+  const int64_t rows = (int64_t)a.tokens * a.group, sequences = (a.tokens + max_q - 1) / max_q;
   p.slots = rows / p.rows + a.batch;
-  const int64_t tiles = std::max<int64_t>(1, rows / p.rows) * a.kv_heads;
-  p.pieces = (int)std::min<int64_t>(16, std::max<int64_t>(1, 512 / tiles));
+  const int64_t wgs = (rows / p.rows + (sequences + 1) / 2) * a.kv_heads;
+  p.pieces = (int)std::min<int64_t>(32, std::max<int64_t>(1, (512 + wgs / 2) / wgs));
   return p;
 }
 
 template <int DP, int WAVES, class T>
-hipError_t run(AttnArgs a, void* workspace, hipStream_t st) {
+hipError_t run(AttnArgs a, int64_t max_q, void* workspace, hipStream_t st) {
   using L = Tile<DP, WAVES>;
-  const TilePlan p = plan(a);
+  const TilePlan p = plan(a, max_q);
   if (p.rows != L::BM) return hipErrorInvalidValue;
   const int64_t wgs = p.slots * a.kv_heads * p.pieces;
   if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
   a.pieces = p.pieces;
+  // p pieces take blocks / p passes of about 1 us, and write and read p tokens heads DP floats (twice 0.1 us per 1000 rows of
+  // 128 and piece): least for p = sqrt(blocks 5000 / (tokens heads)).
+  a.piece_gain = 5000.0f / ((float)a.tokens * (float)a.heads);
   a.stats = static_cast<float*>(workspace);
   a.part = a.stats + (size_t)wgs * L::BM * 2;
   if (a.D == DP) attn_tile_kernel<DP, true, WAVES, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
   else attn_tile_kernel<DP, false, WAVES, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.pieces == 1) return e;
-  attn_tile_join_kernel<DP, L::BM, T><<<dim3((unsigned)(p.slots * a.kv_heads), 8), 256, 0, st>>>(a, (int)p.slots);
+  const int64_t tiles = p.slots * a.kv_heads, shares = std::min<int64_t>(64, std::max<int64_t>(8, 4096 / tiles));
+  attn_tile_join_kernel<DP, L::BM, T><<<dim3((unsigned)tiles, (unsigned)shares), 256, 0, st>>>(a, (int)p.slots);
   return hipGetLastError();
 }
 
 template <class T>
-hipError_t run_dim(const AttnArgs& a, void* workspace, hipStream_t st) {
-  if (a.D <= 64) return run<64, 4, T>(a, workspace, st);
-  if (a.D <= 128) return run<128, 4, T>(a, workspace, st);
-  return run<256, 4, T>(a, workspace, st);
+hipError_t run_dim(const AttnArgs& a, int64_t max_q, void* workspace, hipStream_t st) {
+  if (a.D <= 64) return run<64, 4, T>(a, max_q, workspace, st);
+  if (a.D <= 128) return run<128, 4, T>(a, max_q, workspace, st);
+  return run<256, 4, T>(a, max_q, workspace, st);
 }
 
 }  // namespace
 
-size_t attention_tile_bytes(const AttnArgs& a) {
+size_t attention_tile_bytes(const AttnArgs& a, int64_t max_q) {
   const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
-  const TilePlan p = plan(a);
+  const TilePlan p = plan(a, max_q);
   return p.pieces == 1 ? 0 : (size_t)p.slots * a.kv_heads * p.pieces * p.rows * (2 + DP) * sizeof(float);
 }
 
-hipError_t launch_attention_tile(const AttnArgs& a, int dtype, void* workspace, hipStream_t stream) {
-  return dtype == 0 ? run_dim<Bf16>(a, workspace, stream) : run_dim<F16>(a, workspace, stream);
+hipError_t launch_attention_tile(const AttnArgs& a, int dtype, int64_t max_q, void* workspace, hipStream_t stream) {
+  return dtype == 0 ? run_dim<Bf16>(a, max_q, workspace, stream) : run_dim<F16>(a, max_q, workspace, stream);
 }
 
 }  // namespace w4a4

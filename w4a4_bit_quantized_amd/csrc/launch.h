@@ -160,6 +160,7 @@ struct AttnArgs {
   int window, sinks;
   // set by the launcher: sequences of more than rows_from and at most rows_to rows are this launch's
   int rows_from, rows_to, least, log2_waves, pieces;
+  float piece_gain;
   int32_t* desc;
   float *stats, *part;
 };
@@ -168,8 +169,8 @@ size_t W4A4_KERNELS attention_workspace_bytes(const AttnArgs& a, int64_t max_q);
 hipError_t W4A4_KERNELS launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream);
 
 // Its kernel for many rows per sequence (called by launch_attention).
-size_t attention_tile_bytes(const AttnArgs& a);
-hipError_t launch_attention_tile(const AttnArgs& a, int dtype, void* workspace, hipStream_t stream);
+size_t attention_tile_bytes(const AttnArgs& a, int64_t max_q);
+hipError_t launch_attention_tile(const AttnArgs& a, int dtype, int64_t max_q, void* workspace, hipStream_t stream);
 
 // Device address of the static workspace of svdq_linear_noalloc on the current device (looked up
 // once per device), or NULL when the lookup fails.
