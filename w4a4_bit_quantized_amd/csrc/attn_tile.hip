@@ -1,9 +1,19 @@
 // Attention of many query rows per sequence over a paged cache (gfx950): prompts, pieces of prompts, large trees.
 //
-// Bound: the matrix cores.  A workgroup of WAVES waves owns a tile of WAVES NQ 32 rows of one (sequence, key / value
-// head) pair and walks its keys in blocks of 64, which all waves share in LDS (direct loads, S stages, one barrier
-// per block).  Each wave keeps its rows' queries, maxima, sums and outputs in registers.  With few tiles, each tile's
-// blocks are cut into `pieces` equal runs, one per workgroup, whose results a second kernel joins.
+// A workgroup of four waves owns a tile of 128 rows of one (sequence, key / value head) pair and walks its keys in
+// blocks of 64, which all waves share in LDS (direct loads, two stages each of keys and values, one barrier per block).
+// Each wave keeps its 32 rows' queries, maxima, sums and outputs in registers; the scores of the next block are formed
+// between the exponentials of this one and its product with the values.  With few tiles, each tile's blocks are
+// cut into equal pieces, one per workgroup, whose results a second kernel joins.
+//
+// Bound: the matrix cores, and next to them the LDS.  A block's operands are read from LDS by each wave: a wave of 32 rows
+// reads 2 BN DP 2 bytes for its 4 BN 32 DP flops, so that LDS reads and direct loads together take about as long as the matrix
+// instructions.  One prompt of 8192 tokens, 32 heads of 128 over 8: 545 to 590 us, 0.93 to 1.0 PFLOP/s of the 1.47 that a
+// large library product reaches; with the loads of keys and values left out 436, with the LDS reads left out 331, the matrix
+// instructions alone 275 to 302.  64 rows per wave (half the LDS reads) need more registers than there are; tiles of eight
+// waves measured 588 against 594; one after the other instead of stepped, 590 against 562.  Heads of 64 have half the
+// products for the same exponentials: four prompts of 1000 to 4001 tokens in a window of 1024 take 78 to 90 us (three
+// workgroups on a CU instead of two, with 21 registers spilled: 101).
 //
 // v_mfma_f32_32x32x16: lane l holds row l % 32 of 32, keys 8 (i / 4) + 4 (l / 32) + i % 4 of 32.
 #include "attention.h"
@@ -464,7 +474,9 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(const AttnArgs a, c
 
 // The tiles of a call: rows of one, how many slots they take (see tile_at; without `starts`, sequence by sequence,
 // they take no more), and into how many pieces each tile's keys are cut at most: so many that all tiles' pieces are
-// about the 512 workgroups that the GPU holds (sequences' last tiles are half full on average).
+// about the workgroups that the GPU holds (sequences' last tiles are half full on average).  512 queries of 32 heads
+// over 8 and 16384 keys, us: 160 with 512 workgroups, 195 with 256, 173 with 1024; heads of 256 dimensions, one workgroup per CU:
+// 170 with 256, 186 with 512.  At most 32 (16 queries, 32768 keys: 60 with 16, 47 with 32, 51 with 64).
 struct TilePlan {
   int rows;
   int64_t slots;
@@ -475,8 +487,8 @@ TilePlan plan(const AttnArgs& a, int64_t max_q) {
   p.rows = 128;
   const int64_t rows = (int64_t)a.tokens * a.group, sequences = (a.tokens + max_q - 1) / max_q;
   p.slots = rows / p.rows + a.batch;
-  const int64_t wgs = (rows / p.rows + (sequences + 1) / 2) * a.kv_heads;
-  p.pieces = (int)std::min<int64_t>(32, std::max<int64_t>(1, (512 + wgs / 2) / wgs));
+  const int64_t wgs = (rows / p.rows + (sequences + 1) / 2) * a.kv_heads, resident = a.D <= 128 ? 512 : 256;
+  p.pieces = (int)std::min<int64_t>(32, std::max<int64_t>(1, (resident + wgs / 2) / wgs));
   return p;
 }
 
@@ -489,7 +501,8 @@ hipError_t run(AttnArgs a, int64_t max_q, void* workspace, hipStream_t st) {
   if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
   a.pieces = p.pieces;
   // p pieces take blocks / p passes of about 1 us, and write and read p tokens heads DP floats (twice 0.1 us per 1000 rows of
-  // 128 and piece): least for p = sqrt(blocks 5000 / (tokens heads)).
+  // 128 and piece): least for p = sqrt(blocks 5000 / (tokens heads)).  (32 heads, us: 64 queries and 8192 keys 36, 49 with all
+  // 32 pieces; 16 queries and 8192 keys 22 and 31; 16 and 32768 39 and 47)
   a.piece_gain = 5000.0f / ((float)a.tokens * (float)a.heads);
   a.stats = static_cast<float*>(workspace);
   a.part = a.stats + (size_t)wgs * L::BM * 2;
@@ -497,6 +510,7 @@ hipError_t run(AttnArgs a, int64_t max_q, void* workspace, hipStream_t st) {
   else attn_tile_kernel<DP, false, WAVES, T><<<(unsigned)wgs, 64 * WAVES, L::LDS, st>>>(a, (int)p.slots);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.pieces == 1) return e;
+  // (16 trees of 33 to 64 tokens: 161 us with 64 shares of 41 x 8 tiles, 142 with 12)
   const int64_t tiles = p.slots * a.kv_heads, shares = std::min<int64_t>(64, std::max<int64_t>(8, 4096 / tiles));
   attn_tile_join_kernel<DP, L::BM, T><<<dim3((unsigned)tiles, (unsigned)shares), 256, 0, st>>>(a, (int)p.slots);
   return hipGetLastError();
