@@ -8,7 +8,7 @@
 //
 // Bound: the matrix cores, and next to them the LDS.  A block's operands are read from LDS by each wave: a wave of 32 rows
 // reads 2 BN DP 2 bytes for its 4 BN 32 DP flops, so that LDS reads and direct loads together take about as long as the matrix
-// instructions.  One prompt of 8192 tokens, 32 heads of 128 over 8: 545 to 590 us, 0.93 to 1.0 PFLOP/s of the 1.47 that a
+// instructions.  One prompt of 8192 tokens, 32 heads of 128 over 8: 545 to 605 us, 0.91 to 1.0 PFLOP/s of the 1.47 that a
 // large library product reaches; with the loads of keys and values left out 436, with the LDS reads left out 331, the matrix
 // instructions alone 275 to 302.  64 rows per wave (half the LDS reads) need more registers than there are; tiles of eight
 // waves measured 588 against 594; one after the other instead of stepped, 590 against 562.  Heads of 64 have half the
