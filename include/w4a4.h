@@ -472,13 +472,15 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  *   head_dim    a multiple of 8, 8 .. W4A4_ATTENTION_MAX_HEAD_DIM; dtype W4A4_DTYPE_BF16 or _F16, of q, the
  *               cache and out alike
  *   q, out, k, v  16-byte aligned, with strides that are multiples of 8 elements
- *   tree_mask   [tokens, mask_width] bytes, row t at + t mask_stride
+ *   tree_mask   [tokens, mask_width] bytes, row t at + t mask_stride; NULL is allowed with mask_width 0
  *   positions   [tokens] int32, read with a window only
  * Keys and values that nobody sees are not read into the sums: what they hold (a page's end behind the last
  * token, pages that the window has left) does not matter.  Scores, softmax statistics and sums are float32; the probabilities are
  * rounded to dtype for the second product.  A row whose scores are all -infinity gives zeros; a NaN or +infinity
  * among them gives NaN.  Results do not depend on the stream's other work or on earlier calls, and two calls on the
  * same data give the same bits; those of one sequence may depend, in the order of their sums, on the batch it is in.
+ *
+ * out shares no element with q, the cache, the arrays or the workspace.
  *
  * workspace: at least w4a4_attention_workspace_bytes(a, cache) bytes, 256-byte aligned, contents overwritten and
  * nothing kept there between calls: calls that may overlap (other streams) take one each, captured graphs that

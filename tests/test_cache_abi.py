@@ -129,7 +129,7 @@ def test_attention_strides(lib):
 def test_tree_validation(lib):
     r = lambda mask=P, ms=8, mw=3, pos=P, **kw: attention(lib, tree=(mask, ms, mw, pos), **kw)
     assert r(ms=-1) == ERR_SHAPE and r(mw=-1) == ERR_SHAPE and r(ms=1 << 41) == ERR_SHAPE
-    assert r(mask=None) == ERR_NULL and r(pos=None, window=4) == ERR_NULL
+    assert r(mask=None) == ERR_NULL and r(pos=None, window=4) == ERR_NULL and r(mask=None, mw=0, lens=P + 1) == ERR_ALIGN
     assert r(pos=P + 2, window=4) == ERR_ALIGN and r(pos=None, lens=P + 1) == ERR_ALIGN
 
 

@@ -444,6 +444,19 @@ def test_serving_steps(w4):
         assert (np.abs(f(o) - res[0]) <= limit(res, "bf16", D, max(done))).all() and torch.isfinite(y).all()
 
 
+@pytest.mark.parametrize("n", [3, 40])
+def test_mask_of_no_columns(w4, n):
+    """No drafted token sees another: only the keys before the tree, none of a sequence that has none; numbers past 64 bits."""
+    import torch
+    b = Batch(19, [(n, 150), (n, n), (n - 1, 70)], 4, 2, 64, 16, "bf16")
+    m = np.zeros((b.T, 0), np.uint8)
+    b.check(b.run_tree(w4, m, np.zeros(b.T, np.int32)), "no columns", mask=m)
+    assert torch.equal(b.run(w4, max_q=2 ** 80), b.run(w4, max_q=b.T))
+    for bad in (dict(window=2 ** 64 + 5), dict(window=9, sinks=2 ** 63)):
+        with pytest.raises(ValueError, match="out of range"):
+            b.run(w4, **bad)
+
+
 def test_refusals(w4):
     import torch
     b = Batch(18, [(1, 20), (2, 9)], 4, 2, 64, 16, "bf16")

@@ -1021,6 +1021,8 @@ def _attention(name, q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, 
             raise ValueError(f"max_q = {max_q}, but every sequence has {most} queries")
     if most < 0:
         raise ValueError(f"max_q = {max_q} is negative")
+    if max(window, sinks) >= 2 ** 63:  # (ctypes would drop the upper bits)
+        raise ValueError(f"window = {window} or sinks = {sinks} is out of range")
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         ots, ohs = H * D, D
@@ -1029,7 +1031,7 @@ def _attention(name, q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, 
             raise ValueError("out must match q in shape, dtype and device")
         _, _, _, ots, ohs = _heads_view(out, "out")
     a = Attention(q.data_ptr(), ts, hs, out.data_ptr(), ots, ohs, T, H, page_table.data_ptr(), page_table.stride(0), width,
-                  kv_lens.data_ptr(), _addr(q_starts), B, most, window, sinks, D ** -0.5 if scale is None else scale, D, code)
+                  kv_lens.data_ptr(), _addr(q_starts), B, min(most, T), window, sinks, D ** -0.5 if scale is None else scale, D, code)
     ra, rc = ctypes.byref(a), ctypes.byref(cache)
     need = lib.w4a4_attention_workspace_bytes(ra, rc)
     if workspace is None:
@@ -1067,7 +1069,7 @@ def attention_workspace_bytes(q, k_cache, v_cache, batch, max_q=None):
     """Bytes of workspace of ``paged_attention`` and ``tree_attention`` for q and a cache of these shapes."""
     T, H, D, ts, hs = _heads_view(q, "q")
     cache, _ = _kv_cache(k_cache, v_cache, q.dtype, q.device)
-    a = Attention(None, ts, hs, None, H * D, D, T, H, None, 0, 0, None, 1, batch, T if max_q is None else max_q, 0, 0, 1.0, D,
+    a = Attention(None, ts, hs, None, H * D, D, T, H, None, 0, 0, None, 1, batch, T if max_q is None else min(max_q, T), 0, 0, 1.0, D,
                   _dtype_code(q.dtype, "q"))
     return int(load_library().w4a4_attention_workspace_bytes(ctypes.byref(a), ctypes.byref(cache)))
 
@@ -1085,7 +1087,7 @@ def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max
     T / B.  max_q: at least the largest number of queries of a sequence (default T); it chooses the kernel.  scale
     defaults to D ** -0.5.  window 0 is none.  Rows that see no key, and sequences without keys, give zeros; rows of
     no sequence are not written.  ``workspace`` (u8, attention_workspace_bytes) and ``out`` may be passed to avoid
-    allocation; calls that may overlap take a workspace each."""
+    allocation; calls that may overlap take a workspace each, and out shares no element with the inputs."""
     return _attention("w4a4_paged_attention", q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, scale, window,
                       sinks, workspace, out, None)
 

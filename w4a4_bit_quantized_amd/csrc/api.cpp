@@ -809,7 +809,8 @@ w4a4_status attention(const w4a4_attention* p, const w4a4_kv_cache* c, const Tre
   const bool keys = c->pages > 0 && a.max_len > 0;
   // out would be written while other workgroups read q or the cache
   if (p->out && (p->out == p->q || (keys && (p->out == c->k || p->out == c->v)))) return W4A4_ERR_SHAPE;
-  if (!p->q || !p->out || !p->kv_lens || !workspace || (tree && !tree->mask)) return W4A4_ERR_NULL;
+  if (!p->q || !p->out || !p->kv_lens || !workspace || (tree && !tree->mask && tree->width > 0))
+    return W4A4_ERR_NULL;
   if (keys && (!c->k || !c->v || !p->page_table)) return W4A4_ERR_NULL;
   if (tree && p->window > 0 && !tree->positions) return W4A4_ERR_NULL;
   if (!aligned(p->q, 16) || !aligned(p->out, 16) || !aligned(p->kv_lens, 4) || !aligned(p->q_starts, 4) ||
@@ -824,7 +825,7 @@ w4a4_status attention(const w4a4_attention* p, const w4a4_kv_cache* c, const Tre
   a.lens = static_cast<const int32_t*>(p->kv_lens);
   a.starts = static_cast<const int32_t*>(p->q_starts);
   if (tree) {
-    a.mask = static_cast<const uint8_t*>(tree->mask);
+    a.mask = static_cast<const uint8_t*>(tree->width > 0 ? tree->mask : p->q);  // (no columns: not read)
     a.pos = p->window > 0 ? static_cast<const int32_t*>(tree->positions) : nullptr;
   }
   if (!w4a4::launch_attention) return W4A4_ERR_HIP;
