@@ -258,12 +258,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
             const uint32_t mine = here >> (4 * qd);
 #pragma unroll
             for (int n = 0; n < NQ; ++n) {
-              uint32_t bits = 0;  // (bit 16 t + i)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const int in = 16 * (e >> 2) + (e & 3), j = j0 + 4 * qd + in;
-                bits |= (j < row[n].hi && (j >= row[n].lo || j < a.sinks) ? 1u : 0u) << in;
-              }
+              uint32_t bits = attn_seen(a, row[n], j0 + 4 * qd);  // (bit 16 t + i)
               if (a.mask != nullptr && j0 + KB > sq.ctx && a.mask_width > 0) {
                 const int rr = tile * BM + n * 16 + c16;
                 const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
@@ -272,20 +267,17 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) set[e] = of[min(max(node + 16 * (e >> 2) + (e & 3), 0), a.mask_width - 1)];
                 attn_vm_drain();  // (with one for each, the loop's waits would wait for every load)
-                uint32_t tree = 0, nodes = 0;
+                uint32_t tree = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const int in = 16 * (e >> 2) + (e & 3);
-                  tree |= (set[e] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
-                  nodes |= (node + in >= 0 ? 1u : 0u) << in;
-                }
-                bits = (bits & ~nodes) | (tree & nodes);
+                for (int e = 0; e < 8; ++e) tree |= (set[e] != 0 ? 1u : 0u) << (16 * (e >> 2) + (e & 3));
+                const uint32_t before = attn_below(-node);
+                bits = (bits & before) | (tree & attn_below(a.mask_width - node) & ~before);
               }
               bits &= mine;
               seen[n] = bits;
 #pragma unroll
               for (int e = 0; e < 8; ++e)
-                if (!((bits >> (16 * (e >> 2) + (e & 3))) & 1)) s[n][e >> 2][e & 3] = ATTN_NONE;
+                s[n][e >> 2][e & 3] = attn_hide(s[n][e >> 2][e & 3], ~bits, 16 * (e >> 2) + (e & 3));
             }
           }
 

@@ -309,12 +309,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const uint32_t mine = (uint32_t)(here >> (32 * t)) >> (4 * h);
-        uint32_t bits = 0;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int in = 8 * (i >> 2) + (i & 3), j = j0 + 32 * t + 4 * h + in;
-          bits |= (j < row.hi && (j >= row.lo || j < a.sinks) ? 1u : 0u) << in;
-        }
+        uint32_t bits = attn_seen(a, row, j0 + 32 * t + 4 * h);
         if (a.mask != nullptr && j0 + 32 * t + 32 > sq.ctx && a.mask_width > 0) {
           const int rr = row_of();
           const uint8_t* of = a.mask + (int64_t)(sq.token0 + (rr < rows ? attn_query(a, rr) : 0)) * a.mask_stride;
@@ -323,20 +318,16 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
 #pragma unroll
           for (int i = 0; i < 16; ++i) set[i] = of[min(max(node + 8 * (i >> 2) + (i & 3), 0), a.mask_width - 1)];
           attn_vm_drain();
-          uint32_t tree = 0, nodes = 0;
+          uint32_t tree = 0;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int in = 8 * (i >> 2) + (i & 3);
-            tree |= (set[i] != 0 && node + in < a.mask_width ? 1u : 0u) << in;
-            nodes |= (node + in >= 0 ? 1u : 0u) << in;
-          }
-          bits = (bits & ~nodes) | (tree & nodes);
+          for (int i = 0; i < 16; ++i) tree |= (set[i] != 0 ? 1u : 0u) << (8 * (i >> 2) + (i & 3));
+          const uint32_t before = attn_below(-node);
+          bits = (bits & before) | (tree & attn_below(a.mask_width - node) & ~before);
         }
         bits &= mine;
         seen[t] = bits;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (!((bits >> (8 * (i >> 2) + (i & 3))) & 1)) s[t][i] = ATTN_NONE;
+        for (int i = 0; i < 16; ++i) s[t][i] = attn_hide(s[t][i], ~bits, 8 * (i >> 2) + (i & 3));
       }
       top = fmaxf(s[0][0], s[0][1]);
 #pragma unroll
