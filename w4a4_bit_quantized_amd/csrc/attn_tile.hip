@@ -12,8 +12,8 @@
 // large library product reaches; with the loads of keys and values left out 436, with the LDS reads left out 331, the matrix
 // instructions alone 275 to 302.  64 rows per wave (half the LDS reads) need more registers than there are; tiles of eight
 // waves measured 588 against 594; one after the other instead of stepped, 590 against 562.  Heads of 64 have half the
-// products for the same exponentials: four prompts of 1000 to 4001 tokens in a window of 1024 take 78 to 90 us (three
-// workgroups on a CU instead of two, with 21 registers spilled: 101).
+// products for the same exponentials: four prompts of 1000 to 4001 tokens in a window of 1024 take 78 to 86 us (three
+// workgroups on a CU instead of two, with 21 registers spilled: 101 against 91 then).
 //
 // v_mfma_f32_32x32x16: lane l holds row l % 32 of 32, keys 8 (i / 4) + 4 (l / 32) + i % 4 of 32.
 #include "attention.h"
