@@ -462,7 +462,8 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  *               rows past the last sequence, and all rows of no sequence, are left as they were
  *   page_table  [batch, table_width] int32, row b at + b table_stride; entries that no key seen by anybody
  *               needs are not used (pages that a window has left may be given to others); an entry that
- *               names no page of the pool holds no keys: nobody sees them
+ *               names no page of the pool holds no keys: nobody sees them; not read (NULL is allowed) where the
+ *               pool has no pages or a row no entries
  *   kv_lens     [batch] int32, taken as 0 where negative, and as table_width * page_size where more
  *   q_starts    [batch + 1] int32, rising, within [0, tokens]; NULL: tokens / batch queries per sequence
  *   max_q       at least the largest n: it chooses the kernel (any other value costs time only)

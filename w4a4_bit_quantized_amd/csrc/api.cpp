@@ -782,7 +782,8 @@ w4a4_status attention_sizes(const w4a4_attention& p, const w4a4_kv_cache& c, con
   a.kv_heads = (int)c.heads;
   a.group = (int)(p.heads / c.heads);
   a.D = p.head_dim;
-  a.max_len = (int)std::min<int64_t>(p.table_width * c.page_size, kMaxDim - 64);  // (block ends stay in 32 bits)
+  // (block ends stay in 32 bits; a pool of no pages holds no keys, and the table may be missing)
+  a.max_len = c.pages == 0 ? 0 : (int)std::min<int64_t>(p.table_width * c.page_size, kMaxDim - 64);
   a.pages = (uint32_t)c.pages;
   a.page_size = (int)c.page_size;
   a.page_rows = c.page_size % 16 == 0 && c.k_token_stride <= 1 << 26 && c.v_token_stride <= 1 << 26;
@@ -806,7 +807,7 @@ w4a4_status attention(const w4a4_attention* p, const w4a4_kv_cache* c, const Tre
   if (st != W4A4_OK) return st;
   if (p->tokens == 0 || p->batch == 0) return W4A4_OK;
   if (workspace && workspace_bytes < w4a4_attention_workspace_bytes(p, c)) return W4A4_ERR_SHAPE;
-  const bool keys = c->pages > 0 && a.max_len > 0;
+  const bool keys = a.max_len > 0;
   // out would be written while other workgroups read q or the cache
   if (p->out && (p->out == p->q || (keys && (p->out == c->k || p->out == c->v)))) return W4A4_ERR_SHAPE;
   if (!p->q || !p->out || !p->kv_lens || !workspace || (tree && !tree->mask && tree->width > 0))
