@@ -17,3 +17,14 @@ def test_a_pool_of_no_pages(w4, n):
     m, pos = b.tree()
     b.dk, b.dv = b.dk[:0], b.dv[:0]
     assert (b.run_tree(w4, m, pos, window=9, sinks=2) == 0).all()
+
+
+@pytest.mark.parametrize("big", [5 - 2 ** 64, -2 ** 63 - 1, 2 ** 63, 2 ** 64 + 5])
+def test_numbers_past_64_bits(w4, big):
+    """Refused, also below zero: their lower 64 bits may be a window."""
+    b = Batch(2, [(1, 90)], 4, 2, 64, 16, "bf16")
+    for kw in (dict(window=big), dict(window=9, sinks=big)):
+        with pytest.raises(ValueError, match="out of range"):
+            b.run(w4, **kw)
+    with pytest.raises(w4.W4A4Error, match="SHAPE"):
+        b.run(w4, window=-2 ** 63)

@@ -145,6 +145,13 @@ def _i32(value, name):
     return value
 
 
+def _i64(**values):
+    """Refuses ints that the C interface's int64 does not hold (as ``_i32``, for arguments passed on as they are)."""
+    for name, value in values.items():
+        if not -2 ** 63 <= value < 2 ** 63:
+            raise ValueError(f"{name} = {value} is out of range")
+
+
 def _check(status, what):
     if status != 0:
         name = STATUS_NAMES.get(status, str(status))
@@ -1021,8 +1028,7 @@ def _attention(name, q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, 
             raise ValueError(f"max_q = {max_q}, but every sequence has {most} queries")
     if most < 0:
         raise ValueError(f"max_q = {max_q} is negative")
-    if max(window, sinks) >= 2 ** 63:  # (ctypes would drop the upper bits)
-        raise ValueError(f"window = {window} or sinks = {sinks} is out of range")
+    _i64(window=window, sinks=sinks)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
         ots, ohs = H * D, D
