@@ -3,7 +3,9 @@
 import numpy as np
 import pytest
 
-from test_gpu_attention import DTYPES, Batch, w4  # noqa: F401
+from oracle import hadamard as oh
+from test_gpu_attention import DTYPES, HALF, TINY, Batch, w4  # noqa: F401
+from test_gpu_w8a8 import dev, host
 
 pytestmark = pytest.mark.gpu
 
@@ -28,3 +30,92 @@ def test_numbers_past_64_bits(w4, big):
             b.run(w4, **kw)
     with pytest.raises(w4.W4A4Error, match="SHAPE"):
         b.run(w4, window=-2 ** 63)
+
+
+def sums_limit(res, dtype, D, keys):
+    """The bound of test_gpu_attention.py's head, A (h + 2 e) and the output's half step, for both kernels: the sums below the
+    fraction are of float32 probabilities (in the tiles 16 pairs of each 64 keys first, and one addition to the running sum: less
+    than the 32 + B there).  The reference of these rows is set by their first block and raised by none (no score passes it by
+    2^8): two factors instead of one per block, with the join's.  In f16 a probability of less than 2^-21 of the row's
+    reference is off by 2^-32 of it."""
+    o, absolute, spread, small = res
+    blocks = keys / 32 + 1
+    e = (D + 4) * 2.0 ** -23 * spread + 3 * (2.0 ** -21 + 2.0 ** -23 * spread) + 2.0 ** -23 * (blocks + 32)
+    err = absolute * (HALF[dtype] + 2 * e[..., None])
+    if dtype == "f16":
+        err = err + 2.0 ** -32 * small
+    return err + (np.abs(o) + err) * HALF[dtype] + TINY[dtype]
+
+
+def one_head(w4, n, scores, v, dtype, D=64):
+    """The last n queries of one head over keys of these scores (sums of three elements of each key) and values (keys, D): the
+    kernel's rows, and the oracle's with its bounds."""
+    l = len(scores)
+    b = Batch(20, [(n, l)], 1, 1, D, 16, dtype, poison=0.0)
+    k = np.zeros((l, D), np.float32)
+    rest = np.asarray(scores, np.float64)
+    for c in range(3):
+        k[:, c] = oh.to_f32(oh.from_f32(rest.astype(np.float32), dtype), dtype)
+        rest = rest - k[:, c]
+    j = np.arange(l)
+    for name, x in (("kc", k), ("vc", v)):
+        pool = oh.to_f32(getattr(b, name), dtype).copy()
+        pool[b.table[0, j // 16], j % 16, 0] = x
+        setattr(b, name, oh.from_f32(pool.astype(np.float32), dtype))
+    q = np.zeros((n, 1, D), np.float32)
+    q[:, :, :3] = 1.0
+    b.q = oh.from_f32(q, dtype)
+    b.dq, b.dk, b.dv = (dev(x, dtype) for x in (b.q, b.kc, b.vc))
+    got = oh.to_f32(host(b.run(w4, scale=1.0)), dtype).astype(np.float64)
+    return got, b.expected(scale=1.0)
+
+
+def within(got, res, dtype, keys, what, D=64):
+    off = ~(np.abs(got - res[0]) <= sums_limit(res, dtype, D, keys))
+    at = np.argwhere(off)
+    assert at.size == 0, (f"{what}: {len(at)} of {off.size} off, first {at[:3].tolist()}: {got[tuple(at[0])]} for "
+                          f"{res[0][tuple(at[0])]}, allowed {sums_limit(res, dtype, D, keys)[tuple(at[0])]}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 70], ids=["stream", "tiles"])
+def test_many_small_probabilities(w4, n, dtype):
+    """One strong first key, as a sink is, and tens of thousands far below it, whose probabilities are subnormal in f16 or less
+    than its smallest and together matter."""
+    l = 30000
+    for below in (9.0, 10.5, 13.0, 16.0, 17.4, 18.5):
+        print(f"\n{n} {dtype} {below}", flush=True)
+        scores = np.full(l, -below)
+        scores[0] = 0.0
+        v = np.ones((l, 64)) * np.linspace(0.5, 1.5, 64)
+        v[0] = 0.0
+        got, res = one_head(w4, n, scores, v, dtype)
+        assert (res[0][0, 0] > 2.0 ** -14).all()
+        within(got, res, dtype, l, f"{below} below")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 70], ids=["stream", "tiles"])
+def test_small_probabilities_of_one_reference(w4, n, dtype):
+    """The same in a batch of so many heads that no row's keys are cut into pieces, which would have references of their own:
+    32 sequences on the same pages, of 64 heads."""
+    D, l, heads, page, B = 64, 2048, 64, 16, 32
+    print(f"\n{n} {dtype}", flush=True)
+    b = Batch(22, [(n, l)], heads, heads, D, page, dtype)
+    k = np.zeros((b.pages, page, heads, D), np.float32)
+    j = np.arange(l)
+    low = -np.tile([9.0, 12.0, 15.0, 16.0, 17.0, 17.4, 18.0, 19.0], heads // 8).astype(np.float32)
+    k[b.table[0, j // page], j % page, :, 0] = low - 0.125 * (j % 4)[:, None].astype(np.float32)
+    k[b.table[0, 0], 0, :, 0] = 0.0
+    v = np.zeros_like(k)
+    v[b.table[0, j // page], j % page] = 100.0 * np.linspace(0.5, 1.5, D)
+    v[b.table[0, 0], 0] = 0.0
+    q = np.zeros((n, heads, D), np.float32)
+    q[..., 0] = 1.0
+    b.q, b.kc, b.vc = (oh.from_f32(x, dtype) for x in (q, k, v))
+    res = b.expected(scale=1.0)
+    got = w4.paged_attention(dev(np.tile(b.q, (B, 1, 1)), dtype), dev(b.kc, dtype), dev(b.vc, dtype), b.dt.expand(B, -1).contiguous(),
+                             b.dl.expand(B).contiguous(), scale=1.0)
+    got = oh.to_f32(host(got), dtype).astype(np.float64)
+    for s in range(B):
+        within(got[s * n:s * n + n], res, dtype, l, f"sequence {s}")

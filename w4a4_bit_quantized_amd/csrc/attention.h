@@ -10,10 +10,12 @@
 // O^T = V^T P^T, takes them (its keys are summed in whatever order both operands share).  V's operand comes from
 // the row-major LDS tile through the transposing LDS read.
 //
-// Rounding: scores, maxima, sums and outputs are float32.  The probabilities (at most 1) are rounded to the
-// tensors' 16-bit type for the matrix instruction, half a step each (2^-8 of the value in bf16, 2^-11 in f16, which
-// leaves 2^-25 for what is below 2^-14): less than the output's own rounding on average, and the sums
-// below the fraction are of the unrounded ones.
+// Rounding: scores, maxima, sums and outputs are float32.  The probabilities are rounded to the tensors' 16-bit type for
+// the matrix instruction, half a step each (2^-8 of the value in bf16, 2^-11 in f16): less than the output's own
+// rounding on average, and the sums below the fraction are of the unrounded ones.  They are taken against a
+// reference that a row's maximum passes by at most 2^8 (ATTN_SLACK), in f16 times 2^7 (SHIFT): they end at 2^15 of the 2^16
+// that f16 holds, and what is below 2^-21 of the reference is off by 2^-32 of it.  (Without the shift it was 2^-25: the
+// weight of thousands of keys with scores 15 below a sink's was off by 5 in a hundred, of those 18 below lost.)
 #pragma once
 
 #include <algorithm>
@@ -31,6 +33,7 @@ typedef __attribute__((address_space(3))) attn_short4_t attn_lds_s4;
 struct Bf16 {
   typedef bf16x8_t x8;
   static constexpr uint32_t EXP = 0x7F80;  // the exponent of infinities and NaNs
+  static constexpr float SHIFT = 0.0f;     // log2 of what probabilities are multiplied by
   static __device__ __forceinline__ float value(uint32_t bits) { return __uint_as_float(bits << 16); }
   static __device__ __forceinline__ float4_t mma16(x8 a, x8 b, float4_t c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -52,6 +55,7 @@ struct Bf16 {
 struct F16 {
   typedef half8_t x8;
   static constexpr uint32_t EXP = 0x7C00;
+  static constexpr float SHIFT = 7.0f;
   static __device__ __forceinline__ float value(uint32_t bits) {
     const uint16_t b = (uint16_t)bits;
     return (float)__builtin_bit_cast(_Float16, b);
@@ -333,6 +337,13 @@ constexpr float ATTN_NONE = -__builtin_inff();
 // The reference that exponents are taken against is raised to a row's maximum only when that has passed it by more
 // than this (in powers of two): probabilities up to 2^8 lose nothing, and rescaling becomes rare.
 constexpr float ATTN_SLACK = 8.0f;
+
+// The reference that a largest score asks for.
+template <class T>
+__device__ __forceinline__ float attn_reference(float top, float scale_log2) {
+  if constexpr (T::SHIFT == 0.0f) return top * scale_log2;
+  else return fmaf(top, scale_log2, -T::SHIFT);
+}
 
 // The second kernels' work: joins `pieces` pieces of rows 0 .. rows - 1 of a tile, whose first is row row0 of its sequence
 // and head; piece p lies in slot slot(p) of BM rows.  A row is `split` lines of DP / 4 threads, which take its pieces in

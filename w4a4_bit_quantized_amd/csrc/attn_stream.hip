@@ -286,7 +286,7 @@ __global__ __launch_bounds__(64) void attn_stream_kernel(const AttnArgs a) {
           for (int n = 0; n < NQ; ++n) {
             float top = fmaxf(fmaxf(fmaxf(s[n][0][0], s[n][0][1]), fmaxf(s[n][0][2], s[n][0][3])),
                               fmaxf(fmaxf(s[n][1][0], s[n][1][1]), fmaxf(s[n][1][2], s[n][1][3])));
-            top = attn_max16(attn_max32(top)) * a.scale_log2;
+            top = attn_reference<T>(attn_max16(attn_max32(top)), a.scale_log2);
             if (__any(top > m[n] + ATTN_SLACK)) {
               const float to = fmaxf(m[n], top), f = attn_exp2(m[n] - (to == ATTN_NONE ? 0.0f : to));
               l[n] *= f;

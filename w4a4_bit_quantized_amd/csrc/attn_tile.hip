@@ -334,7 +334,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
       for (int i = 1; i < 16; ++i) top = larger(top, s[i >> 3], i & 7);
       uint8_t* const values = lds + (2 + ODD) * L::BLOCK;
       if (attn_any_odd<T, L::BLOCK>(values, lane)) {  // (the same in all waves)
-        raise(attn_max32(top) * a.scale_log2);        // (nothing is scaled by 0 afterwards)
+        raise(attn_reference<T>(attn_max32(top), a.scale_log2));        // (nothing is scaled by 0 afterwards)
         uint64_t odd = attn_odd_rows<T, L::CPR, BN>(values, lane);
         while (odd != 0) {
           const int j = __ffsll((unsigned long long)odd) - 1;
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(64 * WAVES, DP <= 128 ? 2 : 1) void attn_tile_kerne
         __syncthreads();
       }
     }
-    top = attn_max32(top) * a.scale_log2;
+    top = attn_reference<T>(attn_max32(top), a.scale_log2);
     if (__any(top > m + ATTN_SLACK)) raise(top);
     const float ref = m == ATTN_NONE ? 0.0f : m, sc = a.scale_log2;
 
