@@ -476,8 +476,9 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  *   tree_mask   [tokens, mask_width] bytes, row t at + t mask_stride; NULL is allowed with mask_width 0
  *   positions   [tokens] int32, read with a window only
  * Keys and values that nobody sees are not read into the sums: what they hold (a page's end behind the last
- * token, pages that the window has left) does not matter.  Scores, softmax statistics and sums are float32; the probabilities are
- * rounded to dtype for the second product.  A row whose scores are all -infinity gives zeros; a NaN or +infinity
+ * token, pages that the window has left) does not matter.  Scores, softmax statistics (the denominators too) and sums are float32;
+ * the probabilities are rounded to dtype for the second product, in f16 to 2^-32 of the row's largest at the finest.  A
+ * row whose scores are all -infinity gives zeros; a NaN or +infinity
  * among them gives NaN.  Results do not depend on the stream's other work or on earlier calls, and two calls on the
  * same data give the same bits; those of one sequence may depend, in the order of their sums, on the batch it is in.
  *

@@ -119,3 +119,32 @@ def test_small_probabilities_of_one_reference(w4, n, dtype):
     got = oh.to_f32(host(got), dtype).astype(np.float64)
     for s in range(B):
         within(got[s * n:s * n + n], res, dtype, l, f"sequence {s}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 70], ids=["stream", "tiles"])
+def test_roundings_of_one_sign(w4, n, dtype):
+    """Nearly all probabilities round down, and those of the only keys with values up: the denominator is not rounded with them."""
+    h, l = HALF[dtype], 192                  # (three blocks of 64: the tile's keys are not cut into pieces)
+    scores = np.full(l, np.log1p(h * 0.98))  # 1 + 0.98 h: to 1
+    scores[:64] = 0.0                        # the reference is taken from these
+    up = 64 + 15 * np.arange(4)
+    scores[up] = np.log1p(h * 1.02)          # to 1 + 2 h
+    v = np.zeros((l, 64))
+    v[up] = np.linspace(1.0, 2.0, 64)
+    got, res = one_head(w4, n, scores, v, dtype)
+    within(got, res, dtype, l, "one sign")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n", [1, 70], ids=["stream", "tiles"])
+def test_long_even_rows(w4, n, dtype):
+    """30000 nearly equal scores, some powers of two above the first block's: the running sums take each block's as a whole."""
+    rng = np.random.default_rng(21)
+    l = 30000
+    for above in (0.0, 3.9):
+        scores = above + rng.uniform(-0.01, 0.01, l)
+        scores[:64] = 0.0
+        v = 1.0 + 0.1 * rng.standard_normal((l, 64))
+        got, res = one_head(w4, n, scores, v, dtype)
+        within(got, res, dtype, l, f"{above} above")

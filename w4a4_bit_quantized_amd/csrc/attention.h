@@ -45,11 +45,6 @@ struct Bf16 {
     typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(float2_t{a, b}, bf16x2_t));
   }
-  static __device__ __forceinline__ float sum2(uint32_t p, float c) {  // c + both values of p
-    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-    return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2_t, p), __builtin_bit_cast(bf16x2_t, 0x3F803F80u), c,
-                                           false);
-  }
 };
 
 struct F16 {
@@ -68,9 +63,6 @@ struct F16 {
   }
   static __device__ __forceinline__ uint32_t pack2(float a, float b) {
     return __builtin_bit_cast(uint32_t, half2_t{(_Float16)a, (_Float16)b});
-  }
-  static __device__ __forceinline__ float sum2(uint32_t p, float c) {
-    return __builtin_amdgcn_fdot2(__builtin_bit_cast(half2_t, p), half2_t{(_Float16)1, (_Float16)1}, c, false);
   }
 };
 
