@@ -466,7 +466,8 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  *               pool has no pages or a row no entries
  *   kv_lens     [batch] int32, taken as 0 where negative, and as table_width * page_size where more
  *   q_starts    [batch + 1] int32, rising, within [0, tokens]; NULL: tokens / batch queries per sequence
- *   max_q       at least the largest n: it chooses the kernel (any other value costs time only)
+ *   max_q       at least the largest n: it chooses the kernel (any other value costs time and workspace, and
+ *               changes results only in the order of their sums)
  *   window      0: none; otherwise the number of keys up to the query's own that are seen
  *   sinks       first keys that stay seen behind the window (no effect without one)
  *   scale       positive and finite
@@ -487,12 +488,13 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  * workspace: at least w4a4_attention_workspace_bytes(a, cache) bytes, 256-byte aligned, contents overwritten and
  * nothing kept there between calls: calls that may overlap (other streams) take one each, captured graphs that
  * run one after another may share one.  Its size depends on head_dim, tokens, heads, the cache's heads, batch and
- * max_q only.
+ * max_q only, and stays below 280 MB.
  * Errors: W4A4_ERR_UNSUPPORTED (dtype, head_dim above the maximum), W4A4_ERR_SHAPE (sizes; head_dim % 8;
  * heads % cache heads; strides negative, above 2^40 (a pool's page and
  * token strides: 2^31) or not multiples of 8; out's elements sharing an address;
  * tokens * heads or batch above 2^30; without q_starts, tokens % batch; scale; workspace too small; out == q
- * or in the cache's place), W4A4_ERR_NULL, W4A4_ERR_ALIGN.  tokens == 0 or batch == 0 launches nothing. */
+ * or in the cache's place), W4A4_ERR_NULL, W4A4_ERR_ALIGN; W4A4_ERR_HIP also where long sequences would need 2^24 or more
+ * workgroups.  tokens == 0 or batch == 0 launches nothing. */
 #define W4A4_ATTENTION_MAX_HEAD_DIM 256
 typedef struct {
   const void* q;

@@ -148,3 +148,47 @@ def test_long_even_rows(w4, n, dtype):
         v = 1.0 + 0.1 * rng.standard_normal((l, 64))
         got, res = one_head(w4, n, scores, v, dtype)
         within(got, res, dtype, l, f"{above} above")
+
+
+# (queries, keys) of every sequence; the second of each kind has rows at the border between the kernels
+MIXED = [([(1, 20 + 9 * i) for i in range(100)] + [(256, 3000)], 8, 2, 64, 16), ([(32, 90)] * 30 + [(33, 60)] * 2 + [(400, 900), (3, 700)], 2, 2, 128, 16),
+         ([(1, 300)] * 7 + [(17, 2000)] + [(1, 40)] * 7 + [(60, 900)], 1, 1, 128, 24), ([(4, 100)] * 40 + [(5, 90), (129, 2000), (2, 2)], 8, 1, 256, 32)]
+
+
+@pytest.mark.parametrize("shape", MIXED, ids=[str(i) for i in range(len(MIXED))])
+def test_short_sequences_among_long_ones(w4, shape):
+    """The tiles of a batch of mostly short sequences, in both ways of numbering them: everything computed, within the workspace."""
+    import torch
+    print(f"\n{shape[1:]}", flush=True)
+    b = Batch(30, *shape, "bf16", tail=7)
+    for order in (False, True):
+        if order:
+            b = Batch(31, shape[0][::-1], *shape[1:], "bf16", tail=200)
+        for max_q in (b.max_q, None):
+            need = w4.attention_workspace_bytes(b.dq, b.dk, b.dv, len(b.both), max_q)
+            ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+            out = torch.full_like(b.dq, 7.0)
+            b.check(b.run(w4, workspace=ws[:need], out=out, max_q=max_q))
+            assert (ws[need:] == 0xFF).all() and (out[int(b.starts[-1]):] == 7).all()
+            m, pos = b.tree()
+            b.check(b.run_tree(w4, m, pos, max_q=max_q), "tree", mask=m)
+
+
+@pytest.mark.parametrize("each", [1, 9, 40])
+def test_uniform_batch_with_a_loose_max_q(w4, each):
+    """From C, a uniform batch (no q_starts) may state any max_q."""
+    import ctypes
+    import torch
+    from w4a4_bit_quantized_amd import binding
+    lib = w4.load_library()
+    b = Batch(32, [(each, each + 11 * i) for i in range(50)], 4, 1, 64, 16, "bf16")
+    cache, _ = binding._kv_cache(b.dk, b.dv, b.dq.dtype, b.dq.device)
+    for max_q in (each, b.T, 1):
+        out = torch.empty_like(b.dq)
+        a = binding.Attention(b.dq.data_ptr(), 256, 64, out.data_ptr(), 256, 64, b.T, 4, b.dt.data_ptr(), b.dt.stride(0), b.dt.shape[1],
+                              b.dl.data_ptr(), None, 50, max_q, 0, 0, 0.125, 64, 0)
+        ra, rc = ctypes.byref(a), ctypes.byref(cache)
+        ws = torch.empty(lib.w4a4_attention_workspace_bytes(ra, rc), dtype=torch.uint8, device="cuda")
+        st = torch.cuda.current_stream().cuda_stream
+        assert lib.w4a4_paged_attention(ra, rc, ws.data_ptr(), ws.numel(), st) == 0
+        b.check(out, f"max_q = {max_q}")

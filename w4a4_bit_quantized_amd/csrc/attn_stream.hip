@@ -450,28 +450,34 @@ hipError_t run_dim(const AttnArgs& a, int64_t rows, void* workspace, hipStream_t
 constexpr int STREAM_ROWS = 32;
 static int stream_rows(const AttnArgs& a) { return (int64_t)a.batch * a.kv_heads <= 16 ? 16 : STREAM_ROWS; }
 
-size_t attention_workspace_bytes(const AttnArgs& a, int64_t max_q) {
+// The tiles of a call take sequences of more rows than this.  Of a batch whose sequences have half of max_q queries on average
+// they take the short ones too; in one of prompts among single tokens, a second launch for those is worth its time (4096 keys
+// each, us: 512 queries and 63 sequences of one 241, 265 by the tiles alone; 12 sequences of 64 and 4 of 4 90, 111 by
+// both).
+static int tiles_from(const AttnArgs& a, int64_t max_q) {
+  return (int64_t)a.batch * max_q <= 2 * (int64_t)a.tokens ? 0 : stream_rows(a);
+}
+
+size_t attention_workspace_bytes(const AttnArgs& args, int64_t max_q) {
+  AttnArgs a = args;
   const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
   const size_t W = 1 << log2_waves(DP), BM = STREAM_ROWS;
   const size_t stream = W * 32 + 2 * W * BM * 8 + 2 * W * BM * DP * 4;
-  return max_q * a.group <= stream_rows(a) ? stream : std::max(stream, attention_tile_bytes(a, max_q));
+  if (max_q * a.group <= stream_rows(a)) return stream;
+  a.rows_from = tiles_from(a, max_q);
+  return std::max(stream, attention_tile_bytes(a, max_q));
 }
 
 hipError_t launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream) {
   a.rows_from = 0;
   a.rows_to = 0x7FFFFFFF;
   int64_t rows = max_q * a.group;
-  const int few = stream_rows(a);
-  if (rows > few) {
-    // Of a batch whose sequences have half of max_q queries on average, the tiles take the short ones too; in one of
-    // prompts among single tokens, the second launch is worth its time (4096 keys each, us: 512 queries and 63
-    // sequences of one 241, 265 by the tiles alone; 12 sequences of 64 and 4 of 4 90, 111 by both).
-    const bool all = (int64_t)a.batch * max_q <= 2 * (int64_t)a.tokens;
-    if (!all) a.rows_from = few;
+  if (rows > stream_rows(a)) {
+    a.rows_from = tiles_from(a, max_q);
     hipError_t e = launch_attention_tile(a, dtype, max_q, workspace, stream);
-    if (e != hipSuccess || all) return e;
+    if (e != hipSuccess || a.rows_from == 0) return e;
+    a.rows_to = rows = a.rows_from;
     a.rows_from = 0;
-    a.rows_to = rows = few;
   }
   return dtype == 0 ? run_dim<Bf16>(a, rows, workspace, stream) : run_dim<F16>(a, rows, workspace, stream);
 }

@@ -56,8 +56,12 @@ __device__ __forceinline__ void each(F&& f) {
   }
 }
 
-// Tile slots.  Sequence s's tiles are slots first(s), first(s) + 1, ..., with first(s) = token0(s) group / BM + s:
-// they are at least as many as its tiles (a slot of no tile has a number below 0 or past its sequence's rows).
+// Tile slots.  Sequence s's tiles are slots first(s), first(s) + 1, ..., of which there are at least as many as it has
+// tiles (a slot of no tile has a number below 0 or past its sequence's rows).  With x rows before the sequence, first(s) is
+//   x / BM + s           for any sequences: R rows take at least R / BM + 1 slots, the whole batch rows / BM + batch;
+//   x slot_rate / BM     where those of up to rows_from rows are not the tiles', slot_rate = 1 + BM / rows_from: R > rows_from
+//                        rows take at least R / BM + R / rows_from, cut off, so also R / BM + 1; fewer than the others in a batch of
+//                        many short sequences among long ones.
 struct TileOf {
   int seq, tile;
 };
@@ -68,7 +72,10 @@ __device__ __forceinline__ TileOf tile_at(const AttnArgs& a, int slot) {
     const int s = slot / per;
     return {min(s, a.batch - 1), s < a.batch ? slot - s * per : -1};
   }
-  auto first = [&](int s) { return min(max(a.starts[s], 0), a.tokens) * a.group / BM + s; };
+  auto first = [&](int s) {
+    const int x = min(max(a.starts[s], 0), a.tokens) * a.group;
+    return a.slot_rate == 0 ? x / BM + s : (int)((int64_t)x * a.slot_rate / BM);
+  };
   int lo = 0, hi = a.batch;  // first(lo) <= slot < first(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -472,16 +479,28 @@ __global__ __launch_bounds__(256) void attn_tile_join_kernel(const AttnArgs a, c
 // about the workgroups that the GPU holds (sequences' last tiles are half full on average).  512 queries of 32 heads
 // over 8 and 16384 keys, us: 160 with 512 workgroups, 195 with 256, 173 with 1024; heads of 256 dimensions, one workgroup per CU:
 // 170 with 256, 186 with 512.  At most 32 (16 queries, 32768 keys: 60 with 16, 47 with 32, 51 with 64).
+// Slots are at most about six times the tiles that this counts on, so that grid and workspace stay in proportion to
+// what the GPU holds: a piece of 256 queries among 255 single tokens, 32 heads over 8, has 79 slots (271 in the
+// first way of numbering) and 168 MB of pieces (577).
 struct TilePlan {
   int rows;
   int64_t slots;
-  int pieces;
+  int pieces, slot_rate;
 };
 TilePlan plan(const AttnArgs& a, int64_t max_q) {
   TilePlan p;
   p.rows = 128;
   const int64_t rows = (int64_t)a.tokens * a.group, sequences = (a.tokens + max_q - 1) / max_q;
   p.slots = rows / p.rows + a.batch;
+  p.slot_rate = 0;
+  if (a.rows_from > 0) {
+    const int rate = 1 + (p.rows + a.rows_from - 1) / a.rows_from;
+    const int64_t slots = rows * rate / p.rows;
+    if (slots < p.slots) {
+      p.slots = slots;
+      p.slot_rate = rate;
+    }
+  }
   const int64_t wgs = (rows / p.rows + (sequences + 1) / 2) * a.kv_heads, resident = a.D <= 128 ? 512 : 256;
   p.pieces = (int)std::min<int64_t>(32, std::max<int64_t>(1, (resident + wgs / 2) / wgs));
   return p;
@@ -493,8 +512,9 @@ hipError_t run(AttnArgs a, int64_t max_q, void* workspace, hipStream_t st) {
   const TilePlan p = plan(a, max_q);
   if (p.rows != L::BM) return hipErrorInvalidValue;
   const int64_t wgs = p.slots * a.kv_heads * p.pieces;
-  if (wgs > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (wgs >= 0x1000000) return hipErrorInvalidConfiguration;  // (a grid's threads are counted in 32 bits, and so are tiles' rows)
   a.pieces = p.pieces;
+  a.slot_rate = p.slot_rate;
   // p pieces take blocks / p passes of about 1 us, and write and read p tokens heads DP floats (twice 0.1 us per 1000 rows of
   // 128 and piece): least for p = sqrt(blocks 5000 / (tokens heads)).  (32 heads, us: 64 queries and 8192 keys 36, 49 with all
   // 32 pieces; 16 queries and 8192 keys 22 and 31; 16 and 32768 39 and 47)

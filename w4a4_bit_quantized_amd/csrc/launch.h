@@ -159,7 +159,7 @@ struct AttnArgs {
   float scale_log2;  // scale * log2(e)
   int window, sinks;
   // set by the launcher: sequences of more than rows_from and at most rows_to rows are this launch's
-  int rows_from, rows_to, least, log2_waves, pieces;
+  int rows_from, rows_to, least, log2_waves, pieces, slot_rate;
   float piece_gain;
   int32_t* desc;
   float *stats, *part;
@@ -168,7 +168,7 @@ struct AttnArgs {
 size_t W4A4_KERNELS attention_workspace_bytes(const AttnArgs& a, int64_t max_q);
 hipError_t W4A4_KERNELS launch_attention(AttnArgs a, int dtype, int64_t max_q, void* workspace, hipStream_t stream);
 
-// Its kernel for many rows per sequence (called by launch_attention).
+// Its kernel for many rows per sequence (called by launch_attention, with a.rows_from set).
 size_t attention_tile_bytes(const AttnArgs& a, int64_t max_q);
 hipError_t launch_attention_tile(const AttnArgs& a, int dtype, int64_t max_q, void* workspace, hipStream_t stream);
 
