@@ -6,6 +6,7 @@ import random
 
 import pytest
 
+import w4a4_bit_quantized_amd as w4
 from test_cache_abi import cache, lib  # noqa: F401
 from w4a4_bit_quantized_amd import binding
 
@@ -45,3 +46,43 @@ def test_any_shape(lib):
         mq = min(T, rng.choice([T, max(1, T // B), int(2 ** rng.uniform(0, 17))]))
         if T * H <= 1 << 30:
             assert 0 < need(lib, T, B, H, heads, D, mq) <= bound(D), (T, B, H, heads, D, mq)
+
+
+def tensors(T=6, H=4, heads=2, D=64, dtype=None):
+    import torch
+    dtype = dtype or torch.bfloat16
+    return torch.zeros(T, H, D, dtype=dtype), *(torch.zeros(8, 16, heads, D, dtype=dtype) for _ in range(2))
+
+
+def test_helper_gives_what_the_call_asks_for(lib):
+    t = tensors(T=256, H=32, heads=8, D=128)
+    size = lambda *args, **kw: w4.attention_workspace_bytes(*t, *args, **kw)
+    assert size(256) == need(lib, 256, 256, 32, 8, 128, 256) > 4 * size(256, uniform=True)
+    assert size(256, uniform=True) == size(256, 1) == size(256, 1, uniform=True) == need(lib, 256, 256, 32, 8, 128, 1)
+    assert size(2, uniform=True) == size(2, 128) and size(256, 2 ** 80) == size(256)
+    for args, kw in (((3,), dict(uniform=True)), ((0,), dict(uniform=True)), ((2, 100), dict(uniform=True)), ((-1,), {}), ((256, -1), {}),
+                     ((2 ** 64 + 256,), {}), ((5 - 2 ** 64,), {}), ((2 ** 30 + 1,), {}), ((256, 5 - 2 ** 64), {})):
+        with pytest.raises(ValueError):
+            size(*args, **kw)
+
+
+def test_helper_refuses_what_the_call_refuses(lib):
+    import torch
+    q, k, v = tensors()
+    for bad in ((q[..., :32], k, v), (q, k[..., :60], v[..., :60]), (q[:, :3], k, v), (q, k[:, :, :0], v[:, :, :0]),
+                tensors(D=60), tensors(D=264), (torch.zeros(6, 4, 68, dtype=q.dtype)[..., 2:66].as_strided((6, 4, 64), (270, 66, 1)), k, v)):
+        with pytest.raises(ValueError):
+            w4.attention_workspace_bytes(*bad, 2)
+    with pytest.raises((TypeError, ValueError)):
+        w4.attention_workspace_bytes(*tensors(dtype=torch.float32), 2)
+    assert w4.attention_workspace_bytes(*tensors(T=0), 2) > 0 and w4.attention_workspace_bytes(*tensors(T=0), 0, uniform=True) > 0
+
+
+def test_uniform_batches_need_no_more_than_others(lib):
+    """A workspace for a call with q_starts and the default max_q holds the same batch without them."""
+    rng = random.Random(3)
+    for _ in range(20000):
+        D, heads = rng.choice([64, 128, 256]), rng.choice([1, 2, 4, 8, 16])
+        H = heads * rng.choice([1, 2, 3, 4, 5, 7, 8, 16])
+        B, each = int(2 ** rng.uniform(0, 11)), int(2 ** rng.uniform(0, 9))
+        assert need(lib, B * each, B, H, heads, D, each) <= need(lib, B * each, B, H, heads, D, B * each), (B, each, H, heads, D)

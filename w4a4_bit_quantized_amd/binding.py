@@ -1071,13 +1071,30 @@ def _attention(name, q, k_cache, v_cache, page_table, kv_lens, q_starts, max_q, 
     return out
 
 
-def attention_workspace_bytes(q, k_cache, v_cache, batch, max_q=None):
-    """Bytes of workspace of ``paged_attention`` and ``tree_attention`` for q and a cache of these shapes."""
+def attention_workspace_bytes(q, k_cache, v_cache, batch, max_q=None, uniform=False):
+    """Bytes of workspace of ``paged_attention`` and ``tree_attention`` for q and a cache of these shapes: of a call with q_starts
+    and this max_q (default T, as there), or, where ``uniform`` is set, of one without q_starts, which needs no more."""
     T, H, D, ts, hs = _heads_view(q, "q")
-    cache, _ = _kv_cache(k_cache, v_cache, q.dtype, q.device)
-    a = Attention(None, ts, hs, None, H * D, D, T, H, None, 0, 0, None, 1, batch, T if max_q is None else min(max_q, T), 0, 0, 1.0, D,
+    cache, shape = _kv_cache(k_cache, v_cache, q.dtype, q.device)
+    if shape[3] != D or shape[2] == 0 or H % shape[2] != 0:
+        raise ValueError(f"q has {H} heads of {D}, the cache {shape[2]} of {shape[3]}")
+    most = T if max_q is None else max_q
+    _i64(batch=batch)
+    if uniform:
+        if batch < 0 or (batch and T % batch) or (T and not batch):
+            raise ValueError(f"{T} queries are not the same number for each of {batch} sequences")
+        most = T // batch if batch else 0
+        if max_q is not None and max_q < most:
+            raise ValueError(f"max_q = {max_q}, but every sequence has {most} queries")
+    if most < 0:
+        raise ValueError(f"max_q = {max_q} is negative")
+    a = Attention(None, ts, hs, None, H * D, D, T, H, None, 0, 0, None, 1, batch, min(most, T), 0, 0, 1.0, D,
                   _dtype_code(q.dtype, "q"))
-    return int(load_library().w4a4_attention_workspace_bytes(ctypes.byref(a), ctypes.byref(cache)))
+    need = int(load_library().w4a4_attention_workspace_bytes(ctypes.byref(a), ctypes.byref(cache)))
+    if need == 0:  # (a call that is accepted has some)
+        raise ValueError(f"attention takes no {tuple(q.shape)} of {q.dtype} with strides {q.stride()}, cache {tuple(shape)} with "
+                         f"{k_cache.stride()} and {v_cache.stride()}, batch {batch}")
+    return need
 
 
 def paged_attention(q, k_cache, v_cache, page_table, kv_lens, q_starts=None, max_q=None, scale=None, window=0, sinks=0,
