@@ -480,7 +480,9 @@ w4a4_status w4a4_kv_append(const w4a4_heads* q, const w4a4_heads* k, const w4a4_
  * token, pages that the window has left) does not matter.  Scores, softmax statistics (the denominators too) and sums are float32;
  * the probabilities are rounded to dtype for the second product, in f16 to 2^-32 of the row's largest at the finest.  A
  * row whose scores are all -infinity gives zeros; a NaN or +infinity
- * among them gives NaN.  Results do not depend on the stream's other work or on earlier calls, and two calls on the
+ * among them gives NaN.  A NaN among the values that a query sees gives NaN in that element, an infinity infinity, or NaN where
+ * its probability is 0 in dtype or float32; bf16 values near the type's largest may overflow the sums, whose probabilities
+ * reach 2^8 each before the division.  Results do not depend on the stream's other work or on earlier calls, and two calls on the
  * same data give the same bits; those of one sequence may depend, in the order of their sums, on the batch it is in.
  *
  * out shares no element with q, the cache, the arrays or the workspace.

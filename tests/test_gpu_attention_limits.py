@@ -192,3 +192,34 @@ def test_uniform_batch_with_a_loose_max_q(w4, each):
         st = torch.cuda.current_stream().cuda_stream
         assert lib.w4a4_paged_attention(ra, rc, ws.data_ptr(), ws.numel(), st) == 0
         b.check(out, f"max_q = {max_q}")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("strong", [2, 229], ids=["before", "after"])
+@pytest.mark.parametrize("at", [40, 100, 240], ids=str)
+@pytest.mark.parametrize("n", [1, 70], ids=["stream", "tiles"])
+def test_infinite_values_of_no_weight(w4, n, at, strong, dtype):
+    """An infinite value whose probability is 0 in float32, in blocks that a mask cuts and others, before and behind the largest
+    score: that element of the rows that see it is infinite or NaN, everything else is as without it."""
+    l, D = 300, 64
+    b = Batch(33, [(n, l)], 1, 1, D, 16, dtype)
+    k = oh.to_f32(b.kc, dtype)
+    k[..., 0] = 0.0
+    k[b.table[0, strong // 16], strong % 16, 0, 0] = 120.0
+    q = oh.to_f32(b.q, dtype) * 0.05
+    q[..., 0] = 1.0
+    b.q, b.kc = oh.from_f32(q, dtype), oh.from_f32(k, dtype)
+    b.dq, b.dk = dev(b.q, dtype), dev(b.kc, dtype)
+    for window in (0, 220):  # (the first blocks of 64 are cut by the window, the last ones by the queries)
+        kw = dict(window=window, sinks=3 if window else 0, scale=1.0)
+        ref = oh.to_f32(host(b.run(w4, **kw)), dtype)
+        b.check(b.run(w4, **kw), "without", **kw)
+        old = b.dv.clone()
+        b.dv[int(b.table[0, at // 16]), at % 16, 0, 5] = float("inf")
+        got = oh.to_f32(host(b.run(w4, **kw)), dtype)
+        b.dv = old
+        p = l - n + np.arange(n)
+        sees = (at <= p) & ((window == 0) | (at > p - window))
+        assert not np.isfinite(got[sees, 0, 5]).any() and not (got[sees, 0, 5] == -np.inf).any()
+        got[sees, 0, 5] = ref[sees, 0, 5]
+        assert (got == ref).all()

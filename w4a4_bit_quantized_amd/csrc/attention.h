@@ -269,7 +269,9 @@ __device__ __forceinline__ typename T::x8 attn_read_vt(const uint8_t* __restrict
 
 // Infinities and NaNs among the values of keys that some of a tile's rows see and others do not.  In the product, the
 // others' probability 0 times such a value would be a NaN.  So in a block that a mask cuts, the values are looked
-// through first; those rows that see such a value get it added (their probability is positive), and it is set to 0 for the product.
+// through first; those rows that see such a value get it added, and it is set to 0 for the product.  (Of an infinity that is
+// its product with any positive probability.  One that is too small for the types, 0 here, gives a NaN in the product of
+// a block that no mask cuts, and a later factor of 0 makes a NaN of the infinity: infinite or NaN in either case.)
 // A lane looks at 16 bytes of every 1024 of the tile.
 template <class T>
 __device__ __forceinline__ uint32_t attn_odd(uint32_t w) {  // the halves of w that are infinite or NaN, as masks
