@@ -13,6 +13,11 @@
 // keys 16 us, of which finding the run takes 1.3, its queries and pages 2.3, the first keys 1.8, and the four blocks of a run
 // 6.  Runs of four waves that share the rows' pieces in LDS gained nothing over one-wave workgroups.
 //
+// Registers: 138 to 310, so that LDS alone limits the waves of a CU (8 at 64 dimensions, 4 at 128, 2 at 256).  Heads of
+// 256 with 17 to 32 rows need 484 to 512 and spill 6 to 12 more, to accumulation registers or to memory (a spill only makes the
+// counted waits longer): 64 sequences of 4 and of 6 queries over 4096 keys, 16 heads over 4, 184 and 225 us for the same 177 us
+// of bytes.
+//
 // v_mfma_f32_16x16x32: lane l holds row l % 16 of the tile's NQ blocks of 16 rows, keys 4 (l / 16) .. + 3 of 16.
 #include "attention.h"
 
@@ -26,8 +31,10 @@ constexpr int KB = 32;  // keys of a block
 // (64 sequences of 37 to 8191 keys: 190 us with 0, 183, 184, 180 and 184 with 1 to 4)
 constexpr int START = 3;
 
-// 16 bytes per lane from `src` to LDS at dst + 16 lane, not kept in the caches: nobody reads them again (64 sequences
-// of 4096 keys, 8 heads of 128: 172 us, 191 with ordinary loads).
+// 16 bytes per lane from `src` to LDS at dst + 16 lane, not kept in the caches: of keys that one sequence has to itself, as in
+// most batches, nobody reads them again (64 sequences of 4096 keys, 8 heads of 128: 173 us, 198 with ordinary loads).  Where
+// they are read again it costs some: of 4096 keys half shared by all 64 170 against 161, 3968 shared 161 against 154; several tiles
+// per sequence, 16 times 24 queries with max_q stated as 1, 285 against 245.
 __device__ __forceinline__ void load16(const uint8_t* src, uint8_t* dst) {
   __builtin_amdgcn_global_load_lds(src, (attn_lds_void*)dst, 16, 0, 2);
 }

@@ -6,14 +6,16 @@
 // between the exponentials of this one and its product with the values.  With few tiles, each tile's blocks are
 // cut into equal pieces, one per workgroup, whose results a second kernel joins.
 //
-// Bound: the matrix cores, and next to them the LDS.  A block's operands are read from LDS by each wave: a wave of 32 rows
-// reads 2 BN DP 2 bytes for its 4 BN 32 DP flops, so that LDS reads and direct loads together take about as long as the matrix
-// instructions.  One prompt of 8192 tokens, 32 heads of 128 over 8: 545 to 605 us, 0.91 to 1.0 PFLOP/s of the 1.47 that a
-// large library product reaches; with the loads of keys and values left out 436, with the LDS reads left out 331, the matrix
-// instructions alone 275 to 302.  64 rows per wave (half the LDS reads) need more registers than there are; tiles of eight
-// waves measured 588 against 594; one after the other instead of stepped, 590 against 562.  Heads of 64 have half the
-// products for the same exponentials: four prompts of 1000 to 4001 tokens in a window of 1024 take 78 to 86 us (three
-// workgroups on a CU instead of two, with 21 registers spilled: 101 against 91 then).
+// Bound: the SIMDs' time, of which the matrix instructions take one half and the vector instructions (exponentials, maxima,
+// sums, addresses) nearly the other.  One prompt of 8192 tokens, 32 heads of 128 over 8: 544 to 603 us, 0.91 to 1.0 PFLOP/s of the
+// 1.93 that matrix instructions on random operands reach; matrix cores busy 0.50 of the cycles, vector instructions 0.51, LDS
+// reads 0.26 of the LDS's cycles without bank conflicts, waves waiting 0.24 of their time, at 1.8 GHz.  Left out in copies of an
+// earlier state, which also lowers the power and so raises the clock: the loads of keys and values 436 us, the LDS reads too 331,
+// all but the matrix instructions 275 to 302.  64 rows per wave (half the LDS reads) need more registers than two workgroups of a
+// CU have; tiles of eight waves measured 588 against 594; one after the other instead of stepped, 590 against 562.  Heads of
+// 64 have half the products for the same exponentials: four prompts of 1000 to 4001 tokens in a window of 1024 take 72 to 86 us,
+// matrix cores busy 0.18, vector 0.44, waves waiting 0.28, 1.4 waves of the 2 that fit on a SIMD (three
+// workgroups on a CU, with 21 registers spilled: 101 against 91 then).
 //
 // v_mfma_f32_32x32x16: lane l holds row l % 32 of 32, keys 8 (i / 4) + 4 (l / 32) + i % 4 of 32.
 #include "attention.h"

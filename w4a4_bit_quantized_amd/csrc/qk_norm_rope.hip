@@ -171,9 +171,10 @@ __host__ __device__ constexpr int row_stride(int D) { return 2 * D + 16; }
 //
 // CACHE: the heads of v follow those of k.  k and v go to the token's place in a paged cache, v as it is; each
 // pass's threads find the places while the angles are formed (a 64-bit division per token), and items of tokens
-// that have none store nothing.  Registers for six workgroups per CU, as many as MAX_WGS counts on (8192 tokens of 32 + 8 + 8
-// heads of 128: 38.7 us, 5.2 TB/s; with the five that 90 registers allow 40.7; eight spill: 55; loads that
-// are not kept in the caches, where a projection has just left q, k and v: 51).
+// that have none store nothing.  Registers for six workgroups per CU, as many as MAX_WGS counts on: 80, of which the vector
+// and the element-wise forms spill 4 to 6 (20 to 28 bytes; the staged form none), and still the fastest: 8192 tokens of 32 + 8 +
+// 8 heads of 128 38.7 us, 5.2 TB/s; with the five workgroups that 90 registers allow 40.7; for eight, which spill far more, 55.
+// (Loads that are not kept in the caches, where a projection has just left q, k and v: 51.)
 template <int DT, int V, bool INTER, int IT, int UN, bool STAGED, bool CACHE>
 __global__ __launch_bounds__(RT, CACHE ? 6 : 1) void qk_norm_rope_kernel(const RopeArgs a, const CacheArgs cache) {
   static_assert(!STAGED || (DT != 2 && V == 1 && IT == 4 && UN == 1 && !INTER), "the staged form");
