@@ -465,8 +465,8 @@ static int tiles_from(const AttnArgs& a, int64_t max_q) {
   return (int64_t)a.batch * max_q <= 2 * (int64_t)a.tokens ? 0 : stream_rows(a);
 }
 
-// At least the streams' share for 32 rows, also where 16 are used or the tiles take all: a program that has one workspace for its
-// prompts and for its single tokens sizes it by either.  (For one token 34 MB at 128 dimensions, half of which is used.)
+// At least the streams' share for 32 rows, also where 16 are used or the tiles take all, so that a workspace sized for prompts whose
+// keys are not cut holds single tokens' calls too.  (For one token 34 MB at 128 dimensions, half of which is used.)
 size_t attention_workspace_bytes(const AttnArgs& args, int64_t max_q) {
   AttnArgs a = args;
   const int DP = a.D <= 64 ? 64 : a.D <= 128 ? 128 : 256;
